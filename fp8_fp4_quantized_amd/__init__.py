@@ -27,6 +27,7 @@ MODE_PREFILL, MODE_DECODE, MODE_VERIFY = 0, 1, 2
 STATUS_ID_RANGE, STATUS_PAGE_RANGE, STATUS_PT_RANGE = 1, 2, 4
 STATUS_LATENT_RANGE, STATUS_POS_RANGE, STATUS_REQ_RANGE = 8, 16, 32
 STATUS_TOKEN_RANGE = 64
+STATUS_NO_PAGE = 128
 
 
 class KvcError(RuntimeError):
@@ -65,6 +66,34 @@ class kvc_compress_args(C.Structure):
     ]
 
 
+class kvc_slot_map_args(C.Structure):
+    _fields_ = [
+        ("ratio", C.c_int32), ("page_size", C.c_int32), ("num_pages", C.c_int64),
+        ("num_slots", C.c_int32), ("token_stride", C.c_int32),
+        ("lens", C.c_void_p), ("new_lens", C.c_void_p), ("depth", C.c_void_p),
+        ("page_table", C.c_void_p), ("pt_stride", C.c_int64), ("pt_width", C.c_int64),
+        ("free_pages", C.c_void_p), ("n_free", C.c_int64), ("max_tokens", C.c_int64),
+        ("offsets", C.c_void_p), ("start_pos", C.c_void_p), ("out_loc", C.c_void_p),
+        ("positions", C.c_void_p), ("token_to_req", C.c_void_p), ("totals", C.c_void_p),
+        ("status", C.c_void_p),
+    ]
+
+
+class kvc_attend_args(C.Structure):
+    _fields_ = [
+        ("ratio", C.c_int32), ("num_heads", C.c_int32), ("num_slots", C.c_int32),
+        ("draft_len", C.c_int32),
+        ("q", C.c_void_p), ("q_stride", C.c_int64), ("q_head_stride", C.c_int64),
+        ("q_rows", C.c_int64),
+        ("offsets", C.c_void_p), ("start_pos", C.c_void_p),
+        ("page_table", C.c_void_p), ("pt_stride", C.c_int64), ("pt_width", C.c_int64),
+        ("tree", C.c_void_p), ("scale", C.c_float), ("sink", C.c_void_p),
+        ("out", C.c_void_p), ("out_stride", C.c_int64), ("out_head_stride", C.c_int64),
+        ("lse", C.c_void_p), ("cache", kvc_cache),
+        ("workspace", C.c_void_p), ("workspace_bytes", C.c_int64), ("status", C.c_void_p),
+    ]
+
+
 # symbol -> (restype, argtypes); the same list as include/kvc.h
 _VP, _I32, _I64 = C.c_void_p, C.c_int32, C.c_int64
 SIGNATURES = {
@@ -82,6 +111,10 @@ SIGNATURES = {
     "kvc_kvbuf_begin_forward": (None, [_VP]),
     "kvc_dequant_gather_reuse": (C.c_int, [_VP, C.POINTER(kvc_cache), _VP, _I64, _VP, _I64, _VP,
                                            _I64, _VP, _VP, _VP]),
+    "kvc_slot_map": (C.c_int, [C.POINTER(kvc_slot_map_args), _VP]),
+    "kvc_attend_workspace": (C.c_int, [_I32, _I64, _I32, C.POINTER(_I64)]),
+    "kvc_attend_prefill": (C.c_int, [C.POINTER(kvc_attend_args), _VP]),
+    "kvc_attend_tree": (C.c_int, [C.POINTER(kvc_attend_args), _VP]),
     "kvc_last_error": (C.c_char_p, []),
     "kvc_version": (C.c_int, []),
 }
@@ -407,3 +440,170 @@ def prepare_dequant_gather(cache: Cache, page_table: torch.Tensor | None, ids: t
             _dense(ids, _I32_T, "ids"), ids.numel(), _rows(out, _B16_T, "out"), out.stride(0),
             _opt(status, _dense, _I32_T, "status"))
     return Prepared(lib().kvc_dequant_gather, args, (d, cache, page_table, ids, out, status))
+
+
+# ------------------------------------------------------------------ slot map
+def _one_device(**tensors):
+    """The device that every given tensor is on."""
+    dev = None
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if dev is None:
+            dev = t.device
+        _need(t.device == dev, f"{name}: on {t.device}, other arguments on {dev}")
+    return dev
+
+
+def _pt_stride(page_table) -> int:
+    """Entries between page-table rows (of a single row: its width, whatever
+    stride the tensor carries)."""
+    return page_table.stride(0) if page_table.shape[0] > 1 else page_table.shape[1]
+
+
+def _call_on(dev, stream, fn, args) -> None:
+    """One call with ``dev`` as the current device, on ``stream`` (default:
+    that device's current stream)."""
+    if dev.index is None or dev.index == torch.cuda.current_device():
+        _check(fn(C.byref(args), _stream(stream)))
+        return
+    with torch.cuda.device(dev):
+        _check(fn(C.byref(args), _stream(stream)))
+
+
+def kvc_slot_map(*, ratio: int, page_size: int, num_pages: int, lens: torch.Tensor,
+                 page_table: torch.Tensor, free_pages: torch.Tensor,
+                 new_lens: torch.Tensor | None = None, token_stride: int = 0,
+                 depth: torch.Tensor | None = None, offsets: torch.Tensor | None = None,
+                 start_pos: torch.Tensor | None = None, out_loc: torch.Tensor | None = None,
+                 positions: torch.Tensor | None = None, token_to_req: torch.Tensor | None = None,
+                 totals: torch.Tensor | None = None, max_tokens: int | None = None,
+                 status: torch.Tensor | None = None, stream=None) -> None:
+    """The batch tables of one step from the request lengths ``lens [S]`` and
+    ``new_lens [S]`` (default: ``token_stride`` each): new pages of
+    ``free_pages`` entered in ``page_table [S, pages]``, and the outputs
+    ``offsets [2, S]``, ``start_pos [S]``, ``out_loc`` / ``positions`` /
+    ``token_to_req [max_tokens]``, ``totals [4]`` that are given.
+    ``max_tokens`` defaults to the smallest per-token output."""
+    S = lens.numel()
+    dev = _one_device(lens=lens, new_lens=new_lens, depth=depth, page_table=page_table,
+                      free_pages=free_pages, offsets=offsets, start_pos=start_pos, out_loc=out_loc,
+                      positions=positions, token_to_req=token_to_req, totals=totals, status=status)
+    per_token = {"out_loc": out_loc, "positions": positions, "token_to_req": token_to_req,
+                 "depth": depth}
+    sizes = [t.numel() for t in per_token.values() if t is not None]
+    if max_tokens is None:
+        max_tokens = min(sizes, default=S * token_stride)
+    for name, t in per_token.items():
+        _need(t is None or t.numel() >= max_tokens,
+              f"{name}: {0 if t is None else t.numel()} entries for max_tokens = {max_tokens}")
+    _need(new_lens is None or new_lens.numel() >= S, f"new_lens: fewer than {S} entries")
+    _need(page_table.dim() == 2 and page_table.shape[0] >= S,
+          f"page_table: shape {tuple(page_table.shape)}, need {S} rows")
+    _need(offsets is None or offsets.numel() >= 2 * S, f"offsets: expected [2, {S}] entries")
+    _need(start_pos is None or start_pos.numel() >= S, f"start_pos: fewer than {S} entries")
+    _need(totals is None or totals.numel() >= 4, "totals: expected 4 entries")
+    a = kvc_slot_map_args()
+    a.ratio, a.page_size, a.num_pages = ratio, page_size, num_pages
+    a.num_slots, a.token_stride = S, token_stride
+    a.lens = _dense(lens, _I32_T, "lens")
+    a.new_lens = _opt(new_lens, _dense, _I32_T, "new_lens")
+    a.depth = _opt(depth, _dense, _I32_T, "depth")
+    a.page_table = _rows(page_table, _I32_T, "page_table")
+    a.pt_stride, a.pt_width = _pt_stride(page_table), page_table.shape[1]
+    a.free_pages, a.n_free = _dense(free_pages, _I32_T, "free_pages"), free_pages.numel()
+    a.max_tokens = max_tokens
+    for name, t in (("offsets", offsets), ("start_pos", start_pos), ("out_loc", out_loc),
+                    ("positions", positions), ("token_to_req", token_to_req), ("totals", totals),
+                    ("status", status)):
+        setattr(a, name, _opt(t, _dense, _I32_T, name))
+    _call_on(dev, stream, lib().kvc_slot_map, a)
+
+
+# ----------------------------------------------------------------- attention
+def kvc_attend_workspace(num_slots: int, tokens: int, num_heads: int) -> int:
+    """Workspace bytes of an attention call (``tokens``: rows of q; for
+    kvc_attend_tree, slots times draft_len)."""
+    n = C.c_int64(0)
+    _check(lib().kvc_attend_workspace(num_slots, tokens, num_heads, C.byref(n)))
+    return n.value
+
+
+def _attend(fn, cache: Cache, q, start_pos, page_table, out, *, slots, tokens, ratio, scale, sink, lse,
+            workspace, status, stream, offsets=None, draft_len=0, tree=None) -> None:
+    for name, t in (("q", q), ("out", out)):
+        _need(t.is_cuda and t.dtype in _B16_T and t.dim() == 3 and t.shape[2] == 512 and
+              t.stride(2) == 1, f"{name}: expected a [tokens, heads, 512] bf16 device tensor with "
+                                f"contiguous rows, got {t.dtype} {tuple(t.shape)} strides {t.stride()}")
+    T, H = q.shape[:2]
+    _need(out.shape == q.shape, f"out: shape {tuple(out.shape)}, q has {tuple(q.shape)}")
+    dev = _one_device(q=q, out=out, cache=cache.data, start_pos=start_pos, page_table=page_table,
+                      offsets=offsets, tree=tree, sink=sink, lse=lse, workspace=workspace,
+                      status=status)
+    _need(start_pos.numel() >= slots, f"start_pos: {start_pos.numel()} entries for {slots} slots")
+    _need(page_table.dim() == 2 and page_table.shape[0] >= slots,
+          f"page_table: shape {tuple(page_table.shape)}, need {slots} rows")
+    _need(sink is None or sink.numel() >= H, f"sink: fewer than {H} entries")
+    _need(lse is None or tuple(lse.shape) == (T, H), f"lse: expected shape [{T}, {H}]")
+    # a written row must be its own
+    s0, s1 = out.stride(0), out.stride(1)
+    _need(T <= 1 or H <= 1 or s0 >= (H - 1) * s1 + 512 or s1 >= (T - 1) * s0 + 512,
+          f"out: overlapping rows (strides {out.stride()})")
+    a = kvc_attend_args()
+    a.ratio, a.num_heads, a.num_slots, a.draft_len = ratio, H, slots, draft_len
+    a.q, a.q_stride, a.q_head_stride, a.q_rows = q.data_ptr(), q.stride(0), q.stride(1), T
+    a.offsets = _opt(offsets, _dense, _I32_T, "offsets")
+    a.start_pos = _dense(start_pos, _I32_T, "start_pos")
+    a.page_table = _rows(page_table, _I32_T, "page_table")
+    a.pt_stride, a.pt_width = _pt_stride(page_table), page_table.shape[1]
+    a.tree = _opt(tree, _dense, (torch.int64, torch.uint64), "tree")
+    a.scale = scale
+    a.sink = _opt(sink, _dense, _F32_T, "sink")
+    a.out, a.out_stride, a.out_head_stride = out.data_ptr(), out.stride(0), out.stride(1)
+    a.lse = _opt(lse, _dense, _F32_T, "lse")
+    a.cache = cache.desc()
+    a.status = _opt(status, _dense, _I32_T, "status")
+    if workspace is None:
+        # of the stream the call runs on: the allocator then reuses it in order
+        n = kvc_attend_workspace(slots, tokens, H)
+        with torch.cuda.device(dev), torch.cuda.stream(stream):
+            workspace = torch.empty(n, dtype=torch.uint8, device=dev)
+    a.workspace = _dense(workspace, (torch.uint8,), "workspace")
+    a.workspace_bytes = workspace.numel()
+    _call_on(dev, stream, fn, a)
+
+
+def kvc_attend_prefill(cache: Cache, q: torch.Tensor, offsets: torch.Tensor,
+                       start_pos: torch.Tensor, page_table: torch.Tensor, out: torch.Tensor, *,
+                       scale: float, ratio: int = 1, sink: torch.Tensor | None = None,
+                       lse: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                       status: torch.Tensor | None = None, stream=None) -> None:
+    """Causal attention of packed tokens ``q [T, H, 512]`` (slot b's rows and
+    count in ``offsets [2, S]``, first position in ``start_pos [S]``) over the
+    cached rows; ``out [T, H, 512]``, ``lse [T, H]`` (base 2).  ``workspace``:
+    a uint8 tensor of ``kvc_attend_workspace`` bytes (allocated per call
+    where it is not given)."""
+    S = start_pos.numel()
+    _need(offsets.numel() == 2 * S, f"offsets: expected [2, {S}] entries")
+    _attend(lib().kvc_attend_prefill, cache, q, start_pos, page_table, out, slots=S,
+            tokens=q.shape[0], ratio=ratio, scale=scale, sink=sink, lse=lse, workspace=workspace,
+            status=status, stream=stream, offsets=offsets)
+
+
+def kvc_attend_tree(cache: Cache, q: torch.Tensor, start_pos: torch.Tensor,
+                    page_table: torch.Tensor, out: torch.Tensor, *, scale: float,
+                    draft_len: int = 1, tree: torch.Tensor | None = None, ratio: int = 1,
+                    sink: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+                    workspace: torch.Tensor | None = None, status: torch.Tensor | None = None,
+                    stream=None) -> None:
+    """Attention of ``draft_len`` tokens per slot, ``q [S * draft_len, H,
+    512]``, over the cached rows: a chain, or a tree given by ancestor masks
+    ``tree [S, draft_len]`` (int64 bit patterns).  Other arguments as
+    kvc_attend_prefill."""
+    S = start_pos.numel()
+    _need(q.dim() == 3 and q.shape[0] >= S * draft_len,
+          f"q: shape {tuple(q.shape)} for {S} slots x {draft_len} tokens")
+    _need(tree is None or tree.numel() >= S * draft_len, f"tree: expected [{S}, {draft_len}] masks")
+    _attend(lib().kvc_attend_tree, cache, q, start_pos, page_table, out, slots=S,
+            tokens=S * draft_len, ratio=ratio, scale=scale, sink=sink, lse=lse,
+            workspace=workspace, status=status, stream=stream, draft_len=draft_len, tree=tree)

@@ -17,7 +17,7 @@ import concurrent.futures as cf
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libkvc.so")
-SOURCES = ["kvc_api.cpp", "store_gather.hip", "compress.hip"]
+SOURCES = ["kvc_api.cpp", "store_gather.hip", "compress.hip", "slot_map.hip", "attend.hip"]
 CEILING_LIB = os.path.join(HERE, "libkvc_ceiling.so")
 CEILING_SOURCES = ["ceiling.hip"]
 ARCH = "gfx950"

@@ -5,6 +5,7 @@
 
 #include <hip/hip_runtime.h>
 
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <new>
@@ -78,6 +79,109 @@ bool row_stride_ok(int64_t s) { return s >= 512 && s % 8 == 0; }
 int launched(hipError_t e, const char* who) {
   if (e != hipSuccess) return fail(KVC_ELAUNCH, "%s: launch failed: %s", who, hipGetErrorString(e));
   return ok();
+}
+
+bool page_size_ok(int32_t ps) { return ps >= 1 && ps <= 4096 && (ps & (ps - 1)) == 0; }
+
+// 32-query blocks per unit of the attention.  A unit's wider tiles cost fewer
+// reads of the staged rows per query, a wide unit half full costs its empty
+// half: slots of up to 32 or 64 queries take units of that size.
+int attend_qblocks(int32_t slots, int64_t tokens, int32_t heads) {
+  const int64_t per_slot = tokens * heads / (slots > 0 ? slots : 1);
+  return per_slot <= 32 ? 1 : per_slot <= 64 ? 2 : 4;
+}
+
+constexpr int64_t kMaxQueries = 0x7FFFFF00;   // query indices, rounded up to a unit, stay in int32
+
+int64_t align256(int64_t n) { return (n + 255) & ~int64_t(255); }
+
+// places of the workspace's parts; returns its size
+int64_t attend_layout(int32_t slots, int64_t tokens, int32_t heads, int64_t (&at)[5]) {
+  const int64_t parts = 2 * int64_t(kvc::kAttendWorkgroups) * 32 * attend_qblocks(slots, tokens, heads);
+  int64_t n = 0;
+  at[0] = n, n += align256(sizeof(kvc::AttendHead));
+  at[1] = n, n += align256(kvc::kAttendWorkgroups * sizeof(kvc::AttendStart));
+  at[2] = n, n += align256(kvc::kAttendWorkgroups * sizeof(kvc::AttendSplit));
+  at[3] = n, n += align256(parts * 16);
+  at[4] = n, n += align256(parts * 512 * 4);
+  return n;
+}
+
+// the checks and the call shared by both attention entry points
+int attend(const kvc_attend_args* a, bool tree, void* stream, const char* who) {
+  if (a == nullptr) return fail(KVC_EINVAL, "%s: args is NULL", who);
+  kvc::AttendParams p{};
+  int rc = check_cache(&a->cache, &p.cache, who);
+  if (rc) return rc;
+  if (a->ratio != 1 && a->ratio != 2) return fail(KVC_EUNSUPPORTED, "%s: ratio %d (1 or 2)", who, a->ratio);
+  if (a->num_heads < 1 || a->num_heads > 1024)
+    return fail(KVC_EINVAL, "%s: num_heads %d outside [1, 1024]", who, a->num_heads);
+  if (a->num_slots < 0 || a->num_slots > kvc::kMaxSlots)
+    return fail(KVC_EINVAL, "%s: num_slots %d outside [0, %d]", who, a->num_slots, kvc::kMaxSlots);
+  if (a->q_rows < 0 || a->q_rows > kMaxQueries / a->num_heads)
+    return fail(KVC_EINVAL, "%s: q_rows %lld: q_rows * num_heads must not pass 2^31 - 256", who,
+                (long long)a->q_rows);
+  if (tree) {
+    if (a->draft_len < 1 || a->draft_len > 64)
+      return fail(KVC_EINVAL, "%s: draft_len %d outside [1, 64]", who, a->draft_len);
+    if (a->tree != nullptr && a->ratio != 1)
+      return fail(KVC_EUNSUPPORTED, "%s: a tree needs ratio 1 (a cached row per drafted token)", who);
+    if (a->q_rows < (int64_t)a->num_slots * a->draft_len)
+      return fail(KVC_EINVAL, "%s: q_rows %lld, need num_slots * draft_len = %lld", who,
+                  (long long)a->q_rows, (long long)a->num_slots * a->draft_len);
+  }
+  if (a->num_slots == 0 || a->q_rows == 0) return ok();
+  if (a->q == nullptr || !aligned16(a->q) || a->out == nullptr || !aligned16(a->out))
+    return fail(KVC_EINVAL, "%s: q and out must be non-NULL and 16-byte aligned", who);
+  if (a->q_stride < 0 || a->q_head_stride < 0 || a->q_stride % 8 != 0 || a->q_head_stride % 8 != 0)
+    return fail(KVC_EINVAL, "%s: q strides must be multiples of 8, >= 0", who);
+  if (a->out_stride % 8 != 0 || a->out_head_stride % 8 != 0 ||
+      (a->q_rows > 1 && a->out_stride < 512) || (a->num_heads > 1 && a->out_head_stride < 512))
+    return fail(KVC_EINVAL, "%s: out strides must be multiples of 8, >= 512", who);
+  if (a->start_pos == nullptr) return fail(KVC_EINVAL, "%s: start_pos is NULL", who);
+  if (!tree && a->offsets == nullptr) return fail(KVC_EINVAL, "%s: offsets is NULL", who);
+  if (a->page_table == nullptr || a->pt_width < 1 || a->pt_stride < a->pt_width)
+    return fail(KVC_EINVAL, "%s: page table needs 1 <= pt_width <= pt_stride (%lld, %lld)", who,
+                (long long)a->pt_width, (long long)a->pt_stride);
+  if (!(a->scale > 0.0f) || !std::isfinite(a->scale))
+    return fail(KVC_EINVAL, "%s: scale must be finite and > 0", who);
+  const int64_t tokens = tree ? (int64_t)a->num_slots * a->draft_len : a->q_rows;
+  int64_t at[5];
+  const int64_t need = attend_layout(a->num_slots, tokens, a->num_heads, at);
+  if (a->workspace == nullptr || ((uintptr_t)a->workspace & 255u) != 0 || a->workspace_bytes < need)
+    return fail(KVC_EINVAL, "%s: workspace needs %lld bytes, 256-byte aligned", who, (long long)need);
+  if (kvc::launch_attend == nullptr) return fail(KVC_ELAUNCH, "%s: built without kernels", who);
+  p.ratio = a->ratio;
+  p.heads = a->num_heads;
+  p.head_div = kvc::div_magic((uint32_t)a->num_heads);
+  p.num_slots = a->num_slots;
+  p.draft_len = tree ? a->draft_len : 0;
+  p.q = static_cast<const uint16_t*>(a->q);
+  p.q_stride = a->q_stride;
+  p.q_hstride = a->q_head_stride;
+  p.q_rows = a->q_rows;
+  p.offsets = tree ? nullptr : a->offsets;
+  p.start_pos = a->start_pos;
+  p.page_table = a->page_table;
+  p.pt_stride = a->pt_stride;
+  p.pt_width = a->pt_width;
+  p.tree = tree ? a->tree : nullptr;
+  p.scale_log2 = (float)((double)a->scale * 1.4426950408889634074);
+  p.sink = a->sink;
+  p.out = static_cast<uint16_t*>(a->out);
+  p.out_stride = a->out_stride;
+  p.out_hstride = a->out_head_stride;
+  p.lse = a->lse;
+  p.status = a->status;
+  const int qblocks = attend_qblocks(a->num_slots, tokens, a->num_heads);
+  p.units_max = tokens * a->num_heads / (32 * qblocks) + a->num_slots;
+  uint8_t* w = static_cast<uint8_t*>(a->workspace);
+  p.head = reinterpret_cast<kvc::AttendHead*>(w + at[0]);
+  p.starts = reinterpret_cast<kvc::AttendStart*>(w + at[1]);
+  p.splits = reinterpret_cast<kvc::AttendSplit*>(w + at[2]);
+  p.part_ml = reinterpret_cast<float4*>(w + at[3]);
+  p.part_o = reinterpret_cast<float*>(w + at[4]);
+  return launched(kvc::launch_attend(p, qblocks, static_cast<hipStream_t>(stream)), who);
 }
 
 }  // namespace
@@ -385,6 +489,83 @@ int kvc_dequant_gather_reuse(kvc_kvbuf* kb, const kvc_cache* cache, const int32_
   kb->out = out_bf16;
   kb->out_stride = out_row_stride;
   return KVC_OK;
+}
+
+// ---------------------------------------------------------------- slot map
+int kvc_slot_map(const kvc_slot_map_args* a, void* stream) {
+  const char* who = "kvc_slot_map";
+  if (a == nullptr) return fail(KVC_EINVAL, "%s: args is NULL", who);
+  if (a->ratio != 1 && a->ratio != 2) return fail(KVC_EUNSUPPORTED, "%s: ratio %d (1 or 2)", who, a->ratio);
+  if (!page_size_ok(a->page_size))
+    return fail(KVC_EINVAL, "%s: page_size %d is not a power of two in [1, 4096]", who, a->page_size);
+  if (a->num_pages < 1 || a->num_pages > ((int64_t)1 << 31) / a->page_size)
+    return fail(KVC_EINVAL, "%s: num_pages must be >= 1 with num_pages * page_size in int32", who);
+  if (a->num_slots < 0 || a->num_slots > kvc::kMaxSlots)
+    return fail(KVC_EINVAL, "%s: num_slots %d outside [0, %d]", who, a->num_slots, kvc::kMaxSlots);
+  if (a->max_tokens < 0 || a->max_tokens > 0x7FFFFFFF || a->n_free < 0 || a->n_free > 0x7FFFFFFF)
+    return fail(KVC_EINVAL, "%s: max_tokens and n_free must lie in [0, 2^31 - 1]", who);
+  if (a->token_stride < 0 || (int64_t)a->num_slots * a->token_stride > a->max_tokens)
+    return fail(KVC_EINVAL, "%s: token_stride %d: num_slots * token_stride must not pass max_tokens",
+                who, a->token_stride);
+  if (a->depth != nullptr && a->ratio != 1)
+    return fail(KVC_EUNSUPPORTED, "%s: depths need ratio 1 (a cached row per drafted token)", who);
+  if (a->num_slots > 0) {
+    if (a->lens == nullptr) return fail(KVC_EINVAL, "%s: lens is NULL", who);
+    if (a->new_lens == nullptr && a->token_stride == 0)
+      return fail(KVC_EINVAL, "%s: new_lens may be NULL only with a token_stride", who);
+    if (a->start_pos != nullptr && (a->start_pos == a->lens || a->start_pos == a->new_lens))
+      return fail(KVC_EINVAL, "%s: start_pos must not be an input", who);
+    if (a->page_table == nullptr || a->pt_width < 1 || a->pt_stride < a->pt_width)
+      return fail(KVC_EINVAL, "%s: page table needs 1 <= pt_width <= pt_stride (%lld, %lld)", who,
+                  (long long)a->pt_width, (long long)a->pt_stride);
+    if (a->n_free > 0 && a->free_pages == nullptr)
+      return fail(KVC_EINVAL, "%s: free_pages is NULL with n_free > 0", who);
+  }
+  if (kvc::launch_slot_map == nullptr) return fail(KVC_ELAUNCH, "%s: built without kernels", who);
+  kvc::SlotMapParams p{};
+  p.ratio = a->ratio;
+  p.page_bits = page_bits_of(a->page_size);
+  p.num_pages = a->num_pages;
+  p.num_slots = a->num_slots;
+  p.token_stride = a->token_stride;
+  p.stride_div = kvc::div_magic((uint32_t)(a->token_stride > 0 ? a->token_stride : 1));
+  p.lens = a->lens;
+  p.new_lens = a->new_lens;
+  p.depth = a->depth;
+  p.page_table = a->page_table;
+  p.pt_stride = a->pt_stride;
+  p.pt_width = a->pt_width;
+  p.free_pages = a->free_pages;
+  p.n_free = a->n_free;
+  p.max_tokens = a->max_tokens;
+  p.offsets = a->offsets;
+  p.start_pos = a->start_pos;
+  p.out_loc = a->out_loc;
+  p.positions = a->positions;
+  p.token_to_req = a->token_to_req;
+  p.totals = a->totals;
+  p.status = a->status;
+  return launched(kvc::launch_slot_map(p, static_cast<hipStream_t>(stream)), who);
+}
+
+// --------------------------------------------------------------- attention
+int kvc_attend_workspace(int32_t num_slots, int64_t tokens, int32_t num_heads, int64_t* bytes) {
+  const char* who = "kvc_attend_workspace";
+  if (bytes == nullptr) return fail(KVC_EINVAL, "%s: bytes is NULL", who);
+  if (num_slots < 0 || num_slots > kvc::kMaxSlots || num_heads < 1 || num_heads > 1024 || tokens < 0 ||
+      tokens > kMaxQueries / num_heads)
+    return fail(KVC_EINVAL, "%s: sizes outside those of an attention call", who);
+  int64_t at[5];
+  *bytes = attend_layout(num_slots, tokens, num_heads, at);
+  return ok();
+}
+
+int kvc_attend_prefill(const kvc_attend_args* args, void* stream) {
+  return attend(args, false, stream, "kvc_attend_prefill");
+}
+
+int kvc_attend_tree(const kvc_attend_args* args, void* stream) {
+  return attend(args, true, stream, "kvc_attend_tree");
 }
 
 }  // extern "C"

@@ -82,6 +82,7 @@ enum : int32_t {
   kStPosRange = 16,
   kStReqRange = 32,
   kStTokenRange = 64,
+  kStNoPage = 128,
 };
 
 }  // namespace kvc

@@ -72,7 +72,8 @@ enum {
   KVC_STATUS_LATENT_RANGE = 8, /* latent row index >= max_out_rows                         */
   KVC_STATUS_POS_RANGE = 16,   /* rotary position < 0 or >= max_pos: row skipped           */
   KVC_STATUS_REQ_RANGE = 32,   /* request index outside the block table: row dropped        */
-  KVC_STATUS_TOKEN_RANGE = 64  /* prefill slot's token rows outside [0, kv_rows): slot skipped */
+  KVC_STATUS_TOKEN_RANGE = 64, /* prefill slot's token rows outside [0, kv_rows): slot skipped */
+  KVC_STATUS_NO_PAGE = 128     /* slot map: the free list is short of a slot's pages: refused */
 };
 
 /* ---------------------------------------------------------------- layouts
@@ -360,6 +361,145 @@ int kvc_dequant_gather_reuse(kvc_kvbuf* kb, const kvc_cache* cache, const int32_
                              int64_t n_pages, const int32_t* ids, int64_t n, void* out_bf16,
                              int64_t out_row_stride, int32_t* status, int32_t* hit,
                              void* stream);
+
+/* ---------------------------------------------------------------- slot map
+ * The tables of one batch step, built on the device from the request lengths
+ * alone: new pages taken from a free list and entered in the block table, the
+ * token rows of every slot, and for every token its cache slot, position and
+ * request.  They are what the other calls read: offsets and start_pos
+ * (compress, attend), page_table (all of them), out_loc (the stores, decode,
+ * verify), positions (the rotary store), token_to_req (the DCP filter).
+ *
+ * Slot b holds len = lens[b] tokens (lens[b] < 0: an inactive slot) and adds n
+ * = new_lens[b] (negative: 0).  Its compressed rows grow from len / ratio to
+ * (len + n) / ratio; the entries of page_table row b for the pages of the
+ * first len / ratio rows are read, and one free page is entered for each
+ * further page those rows reach.  free_pages are taken from the front, slots
+ * in order.  Token j of the slot has row
+ *   packed (token_stride 0):  (tokens accepted before slot b) + j
+ *   token_stride D > 0:       b * D + j   (verify and decode layout)
+ * and   out_loc      = the slot of compressed row (len + j) / ratio for a token
+ *                      that completes a row (ratio 1: every token; ratio 2:
+ *                      (len + j) odd), else 0
+ *       positions    = len + j, or len + depth[row] where depth is given
+ *                      (a drafted tree: a token's depth below the context)
+ *       token_to_req = b.
+ * Rows up to max_tokens that belong to no token are padding: out_loc 0,
+ * positions 0, token_to_req -1.
+ *   offsets    [2, S]: first token row of each slot, token count
+ *   start_pos  [S]: len, or -1 for an inactive or refused slot
+ *   totals     [4]: tokens, compressed rows completed, pages taken (the
+ *              caller drops that many from the front of its list), slots
+ *              refused
+ * A slot is refused whole (count 0, start_pos -1, nothing entered) when its
+ * rows pass pt_width pages or its length 2^31 - 1 (KVC_STATUS_PT_RANGE), when
+ * it adds more than token_stride tokens (KVC_STATUS_TOKEN_RANGE), when the
+ * pages asked for up to and including it pass n_free (KVC_STATUS_NO_PAGE; a
+ * later slot that asks for pages is refused with it), or, packed, when the
+ * tokens up to and including it pass max_tokens (KVC_STATUS_TOKEN_RANGE; as
+ * is a later slot with tokens).  A page outside [0, num_pages) gives out_loc 0
+ * with KVC_STATUS_PAGE_RANGE.  The call reads its lengths on the device, so it
+ * can be captured, and gives the same tables when it is repeated; outputs
+ * must not overlap inputs or each other (page_table: entries past the pages
+ * held are outputs). */
+typedef struct kvc_slot_map_args {
+  int32_t ratio;              /* 1 or 2 */
+  int32_t page_size;          /* compressed rows per page: power of two, 1..4096 */
+  int64_t num_pages;          /* pages of the cache, as kvc_cache */
+  int32_t num_slots;          /* S, 0..8191 */
+  int32_t token_stride;       /* 0, or D >= 1 with S * D <= max_tokens */
+  const int32_t* lens;        /* device int32 [S] */
+  const int32_t* new_lens;    /* device int32 [S], or NULL (token_stride each) */
+  const int32_t* depth;       /* device int32 [max_tokens] or NULL; ratio 1 */
+  int32_t* page_table;        /* device int32, row b at page_table + b * pt_stride */
+  int64_t pt_stride;          /* entries between rows, >= pt_width */
+  int64_t pt_width;           /* entries per row, >= 1 */
+  const int32_t* free_pages;  /* device int32 [n_free] (NULL when n_free is 0) */
+  int64_t n_free;             /* 0 .. 2^31 - 1 */
+  int64_t max_tokens;         /* entries of each per-token output, 0 .. 2^31 - 1 */
+  int32_t* offsets;           /* device int32 outputs, each may be NULL */
+  int32_t* start_pos;
+  int32_t* out_loc;
+  int32_t* positions;
+  int32_t* token_to_req;
+  int32_t* totals;
+  int32_t* status;            /* device int32 or NULL */
+} kvc_slot_map_args;
+
+int kvc_slot_map(const kvc_slot_map_args* args, void* stream);
+
+/* ---------------------------------------------------------------- attention
+ * Attention over the paged cache (flashinfer_sparse.py: q [T, heads, 512], one
+ * cached row of 512 dims shared by every head as key and value, an optional
+ * sink per head, base-2 log-sum-exp for a merge across ranks).  With x_r the
+ * dequantized row r of the token's request (the values kvc_dequant_gather
+ * gives), for every token and head
+ *   s_r = scale * (q . x_r) over the visible rows r,
+ *   out = sum_r e^(s_r) x_r / (sum_r e^(s_r) + e^(sink)),
+ *   lse = log2(sum_r e^(s_r) + e^(sink))        (no sink: e^(sink) is 0).
+ * A query that sees no row gives out = 0 and lse = sink * log2(e), or -inf
+ * without a sink.  Scores and sums are fp32; the weights e^(s_r) are rounded
+ * to bf16 for the second product (and the sum out is divided by is that of
+ * the rounded weights), out is rounded to bf16.
+ *
+ * kvc_attend_prefill (packed tokens of different lengths, whole prompts or
+ *   extends): slot b's tokens are rows offsets[b] .. + count - 1 of q, at
+ *   positions start_pos[b] + j, as the tokens of a prefill compress; a token
+ *   at position p sees the compressed rows r < (p + 1) / ratio -- its request's
+ *   rows up to the one it completes, which the caller has stored.  start_pos <
+ *   0 or count <= 0: no tokens; rows outside [0, q_rows) skip the slot with
+ *   KVC_STATUS_TOKEN_RANGE.  Slots' token rows must not overlap.  (Either
+ *   call: positions past 2^31 - 257 skip the slot with KVC_STATUS_POS_RANGE.)
+ * kvc_attend_tree (D = draft_len tokens per slot, rows b*D .. b*D + D - 1; D = 1
+ *   is plain decode): tree = NULL: a chain, token j is at position start_pos[b]
+ *   + j and sees as in prefill.  tree given (ratio 1): token j sees the rows
+ *   r < start_pos[b] and the drafted rows start_pos[b] + i whose bit i of
+ *   tree[b*D + j] is set (i < D; its own bit included or not, as given):
+ *   drafted token i's row is stored as row start_pos[b] + i, whatever its
+ *   depth (kvc_slot_map gives that slot, and the depth's position).
+ * Rows of q, out and lse that belong to no token (skipped slots, padding) are
+ * neither read nor written.
+ * A row whose logical page is past pt_width (KVC_STATUS_PT_RANGE) or whose
+ * page is outside the cache (KVC_STATUS_PAGE_RANGE) is left out, as if masked.
+ * Rows that a query does not see do not reach it, whatever they hold; a row
+ * holding a NaN makes NaN of the queries that see it.
+ *
+ * workspace: kvc_attend_workspace bytes of device memory, 256-byte aligned,
+ * written and read by the call (no state is kept in it); two calls that may
+ * run at the same time -- other streams, other captured graphs -- need two. */
+typedef struct kvc_attend_args {
+  int32_t ratio;              /* 1 or 2 */
+  int32_t num_heads;          /* H, 1..1024 */
+  int32_t num_slots;          /* S, 0..8191 */
+  int32_t draft_len;          /* tree: D, 1..64 (prefill: ignored) */
+  const void* q;              /* device bf16: token t, head h at q + t*q_stride + h*q_head_stride */
+  int64_t q_stride;           /* elements, multiples of 8; q 16-byte aligned */
+  int64_t q_head_stride;
+  int64_t q_rows;             /* token rows q, out and lse hold; q_rows * H <= 2^31 - 256 */
+  const int32_t* offsets;     /* device int32 [2, S], prefill (tree: ignored) */
+  const int32_t* start_pos;   /* device int32 [S] */
+  const int32_t* page_table;  /* device int32 [S, pt_stride] */
+  int64_t pt_stride;
+  int64_t pt_width;           /* 1 .. pt_stride */
+  const uint64_t* tree;       /* device [S * D] or NULL, tree mode */
+  float scale;                /* finite, > 0 */
+  const float* sink;          /* device fp32 [H] or NULL */
+  void* out;                  /* device bf16, strides as q's; must not overlap an input */
+  int64_t out_stride;
+  int64_t out_head_stride;
+  float* lse;                 /* device fp32 [q_rows, H] or NULL */
+  kvc_cache cache;
+  void* workspace;
+  int64_t workspace_bytes;
+  int32_t* status;            /* device int32 or NULL */
+} kvc_attend_args;
+
+/* Workspace bytes for a call of num_slots slots, `tokens` token rows (q_rows;
+ * tree: num_slots * draft_len) and num_heads heads.  Host only. */
+int kvc_attend_workspace(int32_t num_slots, int64_t tokens, int32_t num_heads, int64_t* bytes);
+
+int kvc_attend_prefill(const kvc_attend_args* args, void* stream);
+int kvc_attend_tree(const kvc_attend_args* args, void* stream);
 
 /* ---------------------------------------------------------------- misc */
 /* Message of the last failed call on this thread ("" if none). */
