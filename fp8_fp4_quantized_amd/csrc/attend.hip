@@ -14,8 +14,10 @@
 // joins the units that were cut between workgroups.  The split follows the
 // lengths on the device, so a captured call adapts to refreshed lengths, and
 // it is a function of the lengths alone, so results repeat bit for bit.
+#include <type_traits>
+
 #include "launch.hpp"
-#include "row_load.hpp"
+#include "row_ops.hpp"
 
 namespace kvc {
 
@@ -154,85 +156,387 @@ __global__ __launch_bounds__(kPlanBlock) void attend_plan_kernel(AttendParams p,
       f(b, k, (int64_t)unit_tiles(unit_rows(p, s, k * qt, qt), nt));
     }
   };
+  // A unit costs its tiles and its begin and end (kAttendUnitTiles); a boundary
+  // that falls into the latter is moved to the unit's first tile.
   int64_t mine = 0, total = 0;
-  walk([&](int, int32_t, int64_t t) { mine += t; });
+  walk([&](int, int32_t, int64_t t) { mine += t + kAttendUnitTiles; });
   int64_t c = plan_excl_scan(mine, buf, &total);
   int64_t quota = (total + kAttendGrid - 1) / kAttendGrid;
   const int64_t least = kAttendLeastRows / nt;
   if (quota < least) quota = least;
-  if (tid == 0) p.head->quota = quota;
-  for (int64_t w = tid; w < kAttendGrid; w += kPlanBlock)
-    if (w * quota >= total) p.starts[w].slot = -1;
+  // boundary kAttendGrid, and every one past the last unit: the end
+  for (int64_t w = tid; w <= kAttendGrid; w += kPlanBlock)
+    if (w * quota >= total) p.starts[w] = AttendStart{S, 0, 0, 0};
   walk([&](int b, int32_t k, int64_t t) {
-    const int64_t w0 = c / quota, w1 = (c + t - 1) / quota;
-    for (int64_t w = w0 * quota == c ? w0 : w0 + 1; w <= w1; ++w)
-      p.starts[w] = AttendStart{b, k, (int32_t)(w * quota - c), 0};
-    if (w1 > w0)
-      p.splits[atomicAdd(&nsplit, 1)] = AttendSplit{b, k, (int32_t)w0, (int32_t)(w1 - w0 + 1)};
-    c += t;
+    const int64_t end = c + kAttendUnitTiles + t;
+    int64_t cut = 0;                          // first boundary inside the tiles
+    int32_t parts = 1;
+    for (int64_t w = (c + quota - 1) / quota; w * quota < end && w < kAttendGrid; ++w) {
+      const int64_t tile = max(w * quota - c - kAttendUnitTiles, int64_t(0));
+      p.starts[w] = AttendStart{b, k, (int32_t)tile, 0};
+      if (tile > 0 && ++parts == 2) cut = w;
+    }
+    if (parts > 1) p.splits[atomicAdd(&nsplit, 1)] = AttendSplit{b, k, (int32_t)(cut - 1), parts};
+    c = end;
   });
   __syncthreads();
   if (tid == 0) p.head->nsplit = nsplit;
 }
 
-// ------------------------------------------------------------------ attend
-// The 16-byte chunks of an LDS row are permuted by the row index, so that a
+// ------------------------------------------------------------------ staging
+// The 16-byte chunks of a staged row are permuted by the row index, so that a
 // product's reads of one chunk column over many rows spread over the banks.
 __device__ __forceinline__ uint32_t swz(uint32_t row) { return row & 7u; }
 
-__device__ __forceinline__ float swap_halves(float v) { return __shfl_xor(v, 32); }
+typedef const __attribute__((address_space(3))) uint8_t* lds_cptr;
+typedef __attribute__((address_space(3))) uint8_t* lds_ptr;
 
-// Four steps of 16 dims of a 32 x 32 score block.  Written out so that the
-// scores live in the vector registers their softmax works in: the compiler
-// gives every matrix-instruction result of a kernel with an accumulator
-// register file to that file, which O fills (256 registers for QB = 4).  A
-// result feeding the next instruction's C operand needs no wait; s_nop 1
-// covers operands a vector instruction has just written, and score_done's
-// s_nop the 16 wait states from the last result to its first use.
-__device__ __forceinline__ void score_mfma4(f32x16& sc, const bf16x8 (&x)[4], const bf16x8* q,
-                                            bool first) {
+// The lanes' part of an 8-row group that lies in one page: N loads of 16 bytes
+// of codes a lane (V4: the last one of bf16 rope dims) with the scale bytes of
+// their dims, and their expansion into 8 rows of a tile.  Every load's offsets
+// are a base of the lane and a constant.
+//   V41      load k: rows 2k, 2k + 1, 32 lanes a row, 16 dims a lane
+//   V41_FP4  load k: rows 4k .. 4k + 3, 16 lanes a row, 32 dims a lane
+//   V4       8 lanes a row; load k < 4: dims 128k + 16 (lane % 8) -- of load 3
+//            the upper lanes' are past the codes, and what they put is
+//            overwritten by load 4's rope dims, 8 a lane
+template <int L> struct GroupShape;
+template <> struct GroupShape<kV41> { static constexpr int kLoads = 4; };
+template <> struct GroupShape<kV41Fp4> { static constexpr int kLoads = 2; };
+template <> struct GroupShape<kV4> { static constexpr int kLoads = 5; };
+
+template <int L>
+struct Group {
+  static constexpr int N = GroupShape<L>::kLoads;
+  u32x4 codes[N];
+  uint32_t scale[N];
+
+  static __device__ __forceinline__ int row(int k, int lane) {
+    return L == kV41 ? 2 * k + (lane >> 5) : L == kV41Fp4 ? 4 * k + (lane >> 4) : lane >> 3;
+  }
+  // the lane's data and scale offsets, and load k's constants on top of them
+  static __device__ __forceinline__ uint32_t data_off(int lane) {
+    return L == kV4 ? (lane >> 3) * LayoutTraits<L>::kData + 16 * (lane & 7) : 16 * lane;
+  }
+  static constexpr uint32_t data_step(int k) { return L == kV4 ? (k < 4 ? 128 * k : kNope) : 1024 * k; }
+  static __device__ __forceinline__ uint32_t scale_off(int lane) {
+    return L == kV41 ? lane >> 1 : L == kV41Fp4 ? 2 * lane
+                     : (lane >> 3) * LayoutTraits<L>::kScale + ((lane & 7) >> 2);
+  }
+  static constexpr uint32_t scale_step(int k) { return L == kV41 ? 32 * k : L == kV41Fp4 ? 128 * k : k < 4 ? 2 * k : 0; }
+  // load k of the group whose data and scale parts begin there
+  __device__ __forceinline__ void load(const uint8_t* data, const uint8_t* sc, uint32_t doff, uint32_t soff, int k) {
+    codes[k] = __builtin_amdgcn_raw_buffer_load_b128(raw_rsrc(data), (int)doff, (int)data_step(k), kCpolSc1);
+    if (L == kV4 && k == 4) return;
+    if constexpr (L == kV41Fp4)
+      scale[k] = __builtin_amdgcn_raw_buffer_load_b16(raw_rsrc(sc), (int)soff, (int)scale_step(k), kCpolSc1);
+    else
+      scale[k] = __builtin_amdgcn_raw_buffer_load_b8(raw_rsrc(sc), (int)soff, (int)scale_step(k), kCpolSc1);
+  }
+  // load k of rows in pages of their own: the lane's data and scale bytes
+  __device__ __forceinline__ void load_apart(const uint8_t* data, const uint8_t* sc, int k) {
+    codes[k] = *(const u32x4*)data;
+    if constexpr (L == kV41Fp4) scale[k] = *(const uint16_t*)sc;
+    else scale[k] = *sc;
+  }
+  // part j of load k, 8 dims, to its row in a tile: the place of the lane's
+  // first part in the group, whose bits the other parts and loads change
+  static __device__ __forceinline__ uint32_t place(int lane) {
+    if constexpr (L == kV41) return (lane >> 5) * 1024 + (((2 * (lane & 31)) ^ (lane >> 5)) << 4);
+    else if constexpr (L == kV41Fp4) return (lane >> 4) * 1024 + (((4 * (lane & 15)) ^ (lane >> 4)) << 4);
+    else return (lane >> 3) * 1024 + (((2 * (lane & 7)) ^ (lane >> 3)) << 4);
+  }
+  static constexpr int parts(int k) { return L == kV41Fp4 ? 4 : L == kV4 && k == 4 ? 1 : 2; }
+  __device__ __forceinline__ void put(lds_ptr rows, uint32_t place, int lane, int k, int j) const {
+    uint4 v;
+    uint32_t at;
+    if constexpr (L == kV41Fp4) {
+      v = dq_fp4x8(codes[k][j], j < 2 ? scale[k] & 0xFFu : scale[k] >> 8);
+      at = (place ^ (16 * ((4 * k & 7) ^ j))) + 4096 * k;
+    } else if (L == kV4 && k == 4) {
+      v = make_uint4(codes[k][0], codes[k][1], codes[k][2], codes[k][3]);
+      at = (lane >> 3) * 1024 + (((lane & 7) ^ (lane >> 3)) << 4) + 2 * kNope;
+    } else {
+      v = dq_fp8x8(make_uint2(codes[k][2 * j], codes[k][2 * j + 1]), scale[k]);
+      at = L == kV41 ? (place ^ (16 * ((2 * k) ^ j))) + 2048 * k : (place ^ (16 * j)) + 256 * k;
+    }
+    *(__attribute__((address_space(3))) u32x4*)(rows + at) = u32x4{v.x, v.y, v.z, v.w};
+  }
+};
+
+// Where the rows of a slot lie.
+template <int L>
+struct Rows {
+  PagedKV<L> kv;
+  const int32_t* table;
+  int32_t width;                              // (rows end below 2^31: a wider table is not reached)
+  int32_t rows;                               // rows any query of the unit sees
+
+  // page-table entry of row r (clamped into the table: always in bounds)
+  __device__ __forceinline__ int32_t entry(int32_t r) const {
+    const int32_t lp = r >> kv.page_bits;
+    return table[lp < width ? lp : width - 1];
+  }
+  // whether row r, with its entry, is a row of the cache; flags one that should be
+  __device__ __forceinline__ bool valid(int32_t r, int32_t page, int32_t* status) const {
+    if (r >= rows) return false;
+    const bool in = (r >> kv.page_bits) < width;
+    if (in && page >= 0 && page < kv.num_pages) return true;
+    if (status != nullptr) atomicOr(status, in ? kStPageRange : kStPtRange);
+    return false;
+  }
+  __device__ __forceinline__ const uint8_t* data(int64_t page, int32_t r) const {
+    return kv.base + page * kv.page_stride +
+           (int64_t)(r & ((1 << kv.page_bits) - 1)) * LayoutTraits<L>::kData;
+  }
+  __device__ __forceinline__ const uint8_t* scale(int64_t page, int32_t r) const {
+    return kv.base + page * kv.page_stride + ((int64_t)LayoutTraits<L>::kData << kv.page_bits) +
+           (int64_t)(r & ((1 << kv.page_bits) - 1)) * LayoutTraits<L>::kScale;
+  }
+};
+
+// ------------------------------------------------------------------ products
+// Matrix instructions written out, so that scores live in the vector
+// registers their softmax works in and O in accumulator registers: the
+// compiler gives every matrix-instruction result of a kernel of this size to
+// the accumulator file, which O fills (256 registers for 128 queries).
+// A result feeding the next instruction's C operand needs no wait; s_nop 0
+// covers an operand that a vector instruction has just written.  scores_done
+// and out_done give the 16 wait states from a last result to a vector
+// instruction that reads it.
+__device__ __forceinline__ void score_mfma(f32x16& sc, bf16x8 x, bf16x8 q, bool first) {
   if (first)
-    asm("s_nop 1\n\t"
-        "v_mfma_f32_32x32x16_bf16 %0, %1, %5, 0\n\t"
-        "v_mfma_f32_32x32x16_bf16 %0, %2, %6, %0\n\t"
-        "v_mfma_f32_32x32x16_bf16 %0, %3, %7, %0\n\t"
-        "v_mfma_f32_32x32x16_bf16 %0, %4, %8, %0"
-        : "=&v"(sc)
-        : "v"(x[0]), "v"(x[1]), "v"(x[2]), "v"(x[3]), "v"(q[0]), "v"(q[1]), "v"(q[2]), "v"(q[3]));
+    asm("s_nop 0\n\tv_mfma_f32_32x32x16_bf16 %0, %1, %2, 0" : "=&v"(sc) : "v"(x), "v"(q));
   else
-    asm("s_nop 1\n\t"
-        "v_mfma_f32_32x32x16_bf16 %0, %1, %5, %0\n\t"
-        "v_mfma_f32_32x32x16_bf16 %0, %2, %6, %0\n\t"
-        "v_mfma_f32_32x32x16_bf16 %0, %3, %7, %0\n\t"
-        "v_mfma_f32_32x32x16_bf16 %0, %4, %8, %0"
-        : "+&v"(sc)
-        : "v"(x[0]), "v"(x[1]), "v"(x[2]), "v"(x[3]), "v"(q[0]), "v"(q[1]), "v"(q[2]), "v"(q[3]));
+    asm("s_nop 0\n\tv_mfma_f32_32x32x16_bf16 %0, %1, %2, %0" : "+&v"(sc) : "v"(x), "v"(q));
 }
-__device__ __forceinline__ void score_done(f32x16& sc) { asm("s_nop 15" : "+v"(sc)); }
-
-// One step of 16 rows of O^T for a dim block and QB query blocks, O kept in
-// accumulator registers; out_done stands before vector instructions read it.
-template <int QB>
-__device__ __forceinline__ void out_mfma(f32x16 (&o)[QB], bf16x8 x, const bf16x8 (&w)[QB]) {
-  if constexpr (QB == 1)
-    asm("s_nop 1\n\t"
-        "v_mfma_f32_32x32x16_bf16 %0, %1, %2, %0"
-        : "+a"(o[0]) : "v"(x), "v"(w[0]));
-  else if constexpr (QB == 2)
-    asm("s_nop 1\n\t"
-        "v_mfma_f32_32x32x16_bf16 %0, %2, %3, %0\n\t"
-        "v_mfma_f32_32x32x16_bf16 %1, %2, %4, %1"
-        : "+a"(o[0]), "+a"(o[1]) : "v"(x), "v"(w[0]), "v"(w[1]));
-  else
-    asm("s_nop 1\n\t"
-        "v_mfma_f32_32x32x16_bf16 %0, %4, %5, %0\n\t"
-        "v_mfma_f32_32x32x16_bf16 %1, %4, %6, %1\n\t"
-        "v_mfma_f32_32x32x16_bf16 %2, %4, %7, %2\n\t"
-        "v_mfma_f32_32x32x16_bf16 %3, %4, %8, %3"
-        : "+a"(o[0]), "+a"(o[1]), "+a"(o[2]), "+a"(o[3])
-        : "v"(x), "v"(w[0]), "v"(w[1]), "v"(w[2]), "v"(w[3]));
+__device__ __forceinline__ void out_mfma(f32x16& o, bf16x8 x, bf16x8 w) {
+  asm("s_nop 0\n\tv_mfma_f32_32x32x16_bf16 %0, %1, %2, %0" : "+a"(o) : "v"(x), "v"(w));
 }
+__device__ __forceinline__ void scores_done(f32x16& sc) { asm("s_nop 15" : "+v"(sc)); }
 __device__ __forceinline__ void out_done(f32x16& o) { asm("s_nop 15" : "+a"(o)); }
+
+// max of three, the ordinary one or the NaN-free operand (fmaxf would first
+// make each operand canonical)
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
+  return r;
+}
+__device__ __forceinline__ float max_halves(float v) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return max3(__uint_as_float(r[0]), __uint_as_float(r[1]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float sum_halves(float v) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+// sum of a bf16 pair added to v
+__device__ __forceinline__ float add_pair(float v, uint32_t pair) {
+  typedef __bf16 bf16x2v __attribute__((ext_vector_type(2)));
+  const uint32_t ones = 0x3F803F80u;
+  return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2v, pair),
+                                         __builtin_bit_cast(bf16x2v, ones), v, false);
+}
+
+// ------------------------------------------------------------------ a query
+// What a lane knows of its query, and the softmax state of it
+struct Query {
+  int32_t tok, head;           // of the slot
+  bool ok;                     // a query of the slot (else a copy of its last one)
+  int32_t lim;                 // rows below are visible ...
+  uint64_t bits;               // ... and of the rows from base on those of bits
+  float mx, sum, rsum;         // reference maximum (log2), sums of weights and rounded weights
+};
+
+__device__ __forceinline__ Query query_of(const AttendParams& p, int b, const SlotTokens& s, int32_t m) {
+  Query q;
+  const int32_t nq = s.n * p.heads;
+  q.ok = m < nq;
+  const int32_t mm = q.ok ? m : nq - 1;
+  q.tok = (int32_t)udiv_magic((uint32_t)mm, p.head_div.m, p.head_div.sh1, p.head_div.sh2);
+  q.head = mm - q.tok * p.heads;
+  q.bits = 0;
+  if (p.tree != nullptr) {
+    q.lim = s.pos;
+    q.bits = p.tree[(int64_t)b * p.draft_len + q.tok];
+    if (s.n < 64) q.bits &= (uint64_t(1) << s.n) - 1;
+  } else {
+    q.lim = (s.pos + q.tok + 1) >> (p.ratio - 1);
+  }
+  q.mx = kNegInf;
+  q.sum = q.rsum = 0.0f;
+  return q;
+}
+
+// Masks the scores of rows r0 + 8 (i / 4) + 4 h + i % 4 of a block; okw: which
+// of its 32 rows are rows of the cache.  Returns whether a row that some query
+// does not see gave a score that is not finite (it holds a NaN or an infinity).
+__device__ __forceinline__ bool mask_scores(f32x16& sc, const Query& q, int32_t r0, int h, int32_t base,
+                                            bool tree, uint32_t okw) {
+  bool nf = false;
+  // (kept from being computed ahead of the loop, for every tile's registers)
+  asm volatile("" : "+v"(h));
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const int rl = 8 * (i >> 2) + 4 * h + (i & 3);
+    const int32_t r = r0 + rl;
+    bool see = r < q.lim;
+    if (tree) {
+      const uint32_t x = (uint32_t)(r - base);
+      see |= x < 64u && (q.bits >> (x & 63u) & 1) != 0;
+    }
+    see &= (okw >> rl & 1) != 0;
+    nf |= !see && !(__builtin_fabsf(sc[i]) < __builtin_inff());
+    sc[i] = see ? sc[i] : kNegInf;
+  }
+  return __ballot(nf) != 0;
+}
+
+// zeroes every NaN and infinity of a staged tile (BYTES long); all threads
+template <int BYTES>
+__device__ __forceinline__ void zero_not_finite(lds_ptr tile) {
+  typedef __attribute__((address_space(3))) u32x4* vec;
+  for (int x = threadIdx.x; x < BYTES / 16; x += kAttendBlock) {
+    u32x4 v = *(vec)(tile + 16 * x);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if ((v[k] & 0x7F80u) == 0x7F80u) v[k] &= 0xFFFF0000u;
+      if ((v[k] & 0x7F800000u) == 0x7F800000u) v[k] &= 0xFFFFu;
+    }
+    *(vec)(tile + 16 * x) = v;
+  }
+}
+
+// The reference maximum moves only when it is passed by 8 (in log2): weights
+// up to 2^8 lose nothing in fp32, and O is rescaled rarely.  Returns the
+// factor for what was summed before.
+__device__ __forceinline__ float raise_max(Query& q, float tile_max) {
+  const float old = q.mx;
+  if (tile_max > old + 8.0f) q.mx = tile_max;
+  const float alpha = q.mx == old ? 1.0f : __builtin_amdgcn_exp2f(old - q.mx);
+  q.sum *= alpha;
+  q.rsum *= alpha;
+  return alpha;
+}
+
+// Out and lse factors of a query from its complete sums (or, with a cut unit,
+// the joined ones)
+struct Final {
+  float f, lse;
+};
+__device__ __forceinline__ Final finish(const AttendParams& p, int32_t head, float mx, float sum,
+                                        float rsum) {
+  const float snk = p.sink != nullptr ? p.sink[head] * kLog2e : kNegInf;
+  const float mm = fmaxf(mx, snk);
+  const float e = mx == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(mx - mm);
+  const float es = snk == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(snk - mm);
+  return Final{e == 0.0f ? 0.0f : e / (rsum * e + es), mm + __builtin_log2f(sum * e + es)};
+}
+
+// ------------------------------------------------------------------ attend
+// A workgroup's walk over its tiles, from its start to the next workgroup's:
+// the piece at hand (tiles [t0, t1) of unit ub of slot b) and the step to the
+// next one.
+struct Walk {
+  int b, ub;
+  int32_t t0, t1, tiles, rows;
+  int eb, eub, et;             // the end: slot, unit, tile
+  SlotTokens s;
+
+  __device__ __forceinline__ void piece(const AttendParams& p, int qt, int nt) {
+    rows = unit_rows(p, s, ub * qt, qt);
+    tiles = unit_tiles(rows, nt);
+    t1 = b == eb && ub == eub ? et : tiles;
+  }
+  __device__ __forceinline__ bool begin(const AttendParams& p, int qt, int nt) {
+    const AttendStart st = p.starts[blockIdx.x], en = p.starts[blockIdx.x + 1];
+    int32_t none = 0;
+    b = uniform(st.slot), ub = uniform(st.unit), t0 = uniform(st.tile);
+    eb = uniform(en.slot), eub = uniform(en.unit), et = uniform(en.tile);
+    if (b >= p.num_slots || (b == eb && ub == eub && t0 == et)) return false;
+    s = slot_tokens(p, b, &none);
+    piece(p, qt, nt);
+    return true;
+  }
+  __device__ __forceinline__ bool next(const AttendParams& p, int qt, int nt) {
+    if (b == eb && ub == eub) return false;
+    t0 = 0;
+    ++ub;
+    if ((int64_t)ub * qt >= (int64_t)s.n * p.heads) {
+      ub = 0;
+      int32_t none = 0;
+      // the next slot that has tokens, 64 at a time
+      for (int bn = b + 1;; bn += kLanes) {
+        if (bn >= p.num_slots) return false;
+        SlotTokens c{};
+        if (bn + lane_id() < p.num_slots) c = slot_tokens(p, bn + lane_id(), &none);
+        const uint64_t has = __ballot(c.n > 0);
+        if (has != 0) {
+          b = bn + __builtin_ctzll(has);
+          break;
+        }
+      }
+      s = slot_tokens(p, b, &none);
+    }
+    if (b == eb && ub == eub && et == 0) return false;
+    piece(p, qt, nt);
+    return true;
+  }
+};
+
+// The end of a piece: the sums of each query over the lanes and waves that
+// hold rows of it, then its outputs, or its partial sums for the join.
+template <int QB>
+__device__ __forceinline__ void end_piece(const AttendParams& p, const Walk& w, Query& q,
+                                          const f32x16 (&o)[4][QB], int qb, int nb,
+                                          float (*ssum)[32 * QB], float (*srsum)[32 * QB],
+                                          float* sfac) {
+  constexpr int NB = 4 / QB, QT = 32 * QB;
+  const int lane = lane_id(), wave = uniform((int)(threadIdx.x >> 6));
+  const int ql = lane & 31, h = lane >> 5, qi = qb * 32 + ql;
+  q.sum = sum_halves(q.sum);
+  q.rsum = sum_halves(q.rsum);
+  if (h == 0) { ssum[nb][qi] = q.sum; srsum[nb][qi] = q.rsum; }
+  __syncthreads();
+  const bool whole = w.t0 == 0 && w.t1 == w.tiles;
+  // a part that began inside its unit lies in the workgroup's first place
+  const int64_t part = ((int64_t)blockIdx.x * 2 + (w.t0 > 0 ? 0 : 1)) * QT;
+  if (nb == 0 && h == 0) {
+    float sum = ssum[0][qi], rsum = srsum[0][qi];
+#pragma unroll
+    for (int x = 1; x < NB; ++x) { sum += ssum[x][qi]; rsum += srsum[x][qi]; }
+    if (whole) {
+      const Query me = query_of(p, w.b, w.s, w.ub * QT + qi);
+      const Final f = finish(p, me.head, q.mx, sum, rsum);
+      sfac[qi] = f.f;
+      if (p.lse != nullptr && me.ok) p.lse[(int64_t)(w.s.first + me.tok) * p.heads + me.head] = f.lse;
+    } else {
+      p.part_ml[part + qi] = make_float4(q.mx, sum, rsum, 0.0f);
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int x = 0; x < QB; ++x) {
+    const Query y = query_of(p, w.b, w.s, w.ub * QT + x * 32 + ql);
+    if (!y.ok) continue;
+    uint16_t* op = p.out + (int64_t)(w.s.first + y.tok) * p.out_stride + (int64_t)y.head * p.out_hstride;
+    float* pp = p.part_o + (part + x * 32 + ql) * kDim;
+    const float f = whole ? sfac[x * 32 + ql] : 1.0f;
+#pragma unroll
+    for (int d = 0; d < 4; ++d)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int dim = 128 * wave + 32 * d + 8 * j + 4 * h;
+        const float a0 = o[d][x][4 * j], a1 = o[d][x][4 * j + 1], a2 = o[d][x][4 * j + 2],
+                    a3 = o[d][x][4 * j + 3];
+        if (whole)
+          *(u32x2*)(op + dim) = u32x2{pack_bf16(a0 * f, a1 * f), pack_bf16(a2 * f, a3 * f)};
+        else
+          *(f32x4*)(pp + dim) = f32x4{a0, a1, a2, a3};
+      }
+  }
+}
 
 // One workgroup, one unit's tiles at a time: scores S^T[row][query] = X Q^T
 // with each wave on one 32 x 32 block (a lane owns one query, so the softmax
@@ -243,14 +547,16 @@ __device__ __forceinline__ void out_done(f32x16& o) { asm("s_nop 15" : "+a"(o));
 // The weights are rounded to bf16 for the matrix product, the one rounding
 // before the output's own; the sum they are divided by is of the rounded
 // weights, so the division undoes a common part of it, while lse uses the
-// exact weights.  The running maximum moves only when it is passed by 8 (in
-// log2): weights up to 2^8 lose nothing in fp32, and O is rescaled rarely.
-template <int L, int QB>
+// exact weights.
+// RUN: pages of 8 rows or more, so that an 8-row group lies in one page; smaller
+// pages look up every row.
+template <int L, int QB, bool RUN>
 __global__ __launch_bounds__(kAttendBlock) __attribute__((amdgpu_waves_per_eu(1, 1)))
 void attend_kernel(AttendParams p) {
   constexpr int NB = 4 / QB;
   constexpr int QT = 32 * QB, NT = 32 * NB;
   constexpr int RW = NT / 4;                  // rows a wave stages per tile
+  constexpr int G = RW / 8;                   // in groups of 8
   constexpr int PS = NT + 8;                  // elements per query in the weights' tile
   __shared__ __attribute__((aligned(1024))) uint8_t tile[NT * 1024];
   __shared__ __attribute__((aligned(16))) uint16_t wts[QT * PS];
@@ -260,18 +566,16 @@ void attend_kernel(AttendParams p) {
   const int lane = lane_id(), wave = uniform((int)(threadIdx.x >> 6));
   const int ql = lane & 31, h = lane >> 5;
   const int qb = wave % QB, nb = wave / QB;
-  const PagedKV<L> kv{p.cache.base, p.cache.page_stride, p.cache.num_pages, p.cache.page_bits};
-  const int32_t H = p.heads;
+  const int qi = qb * 32 + ql;                // the lane's query in the unit
   const float c2 = p.scale_log2;
+  const bool tree = p.tree != nullptr;
 
-  // this lane's LDS addresses: row ql of the wave's score block, and the
-  // transposing reads of its dim blocks
-  // (the permutation touches the low 3 bits of a chunk's index only, so a few
-  // bases and constant offsets reach every chunk)
-  typedef const __attribute__((address_space(3))) uint8_t* lds_ptr;
+  // LDS addresses: row ql of the wave's score block, and the transposing reads
+  // of its dim blocks (the permutation touches the low 3 bits of a chunk's
+  // index only, so a few bases and constant offsets reach every chunk)
   const lds_ptr tile3 = (lds_ptr)tile;
   const int i16 = lane & 15, g1 = (lane >> 4) & 1;
-  lds_ptr kp[4], vp[2][2];
+  lds_cptr kp[4], vp[2][2];
 #pragma unroll
   for (int k = 0; k < 4; ++k) kp[k] = tile3 + (nb * 32 + ql) * 1024 + (((2 * k + h) ^ swz(ql)) << 4);
 #pragma unroll
@@ -283,204 +587,134 @@ void attend_kernel(AttendParams p) {
       vp[e][d] = tile3 + rr * 1024 + 256 * wave + (chunk << 4) + 8 * (i16 & 1);
     }
 
-  const AttendStart st = p.starts[blockIdx.x];
-  int b = st.slot, ub = st.unit;
-  int32_t t0 = st.tile;
-  int64_t left = p.head->quota;
-  int32_t none = 0;
-  bool first_piece = true;
-  if (b < 0) return;
-  SlotTokens s = slot_tokens(p, b, &none);
+  const uint32_t place = Group<L>::place(lane), doff = Group<L>::data_off(lane),
+                 soff = Group<L>::scale_off(lane);
 
-  while (left > 0) {
-    // ---- the piece: tiles [t0, t1) of unit ub of slot b
-    const int32_t nq = s.n * H, m0 = ub * QT;
-    const int32_t rows = unit_rows(p, s, m0, QT);
-    const int32_t tiles = unit_tiles(rows, NT);
-    const int32_t t1 = (int32_t)min((int64_t)tiles, t0 + left);
-    const int32_t* pt = p.page_table + (int64_t)b * p.pt_stride;
+  const int32_t width = (int32_t)min(p.pt_width, (int64_t)0x7FFFFFFF);
 
-    // this lane's query
-    // (one past the slot's last takes the last one's place; nothing of it is
-    // written)
-    const bool qok = m0 + qb * 32 + ql < nq;
-    const int32_t m = qok ? m0 + qb * 32 + ql : nq - 1;
-    const int32_t tok = (int32_t)udiv_magic((uint32_t)m, p.head_div.m, p.head_div.sh1,
-                                            p.head_div.sh2);
-    const int32_t head = m - tok * H;
-    const uint16_t* qp = p.q + (int64_t)(s.first + tok) * p.q_stride + (int64_t)head * p.q_hstride;
-    bf16x8 q[32];
+  Walk w;
+  if (!w.begin(p, QT, NT)) return;
+  do {
+    const int32_t m0 = w.ub * QT;
+    Query q = query_of(p, w.b, w.s, m0 + qi);
+    const uint16_t* qp = p.q + (int64_t)(w.s.first + q.tok) * p.q_stride + (int64_t)q.head * p.q_hstride;
+    bf16x8 qv[32];
 #pragma unroll
-    for (int k = 0; k < 32; ++k) {
-      q[k] = __builtin_bit_cast(bf16x8, ld_u4(qp + 16 * k + 8 * h));
-    }
-    // rows below lim are visible; of the rows from base on, those of bits
-    int32_t lim;
-    uint64_t bits = 0;
-    const int32_t base = s.pos;
-    int32_t lim_first;                        // every query sees the rows below
-    if (p.tree != nullptr) {
-      lim = s.pos;
-      bits = p.tree[(int64_t)b * p.draft_len + tok];
-      if (s.n < 64) bits &= (uint64_t(1) << s.n) - 1;
-      lim_first = s.pos;
-    } else {
-      lim = (s.pos + tok + 1) >> (p.ratio - 1);
-      const int32_t tok0 = (int32_t)udiv_magic((uint32_t)m0, p.head_div.m, p.head_div.sh1,
-                                               p.head_div.sh2);
-      lim_first = (s.pos + tok0 + 1) >> (p.ratio - 1);
-    }
-
-    // row r's page-table entry, row r's slot
-    auto page_of = [&](int32_t tl) -> int32_t {
-      const int32_t r = tl * NT + wave * RW + lane;
-      const int32_t lp = r >> p.cache.page_bits;
-      if (lane >= RW || tl >= t1 || r >= rows) return -1;
-      if (lp >= p.pt_width) {
-        if (p.status != nullptr) atomicOr(p.status, kStPtRange);
-        return -1;
-      }
-      return pt[lp];
-    };
-    auto slot_of = [&](int32_t tl, int32_t page) -> int32_t {
-      const int32_t r = tl * NT + wave * RW + lane;
-      if (lane >= RW || tl >= t1 || r >= rows || (r >> p.cache.page_bits) >= p.pt_width) return -1;
-      if (page < 0 || page >= kv.num_pages) {
-        if (p.status != nullptr) atomicOr(p.status, kStPageRange);
-        return -1;
-      }
-      return (page << p.cache.page_bits) | (r & ((1 << p.cache.page_bits) - 1));
-    };
-    LaneCodes<L> codes[RW];
-    int32_t slot = slot_of(t0, page_of(t0));
-    // a row without a slot loads slot 0 (any cache has one) and is zeroed below
+    for (int k = 0; k < 32; ++k) qv[k] = __builtin_bit_cast(bf16x8, ld_u4(qp + 16 * k + 8 * h));
+    // every query of the unit sees the rows below
+    const int32_t lim_first = tree ? w.s.pos : uniform(
+        (w.s.pos + (int32_t)udiv_magic((uint32_t)m0, p.head_div.m, p.head_div.sh1, p.head_div.sh2) + 1) >>
+        (p.ratio - 1));
+    const Rows<L> rw{{p.cache.base, p.cache.page_stride, p.cache.num_pages, p.cache.page_bits},
+                     p.page_table + (int64_t)w.b * p.pt_stride, width, w.rows};
+    const int32_t row0 = wave * RW;           // of the tile: this wave's first row to stage
+    auto entry = [&](int32_t tl) { return rw.entry(tl * NT + row0 + (lane & (RW - 1))); };
+    auto load = [&](Group<L> (&gr)[G], int32_t tl, int32_t page) -> uint32_t {
+      const int32_t r0 = tl * NT + row0;
+      const bool ok = lane < RW && rw.valid(r0 + lane, page, p.status);
+      const uint32_t okm = (uint32_t)__ballot(ok);
 #pragma unroll
-    for (int u = 0; u < RW; ++u) {
-      const int32_t sl = __builtin_amdgcn_readlane(slot, u);
-      codes[u] = load_lane<L, kCpolSc1>(kv, sl < 0 ? 0 : sl, lane);
-    }
-    int32_t page = page_of(t0 + 1);
-
-    float mx = kNegInf, sum = 0.0f, rsum = 0.0f;
+      for (int g = 0; g < G; ++g) {
+        // rows that are none load page 0's, which any cache has; they are masked
+        if constexpr (RUN) {
+          const int32_t pg = okm >> (8 * g) & 1 ? __builtin_amdgcn_readlane(page, 8 * g) : 0;
+          const uint8_t* d = rw.data(pg, r0 + 8 * g);
+          const uint8_t* sc = rw.scale(pg, r0 + 8 * g);
+#pragma unroll
+          for (int k = 0; k < Group<L>::N; ++k) gr[g].load(d, sc, doff, soff, k);
+        } else {
+          const int32_t safe = ok ? page : 0;
+#pragma unroll
+          for (int k = 0; k < Group<L>::N; ++k) {
+            const int row = Group<L>::row(k, lane);
+            const int64_t pg = __shfl(safe, 8 * g + row);
+            const int32_t r = r0 + 8 * g + row;
+            gr[g].load_apart(
+                rw.data(pg, r) + (doff + Group<L>::data_step(k) - row * LayoutTraits<L>::kData),
+                rw.scale(pg, r) + (soff + Group<L>::scale_step(k) - row * LayoutTraits<L>::kScale), k);
+          }
+        }
+      }
+      return okm;
+    };
+    Group<L> gr[G];
+    uint32_t okm = load(gr, w.t0, entry(w.t0));
+    int32_t page = entry(min(w.t0 + 1, w.t1 - 1));
     f32x16 o[4][QB];
 #pragma unroll
     for (int d = 0; d < 4; ++d)
 #pragma unroll
       for (int x = 0; x < QB; ++x) o[d][x] = f32x16{};
 
-    for (int32_t tl = t0; tl < t1; ++tl) {
+    for (int32_t tl = w.t0; tl < w.t1; ++tl) {
       // ---- stage the tile's rows, request the next tile's
-      const uint64_t okm = __ballot(slot >= 0);
 #pragma unroll
-      for (int u = 0; u < RW; ++u) {
-        const int row = wave * RW + u;
-        uint4 v = decode_lane<L>(codes[u], lane);
-        if ((okm >> u & 1) == 0) v = make_uint4(0, 0, 0, 0);
-        *(u32x4*)(tile + row * 1024 + ((lane ^ swz(row)) << 4)) = u32x4{v.x, v.y, v.z, v.w};
-      }
-      if (lane < RW / 8) svalid[wave * (RW / 8) + lane] = (uint8_t)(okm >> (8 * lane));
-      if (tl + 1 < t1) {
-        slot = slot_of(tl + 1, page);
+      for (int g = 0; g < G; ++g)
 #pragma unroll
-        for (int u = 0; u < RW; ++u) {
-          const int32_t sl = __builtin_amdgcn_readlane(slot, u);
-          codes[u] = load_lane<L, kCpolSc1>(kv, sl < 0 ? 0 : sl, lane);
-        }
-        page = page_of(tl + 2);
-      }
+        for (int k = 0; k < Group<L>::N; ++k)
+#pragma unroll
+          for (int j = 0; j < Group<L>::parts(k); ++j)
+            gr[g].put(tile3 + (row0 + 8 * g) * 1024, place, lane, k, j);
+      if (lane < G) svalid[wave * G + lane] = (uint8_t)(okm >> (8 * lane));
+      if (tl + 1 < w.t1) okm = load(gr, tl + 1, page);
+      page = entry(min(tl + 2, w.t1 - 1));
       __syncthreads();
 
       // ---- scores of this wave's 32 rows and 32 queries
       f32x16 sc;
 #pragma unroll
-      for (int k = 0; k < 32; k += 4) {
-        bf16x8 x[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          x[i] = __builtin_bit_cast(
-              bf16x8, *(const __attribute__((address_space(3))) u32x4*)(kp[i] + 32 * k));
-        score_mfma4(sc, x, q + k, k == 0);
+      for (int k = 0; k < 32; ++k) {
+        const u32x4 x = *(const __attribute__((address_space(3))) u32x4*)(kp[k & 3] + 32 * (k & ~3));
+        score_mfma(sc, __builtin_bit_cast(bf16x8, x), qv[k], k == 0);
       }
-      score_done(sc);
+      scores_done(sc);
       // ---- mask (only a tile that some query does not see whole)
       bool holes = (tl + 1) * NT > lim_first;
 #pragma unroll
-      for (int w = 0; w < NT / 32; ++w) holes |= *(const uint32_t*)(svalid + 4 * w) != 0xFFFFFFFFu;
+      for (int x = 0; x < NB; ++x) holes |= *(const uint32_t*)(svalid + 4 * x) != 0xFFFFFFFFu;
       if (holes) {
-        const uint32_t okw = *(const uint32_t*)(svalid + 4 * nb);
-        bool nf = false;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int rl = 8 * (i >> 2) + 4 * h + (i & 3);
-          const int32_t r = tl * NT + nb * 32 + rl;
-          bool see = r < lim;
-          if (p.tree != nullptr) {
-            const uint32_t x = (uint32_t)(r - base);
-            see |= x < 64u && (bits >> x & 1) != 0;
-          }
-          see &= (okw >> rl & 1) != 0;
-          nf |= !see && !(__builtin_fabsf(sc[i]) < __builtin_inff());
-          sc[i] = see ? sc[i] : kNegInf;
-        }
-        const bool any = __ballot(nf) != 0;
+        const bool any = mask_scores(sc, q, tl * NT + nb * 32, h, w.s.pos, tree,
+                                     *(const uint32_t*)(svalid + 4 * nb));
         if (lane == 0) snf[wave] = any;
       }
       // ---- the query's new reference maximum
-      float tm = sc[0];
+      float tm = max3(sc[0], sc[1], sc[2]);
 #pragma unroll
-      for (int i = 1; i < 16; ++i) tm = fmaxf(tm, sc[i]);
-      tm = fmaxf(tm, swap_halves(tm));
+      for (int i = 3; i < 15; i += 2) tm = max3(tm, sc[i], sc[i + 1]);
+      tm = max_halves(max3(tm, sc[15], sc[15]));
       if constexpr (NB > 1) {
-        if (h == 0) smax[nb][qb * 32 + ql] = tm;
+        if (h == 0) smax[nb][qi] = tm;
         __syncthreads();
 #pragma unroll
-        for (int x = 0; x < NB; ++x) tm = fmaxf(tm, smax[x][qb * 32 + ql]);
+        for (int x = 0; x < NB; ++x) tm = fmaxf(tm, smax[x][qi]);
       }
-      tm *= c2;
-      const float old = mx;
-      if (tm > mx + 8.0f) mx = tm;
-      const float alpha = mx == old ? 1.0f : __builtin_amdgcn_exp2f(old - mx);
-      const float ref = mx == kNegInf ? 0.0f : mx;
-      sum *= alpha;
-      rsum *= alpha;
+      const float alpha = raise_max(q, tm * c2);
+      const float ref = q.mx == kNegInf ? 0.0f : q.mx;
       // ---- weights, their sums, and their bf16 to LDS
-      uint16_t* const wrow = wts + (qb * 32 + ql) * PS + nb * 32 + 4 * h;
+      uint16_t* const wrow = wts + qi * PS + nb * 32 + 4 * h;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         float e[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           e[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[4 * j + i], c2, -ref));
-          sum += e[i];
+          q.sum += e[i];
         }
         const uint32_t w0 = pack_bf16(e[0], e[1]), w1 = pack_bf16(e[2], e[3]);
-        rsum += (bf16_lo(w0) + bf16_hi(w0)) + (bf16_lo(w1) + bf16_hi(w1));
+        q.rsum = add_pair(add_pair(q.rsum, w0), w1);
         *(u32x2*)(wrow + 8 * j) = u32x2{w0, w1};
       }
       const bool rescale = __ballot(alpha != 1.0f) != 0;
       if (nb == 0) {
-        if (h == 0) salpha[qb * 32 + ql] = alpha;
+        if (h == 0) salpha[qi] = alpha;
         if (lane == 0) sscale[qb] = rescale;
       }
       __syncthreads();
       // ---- a NaN or an infinity in a row that some query does not see: its
       // weight there is 0, and 0 times it would not be
-      if (holes) {
-        int32_t any = 0;
-#pragma unroll
-        for (int w = 0; w < 4; ++w) any |= snf[w];
-        if (any != 0) {
-          for (int x = threadIdx.x; x < NT * 64; x += kAttendBlock) {
-            u32x4 v = *(u32x4*)(tile + 16 * x);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              if ((v[k] & 0x7F80u) == 0x7F80u) v[k] &= 0xFFFF0000u;
-              if ((v[k] & 0x7F800000u) == 0x7F800000u) v[k] &= 0xFFFFu;
-            }
-            *(u32x4*)(tile + 16 * x) = v;
-          }
-          __syncthreads();
-        }
+      if (holes && (snf[0] | snf[1] | snf[2] | snf[3]) != 0) {
+        zero_not_finite<NT * 1024>(tile3);
+        __syncthreads();
       }
       // ---- O += X^T P^T on dims [128 wave, 128 wave + 128)
 #pragma unroll
@@ -495,105 +729,282 @@ void attend_kernel(AttendParams p) {
       }
 #pragma unroll
       for (int k = 0; k < NT / 16; ++k) {
-        bf16x8 w[QB];
+        bf16x8 wv[QB];
 #pragma unroll
         for (int x = 0; x < QB; ++x)
-          w[x] = __builtin_bit_cast(bf16x8, *(const u32x4*)(wts + (x * 32 + ql) * PS + 16 * k + 8 * h));
+          wv[x] = __builtin_bit_cast(bf16x8, *(const u32x4*)(wts + (x * 32 + ql) * PS + 16 * k + 8 * h));
 #pragma unroll
         for (int d = 0; d < 4; ++d) {
           union { s16x4 half[2]; bf16x8 v; } x;
 #pragma unroll
           for (int e = 0; e < 2; ++e)
             x.half[e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                (__attribute__((address_space(3))) s16x4*)(vp[e][d & 1] + 128 * (d >> 1) +
-                                                           16384 * k));
-          out_mfma<QB>(o[d], x.v, w);
+                (__attribute__((address_space(3))) s16x4*)(vp[e][d & 1] + 128 * (d >> 1) + 16384 * k));
+#pragma unroll
+          for (int y = 0; y < QB; ++y) out_mfma(o[d][y], x.v, wv[y]);
         }
         __builtin_amdgcn_sched_barrier(0);
       }
       __syncthreads();                        // the tile and the weights are free
     }
-
 #pragma unroll
     for (int d = 0; d < 4; ++d)
 #pragma unroll
       for (int x = 0; x < QB; ++x) out_done(o[d][x]);
-    // ---- the piece's end: its sums over the lanes and waves of a query
-    sum += swap_halves(sum);
-    rsum += swap_halves(rsum);
-    const int qi = qb * 32 + ql;
-    if (h == 0) { ssum[nb][qi] = sum; srsum[nb][qi] = rsum; }
+
+    end_piece<QB>(p, w, q, o, qb, nb, ssum, srsum, sfac);
     __syncthreads();
-    const bool whole = t0 == 0 && t1 == tiles;
-    const int64_t part = ((int64_t)blockIdx.x * 2 + (first_piece && t0 > 0 ? 0 : 1));
-    if (nb == 0) {
-      sum = ssum[0][qi];
-      rsum = srsum[0][qi];
+  } while (w.next(p, QT, NT));
+}
+
+// The kernel for 128 queries a unit (QB = 4): the same products, arranged so
+// that the matrix instructions follow one another.  A wave is alone on its
+// SIMD and issues in order, so everything else is placed by hand between
+// them: the next tile's expansion and the loads after it between the score
+// products, the softmax of this tile between the O products of the previous
+// one.  That takes three tile buffers and two of weights, and one barrier a
+// tile.  Pages of 8 rows or more.
+template <int L>
+__global__ __launch_bounds__(kAttendBlock) __attribute__((amdgpu_waves_per_eu(1, 1)))
+void attend_wide_kernel(AttendParams p) {
+  constexpr int QB = 4, QT = 128, NT = 32, PS = NT + 8, TB = NT * 1024, WB = QT * PS * 2;
+  __shared__ __attribute__((aligned(1024))) uint8_t tiles[3 * TB];
+  __shared__ __attribute__((aligned(16))) uint8_t wts[2 * WB];
+  __shared__ float ssum[1][QT], srsum[1][QT], sfac[QT], salpha[2][QT];
+  __shared__ int32_t svalid[2][4], sscale[2][4], snf[2][4];
+  const int lane = lane_id(), wave = uniform((int)(threadIdx.x >> 6));
+  const int ql = lane & 31, h = lane >> 5;
+  const int qi = wave * 32 + ql;
+  const float c2 = p.scale_log2;
+  const bool tree = p.tree != nullptr;
+  const lds_ptr tiles3 = (lds_ptr)tiles, wts3 = (lds_ptr)wts;
+  const int i16 = lane & 15, g1 = (lane >> 4) & 1;
+  // LDS offsets within a tile (see attend_kernel) and within a weights' buffer
+  uint32_t kp[4], vp[2][2];
 #pragma unroll
-      for (int x = 1; x < NB; ++x) { sum += ssum[x][qi]; rsum += srsum[x][qi]; }
-      if (whole) {
-        const float snk = p.sink != nullptr ? p.sink[head] * kLog2e : kNegInf;
-        const float mm = fmaxf(mx, snk);
-        const float e = mx == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(mx - mm);
-        const float es = snk == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(snk - mm);
-        if (h == 0) {
-          sfac[qi] = e == 0.0f ? 0.0f : e / (rsum * e + es);
-          if (p.lse != nullptr && qok)
-            p.lse[(int64_t)(s.first + tok) * H + head] = mm + __builtin_log2f(sum * e + es);
-        }
-      } else if (h == 0) {
-        p.part_ml[part * QT + qi] = make_float4(mx, sum, rsum, 0.0f);
-      }
+  for (int k = 0; k < 4; ++k) kp[k] = ql * 1024 + (((2 * k + h) ^ swz(ql)) << 4);
+#pragma unroll
+  for (int e = 0; e < 2; ++e)
+#pragma unroll
+    for (int d = 0; d < 2; ++d) {
+      const int rr = 8 * h + 4 * e + (i16 >> 2);
+      vp[e][d] = rr * 1024 + 256 * wave + (((4 * d + 2 * g1 + ((i16 >> 1) & 1)) ^ swz(rr)) << 4) +
+                 8 * (i16 & 1);
     }
-    __syncthreads();
+  const uint32_t place = Group<L>::place(lane), doff = Group<L>::data_off(lane),
+                 soff = Group<L>::scale_off(lane);
+
+  const int32_t width = (int32_t)min(p.pt_width, (int64_t)0x7FFFFFFF);
+
+  Walk w;
+  if (!w.begin(p, QT, NT)) return;
+  do {
+    const int32_t m0 = w.ub * QT;
+    Query q = query_of(p, w.b, w.s, m0 + qi);
+    bf16x8 qv[32];
+    {
+      const uint16_t* qp = p.q + (int64_t)(w.s.first + q.tok) * p.q_stride +
+                           (int64_t)q.head * p.q_hstride + 8 * h;
 #pragma unroll
-    for (int x = 0; x < QB; ++x) {
-      const int32_t mq = m0 + x * 32 + ql;
-      if (mq < nq) {
-        const int32_t tk = (int32_t)udiv_magic((uint32_t)mq, p.head_div.m, p.head_div.sh1, p.head_div.sh2);
-        uint16_t* op = p.out + (int64_t)(s.first + tk) * p.out_stride + (int64_t)(mq - tk * H) * p.out_hstride;
-        float* pp = p.part_o + (part * QT + x * 32 + ql) * kDim;
-        const float f = whole ? sfac[x * 32 + ql] : 1.0f;
-#pragma unroll
-        for (int d = 0; d < 4; ++d) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int dim = 128 * wave + 32 * d + 8 * j + 4 * h;
-            const float a0 = o[d][x][4 * j], a1 = o[d][x][4 * j + 1], a2 = o[d][x][4 * j + 2],
-                        a3 = o[d][x][4 * j + 3];
-            if (whole)
-              *(u32x2*)(op + dim) = u32x2{pack_bf16(a0 * f, a1 * f), pack_bf16(a2 * f, a3 * f)};
-            else
-              *(f32x4*)(pp + dim) = f32x4{a0, a1, a2, a3};
-          }
-        }
-      }
+      for (int k = 0; k < 32; ++k) qv[k] = __builtin_bit_cast(bf16x8, ld_u4(qp + 16 * k));
     }
+    const int32_t lim_first = tree ? w.s.pos : uniform(
+        (w.s.pos + (int32_t)udiv_magic((uint32_t)m0, p.head_div.m, p.head_div.sh1, p.head_div.sh2) + 1) >>
+        (p.ratio - 1));
+    const Rows<L> rw{{p.cache.base, p.cache.page_stride, p.cache.num_pages, p.cache.page_bits},
+                     p.page_table + (int64_t)w.b * p.pt_stride, width, w.rows};
+    // the wave's 8-row group of tile tl lies in one page
+    auto first_row = [&](int32_t tl) { return min(tl, w.t1 - 1) * NT + wave * 8; };
+    auto entry = [&](int32_t tl) { return rw.entry(first_row(tl)); };
+    const uint8_t *ldata, *lscale;            // of the tile being loaded
+    auto locate = [&](int32_t tl, int32_t page) -> bool {
+      const int32_t r0 = first_row(tl);
+      // a group of a page that is none loads page 0's rows; they are masked
+      // (one lane asks, so that a bad page is flagged once)
+      page = uniform(page);
+      const bool in = (r0 >> p.cache.page_bits) < width, ok = in && page >= 0 && page < p.cache.num_pages;
+      if (!ok && r0 < w.rows) raise_status(p.status, in ? kStPageRange : kStPtRange);
+      ldata = rw.data(ok ? page : 0, r0);
+      lscale = rw.scale(ok ? page : 0, r0);
+      return ok;
+    };
+    Group<L> gr;
+    constexpr int NL = Group<L>::N;
+    bool valid = locate(w.t0, entry(w.t0)), valid_next;
+#pragma unroll
+    for (int k = 0; k < NL; ++k) gr.load(ldata, lscale, doff, soff, k);
+#pragma unroll
+    for (int k = 0; k < NL; ++k)
+#pragma unroll
+      for (int j = 0; j < Group<L>::parts(k); ++j) gr.put(tiles3 + wave * 8192, place, lane, k, j);
+    if (lane == 0) svalid[0][wave] = valid;
+    valid = locate(w.t0 + 1, entry(w.t0 + 1));
+#pragma unroll
+    for (int k = 0; k < NL; ++k) gr.load(ldata, lscale, doff, soff, k);
+    int32_t page = entry(w.t0 + 2);
+    f32x16 o[4][QB];
+#pragma unroll
+    for (int d = 0; d < 4; ++d)
+#pragma unroll
+      for (int x = 0; x < QB; ++x) o[d][x] = f32x16{};
+    uint32_t cur = 0;                         // offset of the tile at hand in tiles
     __syncthreads();
 
-    // ---- the next piece
-    left -= t1 - t0;
-    t0 = 0;
-    first_piece = false;
-    ++ub;
-    if (left > 0 && (int64_t)ub * QT >= (int64_t)s.n * H) {
-      ub = 0;
-      // the next slot that has tokens, 64 at a time
-      int bn = b + 1;
-      for (;;) {
-        if (bn >= p.num_slots) return;
-        SlotTokens c{};
-        if (bn + lane < p.num_slots) c = slot_tokens(p, bn + lane, &none);
-        const uint64_t has = __ballot(c.n > 0);
-        if (has != 0) {
-          b = bn + __builtin_ctzll(has);
-          break;
+    f32x16 sc;
+    bool holes = false, holes_before;
+    // ---- scores of tile tl, which lies at cur; tile tl + 1 is expanded into the
+    // buffer after it, tile tl + 2 requested
+    auto scores = [&](int32_t tl, uint32_t nxt) {
+      // (opaque, so that the few bits each put changes are not kept in registers
+      // of their own)
+      uint32_t pl = place;
+      asm volatile("" : "+v"(pl));
+      bf16x8 x[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        x[k] = __builtin_bit_cast(bf16x8, *(const __attribute__((address_space(3))) u32x4*)(tiles3 + cur + kp[k]));
+      if (lane == 0) svalid[(tl - w.t0 + 1) & 1][wave] = valid;
+      valid_next = locate(tl + 2, page);
+      page = entry(tl + 3);
+      __builtin_amdgcn_sched_barrier(0);
+      int load = 0, in_load = 0;              // constants after unrolling
+#pragma unroll
+      for (int k = 0; k < 32; ++k) {
+        score_mfma(sc, x[k & 3], qv[k], k == 0);
+        if (k + 4 < 32)
+          x[k & 3] = __builtin_bit_cast(
+              bf16x8, *(const __attribute__((address_space(3))) u32x4*)(tiles3 + cur + kp[k & 3] + 32 * ((k + 4) & ~3)));
+        if (k % 3 == 2 && load < NL) {
+          gr.put(tiles3 + nxt + wave * 8192, pl, lane, load, in_load);
+          if (++in_load == Group<L>::parts(load)) {
+            gr.load(ldata, lscale, doff, soff, load);
+            ++load;
+            in_load = 0;
+          }
         }
-        bn += kLanes;
+        __builtin_amdgcn_sched_barrier(0);
       }
-      s = slot_tokens(p, b, &none);
+      valid = valid_next;
+    };
+    // ---- mask (only a tile that some query does not see whole)
+    auto mask = [&](int32_t tl) {
+      const int32_t par = (tl - w.t0) & 1;
+      holes_before = holes;
+      uint32_t okw = 0;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) okw |= svalid[par][x] != 0 ? 0xFFu << (8 * x) : 0u;
+      holes = (tl + 1) * NT > lim_first || okw != 0xFFFFFFFFu;
+      if (holes) {
+        scores_done(sc);
+        const bool any = mask_scores(sc, q, tl * NT, h, w.s.pos, tree, okw);
+        if (lane == 0) snf[par][wave] = any;
+      }
+    };
+    // ---- the softmax of a tile in 32 steps: maximum, then a weight a step
+    float tm, ref, alpha, e[4];
+    // (ln: the lane, as the caller holds it)
+    auto soften = [&](int step, int32_t par, int ln) {
+      if (step == 1) scores_done(sc);
+      if (step >= 1 && step < 5) {
+        const int i = 4 * (step - 1);
+        tm = step == 1 ? max3(sc[0], sc[1], sc[2]) : max3(tm, sc[i - 1], sc[i]);
+        tm = step == 1 ? tm : max3(tm, sc[i + 1], sc[i + 2]);
+      }
+      if (step == 5) tm = max_halves(max3(tm, sc[15], sc[15]));
+      if (step == 6) {
+        alpha = raise_max(q, tm * c2);
+        ref = q.mx == kNegInf ? 0.0f : q.mx;
+      }
+      if (step == 7) {
+        const bool rescale = __ballot(alpha != 1.0f) != 0;
+        if (ln < 32) salpha[par][wave * 32 + ln] = alpha;
+        if (ln == 0) sscale[par][wave] = rescale;
+      }
+      if (step >= 8 && step < 24) {
+        const int i = step - 8;
+        e[i & 3] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[i], c2, -ref));
+        q.sum += e[i & 3];
+        if ((i & 3) == 3) {
+          const uint32_t w0 = pack_bf16(e[0], e[1]), w1 = pack_bf16(e[2], e[3]);
+          q.rsum = add_pair(add_pair(q.rsum, w0), w1);
+          const uint32_t wwrite = ((ln & 31) + 32 * wave) * (2 * PS) + 8 * (ln >> 5);
+          *(__attribute__((address_space(3))) u32x2*)(wts3 + par * WB + wwrite + 16 * (i >> 2)) = u32x2{w0, w1};
+        }
+      }
+    };
+    // ---- O += X^T P^T of the tile at `at` with the weights of parity par, on dims
+    // [128 wave, 128 wave + 128); with = true: the softmax of the next tile between
+    auto out = [&](uint32_t at, int32_t par, auto with) {
+      // a NaN or an infinity in a row that some query does not see: its weight
+      // there is 0, and 0 times it would not be
+      if ((with.value ? holes_before : holes) && (snf[par][0] | snf[par][1] | snf[par][2] | snf[par][3]) != 0) {
+        zero_not_finite<TB>(tiles3 + at);
+        __syncthreads();
+      }
+#pragma unroll
+      for (int x = 0; x < QB; ++x) {
+        if (sscale[par][x] == 0) continue;
+        const float a = salpha[par][x * 32 + ql];
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+          out_done(o[d][x]);
+          o[d][x] *= a;
+        }
+      }
+      int ln = lane;                          // opaque: kept from taking registers of its own
+      asm volatile("" : "+v"(ln));
+      const uint32_t wread = (ln & 31) * (2 * PS) + 16 * (ln >> 5);
+      typedef __attribute__((address_space(3))) s16x4* trp;
+      union Frag { s16x4 half[2]; bf16x8 v; };
+      auto dims = [&](int i) {                // dim block i & 3, rows 16 (i >> 2) ..
+        Frag f;
+#pragma unroll
+        for (int y = 0; y < 2; ++y)
+          f.half[y] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+              (trp)(tiles3 + at + vp[y][i & 1] + 128 * ((i >> 1) & 1) + 16384 * (i >> 2)));
+        return f.v;
+      };
+      bf16x8 wv[QB], xv = dims(0), xn;
+#pragma unroll
+      for (int x = 0; x < QB; ++x)
+        wv[x] = __builtin_bit_cast(bf16x8, *(const __attribute__((address_space(3))) u32x4*)(wts3 + par * WB + wread + x * 64 * PS));
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (i < 7) xn = dims(i + 1);
+#pragma unroll
+        for (int x = 0; x < QB; ++x) {
+          out_mfma(o[i & 3][x], xv, wv[x]);
+          if (i == 3)
+            wv[x] = __builtin_bit_cast(bf16x8, *(const __attribute__((address_space(3))) u32x4*)(wts3 + par * WB + wread + x * 64 * PS + 32));
+          if constexpr (with.value) soften(4 * i + x, par ^ 1, ln);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        xv = xn;
+      }
+    };
+    auto after = [](uint32_t at) { return at == 2 * TB ? 0u : at + TB; };
+    scores(w.t0, after(cur));
+    mask(w.t0);
+#pragma unroll
+    for (int i = 0; i < 24; ++i) soften(i, 0, lane);
+    __syncthreads();
+    for (int32_t tl = w.t0 + 1; tl < w.t1; ++tl) {
+      const uint32_t before = cur;
+      cur = after(cur);
+      scores(tl, after(cur));
+      mask(tl);
+      out(before, (tl - w.t0 - 1) & 1, std::true_type{});
+      __syncthreads();
     }
-  }
+    out(cur, (w.t1 - 1 - w.t0) & 1, std::false_type{});
+#pragma unroll
+    for (int d = 0; d < 4; ++d)
+#pragma unroll
+      for (int x = 0; x < QB; ++x) out_done(o[d][x]);
+    end_piece<QB>(p, w, q, o, wave, 0, ssum, srsum, sfac);
+    __syncthreads();
+  } while (w.next(p, QT, NT));
 }
 
 // ------------------------------------------------------------------ join
@@ -652,27 +1063,32 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendParams p, int qt
     for (int i = 0; i < 8; ++i) a[i] += acc[w][8 * lane + i];
   const int32_t tok = (int32_t)udiv_magic((uint32_t)m, p.head_div.m, p.head_div.sh1, p.head_div.sh2);
   const int32_t head = m - tok * p.heads;
-  const float snk = p.sink != nullptr ? p.sink[head] * kLog2e : kNegInf;
-  const float mm = fmaxf(mx, snk);
-  const float e = mx == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(mx - mm);
-  const float es = snk == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(snk - mm);
-  const float f = e == 0.0f ? 0.0f : e / (rsum * e + es);
+  const Final fin = finish(p, head, mx, sum, rsum);
+  const float f = fin.f;
   uint16_t* op = p.out + (int64_t)(s.first + tok) * p.out_stride + (int64_t)head * p.out_hstride;
   st_u4(op + 8 * lane, make_uint4(pack_bf16(a[0] * f, a[1] * f), pack_bf16(a[2] * f, a[3] * f),
                                   pack_bf16(a[4] * f, a[5] * f), pack_bf16(a[6] * f, a[7] * f)));
   if (p.lse != nullptr && lane == 0)
-    p.lse[(int64_t)(s.first + tok) * p.heads + head] = mm + __builtin_log2f(sum * e + es);
+    p.lse[(int64_t)(s.first + tok) * p.heads + head] = fin.lse;
+}
+
+template <int L, bool RUN>
+hipError_t attend(const AttendParams& p, int qblocks, hipStream_t stream) {
+  const dim3 grid(kAttendGrid), block(kAttendBlock);
+  switch (qblocks) {
+    case 1: hipLaunchKernelGGL((attend_kernel<L, 1, RUN>), grid, block, 0, stream, p); break;
+    case 2: hipLaunchKernelGGL((attend_kernel<L, 2, RUN>), grid, block, 0, stream, p); break;
+    default:
+      if constexpr (RUN) hipLaunchKernelGGL((attend_wide_kernel<L>), grid, block, 0, stream, p);
+      else hipLaunchKernelGGL((attend_kernel<L, 4, false>), grid, block, 0, stream, p);
+  }
+  return hipGetLastError();
 }
 
 template <int L>
 hipError_t attend(const AttendParams& p, int qblocks, hipStream_t stream) {
-  const dim3 grid(kAttendGrid), block(kAttendBlock);
-  switch (qblocks) {
-    case 1: hipLaunchKernelGGL((attend_kernel<L, 1>), grid, block, 0, stream, p); break;
-    case 2: hipLaunchKernelGGL((attend_kernel<L, 2>), grid, block, 0, stream, p); break;
-    default: hipLaunchKernelGGL((attend_kernel<L, 4>), grid, block, 0, stream, p); break;
-  }
-  return hipGetLastError();
+  return p.cache.page_bits >= 3 ? attend<L, true>(p, qblocks, stream)
+                                : attend<L, false>(p, qblocks, stream);
 }
 
 }  // namespace

@@ -100,7 +100,7 @@ int64_t attend_layout(int32_t slots, int64_t tokens, int32_t heads, int64_t (&at
   const int64_t parts = 2 * int64_t(kvc::kAttendWorkgroups) * 32 * attend_qblocks(slots, tokens, heads);
   int64_t n = 0;
   at[0] = n, n += align256(sizeof(kvc::AttendHead));
-  at[1] = n, n += align256(kvc::kAttendWorkgroups * sizeof(kvc::AttendStart));
+  at[1] = n, n += align256((kvc::kAttendWorkgroups + 1) * sizeof(kvc::AttendStart));
   at[2] = n, n += align256(kvc::kAttendWorkgroups * sizeof(kvc::AttendSplit));
   at[3] = n, n += align256(parts * 16);
   at[4] = n, n += align256(parts * 512 * 4);

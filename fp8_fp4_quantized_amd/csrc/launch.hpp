@@ -153,12 +153,14 @@ struct SlotMapParams {
 constexpr int kAttendWorkgroups = 256;
 constexpr int kAttendLeastRows = 256;
 
+// A unit's begin and end (its queries in, its outputs out), in tiles.
+constexpr int kAttendUnitTiles = 6;
+
 struct AttendHead {            // written by the plan
-  int64_t quota;               // tiles per workgroup
   int32_t nsplit;              // units cut between workgroups
-  int32_t pad;
+  int32_t pad[3];
 };
-struct AttendStart {           // where a workgroup begins (slot -1: nothing to do)
+struct AttendStart {           // where a workgroup begins, and the one before it ends (slot S: the end)
   int32_t slot, unit, tile, pad;
 };
 struct AttendSplit {           // a cut unit: its parts lie with workgroups wg0 ..
@@ -192,7 +194,7 @@ struct AttendParams {
   int64_t units_max;           // units the call can have at the most
   // workspace
   AttendHead* head;
-  AttendStart* starts;         // [kAttendWorkgroups]
+  AttendStart* starts;         // [kAttendWorkgroups + 1]
   AttendSplit* splits;         // [kAttendWorkgroups]
   float4* part_ml;             // [2 * kAttendWorkgroups][queries of a unit]: max, sum, rounded sum
   float* part_o;               // the same, 512 dims each
