@@ -184,9 +184,12 @@ __global__ __launch_bounds__(kPlanBlock) void attend_plan_kernel(AttendParams p,
 }
 
 // ------------------------------------------------------------------ staging
-// The 16-byte chunks of a staged row are permuted by the row index, so that a
-// product's reads of one chunk column over many rows spread over the banks.
-__device__ __forceinline__ uint32_t swz(uint32_t row) { return row & 7u; }
+// The 16-byte chunks of a staged row are permuted by XOR with a function of
+// the row index, so that both products' reads spread over all 64 banks: the
+// scores' read one chunk column of 16 consecutive rows at a time, which the
+// four bits keep apart; the transposing reads 64 bytes of 4 consecutive rows,
+// which the row's low bits, in the chunk index's upper two, keep apart.
+__device__ __forceinline__ uint32_t swz(uint32_t row) { return (row & 3u) << 2 | (row >> 2 & 3u); }
 
 typedef const __attribute__((address_space(3))) uint8_t* lds_cptr;
 typedef __attribute__((address_space(3))) uint8_t* lds_ptr;
@@ -240,25 +243,27 @@ struct Group {
     else scale[k] = *sc;
   }
   // part j of load k, 8 dims, to its row in a tile: the place of the lane's
-  // first part in the group, whose bits the other parts and loads change
-  static __device__ __forceinline__ uint32_t place(int lane) {
-    if constexpr (L == kV41) return (lane >> 5) * 1024 + (((2 * (lane & 31)) ^ (lane >> 5)) << 4);
-    else if constexpr (L == kV41Fp4) return (lane >> 4) * 1024 + (((4 * (lane & 15)) ^ (lane >> 4)) << 4);
-    else return (lane >> 3) * 1024 + (((2 * (lane & 7)) ^ (lane >> 3)) << 4);
+  // first part in the group, whose bits the other parts and loads change.  odd:
+  // the group's first row is an odd multiple of 8 (of the tile).
+  static __device__ __forceinline__ uint32_t place(int lane, int odd) {
+    const uint32_t r = row(0, lane);
+    const uint32_t chunk = L == kV41 ? 2 * (lane & 31) : L == kV41Fp4 ? 4 * (lane & 15) : 2 * (lane & 7);
+    return r * 1024 + ((chunk ^ swz(r + 8 * odd)) << 4);
   }
   static constexpr int parts(int k) { return L == kV41Fp4 ? 4 : L == kV4 && k == 4 ? 1 : 2; }
   __device__ __forceinline__ void put(lds_ptr rows, uint32_t place, int lane, int k, int j) const {
     uint4 v;
     uint32_t at;
-    if constexpr (L == kV41Fp4) {
+    if constexpr (L == kV41Fp4) {             // rows 4k ..: bit 0 of the permutation
       v = dq_fp4x8(codes[k][j], j < 2 ? scale[k] & 0xFFu : scale[k] >> 8);
-      at = (place ^ (16 * ((4 * k & 7) ^ j))) + 4096 * k;
-    } else if (L == kV4 && k == 4) {
+      at = (place ^ (16 * (k ^ j))) + 4096 * k;
+    } else if (L == kV4 && k == 4) {          // chunks 56 .. 63, from place's chunks 0, 2, .. 14
       v = make_uint4(codes[k][0], codes[k][1], codes[k][2], codes[k][3]);
-      at = (lane >> 3) * 1024 + (((lane & 7) ^ (lane >> 3)) << 4) + 2 * kNope;
+      at = (place ^ (16 * (((2 * (lane & 7)) ^ (8 + (lane & 7)))))) + 768;
     } else {
       v = dq_fp8x8(make_uint2(codes[k][2 * j], codes[k][2 * j + 1]), scale[k]);
-      at = L == kV41 ? (place ^ (16 * ((2 * k) ^ j))) + 2048 * k : (place ^ (16 * j)) + 256 * k;
+      // V41: rows 2k ..: bits 3 (from bit 1 of the row) and 0 (bit 2)
+      at = L == kV41 ? (place ^ (16 * ((k & 1) << 3 ^ k >> 1 ^ j))) + 2048 * k : (place ^ (16 * j)) + 256 * k;
     }
     *(__attribute__((address_space(3))) u32x4*)(rows + at) = u32x4{v.x, v.y, v.z, v.w};
   }
@@ -571,23 +576,22 @@ void attend_kernel(AttendParams p) {
   const bool tree = p.tree != nullptr;
 
   // LDS addresses: row ql of the wave's score block, and the transposing reads
-  // of its dim blocks (the permutation touches the low 3 bits of a chunk's
+  // of its dim blocks (the permutation touches the low 4 bits of a chunk's
   // index only, so a few bases and constant offsets reach every chunk)
   const lds_ptr tile3 = (lds_ptr)tile;
   const int i16 = lane & 15, g1 = (lane >> 4) & 1;
-  lds_cptr kp[4], vp[2][2];
+  lds_cptr kp[8], vp[2][4];
 #pragma unroll
-  for (int k = 0; k < 4; ++k) kp[k] = tile3 + (nb * 32 + ql) * 1024 + (((2 * k + h) ^ swz(ql)) << 4);
+  for (int k = 0; k < 8; ++k) kp[k] = tile3 + (nb * 32 + ql) * 1024 + (((2 * k + h) ^ swz(ql)) << 4);
 #pragma unroll
   for (int e = 0; e < 2; ++e)
 #pragma unroll
-    for (int d = 0; d < 2; ++d) {
+    for (int d = 0; d < 4; ++d) {
       const int rr = 8 * h + 4 * e + (i16 >> 2);
       const int chunk = (4 * d + 2 * g1 + ((i16 >> 1) & 1)) ^ swz(rr);
       vp[e][d] = tile3 + rr * 1024 + 256 * wave + (chunk << 4) + 8 * (i16 & 1);
     }
-
-  const uint32_t place = Group<L>::place(lane), doff = Group<L>::data_off(lane),
+  const uint32_t place = Group<L>::place(lane, G > 1 ? 0 : wave & 1), doff = Group<L>::data_off(lane),
                  soff = Group<L>::scale_off(lane);
 
   const int32_t width = (int32_t)min(p.pt_width, (int64_t)0x7FFFFFFF);
@@ -654,7 +658,7 @@ void attend_kernel(AttendParams p) {
         for (int k = 0; k < Group<L>::N; ++k)
 #pragma unroll
           for (int j = 0; j < Group<L>::parts(k); ++j)
-            gr[g].put(tile3 + (row0 + 8 * g) * 1024, place, lane, k, j);
+            gr[g].put(tile3 + (row0 + 8 * g) * 1024, G > 1 ? place ^ (32 * (g & 1)) : place, lane, k, j);
       if (lane < G) svalid[wave * G + lane] = (uint8_t)(okm >> (8 * lane));
       if (tl + 1 < w.t1) okm = load(gr, tl + 1, page);
       page = entry(min(tl + 2, w.t1 - 1));
@@ -664,7 +668,7 @@ void attend_kernel(AttendParams p) {
       f32x16 sc;
 #pragma unroll
       for (int k = 0; k < 32; ++k) {
-        const u32x4 x = *(const __attribute__((address_space(3))) u32x4*)(kp[k & 3] + 32 * (k & ~3));
+        const u32x4 x = *(const __attribute__((address_space(3))) u32x4*)(kp[k & 7] + 32 * (k & ~7));
         score_mfma(sc, __builtin_bit_cast(bf16x8, x), qv[k], k == 0);
       }
       scores_done(sc);
@@ -739,7 +743,7 @@ void attend_kernel(AttendParams p) {
 #pragma unroll
           for (int e = 0; e < 2; ++e)
             x.half[e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                (__attribute__((address_space(3))) s16x4*)(vp[e][d & 1] + 128 * (d >> 1) + 16384 * k));
+                (__attribute__((address_space(3))) s16x4*)(vp[e][d] + 16384 * k));
 #pragma unroll
           for (int y = 0; y < QB; ++y) out_mfma(o[d][y], x.v, wv[y]);
         }
@@ -779,19 +783,15 @@ void attend_wide_kernel(AttendParams p) {
   const bool tree = p.tree != nullptr;
   const lds_ptr tiles3 = (lds_ptr)tiles, wts3 = (lds_ptr)wts;
   const int i16 = lane & 15, g1 = (lane >> 4) & 1;
-  // LDS offsets within a tile (see attend_kernel) and within a weights' buffer
-  uint32_t kp[4], vp[2][2];
+  // LDS offsets within a tile (see attend_kernel); other chunks by XOR
+  const uint32_t kbase = ql * 1024 + ((h ^ swz(ql)) << 4);
+  uint32_t vbase[2];
 #pragma unroll
-  for (int k = 0; k < 4; ++k) kp[k] = ql * 1024 + (((2 * k + h) ^ swz(ql)) << 4);
-#pragma unroll
-  for (int e = 0; e < 2; ++e)
-#pragma unroll
-    for (int d = 0; d < 2; ++d) {
-      const int rr = 8 * h + 4 * e + (i16 >> 2);
-      vp[e][d] = rr * 1024 + 256 * wave + (((4 * d + 2 * g1 + ((i16 >> 1) & 1)) ^ swz(rr)) << 4) +
-                 8 * (i16 & 1);
-    }
-  const uint32_t place = Group<L>::place(lane), doff = Group<L>::data_off(lane),
+  for (int e = 0; e < 2; ++e) {
+    const int rr = 8 * h + 4 * e + (i16 >> 2);
+    vbase[e] = rr * 1024 + 256 * wave + (((2 * g1 + ((i16 >> 1) & 1)) ^ swz(rr)) << 4) + 8 * (i16 & 1);
+  }
+  const uint32_t place = Group<L>::place(lane, wave & 1), doff = Group<L>::data_off(lane),
                  soff = Group<L>::scale_off(lane);
 
   const int32_t width = (int32_t)min(p.pt_width, (int64_t)0x7FFFFFFF);
@@ -857,12 +857,17 @@ void attend_wide_kernel(AttendParams p) {
     auto scores = [&](int32_t tl, uint32_t nxt) {
       // (opaque, so that the few bits each put changes are not kept in registers
       // of their own)
-      uint32_t pl = place;
-      asm volatile("" : "+v"(pl));
+      uint32_t pl = place, kb = kbase;
+      asm volatile("" : "+v"(pl), "+v"(kb));
       bf16x8 x[4];
+      uint32_t kp[8];                         // this tile's chunk columns
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        x[k] = __builtin_bit_cast(bf16x8, *(const __attribute__((address_space(3))) u32x4*)(tiles3 + cur + kp[k]));
+      for (int k = 0; k < 8; ++k) kp[k] = (kb ^ (32 * k)) + cur;
+      auto rows16 = [&](int k) {
+        return __builtin_bit_cast(bf16x8, *(const __attribute__((address_space(3))) u32x4*)(tiles3 + kp[k & 7] + 32 * (k & ~7)));
+      };
+#pragma unroll
+      for (int k = 0; k < 4; ++k) x[k] = rows16(k);
       if (lane == 0) svalid[(tl - w.t0 + 1) & 1][wave] = valid;
       valid_next = locate(tl + 2, page);
       page = entry(tl + 3);
@@ -871,9 +876,7 @@ void attend_wide_kernel(AttendParams p) {
 #pragma unroll
       for (int k = 0; k < 32; ++k) {
         score_mfma(sc, x[k & 3], qv[k], k == 0);
-        if (k + 4 < 32)
-          x[k & 3] = __builtin_bit_cast(
-              bf16x8, *(const __attribute__((address_space(3))) u32x4*)(tiles3 + cur + kp[k & 3] + 32 * ((k + 4) & ~3)));
+        if (k + 4 < 32) x[k & 3] = rows16(k + 4);
         if (k % 3 == 2 && load < NL) {
           gr.put(tiles3 + nxt + wave * 8192, pl, lane, load, in_load);
           if (++in_load == Group<L>::parts(load)) {
@@ -952,7 +955,8 @@ void attend_wide_kernel(AttendParams p) {
         }
       }
       int ln = lane;                          // opaque: kept from taking registers of its own
-      asm volatile("" : "+v"(ln));
+      uint32_t vb[2] = {vbase[0], vbase[1]};
+      asm volatile("" : "+v"(ln), "+v"(vb[0]), "+v"(vb[1]));
       const uint32_t wread = (ln & 31) * (2 * PS) + 16 * (ln >> 5);
       typedef __attribute__((address_space(3))) s16x4* trp;
       union Frag { s16x4 half[2]; bf16x8 v; };
@@ -961,7 +965,7 @@ void attend_wide_kernel(AttendParams p) {
 #pragma unroll
         for (int y = 0; y < 2; ++y)
           f.half[y] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-              (trp)(tiles3 + at + vp[y][i & 1] + 128 * ((i >> 1) & 1) + 16384 * (i >> 2)));
+              (trp)(tiles3 + (vb[y] ^ (64 * (i & 3))) + at + 16384 * (i >> 2)));
         return f.v;
       };
       bf16x8 wv[QB], xv = dims(0), xn;
