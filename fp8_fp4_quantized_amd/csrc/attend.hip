@@ -553,21 +553,32 @@ __device__ __forceinline__ void end_piece(const AttendParams& p, const Walk& w, 
 // before the output's own; the sum they are divided by is of the rounded
 // weights, so the division undoes a common part of it, while lse uses the
 // exact weights.
+//
+// This is the kernel for units of 32 (QB = 1) and 64 queries; a query's rows
+// are spread over NB waves, which agree on its reference maximum a tile late:
+// a tile's weights are taken against the maximum of the tiles before it, and
+// only where a score passes that by more than 16 (in log2; always in a piece's
+// first tile) are they taken again, after the waves have compared.  Two
+// barriers a tile then (QB = 1: three).  QB = 2 has two tile buffers and
+// expands the next tile between the score products; the 128-row tiles of
+// QB = 1 leave room for one.
+//
 // RUN: pages of 8 rows or more, so that an 8-row group lies in one page; smaller
 // pages look up every row.
 template <int L, int QB, bool RUN>
 __global__ __launch_bounds__(kAttendBlock) __attribute__((amdgpu_waves_per_eu(1, 1)))
 void attend_kernel(AttendParams p) {
   constexpr int NB = 4 / QB;
-  constexpr int QT = 32 * QB, NT = 32 * NB;
+  constexpr int QT = 32 * QB, NT = 32 * NB, TB = NT * 1024;
+  constexpr int BUF = QB == 2 ? 2 : 1;
   constexpr int RW = NT / 4;                  // rows a wave stages per tile
   constexpr int G = RW / 8;                   // in groups of 8
   constexpr int PS = NT + 8;                  // elements per query in the weights' tile
-  __shared__ __attribute__((aligned(1024))) uint8_t tile[NT * 1024];
+  __shared__ __attribute__((aligned(1024))) uint8_t tiles[BUF * TB];
   __shared__ __attribute__((aligned(16))) uint16_t wts[QT * PS];
-  __shared__ float smax[NB][QT], ssum[NB][QT], srsum[NB][QT], salpha[QT], sfac[QT];
-  __shared__ __attribute__((aligned(16))) uint8_t svalid[16];
-  __shared__ int32_t sscale[4], snf[4];
+  __shared__ float smax[NB][QT], ssum[NB][QT], srsum[NB][QT], sfac[QT];
+  __shared__ __attribute__((aligned(16))) uint8_t svalid[BUF][16];
+  __shared__ __attribute__((aligned(4))) uint8_t sjump[4], snf[4];
   const int lane = lane_id(), wave = uniform((int)(threadIdx.x >> 6));
   const int ql = lane & 31, h = lane >> 5;
   const int qb = wave % QB, nb = wave / QB;
@@ -578,22 +589,21 @@ void attend_kernel(AttendParams p) {
   // LDS addresses: row ql of the wave's score block, and the transposing reads
   // of its dim blocks (the permutation touches the low 4 bits of a chunk's
   // index only, so a few bases and constant offsets reach every chunk)
-  const lds_ptr tile3 = (lds_ptr)tile;
+  const lds_ptr tiles3 = (lds_ptr)tiles;
   const int i16 = lane & 15, g1 = (lane >> 4) & 1;
-  lds_cptr kp[8], vp[2][4];
+  uint32_t kp[8], vp[2][4];
 #pragma unroll
-  for (int k = 0; k < 8; ++k) kp[k] = tile3 + (nb * 32 + ql) * 1024 + (((2 * k + h) ^ swz(ql)) << 4);
+  for (int k = 0; k < 8; ++k) kp[k] = (nb * 32 + ql) * 1024 + (((2 * k + h) ^ swz(ql)) << 4);
 #pragma unroll
   for (int e = 0; e < 2; ++e)
 #pragma unroll
     for (int d = 0; d < 4; ++d) {
       const int rr = 8 * h + 4 * e + (i16 >> 2);
       const int chunk = (4 * d + 2 * g1 + ((i16 >> 1) & 1)) ^ swz(rr);
-      vp[e][d] = tile3 + rr * 1024 + 256 * wave + (chunk << 4) + 8 * (i16 & 1);
+      vp[e][d] = rr * 1024 + 256 * wave + (chunk << 4) + 8 * (i16 & 1);
     }
   const uint32_t place = Group<L>::place(lane, G > 1 ? 0 : wave & 1), doff = Group<L>::data_off(lane),
                  soff = Group<L>::scale_off(lane);
-
   const int32_t width = (int32_t)min(p.pt_width, (int64_t)0x7FFFFFFF);
 
   Walk w;
@@ -601,161 +611,255 @@ void attend_kernel(AttendParams p) {
   do {
     const int32_t m0 = w.ub * QT;
     Query q = query_of(p, w.b, w.s, m0 + qi);
-    const uint16_t* qp = p.q + (int64_t)(w.s.first + q.tok) * p.q_stride + (int64_t)q.head * p.q_hstride;
-    bf16x8 qv[32];
-#pragma unroll
-    for (int k = 0; k < 32; ++k) qv[k] = __builtin_bit_cast(bf16x8, ld_u4(qp + 16 * k + 8 * h));
-    // every query of the unit sees the rows below
     const int32_t lim_first = tree ? w.s.pos : uniform(
         (w.s.pos + (int32_t)udiv_magic((uint32_t)m0, p.head_div.m, p.head_div.sh1, p.head_div.sh2) + 1) >>
         (p.ratio - 1));
     const Rows<L> rw{{p.cache.base, p.cache.page_stride, p.cache.num_pages, p.cache.page_bits},
                      p.page_table + (int64_t)w.b * p.pt_stride, width, w.rows};
     const int32_t row0 = wave * RW;           // of the tile: this wave's first row to stage
-    auto entry = [&](int32_t tl) { return rw.entry(tl * NT + row0 + (lane & (RW - 1))); };
-    auto load = [&](Group<L> (&gr)[G], int32_t tl, int32_t page) -> uint32_t {
-      const int32_t r0 = tl * NT + row0;
-      const bool ok = lane < RW && rw.valid(r0 + lane, page, p.status);
-      const uint32_t okm = (uint32_t)__ballot(ok);
-#pragma unroll
-      for (int g = 0; g < G; ++g) {
-        // rows that are none load page 0's, which any cache has; they are masked
-        if constexpr (RUN) {
-          const int32_t pg = okm >> (8 * g) & 1 ? __builtin_amdgcn_readlane(page, 8 * g) : 0;
-          const uint8_t* d = rw.data(pg, r0 + 8 * g);
-          const uint8_t* sc = rw.scale(pg, r0 + 8 * g);
-#pragma unroll
-          for (int k = 0; k < Group<L>::N; ++k) gr[g].load(d, sc, doff, soff, k);
-        } else {
-          const int32_t safe = ok ? page : 0;
-#pragma unroll
-          for (int k = 0; k < Group<L>::N; ++k) {
-            const int row = Group<L>::row(k, lane);
-            const int64_t pg = __shfl(safe, 8 * g + row);
-            const int32_t r = r0 + 8 * g + row;
-            gr[g].load_apart(
-                rw.data(pg, r) + (doff + Group<L>::data_step(k) - row * LayoutTraits<L>::kData),
-                rw.scale(pg, r) + (soff + Group<L>::scale_step(k) - row * LayoutTraits<L>::kScale), k);
-          }
-        }
-      }
-      return okm;
-    };
+    auto first_row = [&](int32_t tl) { return min(tl, w.t1 - 1) * NT + row0; };
+    auto entry = [&](int32_t tl) { return rw.entry(first_row(tl) + (lane & (RW - 1))); };
+    // group g of a tile whose rows' pages are given; the pages' rows that are
+    // none load page 0's, which any cache has; they are masked
     Group<L> gr[G];
-    uint32_t okm = load(gr, w.t0, entry(w.t0));
-    int32_t page = entry(min(w.t0 + 1, w.t1 - 1));
+    constexpr int NL = Group<L>::N;
+    uint32_t okm, okm_next;
+    int32_t pages, r0;
+    auto locate = [&](int32_t tl, int32_t page) {
+      r0 = first_row(tl);
+      const bool ok = lane < RW && rw.valid(r0 + lane, page, p.status);
+      okm_next = (uint32_t)__ballot(ok);
+      pages = ok ? page : 0;
+    };
+    auto load = [&](int g, int k) {
+      if constexpr (RUN) {
+        const int32_t pg = __builtin_amdgcn_readlane(pages, 8 * g);
+        gr[g].load(rw.data(pg, r0 + 8 * g), rw.scale(pg, r0 + 8 * g), doff, soff, k);
+      } else {
+        const int row = Group<L>::row(k, lane);
+        const int64_t pg = __shfl(pages, 8 * g + row);
+        const int32_t r = r0 + 8 * g + row;
+        gr[g].load_apart(rw.data(pg, r) + (doff + Group<L>::data_step(k) - row * LayoutTraits<L>::kData),
+                         rw.scale(pg, r) + (soff + Group<L>::scale_step(k) - row * LayoutTraits<L>::kScale), k);
+      }
+    };
+    auto load_all = [&]() {
+#pragma unroll
+      for (int g = 0; g < G; ++g)
+#pragma unroll
+        for (int k = 0; k < NL; ++k) load(g, k);
+      okm = okm_next;
+    };
+    auto put = [&](uint32_t buf, int g, int k, int j) {
+      gr[g].put(tiles3 + buf + (row0 + 8 * g) * 1024, G > 1 ? place ^ (32 * (g & 1)) : place, lane, k, j);
+    };
+    auto put_all = [&](uint32_t buf) {
+#pragma unroll
+      for (int g = 0; g < G; ++g)
+#pragma unroll
+        for (int k = 0; k < NL; ++k)
+#pragma unroll
+          for (int j = 0; j < Group<L>::parts(k); ++j) put(buf, g, k, j);
+    };
+    auto note_valid = [&](int buf) {
+      if (lane < G) svalid[buf][wave * G + lane] = (uint8_t)(okm >> (8 * lane));
+    };
+    // the table entries of the first tiles and the first tile's rows are asked
+    // for before the queries are waited for
+    const int32_t page0 = entry(w.t0), page1 = entry(w.t0 + 1);
+    int32_t page = entry(w.t0 + 2);
+    locate(w.t0, page0);
+    load_all();
+    bf16x8 qv[32];
+    {
+      const uint16_t* qp = p.q + (int64_t)(w.s.first + q.tok) * p.q_stride +
+                           (int64_t)q.head * p.q_hstride + 8 * h;
+#pragma unroll
+      for (int k = 0; k < 32; ++k) qv[k] = __builtin_bit_cast(bf16x8, ld_u4(qp + 16 * k));
+    }
+    put_all(0);
+    note_valid(0);
+    locate(w.t0 + 1, page1);
+    load_all();
     f32x16 o[4][QB];
 #pragma unroll
     for (int d = 0; d < 4; ++d)
 #pragma unroll
       for (int x = 0; x < QB; ++x) o[d][x] = f32x16{};
+    float ref[QB];                            // reference maxima of all the unit's queries ql, 32 + ql
+#pragma unroll
+    for (int x = 0; x < QB; ++x) ref[x] = kNegInf;
+    __syncthreads();
 
+    typedef const __attribute__((address_space(3))) u32x4* vec;
+    typedef __attribute__((address_space(3))) s16x4* trp;
     for (int32_t tl = w.t0; tl < w.t1; ++tl) {
-      // ---- stage the tile's rows, request the next tile's
-#pragma unroll
-      for (int g = 0; g < G; ++g)
-#pragma unroll
-        for (int k = 0; k < Group<L>::N; ++k)
-#pragma unroll
-          for (int j = 0; j < Group<L>::parts(k); ++j)
-            gr[g].put(tile3 + (row0 + 8 * g) * 1024, G > 1 ? place ^ (32 * (g & 1)) : place, lane, k, j);
-      if (lane < G) svalid[wave * G + lane] = (uint8_t)(okm >> (8 * lane));
-      if (tl + 1 < w.t1) okm = load(gr, tl + 1, page);
-      page = entry(min(tl + 2, w.t1 - 1));
-      __syncthreads();
-
-      // ---- scores of this wave's 32 rows and 32 queries
+      const int par = BUF == 2 ? (tl - w.t0) & 1 : 0;
+      const uint32_t cur = par * TB;
+      if constexpr (BUF == 1) {
+        if (tl > w.t0) {
+          // ---- stage the tile's rows, request the next tile's
+          put_all(0);
+          note_valid(0);
+          locate(tl + 1, page);
+          page = entry(tl + 2);
+          load_all();
+          __syncthreads();
+        }
+      } else {
+        note_valid(par ^ 1);
+        locate(tl + 2, page);
+        page = entry(tl + 3);
+      }
+      // ---- scores of this wave's 32 rows and 32 queries; with two buffers, tile
+      // tl + 1 is expanded into the other one between, tile tl + 2 requested
       f32x16 sc;
+      {
+        constexpr int LA = 6;
+        bf16x8 x[LA];
+        auto rows16 = [&](int k) {
+          return __builtin_bit_cast(bf16x8, *(vec)(tiles3 + cur + kp[k & 7] + 32 * (k & ~7)));
+        };
 #pragma unroll
-      for (int k = 0; k < 32; ++k) {
-        const u32x4 x = *(const __attribute__((address_space(3))) u32x4*)(kp[k & 7] + 32 * (k & ~7));
-        score_mfma(sc, __builtin_bit_cast(bf16x8, x), qv[k], k == 0);
+        for (int k = 0; k < LA; ++k) x[k] = rows16(k);
+        int g = 0, ld = 0, in_load = 0;       // constants after unrolling
+#pragma unroll
+        for (int k = 0; k < 32; ++k) {
+          score_mfma(sc, x[k % LA], qv[k], k == 0);
+          if (k + LA < 32) x[k % LA] = rows16(k + LA);
+          if constexpr (BUF == 2) {
+            if (k % 3 != 0 && g < G) {
+              put(cur ^ TB, g, ld, in_load);
+              if (++in_load == Group<L>::parts(ld)) {
+                load(g, ld);
+                in_load = 0;
+                if (++ld == NL) ld = 0, ++g;
+              }
+            }
+          }
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        if constexpr (BUF == 2) okm = okm_next;
       }
       scores_done(sc);
       // ---- mask (only a tile that some query does not see whole)
       bool holes = (tl + 1) * NT > lim_first;
 #pragma unroll
-      for (int x = 0; x < NB; ++x) holes |= *(const uint32_t*)(svalid + 4 * x) != 0xFFFFFFFFu;
+      for (int x = 0; x < NB; ++x) holes |= uniform(*(const int32_t*)(svalid[par] + 4 * x)) != -1;
       if (holes) {
         const bool any = mask_scores(sc, q, tl * NT + nb * 32, h, w.s.pos, tree,
-                                     *(const uint32_t*)(svalid + 4 * nb));
+                                     *(const uint32_t*)(svalid[par] + 4 * nb));
         if (lane == 0) snf[wave] = any;
       }
-      // ---- the query's new reference maximum
+      // ---- the block's maximum
       float tm = max3(sc[0], sc[1], sc[2]);
 #pragma unroll
       for (int i = 3; i < 15; i += 2) tm = max3(tm, sc[i], sc[i + 1]);
-      tm = max_halves(max3(tm, sc[15], sc[15]));
-      if constexpr (NB > 1) {
-        if (h == 0) smax[nb][qi] = tm;
-        __syncthreads();
-#pragma unroll
-        for (int x = 0; x < NB; ++x) tm = fmaxf(tm, smax[x][qi]);
-      }
-      const float alpha = raise_max(q, tm * c2);
-      const float ref = q.mx == kNegInf ? 0.0f : q.mx;
+      tm = max_halves(max3(tm, sc[15], sc[15])) * c2;
+      smax[nb][qi] = tm;                      // (both halves of the wave write the same)
+      float mine = QB == 1 || qb == 0 ? ref[0] : ref[QB - 1];
+      const bool jump = __ballot(tm > mine + 16.0f) != 0;
+      if (lane == 0) sjump[wave] = jump;
       // ---- weights, their sums, and their bf16 to LDS
       uint16_t* const wrow = wts + qi * PS + nb * 32 + 4 * h;
+      float ts, tr;
+      auto weigh = [&](float at) {
+        const float base = at == kNegInf ? 0.0f : at;
+        ts = tr = 0.0f;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        float e[4];
+        for (int j = 0; j < 4; ++j) {
+          float e[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          e[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[4 * j + i], c2, -ref));
-          q.sum += e[i];
+          for (int i = 0; i < 4; ++i) {
+            e[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[4 * j + i], c2, -base));
+            ts += e[i];
+          }
+          const uint32_t w0 = pack_bf16(e[0], e[1]), w1 = pack_bf16(e[2], e[3]);
+          tr = add_pair(add_pair(tr, w0), w1);
+          *(u32x2*)(wrow + 8 * j) = u32x2{w0, w1};
         }
-        const uint32_t w0 = pack_bf16(e[0], e[1]), w1 = pack_bf16(e[2], e[3]);
-        q.rsum = add_pair(add_pair(q.rsum, w0), w1);
-        *(u32x2*)(wrow + 8 * j) = u32x2{w0, w1};
-      }
-      const bool rescale = __ballot(alpha != 1.0f) != 0;
-      if (nb == 0) {
-        if (h == 0) salpha[qi] = alpha;
-        if (lane == 0) sscale[qb] = rescale;
-      }
+      };
+      weigh(mine);
       __syncthreads();
-      // ---- a NaN or an infinity in a row that some query does not see: its
-      // weight there is 0, and 0 times it would not be
-      if (holes && (snf[0] | snf[1] | snf[2] | snf[3]) != 0) {
-        zero_not_finite<NT * 1024>(tile3);
-        __syncthreads();
-      }
-      // ---- O += X^T P^T on dims [128 wave, 128 wave + 128)
+      // ---- the tile's maxima over the waves of each query
+      float top[QB];
 #pragma unroll
       for (int x = 0; x < QB; ++x) {
-        if (sscale[x] == 0) continue;
-        const float a = salpha[x * 32 + ql];
+        top[x] = smax[0][x * 32 + ql];
 #pragma unroll
-        for (int d = 0; d < 4; ++d) {
-          out_done(o[d][x]);
-          o[d][x] *= a;
-        }
+        for (int y = 1; y < NB; ++y) top[x] = fmaxf(top[x], smax[y][x * 32 + ql]);
       }
+      const bool again = uniform(*(const int32_t*)sjump) != 0;
+      const bool dirty = holes && uniform(*(const int32_t*)snf) != 0;
+      // raises the references passed by more than 8 and rescales what was summed
+      auto raise = [&]() {
 #pragma unroll
-      for (int k = 0; k < NT / 16; ++k) {
-        bf16x8 wv[QB];
+        for (int x = 0; x < QB; ++x) {
+          const float old = ref[x];
+          if (top[x] > old + 8.0f) ref[x] = top[x];
+          const float alpha = ref[x] == old ? 1.0f : __builtin_amdgcn_exp2f(old - ref[x]);
+          if (__ballot(alpha != 1.0f) == 0) continue;
+          if (x == qb) {
+            q.sum *= alpha;
+            q.rsum *= alpha;
+          }
 #pragma unroll
-        for (int x = 0; x < QB; ++x)
-          wv[x] = __builtin_bit_cast(bf16x8, *(const u32x4*)(wts + (x * 32 + ql) * PS + 16 * k + 8 * h));
-#pragma unroll
-        for (int d = 0; d < 4; ++d) {
-          union { s16x4 half[2]; bf16x8 v; } x;
+          for (int d = 0; d < 4; ++d) {
+            out_done(o[d][x]);
+            o[d][x] *= alpha;
+          }
+        }
+      };
+      if (again) {
+        raise();
+        weigh(QB == 1 || qb == 0 ? ref[0] : ref[QB - 1]);
+      }
+      // a NaN or an infinity in a row that some query does not see: its weight
+      // there is 0, and 0 times it would not be
+      if (dirty) zero_not_finite<TB>(tiles3 + cur);
+      if (again || dirty) __syncthreads();
+      q.sum += ts;
+      q.rsum += tr;
+      // ---- O += X^T P^T on dims [128 wave, 128 wave + 128)
+      {
+        union Frag { s16x4 half[2]; bf16x8 v; };
+        auto dims = [&](int i) {              // dim block i & 3, rows 16 (i >> 2) ..
+          Frag f;
 #pragma unroll
           for (int e = 0; e < 2; ++e)
-            x.half[e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                (__attribute__((address_space(3))) s16x4*)(vp[e][d] + 16384 * k));
+            f.half[e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                (trp)(tiles3 + cur + vp[e][i & 3] + 16384 * (i >> 2)));
+          return f.v;
+        };
+        auto weights = [&](int k, int x) {
+          return __builtin_bit_cast(bf16x8, *(const u32x4*)(wts + (x * 32 + ql) * PS + 16 * k + 8 * h));
+        };
+        constexpr int N = NT / 4;             // dim blocks times 16-row steps
+        bf16x8 xv[3], wv[2][QB];
 #pragma unroll
-          for (int y = 0; y < QB; ++y) out_mfma(o[d][y], x.v, wv[y]);
+        for (int x = 0; x < QB; ++x) wv[0][x] = weights(0, x);
+#pragma unroll
+        for (int i = 0; i < 3; ++i) xv[i] = dims(i);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+#pragma unroll
+          for (int x = 0; x < QB; ++x) out_mfma(o[i & 3][x], xv[i % 3], wv[(i >> 2) & 1][x]);
+          if (i + 3 < N) xv[i % 3] = dims(i + 3);
+          if ((i & 3) == 1 && i + 4 < N) {
+#pragma unroll
+            for (int x = 0; x < QB; ++x) wv[((i >> 2) + 1) & 1][x] = weights((i >> 2) + 1, x);
+          }
+          __builtin_amdgcn_sched_barrier(0);
         }
-        __builtin_amdgcn_sched_barrier(0);
       }
-      __syncthreads();                        // the tile and the weights are free
+      if (!again) raise();
+      __syncthreads();                        // the tile, the weights and the maxima are free
     }
 #pragma unroll
     for (int d = 0; d < 4; ++d)
 #pragma unroll
       for (int x = 0; x < QB; ++x) out_done(o[d][x]);
-
+    q.mx = QB == 1 || qb == 0 ? ref[0] : ref[QB - 1];
     end_piece<QB>(p, w, q, o, qb, nb, ssum, srsum, sfac);
     __syncthreads();
   } while (w.next(p, QT, NT));
@@ -774,8 +878,12 @@ void attend_wide_kernel(AttendParams p) {
   constexpr int QB = 4, QT = 128, NT = 32, PS = NT + 8, TB = NT * 1024, WB = QT * PS * 2;
   __shared__ __attribute__((aligned(1024))) uint8_t tiles[3 * TB];
   __shared__ __attribute__((aligned(16))) uint8_t wts[2 * WB];
+  constexpr int kTail = 8;
+  __shared__ __attribute__((aligned(16))) uint8_t qtail[4 * kTail * 1024];
   __shared__ float ssum[1][QT], srsum[1][QT], sfac[QT], salpha[2][QT];
-  __shared__ int32_t svalid[2][4], sscale[2][4], snf[2][4];
+  // a byte a wave: the tile's valid 8-row groups, the rescaled query blocks, the
+  // blocks that met a score that is not finite where it is masked
+  __shared__ __attribute__((aligned(4))) uint8_t svalid[2][4], sscale[2][4], snf[2][4];
   const int lane = lane_id(), wave = uniform((int)(threadIdx.x >> 6));
   const int ql = lane & 31, h = lane >> 5;
   const int qi = wave * 32 + ql;
@@ -801,13 +909,6 @@ void attend_wide_kernel(AttendParams p) {
   do {
     const int32_t m0 = w.ub * QT;
     Query q = query_of(p, w.b, w.s, m0 + qi);
-    bf16x8 qv[32];
-    {
-      const uint16_t* qp = p.q + (int64_t)(w.s.first + q.tok) * p.q_stride +
-                           (int64_t)q.head * p.q_hstride + 8 * h;
-#pragma unroll
-      for (int k = 0; k < 32; ++k) qv[k] = __builtin_bit_cast(bf16x8, ld_u4(qp + 16 * k));
-    }
     const int32_t lim_first = tree ? w.s.pos : uniform(
         (w.s.pos + (int32_t)udiv_magic((uint32_t)m0, p.head_div.m, p.head_div.sh1, p.head_div.sh2) + 1) >>
         (p.ratio - 1));
@@ -830,54 +931,115 @@ void attend_wide_kernel(AttendParams p) {
     };
     Group<L> gr;
     constexpr int NL = Group<L>::N;
-    bool valid = locate(w.t0, entry(w.t0)), valid_next;
+    // the table entries of the first three tiles, then the first tile's rows,
+    // are asked for before the queries are waited for
+    const int32_t page0 = entry(w.t0), page1 = entry(w.t0 + 1);
+    int32_t page = entry(w.t0 + 2);
+    bool valid = locate(w.t0, page0);
 #pragma unroll
     for (int k = 0; k < NL; ++k) gr.load(ldata, lscale, doff, soff, k);
+    // the queries' fragments: the last kTail of them in LDS (the registers do not
+    // hold all beside the rest)
+    bf16x8 qv[32 - kTail];
+    {
+      const uint16_t* qp = p.q + (int64_t)(w.s.first + q.tok) * p.q_stride +
+                           (int64_t)q.head * p.q_hstride + 8 * h;
+#pragma unroll
+      for (int k = 0; k < 32 - kTail; ++k) qv[k] = __builtin_bit_cast(bf16x8, ld_u4(qp + 16 * k));
+#pragma unroll
+      for (int k = 0; k < kTail; ++k)
+        *(u32x4*)(qtail + (wave * kTail + k) * 1024 + 16 * lane) = *(const u32x4*)(qp + 16 * (32 - kTail + k));
+    }
 #pragma unroll
     for (int k = 0; k < NL; ++k)
 #pragma unroll
       for (int j = 0; j < Group<L>::parts(k); ++j) gr.put(tiles3 + wave * 8192, place, lane, k, j);
-    if (lane == 0) svalid[0][wave] = valid;
-    valid = locate(w.t0 + 1, entry(w.t0 + 1));
+    if (lane == 0) svalid[0][wave] = valid ? 0xFF : 0;
+    valid = locate(w.t0 + 1, page1);
 #pragma unroll
     for (int k = 0; k < NL; ++k) gr.load(ldata, lscale, doff, soff, k);
-    int32_t page = entry(w.t0 + 2);
     f32x16 o[4][QB];
 #pragma unroll
     for (int d = 0; d < 4; ++d)
 #pragma unroll
       for (int x = 0; x < QB; ++x) o[d][x] = f32x16{};
-    uint32_t cur = 0;                         // offset of the tile at hand in tiles
     __syncthreads();
 
+    typedef const __attribute__((address_space(3))) u32x4* vec;
+    typedef __attribute__((address_space(3))) s16x4* trp;
     f32x16 sc;
-    bool holes = false, holes_before;
-    // ---- scores of tile tl, which lies at cur; tile tl + 1 is expanded into the
-    // buffer after it, tile tl + 2 requested
-    auto scores = [&](int32_t tl, uint32_t nxt) {
-      // (opaque, so that the few bits each put changes are not kept in registers
-      // of their own)
-      uint32_t pl = place, kb = kbase;
-      asm volatile("" : "+v"(pl), "+v"(kb));
-      bf16x8 x[4];
-      uint32_t kp[8];                         // this tile's chunk columns
+    bf16x8 x[6];                              // row fragments ahead of the score products
+    bf16x8 wv[QB], xv[2];                     // weights, dim fragments ahead of the O products
+    uint32_t kp[8];                           // the tile's chunk columns
+    bool holes = false, holes_before = false;
+    uint32_t okg, cuts;                       // svalid, sscale as words
+    // (lane bases opaque to the compiler, which would otherwise keep what is
+    // derived from them in registers of its own)
+    auto fresh = [](uint32_t v) { asm volatile("" : "+v"(v)); return v; };
+    auto score_rows = [&](int k) {
+      return __builtin_bit_cast(bf16x8, *(vec)(tiles3 + kp[k & 7] + 32 * (k & ~7)));
+    };
+    auto query_tail = [&](int k) {
+      return __builtin_bit_cast(bf16x8, *(vec)((lds_cptr)qtail + (wave * kTail + k - (32 - kTail)) * 1024 + 16 * fresh(lane)));
+    };
+    // the first fragments of the tile at cur, and what was noted of it and of
+    // the tile before (parity par: the tile's)
+    auto ahead = [&](int i, uint32_t cur, int32_t par) {
+      if (i == 0) {
+        const uint32_t kb = fresh(kbase);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) kp[k] = (kb ^ (32 * k)) + cur;
-      auto rows16 = [&](int k) {
-        return __builtin_bit_cast(bf16x8, *(const __attribute__((address_space(3))) u32x4*)(tiles3 + kp[k & 7] + 32 * (k & ~7)));
-      };
+        for (int k = 0; k < 8; ++k) kp[k] = (kb ^ (32 * k)) + cur;
+        okg = *(const uint32_t*)svalid[par];
+        cuts = *(const uint32_t*)sscale[par ^ 1];
+      }
+      x[i] = score_rows(i);
+    };
+    union Frag { s16x4 half[2]; bf16x8 v; };
+    uint32_t vb[2], wread;
+    auto out_dims = [&](int i, uint32_t at) { // dim block i & 3, rows 16 (i >> 2) ..
+      Frag f;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) x[k] = rows16(k);
-      if (lane == 0) svalid[(tl - w.t0 + 1) & 1][wave] = valid;
-      valid_next = locate(tl + 2, page);
+      for (int y = 0; y < 2; ++y)
+        f.half[y] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+            (trp)(tiles3 + (vb[y] ^ (64 * (i & 3))) + at + 16384 * (i >> 2)));
+      return f.v;
+    };
+    auto out_weights = [&](int i, int y, int32_t par) {
+      return __builtin_bit_cast(bf16x8, *(vec)(wts3 + par * WB + wread + y * 64 * PS + 32 * i));
+    };
+    // the first fragments of O's products: the tile at `at`, weights of parity par
+    auto out_ahead = [&](int i, uint32_t at, int32_t par) {
+      if (i == 0) {
+        vb[0] = fresh(vbase[0]), vb[1] = fresh(vbase[1]);
+        const uint32_t ln = fresh(lane);
+        wread = (ln & 31) * (2 * PS) + 16 * (ln >> 5);
+        xv[0] = out_dims(0, at);
+      } else if (i == 1) {
+        wv[0] = out_weights(0, 0, par), wv[1] = out_weights(0, 1, par);
+      } else if (i == 2) {
+        wv[2] = out_weights(0, 2, par), wv[3] = out_weights(0, 3, par);
+      } else {
+        xv[1] = out_dims(1, at);
+      }
+    };
+    // ---- scores of tile tl at cur (its first fragments in x); tile tl + 1 is
+    // expanded into the buffer at nxt, tile tl + 2 requested; at the end the first
+    // fragments of O's products over the tile before are read
+    auto scores = [&](int32_t tl, uint32_t nxt, uint32_t before) {
+      const int32_t par = (tl - w.t0) & 1;
+      const uint32_t pl = fresh(place);
+      if (lane == 0) svalid[par ^ 1][wave] = valid ? 0xFF : 0;
+      const bool valid_next = locate(tl + 2, page);
       page = entry(tl + 3);
-      __builtin_amdgcn_sched_barrier(0);
+      bf16x8 qt[3];
       int load = 0, in_load = 0;              // constants after unrolling
 #pragma unroll
       for (int k = 0; k < 32; ++k) {
-        score_mfma(sc, x[k & 3], qv[k], k == 0);
-        if (k + 4 < 32) x[k & 3] = rows16(k + 4);
-        if (k % 3 == 2 && load < NL) {
+        score_mfma(sc, x[k % 6], k < 32 - kTail ? qv[k < 32 - kTail ? k : 0] : qt[k % 3], k == 0);
+        if (k + 3 >= 32 - kTail && k + 3 < 32) qt[k % 3] = query_tail(k + 3);
+        if (k + 6 < 32) x[k % 6] = score_rows(k + 6);
+        if (k >= 28) out_ahead(k - 28, before, par ^ 1);
+        if (k % 3 == 1 && load < NL) {
           gr.put(tiles3 + nxt + wave * 8192, pl, lane, load, in_load);
           if (++in_load == Group<L>::parts(load)) {
             gr.load(ldata, lscale, doff, soff, load);
@@ -891,22 +1053,18 @@ void attend_wide_kernel(AttendParams p) {
     };
     // ---- mask (only a tile that some query does not see whole)
     auto mask = [&](int32_t tl) {
-      const int32_t par = (tl - w.t0) & 1;
       holes_before = holes;
-      uint32_t okw = 0;
-#pragma unroll
-      for (int x = 0; x < 4; ++x) okw |= svalid[par][x] != 0 ? 0xFFu << (8 * x) : 0u;
+      const uint32_t okw = (uint32_t)uniform((int32_t)okg);
       holes = (tl + 1) * NT > lim_first || okw != 0xFFFFFFFFu;
       if (holes) {
         scores_done(sc);
         const bool any = mask_scores(sc, q, tl * NT, h, w.s.pos, tree, okw);
-        if (lane == 0) snf[par][wave] = any;
+        if (lane == 0) snf[(tl - w.t0) & 1][wave] = any;
       }
     };
-    // ---- the softmax of a tile in 32 steps: maximum, then a weight a step
+    // ---- the softmax of a tile in 24 steps: maximum, then a weight a step
     float tm, ref, alpha, e[4];
-    // (ln: the lane, as the caller holds it)
-    auto soften = [&](int step, int32_t par, int ln) {
+    auto soften = [&](int step, int32_t par) {
       if (step == 1) scores_done(sc);
       if (step >= 1 && step < 5) {
         const int i = 4 * (step - 1);
@@ -920,8 +1078,10 @@ void attend_wide_kernel(AttendParams p) {
       }
       if (step == 7) {
         const bool rescale = __ballot(alpha != 1.0f) != 0;
-        if (ln < 32) salpha[par][wave * 32 + ln] = alpha;
-        if (ln == 0) sscale[par][wave] = rescale;
+        const uint32_t ln = fresh(lane);
+        // (both halves of the wave write the same values)
+        salpha[par][wave * 32 + (ln & 31)] = alpha;
+        sscale[par][wave] = rescale ? 1 : 0;
       }
       if (step >= 8 && step < 24) {
         const int i = step - 8;
@@ -930,82 +1090,85 @@ void attend_wide_kernel(AttendParams p) {
         if ((i & 3) == 3) {
           const uint32_t w0 = pack_bf16(e[0], e[1]), w1 = pack_bf16(e[2], e[3]);
           q.rsum = add_pair(add_pair(q.rsum, w0), w1);
-          const uint32_t wwrite = ((ln & 31) + 32 * wave) * (2 * PS) + 8 * (ln >> 5);
-          *(__attribute__((address_space(3))) u32x2*)(wts3 + par * WB + wwrite + 16 * (i >> 2)) = u32x2{w0, w1};
+          const uint32_t ln = fresh(lane);
+          const uint32_t at = ((ln & 31) + 32 * wave) * (2 * PS) + 8 * (ln >> 5) + 16 * (i >> 2);
+          *(__attribute__((address_space(3))) u32x2*)(wts3 + par * WB + at) = u32x2{w0, w1};
+        }
+      }
+    };
+    // ---- what must precede O's products over the tile at `at` (parity par)
+    auto out_begin = [&](uint32_t at, int32_t par, bool dirty) {
+      // a NaN or an infinity in a row that some query does not see: its weight
+      // there is 0, and 0 times it would not be
+      if (dirty && uniform(*(const int32_t*)snf[par]) != 0) {
+        zero_not_finite<TB>(tiles3 + at);
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) out_ahead(i, at, par);
+      }
+#pragma unroll
+      for (int y = 0; y < QB; ++y) {
+        if ((uniform((int32_t)cuts) >> (8 * y) & 0xFF) == 0) continue;
+        const float a = salpha[par][y * 32 + ql];
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+          out_done(o[d][y]);
+          o[d][y] *= a;
         }
       }
     };
     // ---- O += X^T P^T of the tile at `at` with the weights of parity par, on dims
-    // [128 wave, 128 wave + 128); with = true: the softmax of the next tile between
-    auto out = [&](uint32_t at, int32_t par, auto with) {
-      // a NaN or an infinity in a row that some query does not see: its weight
-      // there is 0, and 0 times it would not be
-      if ((with.value ? holes_before : holes) && (snf[par][0] | snf[par][1] | snf[par][2] | snf[par][3]) != 0) {
-        zero_not_finite<TB>(tiles3 + at);
-        __syncthreads();
-      }
-#pragma unroll
-      for (int x = 0; x < QB; ++x) {
-        if (sscale[par][x] == 0) continue;
-        const float a = salpha[par][x * 32 + ql];
-#pragma unroll
-        for (int d = 0; d < 4; ++d) {
-          out_done(o[d][x]);
-          o[d][x] *= a;
-        }
-      }
-      int ln = lane;                          // opaque: kept from taking registers of its own
-      uint32_t vb[2] = {vbase[0], vbase[1]};
-      asm volatile("" : "+v"(ln), "+v"(vb[0]), "+v"(vb[1]));
-      const uint32_t wread = (ln & 31) * (2 * PS) + 16 * (ln >> 5);
-      typedef __attribute__((address_space(3))) s16x4* trp;
-      union Frag { s16x4 half[2]; bf16x8 v; };
-      auto dims = [&](int i) {                // dim block i & 3, rows 16 (i >> 2) ..
-        Frag f;
-#pragma unroll
-        for (int y = 0; y < 2; ++y)
-          f.half[y] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-              (trp)(tiles3 + (vb[y] ^ (64 * (i & 3))) + at + 16384 * (i >> 2)));
-        return f.v;
-      };
-      bf16x8 wv[QB], xv = dims(0), xn;
-#pragma unroll
-      for (int x = 0; x < QB; ++x)
-        wv[x] = __builtin_bit_cast(bf16x8, *(const __attribute__((address_space(3))) u32x4*)(wts3 + par * WB + wread + x * 64 * PS));
-      __builtin_amdgcn_sched_barrier(0);
+    // [128 wave, 128 wave + 128); with = true: between them the softmax of the
+    // next tile, the barrier after its weights and this tile's last reads, and
+    // the first fragments of the tile at nxt
+    auto out = [&](uint32_t at, int32_t par, uint32_t nxt, auto with) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        if (i < 7) xn = dims(i + 1);
+        const bf16x8 xi = xv[i & 1];
 #pragma unroll
-        for (int x = 0; x < QB; ++x) {
-          out_mfma(o[i & 3][x], xv, wv[x]);
-          if (i == 3)
-            wv[x] = __builtin_bit_cast(bf16x8, *(const __attribute__((address_space(3))) u32x4*)(wts3 + par * WB + wread + x * 64 * PS + 32));
-          if constexpr (with.value) soften(4 * i + x, par ^ 1, ln);
+        for (int y = 0; y < QB; ++y) {
+          out_mfma(o[i & 3][y], xi, wv[y]);
+          if (y == 0 && i + 2 < 8) xv[i & 1] = out_dims(i + 2, at);
+          if (i == 3) wv[y] = out_weights(1, y, par);
+          if constexpr (with.value) {
+            soften(4 * i + y, par ^ 1);
+            if (i == 6 && y == 0) __syncthreads();
+            if (i == 6 && y > 0) ahead(y - 1, nxt, par);
+            if (i == 7 && y < 3) ahead(y + 3, nxt, par);
+          }
           __builtin_amdgcn_sched_barrier(0);
         }
-        xv = xn;
       }
     };
     auto after = [](uint32_t at) { return at == 2 * TB ? 0u : at + TB; };
-    scores(w.t0, after(cur));
+    uint32_t cur = 0;                         // offset of the tile at hand in tiles
+#pragma unroll
+    for (int i = 0; i < 6; ++i) ahead(i, cur, 0);
+    scores(w.t0, after(cur), cur);
     mask(w.t0);
 #pragma unroll
-    for (int i = 0; i < 24; ++i) soften(i, 0, lane);
+    for (int i = 0; i < 24; ++i) soften(i, 0);
     __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 6; ++i) ahead(i, after(cur), 1);
     for (int32_t tl = w.t0 + 1; tl < w.t1; ++tl) {
+      const int32_t par = (tl - w.t0) & 1;
       const uint32_t before = cur;
       cur = after(cur);
-      scores(tl, after(cur));
+      scores(tl, after(cur), before);
       mask(tl);
-      out(before, (tl - w.t0 - 1) & 1, std::true_type{});
-      __syncthreads();
+      out_begin(before, par ^ 1, holes_before);
+      out(before, par ^ 1, after(cur), std::true_type{});
     }
-    out(cur, (w.t1 - 1 - w.t0) & 1, std::false_type{});
+    const int32_t last = (w.t1 - 1 - w.t0) & 1;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) out_ahead(i, cur, last);
+    out_begin(cur, last, holes);
+    out(cur, last, 0, std::false_type{});
 #pragma unroll
     for (int d = 0; d < 4; ++d)
 #pragma unroll
-      for (int x = 0; x < QB; ++x) out_done(o[d][x]);
+      for (int y = 0; y < QB; ++y) out_done(o[d][y]);
     end_piece<QB>(p, w, q, o, wave, 0, ssum, srsum, sfac);
     __syncthreads();
   } while (w.next(p, QT, NT));
@@ -1076,23 +1239,19 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendParams p, int qt
     p.lse[(int64_t)(s.first + tok) * p.heads + head] = fin.lse;
 }
 
-template <int L, bool RUN>
-hipError_t attend(const AttendParams& p, int qblocks, hipStream_t stream) {
-  const dim3 grid(kAttendGrid), block(kAttendBlock);
-  switch (qblocks) {
-    case 1: hipLaunchKernelGGL((attend_kernel<L, 1, RUN>), grid, block, 0, stream, p); break;
-    case 2: hipLaunchKernelGGL((attend_kernel<L, 2, RUN>), grid, block, 0, stream, p); break;
-    default:
-      if constexpr (RUN) hipLaunchKernelGGL((attend_wide_kernel<L>), grid, block, 0, stream, p);
-      else hipLaunchKernelGGL((attend_kernel<L, 4, false>), grid, block, 0, stream, p);
-  }
-  return hipGetLastError();
-}
-
 template <int L>
 hipError_t attend(const AttendParams& p, int qblocks, hipStream_t stream) {
-  return p.cache.page_bits >= 3 ? attend<L, true>(p, qblocks, stream)
-                                : attend<L, false>(p, qblocks, stream);
+  const dim3 grid(kAttendGrid), block(kAttendBlock);
+  const bool run = p.cache.page_bits >= 3;
+  auto go = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, grid, block, 0, stream, p);
+    return hipGetLastError();
+  };
+  switch (qblocks) {
+    case 1: return run ? go(attend_kernel<L, 1, true>) : go(attend_kernel<L, 1, false>);
+    case 2: return run ? go(attend_kernel<L, 2, true>) : go(attend_kernel<L, 2, false>);
+    default: return go(attend_wide_kernel<L>);
+  }
 }
 
 }  // namespace

@@ -173,7 +173,8 @@ int attend(const kvc_attend_args* a, bool tree, void* stream, const char* who) {
   p.out_hstride = a->out_head_stride;
   p.lse = a->lse;
   p.status = a->status;
-  const int qblocks = attend_qblocks(a->num_slots, tokens, a->num_heads);
+  int qblocks = attend_qblocks(a->num_slots, tokens, a->num_heads);
+  if (a->cache.page_size < 8 && qblocks == 4) qblocks = 2;   // the wide kernel's pages hold 8 rows or more
   p.units_max = tokens * a->num_heads / (32 * qblocks) + a->num_slots;
   uint8_t* w = static_cast<uint8_t*>(a->workspace);
   p.head = reinterpret_cast<kvc::AttendHead*>(w + at[0]);
