@@ -443,16 +443,23 @@ def prepare_dequant_gather(cache: Cache, page_table: torch.Tensor | None, ids: t
 
 
 # ------------------------------------------------------------------ slot map
-def _one_device(**tensors):
-    """The device that every given tensor is on."""
-    dev = None
-    for name, t in tensors.items():
-        if t is None:
-            continue
-        if dev is None:
-            dev = t.device
-        _need(t.device == dev, f"{name}: on {t.device}, other arguments on {dev}")
-    return dev
+def _one_device(dev, tensors) -> None:
+    """Refuses (name, tensor) pairs that are on another device than ``dev``
+    (None: left out)."""
+    for name, t in tensors:
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name}: on {t.device}, other arguments on {dev}")
+
+
+def _i32(t, n: int, name: str) -> int | None:
+    """Pointer of a contiguous int32 device tensor of at least n entries, or
+    None for None."""
+    if t is None:
+        return None
+    if t.dtype is torch.int32 and t.numel() >= n and t.is_cuda and t.is_contiguous():
+        return t.data_ptr()
+    _need(t.numel() >= n, f"{name}: {t.numel()} entries, need {n}")
+    return _dense(t, _I32_T, name)
 
 
 def _pt_stride(page_table) -> int:
@@ -486,37 +493,25 @@ def kvc_slot_map(*, ratio: int, page_size: int, num_pages: int, lens: torch.Tens
     ``token_to_req [max_tokens]``, ``totals [4]`` that are given.
     ``max_tokens`` defaults to the smallest per-token output."""
     S = lens.numel()
-    dev = _one_device(lens=lens, new_lens=new_lens, depth=depth, page_table=page_table,
-                      free_pages=free_pages, offsets=offsets, start_pos=start_pos, out_loc=out_loc,
-                      positions=positions, token_to_req=token_to_req, totals=totals, status=status)
-    per_token = {"out_loc": out_loc, "positions": positions, "token_to_req": token_to_req,
-                 "depth": depth}
-    sizes = [t.numel() for t in per_token.values() if t is not None]
+    per_token = (out_loc, positions, token_to_req, depth)
     if max_tokens is None:
-        max_tokens = min(sizes, default=S * token_stride)
-    for name, t in per_token.items():
-        _need(t is None or t.numel() >= max_tokens,
-              f"{name}: {0 if t is None else t.numel()} entries for max_tokens = {max_tokens}")
-    _need(new_lens is None or new_lens.numel() >= S, f"new_lens: fewer than {S} entries")
+        max_tokens = min((t.numel() for t in per_token if t is not None), default=S * token_stride)
+    dev = lens.device
+    _one_device(dev, (("new_lens", new_lens), ("depth", depth), ("page_table", page_table),
+                      ("free_pages", free_pages), ("offsets", offsets), ("start_pos", start_pos),
+                      ("out_loc", out_loc), ("positions", positions),
+                      ("token_to_req", token_to_req), ("totals", totals), ("status", status)))
     _need(page_table.dim() == 2 and page_table.shape[0] >= S,
           f"page_table: shape {tuple(page_table.shape)}, need {S} rows")
-    _need(offsets is None or offsets.numel() >= 2 * S, f"offsets: expected [2, {S}] entries")
-    _need(start_pos is None or start_pos.numel() >= S, f"start_pos: fewer than {S} entries")
-    _need(totals is None or totals.numel() >= 4, "totals: expected 4 entries")
-    a = kvc_slot_map_args()
-    a.ratio, a.page_size, a.num_pages = ratio, page_size, num_pages
-    a.num_slots, a.token_stride = S, token_stride
-    a.lens = _dense(lens, _I32_T, "lens")
-    a.new_lens = _opt(new_lens, _dense, _I32_T, "new_lens")
-    a.depth = _opt(depth, _dense, _I32_T, "depth")
-    a.page_table = _rows(page_table, _I32_T, "page_table")
-    a.pt_stride, a.pt_width = _pt_stride(page_table), page_table.shape[1]
-    a.free_pages, a.n_free = _dense(free_pages, _I32_T, "free_pages"), free_pages.numel()
-    a.max_tokens = max_tokens
-    for name, t in (("offsets", offsets), ("start_pos", start_pos), ("out_loc", out_loc),
-                    ("positions", positions), ("token_to_req", token_to_req), ("totals", totals),
-                    ("status", status)):
-        setattr(a, name, _opt(t, _dense, _I32_T, name))
+    a = kvc_slot_map_args(
+        ratio, page_size, num_pages, S, token_stride, _i32(lens, S, "lens"),
+        _i32(new_lens, S, "new_lens"), _i32(depth, max_tokens, "depth"),
+        _rows(page_table, _I32_T, "page_table"), _pt_stride(page_table), page_table.shape[1],
+        _i32(free_pages, 0, "free_pages"), free_pages.numel(), max_tokens,
+        _i32(offsets, 2 * S, "offsets"), _i32(start_pos, S, "start_pos"),
+        _i32(out_loc, max_tokens, "out_loc"), _i32(positions, max_tokens, "positions"),
+        _i32(token_to_req, max_tokens, "token_to_req"), _i32(totals, 4, "totals"),
+        _i32(status, 1, "status"))
     _call_on(dev, stream, lib().kvc_slot_map, a)
 
 
@@ -535,41 +530,34 @@ def _attend(fn, cache: Cache, q, start_pos, page_table, out, *, slots, tokens, r
         _need(t.is_cuda and t.dtype in _B16_T and t.dim() == 3 and t.shape[2] == 512 and
               t.stride(2) == 1, f"{name}: expected a [tokens, heads, 512] bf16 device tensor with "
                                 f"contiguous rows, got {t.dtype} {tuple(t.shape)} strides {t.stride()}")
-    T, H = q.shape[:2]
+    T, H, _ = q.shape
     _need(out.shape == q.shape, f"out: shape {tuple(out.shape)}, q has {tuple(q.shape)}")
-    dev = _one_device(q=q, out=out, cache=cache.data, start_pos=start_pos, page_table=page_table,
-                      offsets=offsets, tree=tree, sink=sink, lse=lse, workspace=workspace,
-                      status=status)
-    _need(start_pos.numel() >= slots, f"start_pos: {start_pos.numel()} entries for {slots} slots")
+    dev = q.device
+    _one_device(dev, (("out", out), ("cache", cache.data), ("start_pos", start_pos),
+                      ("page_table", page_table), ("offsets", offsets), ("tree", tree),
+                      ("sink", sink), ("lse", lse), ("workspace", workspace), ("status", status)))
     _need(page_table.dim() == 2 and page_table.shape[0] >= slots,
           f"page_table: shape {tuple(page_table.shape)}, need {slots} rows")
     _need(sink is None or sink.numel() >= H, f"sink: fewer than {H} entries")
     _need(lse is None or tuple(lse.shape) == (T, H), f"lse: expected shape [{T}, {H}]")
     # a written row must be its own
-    s0, s1 = out.stride(0), out.stride(1)
+    s0, s1, _ = out.stride()
     _need(T <= 1 or H <= 1 or s0 >= (H - 1) * s1 + 512 or s1 >= (T - 1) * s0 + 512,
           f"out: overlapping rows (strides {out.stride()})")
-    a = kvc_attend_args()
-    a.ratio, a.num_heads, a.num_slots, a.draft_len = ratio, H, slots, draft_len
-    a.q, a.q_stride, a.q_head_stride, a.q_rows = q.data_ptr(), q.stride(0), q.stride(1), T
-    a.offsets = _opt(offsets, _dense, _I32_T, "offsets")
-    a.start_pos = _dense(start_pos, _I32_T, "start_pos")
-    a.page_table = _rows(page_table, _I32_T, "page_table")
-    a.pt_stride, a.pt_width = _pt_stride(page_table), page_table.shape[1]
-    a.tree = _opt(tree, _dense, (torch.int64, torch.uint64), "tree")
-    a.scale = scale
-    a.sink = _opt(sink, _dense, _F32_T, "sink")
-    a.out, a.out_stride, a.out_head_stride = out.data_ptr(), out.stride(0), out.stride(1)
-    a.lse = _opt(lse, _dense, _F32_T, "lse")
-    a.cache = cache.desc()
-    a.status = _opt(status, _dense, _I32_T, "status")
     if workspace is None:
         # of the stream the call runs on: the allocator then reuses it in order
         n = kvc_attend_workspace(slots, tokens, H)
         with torch.cuda.device(dev), torch.cuda.stream(stream):
             workspace = torch.empty(n, dtype=torch.uint8, device=dev)
-    a.workspace = _dense(workspace, (torch.uint8,), "workspace")
-    a.workspace_bytes = workspace.numel()
+    a = kvc_attend_args(
+        ratio, H, slots, draft_len, q.data_ptr(), q.stride(0), q.stride(1), T,
+        _i32(offsets, 2 * slots, "offsets"), _i32(start_pos, slots, "start_pos"),
+        _rows(page_table, _I32_T, "page_table"), _pt_stride(page_table), page_table.shape[1],
+        _opt(tree, _dense, (torch.int64, torch.uint64), "tree"), scale,
+        _opt(sink, _dense, _F32_T, "sink"), out.data_ptr(), s0, s1,
+        _opt(lse, _dense, _F32_T, "lse"), cache.desc(),
+        _dense(workspace, (torch.uint8,), "workspace"), workspace.numel(),
+        _i32(status, 1, "status"))
     _call_on(dev, stream, fn, a)
 
 

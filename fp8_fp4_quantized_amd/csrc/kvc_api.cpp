@@ -503,8 +503,8 @@ int kvc_slot_map(const kvc_slot_map_args* a, void* stream) {
     return fail(KVC_EINVAL, "%s: num_pages must be >= 1 with num_pages * page_size in int32", who);
   if (a->num_slots < 0 || a->num_slots > kvc::kMaxSlots)
     return fail(KVC_EINVAL, "%s: num_slots %d outside [0, %d]", who, a->num_slots, kvc::kMaxSlots);
-  if (a->max_tokens < 0 || a->max_tokens > 0x7FFFFFFF || a->n_free < 0 || a->n_free > 0x7FFFFFFF)
-    return fail(KVC_EINVAL, "%s: max_tokens and n_free must lie in [0, 2^31 - 1]", who);
+  if (a->max_tokens < 0 || a->max_tokens >= 0x7FFFFFFF || a->n_free < 0 || a->n_free >= 0x7FFFFFFF)
+    return fail(KVC_EINVAL, "%s: max_tokens and n_free must lie in [0, 2^31 - 2]", who);
   if (a->token_stride < 0 || (int64_t)a->num_slots * a->token_stride > a->max_tokens)
     return fail(KVC_EINVAL, "%s: token_stride %d: num_slots * token_stride must not pass max_tokens",
                 who, a->token_stride);

@@ -21,20 +21,33 @@ constexpr int kMapBlock = 1024;
 constexpr int kMapWaves = kMapBlock / kLanes;
 constexpr int kMapSlots = 8192;              // slots the LDS tables hold
 
-// inclusive sum over the workgroup's threads (64-bit: a batch may ask for
-// more than 2^32 pages or tokens before it is refused); buf: kMapWaves words
-__device__ __forceinline__ int64_t block_incl_scan(int64_t v, int64_t* buf) {
-  const int lane = lane_id(), wave = threadIdx.x >> 6;
-#pragma unroll
-  for (int d = 1; d < kLanes; d <<= 1) {
-    const int64_t o = __shfl_up(v, d);
-    if (lane >= d) v += o;
-  }
-  __syncthreads();                            // buf's last use is over
+// Sums saturate at kSat: a batch may ask for more than 2^32 pages or tokens
+// before it is refused, and every accepted sum stays below kSat.
+constexpr uint32_t kSat = 0x7FFFFFFF;
+__device__ __forceinline__ uint32_t sat_add(uint32_t a, uint32_t b) { return min(a + b, kSat); }
+
+// inclusive saturating sum over the 64 lanes (values up to kSat), the steps of
+// wave_incl_scan_i32
+__device__ __forceinline__ uint32_t wave_sat_scan(uint32_t v) {
+  v = sat_add(v, (uint32_t)dpp_shr_or_zero<0x111>((int32_t)v));
+  v = sat_add(v, (uint32_t)dpp_shr_or_zero<0x112>((int32_t)v));
+  v = sat_add(v, (uint32_t)dpp_shr_or_zero<0x114>((int32_t)v));
+  v = sat_add(v, (uint32_t)dpp_shr_or_zero<0x118>((int32_t)v));
+  v = sat_add(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, kDppRowBcast15, 0xA, 0xF, false));
+  return sat_add(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, kDppRowBcast31, 0xC, 0xF, false));
+}
+
+// Inclusive saturating sum over the workgroup's threads; *total: of all of
+// them.  buf: kMapWaves words that no thread still reads.
+__device__ __forceinline__ uint32_t block_sat_scan(uint32_t v, uint32_t* buf, uint32_t* total) {
+  const int lane = lane_id(), wave = uniform((int)(threadIdx.x >> 6));
+  v = wave_sat_scan(v);
   if (lane == kLanes - 1) buf[wave] = v;
   __syncthreads();
-  for (int w = 0; w < wave; ++w) v += buf[w];
-  return v;
+  // every wave sums the waves' totals in its first lanes
+  const uint32_t t = wave_sat_scan(lane < kMapWaves ? buf[lane] : 0u);
+  *total = (uint32_t)__builtin_amdgcn_readlane((int)t, kLanes - 1);
+  return wave == 0 ? v : sat_add(v, (uint32_t)__builtin_amdgcn_readlane((int)t, wave - 1));
 }
 
 // Last index i in [0, n) with start[i] <= x (start[0] = 0 <= x, ascending)
@@ -83,32 +96,38 @@ __global__ __launch_bounds__(kMapBlock) void slot_map_kernel(SlotMapParams p) {
   __shared__ int32_t tok0[kMapSlots];         // first token row of each slot
   __shared__ int32_t page0[kMapSlots];        // its first place in the free list
   __shared__ uint32_t okbits[kMapSlots / 32];
-  __shared__ int64_t buf[kMapWaves];
-  __shared__ int64_t carry[2];
-  __shared__ unsigned long long top[2];       // accepted pages, accepted tokens
-  __shared__ unsigned long long sums[3];      // tokens, compressed rows, refused slots
-  const int S = p.num_slots, tid = threadIdx.x;
+  __shared__ uint32_t buf[2][kMapWaves];
+  __shared__ int32_t top[kMapWaves][2], sums[kMapWaves][3];
+  const int S = p.num_slots, tid = threadIdx.x, lane = lane_id();
+  const int wave = uniform(tid >> 6);
   const int rl = p.ratio - 1;
   const bool first_block = blockIdx.x == 0;
   int32_t bad = 0;
-  if (tid < 2) { carry[tid] = 0; top[tid] = 0; }
-  if (tid < 3) sums[tid] = 0;
-  __syncthreads();
+  uint32_t page_carry = 0, tok_carry = 0;
+  // accepted places in the free list and token rows, tokens, compressed rows,
+  // refused slots: of this thread
+  int32_t pages = 0, tokens = 0, n_sum = 0, row_sum = 0, refused = 0;
 
+  // (a turn's scans leave a barrier between any read of buf and the next turn's
+  // write of the same words)
   for (int b0 = 0; b0 < S; b0 += kMapBlock) {
     const int b = b0 + tid;
     SlotPlan s{};
     if (b < S) s = slot_plan(p, b, &bad);
-    const int64_t pe = block_incl_scan(s.need, buf) + carry[0];
-    if (s.need > 0 && pe > p.n_free) {
+    // (need and n are below 2^31: the table and the length were checked)
+    uint32_t total;
+    const uint32_t pe = sat_add(block_sat_scan((uint32_t)s.need, buf[0], &total), page_carry);
+    page_carry = sat_add(page_carry, total);
+    if (s.need > 0 && pe > (uint32_t)p.n_free) {
       s.ok = false;
       s.n = 0;
       bad |= kStNoPage;
     }
     // packed tokens are numbered through the batch; with a stride each slot
     // has its own rows, and only their sum is of interest
-    const int64_t te = block_incl_scan(s.n, buf) + carry[1];
-    if (p.token_stride == 0 && s.n > 0 && te > p.max_tokens) {
+    const uint32_t te = sat_add(block_sat_scan((uint32_t)s.n, buf[1], &total), tok_carry);
+    tok_carry = sat_add(tok_carry, total);
+    if (p.token_stride == 0 && s.n > 0 && te > (uint32_t)p.max_tokens) {
       s.ok = false;
       s.n = 0;
       bad |= kStTokenRange;
@@ -116,30 +135,42 @@ __global__ __launch_bounds__(kMapBlock) void slot_map_kernel(SlotMapParams p) {
     const uint64_t okm = __ballot(s.ok);
     if (b < S) {
       // a refused slot's places are cut to the accepted totals below
-      const int64_t pf = pe - s.need, tf = te - s.n;
-      page0[b] = (int32_t)(pf < p.n_free ? pf : p.n_free);
-      tok0[b] = (int32_t)(tf < 0x7FFFFFFF ? tf : 0x7FFFFFFF);
-      if ((tid & 63) == 0) {
+      page0[b] = (int32_t)(pe == kSat ? kSat : pe - (uint32_t)s.need);
+      tok0[b] = (int32_t)(te == kSat ? kSat : te - (uint32_t)s.n);
+      if (lane == 0) {
         okbits[b >> 5] = (uint32_t)okm;
         okbits[(b >> 5) + 1] = (uint32_t)(okm >> 32);
       }
       if (s.ok) {
-        if (s.need > 0) atomicMax(&top[0], (unsigned long long)pe);
-        if (s.n > 0) atomicMax(&top[1], (unsigned long long)te);
-        if (first_block) {
-          atomicAdd(&sums[0], (unsigned long long)s.n);
-          atomicAdd(&sums[1], (unsigned long long)(((s.len + s.n) >> rl) - (s.len >> rl)));
-        }
-      } else if (s.live && first_block) {
-        atomicAdd(&sums[2], 1ull);
+        if (s.need > 0) pages = (int32_t)pe;
+        if (s.n > 0) tokens = (int32_t)te;
+        n_sum += (int32_t)s.n;
+        row_sum += (int32_t)(((s.len + s.n) >> rl) - (s.len >> rl));
+      } else if (s.live) {
+        ++refused;
       }
     }
-    __syncthreads();
-    if (tid == kMapBlock - 1) { carry[0] = pe; carry[1] = te; }
-    __syncthreads();
   }
-  const int32_t pages = (int32_t)top[0];
-  const int32_t tokens = (int32_t)top[1];     // packed token rows in use
+  // the accepted totals: the last accepted ends (ascending over the slots, so
+  // maxima), and the sums, by waves
+#pragma unroll
+  for (int d = 1; d < kLanes; d <<= 1) {
+    pages = max(pages, __shfl_xor(pages, d));
+    tokens = max(tokens, __shfl_xor(tokens, d));
+  }
+  if (first_block) {
+    n_sum = wave_incl_scan_i32(n_sum);
+    row_sum = wave_incl_scan_i32(row_sum);
+    refused = wave_incl_scan_i32(refused);
+    if (lane == kLanes - 1) { sums[wave][0] = n_sum; sums[wave][1] = row_sum; sums[wave][2] = refused; }
+  }
+  if (lane == 0) { top[wave][0] = pages; top[wave][1] = tokens; }
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kMapWaves; ++w) {
+    pages = max(pages, top[w][0]);            // packed token rows and pages in use
+    tokens = max(tokens, top[w][1]);
+  }
   auto accepted = [&](int b) { return (okbits[b >> 5] >> (b & 31) & 1u) != 0; };
   auto added = [&](int b) -> int32_t {
     if (!accepted(b)) return 0;
@@ -162,10 +193,13 @@ __global__ __launch_bounds__(kMapBlock) void slot_map_kernel(SlotMapParams p) {
     if (p.start_pos != nullptr) p.start_pos[b] = accepted((int)b) ? p.lens[b] : -1;
   }
   if (first_block && tid == 0 && p.totals != nullptr) {
-    p.totals[0] = (int32_t)sums[0];
-    p.totals[1] = (int32_t)sums[1];
+    int32_t t[3] = {};
+    for (int w = 0; w < kMapWaves; ++w)
+      for (int i = 0; i < 3; ++i) t[i] += sums[w][i];
+    p.totals[0] = t[0];
+    p.totals[1] = t[1];
     p.totals[2] = pages;
-    p.totals[3] = (int32_t)sums[2];
+    p.totals[3] = t[2];
   }
   // ---- per page taken: the slots' places ascend, so the last slot that
   // starts at or below a page is its owner (slots that take none share the

@@ -415,8 +415,8 @@ typedef struct kvc_slot_map_args {
   int64_t pt_stride;          /* entries between rows, >= pt_width */
   int64_t pt_width;           /* entries per row, >= 1 */
   const int32_t* free_pages;  /* device int32 [n_free] (NULL when n_free is 0) */
-  int64_t n_free;             /* 0 .. 2^31 - 1 */
-  int64_t max_tokens;         /* entries of each per-token output, 0 .. 2^31 - 1 */
+  int64_t n_free;             /* 0 .. 2^31 - 2 */
+  int64_t max_tokens;         /* entries of each per-token output, 0 .. 2^31 - 2 */
   int32_t* offsets;           /* device int32 outputs, each may be NULL */
   int32_t* start_pos;
   int32_t* out_loc;

@@ -27,7 +27,7 @@ def slot_map(kvc, **kw):
 
 
 def test_slot_map_arguments(kvc):
-    big = 1 << 31
+    big = (1 << 31) - 1
     for kw in (dict(page_size=0), dict(page_size=48), dict(page_size=8192), dict(num_pages=0),
                dict(num_pages=1 << 26), dict(num_slots=-1), dict(num_slots=8192),
                dict(max_tokens=-1), dict(max_tokens=big), dict(n_free=-1), dict(n_free=big),
