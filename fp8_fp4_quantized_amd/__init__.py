@@ -471,11 +471,15 @@ def _pt_stride(page_table) -> int:
 def _call_on(dev, stream, fn, args) -> None:
     """One call with ``dev`` as the current device, on ``stream`` (default:
     that device's current stream)."""
-    if dev.index is None or dev.index == torch.cuda.current_device():
-        _check(fn(C.byref(args), _stream(stream)))
-        return
-    with torch.cuda.device(dev):
-        _check(fn(C.byref(args), _stream(stream)))
+    index = dev.index
+    # (the raw handle: torch.cuda.current_stream would build an object per call)
+    handle = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    if index == torch._C._cuda_getDevice():
+        rc = fn(C.byref(args), handle)
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(C.byref(args), handle)
+    _check(rc)
 
 
 def kvc_slot_map(*, ratio: int, page_size: int, num_pages: int, lens: torch.Tensor,

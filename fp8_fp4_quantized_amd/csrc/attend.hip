@@ -447,25 +447,99 @@ struct Walk {
   int b, ub;
   int32_t t0, t1, tiles, rows;
   int eb, eub, et;             // the end: slot, unit, tile
+  int64_t at, quota;           // (plan_here) cost before the unit, cost per workgroup
   SlotTokens s;
 
   __device__ __forceinline__ void piece(const AttendParams& p, int qt, int nt) {
     rows = unit_rows(p, s, ub * qt, qt);
     tiles = unit_tiles(rows, nt);
     t1 = b == eb && ub == eub ? et : tiles;
+    // plan_here: the workgroup with a unit's first tile tells the join how many
+    // workgroups share it
+    if (p.plan_units > 0 && t0 == 0 && threadIdx.x == 0) {
+      int32_t parts = 1;
+      if (t1 < tiles)
+        parts += (int32_t)((at + kAttendUnitTiles + tiles - 1) / quota - (at + kAttendUnitTiles) / quota);
+      p.splits[b * p.plan_units + ub] = AttendSplit{b, ub, (int32_t)blockIdx.x, parts};
+    }
   }
   __device__ __forceinline__ bool begin(const AttendParams& p, int qt, int nt) {
-    const AttendStart st = p.starts[blockIdx.x], en = p.starts[blockIdx.x + 1];
     int32_t none = 0;
-    b = uniform(st.slot), ub = uniform(st.unit), t0 = uniform(st.tile);
-    eb = uniform(en.slot), eub = uniform(en.unit), et = uniform(en.tile);
+    if (p.plan_units > 0) {
+      if (!plan_here(p, qt, nt)) return false;
+    } else {
+      const AttendStart st = p.starts[blockIdx.x], en = p.starts[blockIdx.x + 1];
+      b = uniform(st.slot), ub = uniform(st.unit), t0 = uniform(st.tile);
+      eb = uniform(en.slot), eub = uniform(en.unit), et = uniform(en.tile);
+    }
     if (b >= p.num_slots || (b == eb && ub == eub && t0 == et)) return false;
     s = slot_tokens(p, b, &none);
     piece(p, qt, nt);
     return true;
   }
+  // The plan without a launch of its own, for few units that each workgroup
+  // can sum by itself (plan_units units in every active slot): a share of the
+  // slots per thread, a prefix sum of their costs, and the two threads whose
+  // slots hold this workgroup's start and end write them down.
+  __device__ __forceinline__ bool plan_here(const AttendParams& p, int qt, int nt) {
+    __shared__ int64_t buf[kAttendBlock / kLanes];
+    __shared__ AttendStart ends[2];
+    __shared__ int64_t before;
+    const int tid = threadIdx.x, lane = lane_id(), wave = tid >> 6, U = p.plan_units;
+    const int per = (p.num_slots + kAttendBlock - 1) / kAttendBlock;
+    const int ba = min(p.num_slots, tid * per), bz = min(p.num_slots, ba + per);
+    int32_t bad = 0;
+    int64_t mine = 0;
+    for (int i = ba; i < bz; ++i) {
+      const SlotTokens c = slot_tokens(p, i, &bad);
+      for (int k = 0; k < U; ++k) {
+        if (c.n > 0) mine += unit_tiles(unit_rows(p, c, k * qt, qt), nt) + kAttendUnitTiles;
+        else if (blockIdx.x == 0) p.splits[i * U + k] = AttendSplit{i, k, 0, 0};
+      }
+    }
+    if (bad != 0 && blockIdx.x == 0 && p.status != nullptr) atomicOr(p.status, bad);
+    int64_t x = mine;
+#pragma unroll
+    for (int d = 1; d < kLanes; d <<= 1) {
+      const int64_t y = __shfl_up(x, d);
+      if (lane >= d) x += y;
+    }
+    if (lane == kLanes - 1) buf[wave] = x;
+    if (tid < 2) ends[tid] = AttendStart{p.num_slots, 0, 0, 0};
+    __syncthreads();
+    int64_t total = 0;
+    for (int i = 0; i < kAttendBlock / kLanes; ++i) {
+      if (i == wave) x += total;
+      total += buf[i];
+    }
+    quota = max((total + kAttendGrid - 1) / kAttendGrid, (int64_t)(kAttendLeastRows / nt));
+    int64_t c = x - mine;
+    const int64_t goal0 = blockIdx.x * quota, goal1 = goal0 + quota;
+    if (goal0 >= total) return false;
+    if (mine > 0 && goal1 >= c && goal0 < c + mine) {
+      for (int i = ba; i < bz; ++i) {
+        const SlotTokens sl = slot_tokens(p, i, &bad);
+        for (int k = 0; k < U && sl.n > 0; ++k) {
+          const int64_t end = c + kAttendUnitTiles + unit_tiles(unit_rows(p, sl, k * qt, qt), nt);
+          if (goal0 >= c && goal0 < end) {
+            ends[0] = AttendStart{i, k, (int32_t)max(goal0 - c - kAttendUnitTiles, (int64_t)0), 0};
+            before = c;
+          }
+          if (goal1 >= c && goal1 < end)
+            ends[1] = AttendStart{i, k, (int32_t)max(goal1 - c - kAttendUnitTiles, (int64_t)0), 0};
+          c = end;
+        }
+      }
+    }
+    __syncthreads();
+    b = uniform(ends[0].slot), ub = uniform(ends[0].unit), t0 = uniform(ends[0].tile);
+    eb = uniform(ends[1].slot), eub = uniform(ends[1].unit), et = uniform(ends[1].tile);
+    at = uniform64(before);
+    return true;
+  }
   __device__ __forceinline__ bool next(const AttendParams& p, int qt, int nt) {
     if (b == eb && ub == eub) return false;
+    at += kAttendUnitTiles + tiles;
     t0 = 0;
     ++ub;
     if ((int64_t)ub * qt >= (int64_t)s.n * p.heads) {
@@ -1180,8 +1254,9 @@ void attend_wide_kernel(AttendParams p) {
 // waves' sums added.
 __global__ __launch_bounds__(256) void attend_join_kernel(AttendParams p, int qt) {
   __shared__ float acc[3][kDim];
-  if ((int)blockIdx.x >= p.head->nsplit) return;
+  if (p.plan_units == 0 && (int)blockIdx.x >= p.head->nsplit) return;
   const AttendSplit sp = p.splits[blockIdx.x];
+  if (sp.parts < 2) return;
   int32_t none = 0;
   const SlotTokens s = slot_tokens(p, sp.slot, &none);
   const int qi = blockIdx.y;
@@ -1258,17 +1333,22 @@ hipError_t attend(const AttendParams& p, int qblocks, hipStream_t stream) {
 
 hipError_t launch_attend(const AttendParams& p, int qblocks, hipStream_t stream) {
   const int qt = 32 * qblocks, nt = 128 / qblocks;
-  hipLaunchKernelGGL(attend_plan_kernel, dim3(1), dim3(kPlanBlock), 0, stream, p, qt, nt);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
+  hipError_t e = hipSuccess;
+  if (p.plan_units == 0) {
+    hipLaunchKernelGGL(attend_plan_kernel, dim3(1), dim3(kPlanBlock), 0, stream, p, qt, nt);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
   switch (p.cache.layout) {
     case kV41: e = attend<kV41>(p, qblocks, stream); break;
     case kV41Fp4: e = attend<kV41Fp4>(p, qblocks, stream); break;
     default: e = attend<kV4>(p, qblocks, stream); break;
   }
   if (e != hipSuccess) return e;
-  // a unit cut between workgroups holds at least one boundary between two
-  const int64_t splits = p.units_max < kAttendGrid - 1 ? p.units_max : kAttendGrid - 1;
+  // an entry per unit (plan_units), or per unit that is cut: one holds at least
+  // one boundary between two workgroups
+  const int64_t splits = p.plan_units > 0 ? (int64_t)p.num_slots * p.plan_units
+                                          : min(p.units_max, (int64_t)kAttendGrid - 1);
   hipLaunchKernelGGL(attend_join_kernel, dim3((unsigned)splits, (unsigned)qt), dim3(256), 0, stream,
                      p, qt);
   return hipGetLastError();

@@ -101,7 +101,7 @@ int64_t attend_layout(int32_t slots, int64_t tokens, int32_t heads, int64_t (&at
   int64_t n = 0;
   at[0] = n, n += align256(sizeof(kvc::AttendHead));
   at[1] = n, n += align256((kvc::kAttendWorkgroups + 1) * sizeof(kvc::AttendStart));
-  at[2] = n, n += align256(kvc::kAttendWorkgroups * sizeof(kvc::AttendSplit));
+  at[2] = n, n += align256(kvc::kAttendPlanUnits * sizeof(kvc::AttendSplit));
   at[3] = n, n += align256(parts * 16);
   at[4] = n, n += align256(parts * 512 * 4);
   return n;
@@ -176,6 +176,10 @@ int attend(const kvc_attend_args* a, bool tree, void* stream, const char* who) {
   int qblocks = attend_qblocks(a->num_slots, tokens, a->num_heads);
   if (a->cache.page_size < 8 && qblocks == 4) qblocks = 2;   // the wide kernel's pages hold 8 rows or more
   p.units_max = tokens * a->num_heads / (32 * qblocks) + a->num_slots;
+  if (tree) {
+    const int64_t units = ((int64_t)a->draft_len * a->num_heads + 32 * qblocks - 1) / (32 * qblocks);
+    if (units <= 8 && units * a->num_slots <= kvc::kAttendPlanUnits) p.plan_units = (int32_t)units;
+  }
   uint8_t* w = static_cast<uint8_t*>(a->workspace);
   p.head = reinterpret_cast<kvc::AttendHead*>(w + at[0]);
   p.starts = reinterpret_cast<kvc::AttendStart*>(w + at[1]);

@@ -156,6 +156,11 @@ constexpr int kAttendLeastRows = 256;
 // A unit's begin and end (its queries in, its outputs out), in tiles.
 constexpr int kAttendUnitTiles = 6;
 
+// Most units of a call whose workgroups plan for themselves (no launch for
+// the plan): beyond, the sums over them cost each workgroup more than the
+// launch.
+constexpr int kAttendPlanUnits = 1024;
+
 struct AttendHead {            // written by the plan
   int32_t nsplit;              // units cut between workgroups
   int32_t pad[3];
@@ -163,7 +168,7 @@ struct AttendHead {            // written by the plan
 struct AttendStart {           // where a workgroup begins, and the one before it ends (slot S: the end)
   int32_t slot, unit, tile, pad;
 };
-struct AttendSplit {           // a cut unit: its parts lie with workgroups wg0 ..
+struct AttendSplit {           // a unit and its parts, which lie with workgroups wg0 ..
   int32_t slot, unit, wg0, parts;
 };
 
@@ -192,10 +197,11 @@ struct AttendParams {
   float* lse;                  // nullable
   int32_t* status;
   int64_t units_max;           // units the call can have at the most
+  int32_t plan_units;          // > 0: units per slot, and every workgroup plans for itself
   // workspace
   AttendHead* head;
   AttendStart* starts;         // [kAttendWorkgroups + 1]
-  AttendSplit* splits;         // [kAttendWorkgroups]
+  AttendSplit* splits;         // [kAttendWorkgroups], plan_units: [kAttendPlanUnits]
   float4* part_ml;             // [2 * kAttendWorkgroups][queries of a unit]: max, sum, rounded sum
   float* part_o;               // the same, 512 dims each
 };

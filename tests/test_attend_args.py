@@ -88,7 +88,7 @@ def test_workspace_sizes(kvc):
     # per part of a query: 512 fp32 sums and 16 bytes of statistics, two parts a workgroup
     for slots, tokens, heads, queries in ((1, 1, 32, 32), (1, 2, 32, 64), (4, 4, 65, 128),
                                           (0, 0, 1, 32), (1, 100000, 128, 128)):
-        assert 0 <= f(slots, tokens, heads) - 2 * 256 * queries * (2048 + 16) < 20000
+        assert 0 <= f(slots, tokens, heads) - 2 * 256 * queries * (2048 + 16) < 30000
         assert f(slots, tokens, heads) % 256 == 0
     for args in ((-1, 1, 1), (8192, 1, 1), (1, -1, 1), (1, 1, 0), (1, 1, 1025), (1, 1 << 30, 2)):
         with pytest.raises(kvc.KvcError):
