@@ -194,76 +194,80 @@ __device__ __forceinline__ uint32_t swz(uint32_t row) { return (row & 3u) << 2 |
 typedef const __attribute__((address_space(3))) uint8_t* lds_cptr;
 typedef __attribute__((address_space(3))) uint8_t* lds_ptr;
 
-// The lanes' part of an 8-row group that lies in one page: N loads of 16 bytes
-// of codes a lane (V4: the last one of bf16 rope dims) with the scale bytes of
+// The lanes' part of an 8-row group that lies in one page: N loads of 16 dims'
+// codes a lane (V4: the last one of bf16 rope dims) with the scale bytes of
 // their dims, and their expansion into 8 rows of a tile.  Every load's offsets
 // are a base of the lane and a constant.
 //   V41      load k: rows 2k, 2k + 1, 32 lanes a row, 16 dims a lane
-//   V41_FP4  load k: rows 4k .. 4k + 3, 16 lanes a row, 32 dims a lane
+//   V41_FP4  the same (8 bytes a lane: 16-byte loads would put four chunks a
+//            lane to one bank group)
 //   V4       8 lanes a row; load k < 4: dims 128k + 16 (lane % 8) -- of load 3
 //            the upper lanes' are past the codes, and what they put is
 //            overwritten by load 4's rope dims, 8 a lane
 template <int L> struct GroupShape;
 template <> struct GroupShape<kV41> { static constexpr int kLoads = 4; };
-template <> struct GroupShape<kV41Fp4> { static constexpr int kLoads = 2; };
+template <> struct GroupShape<kV41Fp4> { static constexpr int kLoads = 4; };
 template <> struct GroupShape<kV4> { static constexpr int kLoads = 5; };
 
 template <int L>
 struct Group {
   static constexpr int N = GroupShape<L>::kLoads;
-  u32x4 codes[N];
+  typedef typename std::conditional<L == kV41Fp4, u32x2, u32x4>::type Codes;
+  Codes codes[N];
   uint32_t scale[N];
 
   static __device__ __forceinline__ int row(int k, int lane) {
-    return L == kV41 ? 2 * k + (lane >> 5) : L == kV41Fp4 ? 4 * k + (lane >> 4) : lane >> 3;
+    return L == kV4 ? lane >> 3 : 2 * k + (lane >> 5);
   }
   // the lane's data and scale offsets, and load k's constants on top of them
   static __device__ __forceinline__ uint32_t data_off(int lane) {
-    return L == kV4 ? (lane >> 3) * LayoutTraits<L>::kData + 16 * (lane & 7) : 16 * lane;
+    return L == kV41 ? 16 * lane : L == kV41Fp4 ? 8 * lane
+                     : (lane >> 3) * LayoutTraits<L>::kData + 16 * (lane & 7);
   }
-  static constexpr uint32_t data_step(int k) { return L == kV4 ? (k < 4 ? 128 * k : kNope) : 1024 * k; }
+  static constexpr uint32_t data_step(int k) {
+    return L == kV41 ? 1024 * k : L == kV41Fp4 ? 512 * k : k < 4 ? 128 * k : kNope;
+  }
   static __device__ __forceinline__ uint32_t scale_off(int lane) {
-    return L == kV41 ? lane >> 1 : L == kV41Fp4 ? 2 * lane
+    return L == kV41 ? lane >> 1 : L == kV41Fp4 ? lane
                      : (lane >> 3) * LayoutTraits<L>::kScale + ((lane & 7) >> 2);
   }
-  static constexpr uint32_t scale_step(int k) { return L == kV41 ? 32 * k : L == kV41Fp4 ? 128 * k : k < 4 ? 2 * k : 0; }
+  static constexpr uint32_t scale_step(int k) {
+    return L == kV41 ? 32 * k : L == kV41Fp4 ? 64 * k : k < 4 ? 2 * k : 0;
+  }
   // load k of the group whose data and scale parts begin there
   __device__ __forceinline__ void load(const uint8_t* data, const uint8_t* sc, uint32_t doff, uint32_t soff, int k) {
-    codes[k] = __builtin_amdgcn_raw_buffer_load_b128(raw_rsrc(data), (int)doff, (int)data_step(k), kCpolSc1);
-    if (L == kV4 && k == 4) return;
     if constexpr (L == kV41Fp4)
-      scale[k] = __builtin_amdgcn_raw_buffer_load_b16(raw_rsrc(sc), (int)soff, (int)scale_step(k), kCpolSc1);
+      codes[k] = __builtin_amdgcn_raw_buffer_load_b64(raw_rsrc(data), (int)doff, (int)data_step(k), kCpolSc1);
     else
-      scale[k] = __builtin_amdgcn_raw_buffer_load_b8(raw_rsrc(sc), (int)soff, (int)scale_step(k), kCpolSc1);
+      codes[k] = __builtin_amdgcn_raw_buffer_load_b128(raw_rsrc(data), (int)doff, (int)data_step(k), kCpolSc1);
+    if (L == kV4 && k == 4) return;
+    scale[k] = __builtin_amdgcn_raw_buffer_load_b8(raw_rsrc(sc), (int)soff, (int)scale_step(k), kCpolSc1);
   }
   // load k of rows in pages of their own: the lane's data and scale bytes
   __device__ __forceinline__ void load_apart(const uint8_t* data, const uint8_t* sc, int k) {
-    codes[k] = *(const u32x4*)data;
-    if constexpr (L == kV41Fp4) scale[k] = *(const uint16_t*)sc;
-    else scale[k] = *sc;
+    codes[k] = *(const Codes*)data;
+    scale[k] = *sc;
   }
   // part j of load k, 8 dims, to its row in a tile: the place of the lane's
   // first part in the group, whose bits the other parts and loads change.  odd:
   // the group's first row is an odd multiple of 8 (of the tile).
   static __device__ __forceinline__ uint32_t place(int lane, int odd) {
     const uint32_t r = row(0, lane);
-    const uint32_t chunk = L == kV41 ? 2 * (lane & 31) : L == kV41Fp4 ? 4 * (lane & 15) : 2 * (lane & 7);
+    const uint32_t chunk = L == kV4 ? 2 * (lane & 7) : 2 * (lane & 31);
     return r * 1024 + ((chunk ^ swz(r + 8 * odd)) << 4);
   }
-  static constexpr int parts(int k) { return L == kV41Fp4 ? 4 : L == kV4 && k == 4 ? 1 : 2; }
+  static constexpr int parts(int k) { return L == kV4 && k == 4 ? 1 : 2; }
   __device__ __forceinline__ void put(lds_ptr rows, uint32_t place, int lane, int k, int j) const {
     uint4 v;
-    uint32_t at;
-    if constexpr (L == kV41Fp4) {             // rows 4k ..: bit 0 of the permutation
-      v = dq_fp4x8(codes[k][j], j < 2 ? scale[k] & 0xFFu : scale[k] >> 8);
-      at = (place ^ (16 * (k ^ j))) + 4096 * k;
+    // rows 2k ..: bits 3 (from bit 1 of the row) and 0 (bit 2)
+    uint32_t at = L == kV4 ? (place ^ (16 * j)) + 256 * k : (place ^ (16 * ((k & 1) << 3 ^ k >> 1 ^ j))) + 2048 * k;
+    if constexpr (L == kV41Fp4) {
+      v = dq_fp4x8(codes[k][j], scale[k]);
     } else if (L == kV4 && k == 4) {          // chunks 56 .. 63, from place's chunks 0, 2, .. 14
       v = make_uint4(codes[k][0], codes[k][1], codes[k][2], codes[k][3]);
       at = (place ^ (16 * (((2 * (lane & 7)) ^ (8 + (lane & 7)))))) + 768;
     } else {
       v = dq_fp8x8(make_uint2(codes[k][2 * j], codes[k][2 * j + 1]), scale[k]);
-      // V41: rows 2k ..: bits 3 (from bit 1 of the row) and 0 (bit 2)
-      at = L == kV41 ? (place ^ (16 * ((k & 1) << 3 ^ k >> 1 ^ j))) + 2048 * k : (place ^ (16 * j)) + 256 * k;
     }
     *(__attribute__((address_space(3))) u32x4*)(rows + at) = u32x4{v.x, v.y, v.z, v.w};
   }
@@ -304,7 +308,8 @@ struct Rows {
 // Matrix instructions written out, so that scores live in the vector
 // registers their softmax works in and O in accumulator registers: the
 // compiler gives every matrix-instruction result of a kernel of this size to
-// the accumulator file, which O fills (256 registers for 128 queries).
+// the accumulator file, which O fills (256 registers for 128 queries), and
+// moves O through the vector registers where it allocates it by itself.
 // A result feeding the next instruction's C operand needs no wait; s_nop 0
 // covers an operand that a vector instruction has just written.  scores_done
 // and out_done give the 16 wait states from a last result to a vector
@@ -1009,7 +1014,7 @@ void attend_wide_kernel(AttendParams p) {
     // are asked for before the queries are waited for
     const int32_t page0 = entry(w.t0), page1 = entry(w.t0 + 1);
     int32_t page = entry(w.t0 + 2);
-    bool valid = locate(w.t0, page0);
+    bool valid = locate(w.t0, page0);         // of the tile in gr
 #pragma unroll
     for (int k = 0; k < NL; ++k) gr.load(ldata, lscale, doff, soff, k);
     // the queries' fragments: the last kTail of them in LDS (the registers do not
@@ -1096,34 +1101,33 @@ void attend_wide_kernel(AttendParams p) {
         xv[1] = out_dims(1, at);
       }
     };
-    // ---- scores of tile tl at cur (its first fragments in x); tile tl + 1 is
-    // expanded into the buffer at nxt, tile tl + 2 requested; at the end the first
-    // fragments of O's products over the tile before are read
-    auto scores = [&](int32_t tl, uint32_t nxt, uint32_t before) {
-      const int32_t par = (tl - w.t0) & 1;
-      const uint32_t pl = fresh(place);
-      if (lane == 0) svalid[par ^ 1][wave] = valid ? 0xFF : 0;
-      const bool valid_next = locate(tl + 2, page);
-      page = entry(tl + 3);
+    // ---- scores of tile tl at cur (its first fragments in x); at the end the
+    // first fragments of O's products over the tile before are read
+    auto scores = [&](int32_t tl, uint32_t before) {
       bf16x8 qt[3];
-      int load = 0, in_load = 0;              // constants after unrolling
 #pragma unroll
       for (int k = 0; k < 32; ++k) {
         score_mfma(sc, x[k % 6], k < 32 - kTail ? qv[k < 32 - kTail ? k : 0] : qt[k % 3], k == 0);
         if (k + 3 >= 32 - kTail && k + 3 < 32) qt[k % 3] = query_tail(k + 3);
         if (k + 6 < 32) x[k % 6] = score_rows(k + 6);
-        if (k >= 28) out_ahead(k - 28, before, par ^ 1);
-        if (k % 3 == 1 && load < NL) {
-          gr.put(tiles3 + nxt + wave * 8192, pl, lane, load, in_load);
-          if (++in_load == Group<L>::parts(load)) {
-            gr.load(ldata, lscale, doff, soff, load);
-            ++load;
-            in_load = 0;
-          }
-        }
+        if (k >= 28) out_ahead(k - 28, before, ((tl - w.t0) & 1) ^ 1);
         __builtin_amdgcn_sched_barrier(0);
       }
-      valid = valid_next;
+    };
+    // ---- tile tl + 1 expanded into the buffer at nxt and tile tl + 2 requested, in
+    // 2 NL steps
+    uint32_t pl;
+    auto stage_begin = [&](int32_t tl) {
+      pl = fresh(place);
+      if (lane == 0) svalid[((tl - w.t0) & 1) ^ 1][wave] = valid ? 0xFF : 0;
+      valid = locate(tl + 2, page);
+      page = entry(tl + 3);
+    };
+    auto stage = [&](int step, uint32_t nxt) {
+      const int k = step >> 1, j = step & 1;
+      if (k >= NL) return;
+      if (j < Group<L>::parts(k)) gr.put(tiles3 + nxt + wave * 8192, pl, lane, k, j);
+      if (j == 1) gr.load(ldata, lscale, doff, soff, k);
     };
     // ---- mask (only a tile that some query does not see whole)
     auto mask = [&](int32_t tl) {
@@ -1193,8 +1197,8 @@ void attend_wide_kernel(AttendParams p) {
     };
     // ---- O += X^T P^T of the tile at `at` with the weights of parity par, on dims
     // [128 wave, 128 wave + 128); with = true: between them the softmax of the
-    // next tile, the barrier after its weights and this tile's last reads, and
-    // the first fragments of the tile at nxt
+    // next tile, the expansion of the one after it (at nxt), the barrier after
+    // both and this tile's last reads, and the first fragments at nxt
     auto out = [&](uint32_t at, int32_t par, uint32_t nxt, auto with) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
@@ -1206,6 +1210,7 @@ void attend_wide_kernel(AttendParams p) {
           if (i == 3) wv[y] = out_weights(1, y, par);
           if constexpr (with.value) {
             soften(4 * i + y, par ^ 1);
+            if (4 * i + y < 4 * NL && y % 2 == 1) stage(2 * i + y / 2, nxt);
             if (i == 6 && y == 0) __syncthreads();
             if (i == 6 && y > 0) ahead(y - 1, nxt, par);
             if (i == 7 && y < 3) ahead(y + 3, nxt, par);
@@ -1218,10 +1223,14 @@ void attend_wide_kernel(AttendParams p) {
     uint32_t cur = 0;                         // offset of the tile at hand in tiles
 #pragma unroll
     for (int i = 0; i < 6; ++i) ahead(i, cur, 0);
-    scores(w.t0, after(cur), cur);
+    scores(w.t0, cur);
     mask(w.t0);
+    stage_begin(w.t0);
 #pragma unroll
-    for (int i = 0; i < 24; ++i) soften(i, 0);
+    for (int i = 0; i < 24; ++i) {
+      soften(i, 0);
+      if (i < 2 * NL) stage(i, after(cur));
+    }
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < 6; ++i) ahead(i, after(cur), 1);
@@ -1229,8 +1238,9 @@ void attend_wide_kernel(AttendParams p) {
       const int32_t par = (tl - w.t0) & 1;
       const uint32_t before = cur;
       cur = after(cur);
-      scores(tl, after(cur), before);
+      scores(tl, before);
       mask(tl);
+      stage_begin(tl);
       out_begin(before, par ^ 1, holes_before);
       out(before, par ^ 1, after(cur), std::true_type{});
     }
