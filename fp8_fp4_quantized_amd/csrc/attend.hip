@@ -81,6 +81,9 @@ __device__ __forceinline__ int32_t unit_tiles(int32_t rows, int nt) {
   return rows > 0 ? (rows + nt - 1) / nt : 1;
 }
 
+// what a unit costs besides its tiles, in tiles
+__device__ __forceinline__ int32_t unit_cost(int nt) { return kAttendUnitRows / nt; }
+
 // ------------------------------------------------------------------ plan
 // One workgroup: a prefix sum of the slots' units, then each thread walks an
 // equal share of the units twice, to sum their tiles and to place the
@@ -156,10 +159,10 @@ __global__ __launch_bounds__(kPlanBlock) void attend_plan_kernel(AttendParams p,
       f(b, k, (int64_t)unit_tiles(unit_rows(p, s, k * qt, qt), nt));
     }
   };
-  // A unit costs its tiles and its begin and end (kAttendUnitTiles); a boundary
+  // A unit costs its tiles and its begin and end (unit_cost); a boundary
   // that falls into the latter is moved to the unit's first tile.
   int64_t mine = 0, total = 0;
-  walk([&](int, int32_t, int64_t t) { mine += t + kAttendUnitTiles; });
+  walk([&](int, int32_t, int64_t t) { mine += t + unit_cost(nt); });
   int64_t c = plan_excl_scan(mine, buf, &total);
   int64_t quota = (total + kAttendGrid - 1) / kAttendGrid;
   const int64_t least = kAttendLeastRows / nt;
@@ -168,11 +171,11 @@ __global__ __launch_bounds__(kPlanBlock) void attend_plan_kernel(AttendParams p,
   for (int64_t w = tid; w <= kAttendGrid; w += kPlanBlock)
     if (w * quota >= total) p.starts[w] = AttendStart{S, 0, 0, 0};
   walk([&](int b, int32_t k, int64_t t) {
-    const int64_t end = c + kAttendUnitTiles + t;
+    const int64_t end = c + unit_cost(nt) + t;
     int64_t cut = 0;                          // first boundary inside the tiles
     int32_t parts = 1;
     for (int64_t w = (c + quota - 1) / quota; w * quota < end && w < kAttendGrid; ++w) {
-      const int64_t tile = max(w * quota - c - kAttendUnitTiles, int64_t(0));
+      const int64_t tile = max(w * quota - c - unit_cost(nt), int64_t(0));
       p.starts[w] = AttendStart{b, k, (int32_t)tile, 0};
       if (tile > 0 && ++parts == 2) cut = w;
     }
@@ -257,19 +260,20 @@ struct Group {
     return r * 1024 + ((chunk ^ swz(r + 8 * odd)) << 4);
   }
   static constexpr int parts(int k) { return L == kV4 && k == 4 ? 1 : 2; }
-  __device__ __forceinline__ void put(lds_ptr rows, uint32_t place, int lane, int k, int j) const {
-    uint4 v;
+  __device__ __forceinline__ uint4 expand(int k, int j) const {
+    if constexpr (L == kV41Fp4) return dq_fp4x8(codes[k][j], scale[k]);
+    else if (L == kV4 && k == 4) return make_uint4(codes[k][0], codes[k][1], codes[k][2], codes[k][3]);
+    else return dq_fp8x8(make_uint2(codes[k][2 * j], codes[k][2 * j + 1]), scale[k]);
+  }
+  static __device__ __forceinline__ void write(lds_ptr rows, uint32_t place, int lane, int k, int j, uint4 v) {
     // rows 2k ..: bits 3 (from bit 1 of the row) and 0 (bit 2)
     uint32_t at = L == kV4 ? (place ^ (16 * j)) + 256 * k : (place ^ (16 * ((k & 1) << 3 ^ k >> 1 ^ j))) + 2048 * k;
-    if constexpr (L == kV41Fp4) {
-      v = dq_fp4x8(codes[k][j], scale[k]);
-    } else if (L == kV4 && k == 4) {          // chunks 56 .. 63, from place's chunks 0, 2, .. 14
-      v = make_uint4(codes[k][0], codes[k][1], codes[k][2], codes[k][3]);
+    if (L == kV4 && k == 4)                   // chunks 56 .. 63, from place's chunks 0, 2, .. 14
       at = (place ^ (16 * (((2 * (lane & 7)) ^ (8 + (lane & 7)))))) + 768;
-    } else {
-      v = dq_fp8x8(make_uint2(codes[k][2 * j], codes[k][2 * j + 1]), scale[k]);
-    }
     *(__attribute__((address_space(3))) u32x4*)(rows + at) = u32x4{v.x, v.y, v.z, v.w};
+  }
+  __device__ __forceinline__ void put(lds_ptr rows, uint32_t place, int lane, int k, int j) const {
+    write(rows, place, lane, k, j, expand(k, j));
   }
 };
 
@@ -464,7 +468,7 @@ struct Walk {
     if (p.plan_units > 0 && t0 == 0 && threadIdx.x == 0) {
       int32_t parts = 1;
       if (t1 < tiles)
-        parts += (int32_t)((at + kAttendUnitTiles + tiles - 1) / quota - (at + kAttendUnitTiles) / quota);
+        parts += (int32_t)((at + unit_cost(nt) + tiles - 1) / quota - (at + unit_cost(nt)) / quota);
       p.splits[b * p.plan_units + ub] = AttendSplit{b, ub, (int32_t)blockIdx.x, parts};
     }
   }
@@ -498,7 +502,7 @@ struct Walk {
     for (int i = ba; i < bz; ++i) {
       const SlotTokens c = slot_tokens(p, i, &bad);
       for (int k = 0; k < U; ++k) {
-        if (c.n > 0) mine += unit_tiles(unit_rows(p, c, k * qt, qt), nt) + kAttendUnitTiles;
+        if (c.n > 0) mine += unit_tiles(unit_rows(p, c, k * qt, qt), nt) + unit_cost(nt);
         else if (blockIdx.x == 0) p.splits[i * U + k] = AttendSplit{i, k, 0, 0};
       }
     }
@@ -525,13 +529,13 @@ struct Walk {
       for (int i = ba; i < bz; ++i) {
         const SlotTokens sl = slot_tokens(p, i, &bad);
         for (int k = 0; k < U && sl.n > 0; ++k) {
-          const int64_t end = c + kAttendUnitTiles + unit_tiles(unit_rows(p, sl, k * qt, qt), nt);
+          const int64_t end = c + unit_cost(nt) + unit_tiles(unit_rows(p, sl, k * qt, qt), nt);
           if (goal0 >= c && goal0 < end) {
-            ends[0] = AttendStart{i, k, (int32_t)max(goal0 - c - kAttendUnitTiles, (int64_t)0), 0};
+            ends[0] = AttendStart{i, k, (int32_t)max(goal0 - c - unit_cost(nt), (int64_t)0), 0};
             before = c;
           }
           if (goal1 >= c && goal1 < end)
-            ends[1] = AttendStart{i, k, (int32_t)max(goal1 - c - kAttendUnitTiles, (int64_t)0), 0};
+            ends[1] = AttendStart{i, k, (int32_t)max(goal1 - c - unit_cost(nt), (int64_t)0), 0};
           c = end;
         }
       }
@@ -544,7 +548,7 @@ struct Walk {
   }
   __device__ __forceinline__ bool next(const AttendParams& p, int qt, int nt) {
     if (b == eb && ub == eub) return false;
-    at += kAttendUnitTiles + tiles;
+    at += unit_cost(nt) + tiles;
     t0 = 0;
     ++ub;
     if ((int64_t)ub * qt >= (int64_t)s.n * p.heads) {
@@ -1051,7 +1055,7 @@ void attend_wide_kernel(AttendParams p) {
     bf16x8 wv[QB], xv[2];                     // weights, dim fragments ahead of the O products
     uint32_t kp[8];                           // the tile's chunk columns
     bool holes = false, holes_before = false;
-    uint32_t okg, cuts;                       // svalid, sscale as words
+    uint32_t okg, cuts, okw = 0, cutw = 0;    // svalid, sscale as words, and uniform
     // (lane bases opaque to the compiler, which would otherwise keep what is
     // derived from them in registers of its own)
     auto fresh = [](uint32_t v) { asm volatile("" : "+v"(v)); return v; };
@@ -1101,6 +1105,44 @@ void attend_wide_kernel(AttendParams p) {
         xv[1] = out_dims(1, at);
       }
     };
+    // Finding tile tl + 2's rows (whose table entry is in page) and asking for
+    // tile tl + 3's entry, in steps between the score products.  ldata, lscale:
+    // where the rows lie; valid_next: whether they are rows of the cache.
+    bool valid_next = false, in_table = false;
+    int64_t page_off = 0;
+    int32_t next_row = 0;
+    auto locate_step = [&](int k, int32_t tl) {
+      if (k == 2) {
+        next_row = first_row(tl + 2);
+        page = uniform(page);
+        in_table = (next_row >> p.cache.page_bits) < width;
+      } else if (k == 3) {
+        valid_next = in_table && page >= 0 && page < p.cache.num_pages;
+        if (!valid_next && next_row < w.rows) raise_status(p.status, in_table ? kStPageRange : kStPtRange);
+      } else if (k == 5) {
+        page_off = (int64_t)(valid_next ? page : 0) * p.cache.page_stride;
+      } else if (k == 7) {
+        next_row &= (1 << p.cache.page_bits) - 1;
+        ldata = p.cache.base + page_off;
+      } else if (k == 9) {
+        lscale = ldata + ((int64_t)LayoutTraits<L>::kData << p.cache.page_bits);
+      } else if (k == 11) {
+        ldata += (int64_t)next_row * LayoutTraits<L>::kData;
+      } else if (k == 13) {
+        lscale += (int64_t)next_row * LayoutTraits<L>::kScale;
+      } else if (k == 15) {
+        page = entry(tl + 3);
+      } else if (k == 18) {
+        if (lane == 0) svalid[((tl - w.t0) & 1) ^ 1][wave] = valid ? 0xFF : 0;
+        valid = valid_next;
+      } else if (k == 20) {
+        // what was noted of this tile and of the one before
+        okw = (uint32_t)uniform((int32_t)okg);
+        cutw = (uint32_t)uniform((int32_t)cuts);
+        holes_before = holes;
+        holes = (tl + 1) * NT > lim_first || okw != 0xFFFFFFFFu;
+      }
+    };
     // ---- scores of tile tl at cur (its first fragments in x); at the end the
     // first fragments of O's products over the tile before are read
     auto scores = [&](int32_t tl, uint32_t before) {
@@ -1111,37 +1153,34 @@ void attend_wide_kernel(AttendParams p) {
         if (k + 3 >= 32 - kTail && k + 3 < 32) qt[k % 3] = query_tail(k + 3);
         if (k + 6 < 32) x[k % 6] = score_rows(k + 6);
         if (k >= 28) out_ahead(k - 28, before, ((tl - w.t0) & 1) ^ 1);
+        locate_step(k, tl);
         __builtin_amdgcn_sched_barrier(0);
       }
     };
-    // ---- tile tl + 1 expanded into the buffer at nxt and tile tl + 2 requested, in
-    // 2 NL steps
-    uint32_t pl;
-    auto stage_begin = [&](int32_t tl) {
-      pl = fresh(place);
-      if (lane == 0) svalid[((tl - w.t0) & 1) ^ 1][wave] = valid ? 0xFF : 0;
-      valid = locate(tl + 2, page);
-      page = entry(tl + 3);
-    };
-    auto stage = [&](int step, uint32_t nxt) {
-      const int k = step >> 1, j = step & 1;
-      if (k >= NL) return;
-      if (j < Group<L>::parts(k)) gr.put(tiles3 + nxt + wave * 8192, pl, lane, k, j);
-      if (j == 1) gr.load(ldata, lscale, doff, soff, k);
-    };
     // ---- mask (only a tile that some query does not see whole)
     auto mask = [&](int32_t tl) {
-      holes_before = holes;
-      const uint32_t okw = (uint32_t)uniform((int32_t)okg);
-      holes = (tl + 1) * NT > lim_first || okw != 0xFFFFFFFFu;
-      if (holes) {
-        scores_done(sc);
-        const bool any = mask_scores(sc, q, tl * NT, h, w.s.pos, tree, okw);
-        if (lane == 0) snf[(tl - w.t0) & 1][wave] = any;
-      }
+      if (!holes) return;
+      scores_done(sc);
+      const bool any = mask_scores(sc, q, tl * NT, h, w.s.pos, tree, okw);
+      if (lane == 0) snf[(tl - w.t0) & 1][wave] = any;
     };
-    // ---- the softmax of a tile in 24 steps: maximum, then a weight a step
-    float tm, ref, alpha, e[4];
+    // ---- tile tl + 1 expanded into the buffer at nxt, in steps of their own for
+    // the conversions and the write that waits for them, and each load asked for
+    // again (tile tl + 2) when it has been used
+    uint32_t pl = 0;
+    uint4 put_v = make_uint4(0, 0, 0, 0);
+    auto stage = [&](int step, uint32_t nxt) {
+      if (step == 0) pl = fresh(place);
+      const int part = step / 3, k = part >> 1, j = part & 1;
+      if (k >= NL || j >= Group<L>::parts(k)) return;
+      if (step % 3 == 0) put_v = gr.expand(k, j);
+      if (step % 3 == 1) Group<L>::write(tiles3 + nxt + wave * 8192, pl, lane, k, j, put_v);
+      if (step % 3 == 2 && j == Group<L>::parts(k) - 1) gr.load(ldata, lscale, doff, soff, k);
+    };
+    // ---- the softmax of a tile in 28 steps: the maximum, then a weight a step,
+    // each operation a step after the one it waits for
+    float tm = 0, ref = 0, alpha = 0, swapped = 0, e[16];
+    uint32_t wwrite = 0, pair0 = 0, pair1 = 0;
     auto soften = [&](int step, int32_t par) {
       if (step == 1) scores_done(sc);
       if (step >= 1 && step < 5) {
@@ -1149,30 +1188,48 @@ void attend_wide_kernel(AttendParams p) {
         tm = step == 1 ? max3(sc[0], sc[1], sc[2]) : max3(tm, sc[i - 1], sc[i]);
         tm = step == 1 ? tm : max3(tm, sc[i + 1], sc[i + 2]);
       }
-      if (step == 5) tm = max_halves(max3(tm, sc[15], sc[15]));
-      if (step == 6) {
-        alpha = raise_max(q, tm * c2);
-        ref = q.mx == kNegInf ? 0.0f : q.mx;
+      if (step == 5) {
+        tm = max3(tm, sc[15], sc[15]);
+        const uint32_t ln = fresh(lane);
+        wwrite = ((ln & 31) + 32 * wave) * (2 * PS) + 8 * (ln >> 5);
       }
-      if (step == 7) {
+      if (step == 6) {
+        const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(tm), __float_as_uint(tm), false, false);
+        tm = __uint_as_float(r[0]), swapped = __uint_as_float(r[1]);
+      }
+      if (step == 7) tm = max3(tm, swapped, swapped) * c2;
+      if (step == 8) {
+        // (raise_max, in pieces)
+        alpha = q.mx;
+        q.mx = tm > q.mx + 8.0f ? tm : q.mx;
+      }
+      if (step == 9) {
+        ref = q.mx == kNegInf ? 0.0f : q.mx;
+        tm = __builtin_amdgcn_exp2f(alpha - q.mx);
+      }
+      if (step == 11) {
+        alpha = alpha == q.mx ? 1.0f : tm;
+        q.sum *= alpha;
+        q.rsum *= alpha;
+      }
+      if (step == 12) {
         const bool rescale = __ballot(alpha != 1.0f) != 0;
         const uint32_t ln = fresh(lane);
         // (both halves of the wave write the same values)
         salpha[par][wave * 32 + (ln & 31)] = alpha;
         sscale[par][wave] = rescale ? 1 : 0;
       }
-      if (step >= 8 && step < 24) {
-        const int i = step - 8;
-        e[i & 3] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[i], c2, -ref));
-        q.sum += e[i & 3];
-        if ((i & 3) == 3) {
-          const uint32_t w0 = pack_bf16(e[0], e[1]), w1 = pack_bf16(e[2], e[3]);
-          q.rsum = add_pair(add_pair(q.rsum, w0), w1);
-          const uint32_t ln = fresh(lane);
-          const uint32_t at = ((ln & 31) + 32 * wave) * (2 * PS) + 8 * (ln >> 5) + 16 * (i >> 2);
-          *(__attribute__((address_space(3))) u32x2*)(wts3 + par * WB + at) = u32x2{w0, w1};
-        }
+      // weight i: its exponent at step 10 + i, its power a step later, its sum
+      // another one later; a quad's bf16 and its write behind them
+      if (step >= 10 && step < 26) e[step - 10] = __builtin_fmaf(sc[step - 10], c2, -ref);
+      if (step >= 11 && step < 27) e[step - 11] = __builtin_amdgcn_exp2f(e[step - 11]);
+      if (step >= 12 && step < 28) q.sum += e[step - 12];
+      if (step >= 15 && step < 28 && (step & 3) == 3) {
+        const int i = step - 15;
+        pair0 = pack_bf16(e[i], e[i + 1]), pair1 = pack_bf16(e[i + 2], e[i + 3]);
+        *(__attribute__((address_space(3))) u32x2*)(wts3 + par * WB + wwrite + 4 * i) = u32x2{pair0, pair1};
       }
+      if (step >= 16 && step <= 28 && (step & 3) == 0) q.rsum = add_pair(add_pair(q.rsum, pair0), pair1);
     };
     // ---- what must precede O's products over the tile at `at` (parity par)
     auto out_begin = [&](uint32_t at, int32_t par, bool dirty) {
@@ -1184,9 +1241,10 @@ void attend_wide_kernel(AttendParams p) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) out_ahead(i, at, par);
       }
+      if (cutw == 0) return;
 #pragma unroll
       for (int y = 0; y < QB; ++y) {
-        if ((uniform((int32_t)cuts) >> (8 * y) & 0xFF) == 0) continue;
+        if ((cutw >> (8 * y) & 0xFF) == 0) continue;
         const float a = salpha[par][y * 32 + ql];
 #pragma unroll
         for (int d = 0; d < 4; ++d) {
@@ -1210,10 +1268,12 @@ void attend_wide_kernel(AttendParams p) {
           if (i == 3) wv[y] = out_weights(1, y, par);
           if constexpr (with.value) {
             soften(4 * i + y, par ^ 1);
-            if (4 * i + y < 4 * NL && y % 2 == 1) stage(2 * i + y / 2, nxt);
-            if (i == 6 && y == 0) __syncthreads();
-            if (i == 6 && y > 0) ahead(y - 1, nxt, par);
-            if (i == 7 && y < 3) ahead(y + 3, nxt, par);
+            stage(4 * i + y, nxt);
+            if (i == 7 && y == 0) __syncthreads();
+            if (i == 7 && y > 0) {
+              ahead(2 * y - 2, nxt, par);
+              ahead(2 * y - 1, nxt, par);
+            }
           }
           __builtin_amdgcn_sched_barrier(0);
         }
@@ -1225,11 +1285,10 @@ void attend_wide_kernel(AttendParams p) {
     for (int i = 0; i < 6; ++i) ahead(i, cur, 0);
     scores(w.t0, cur);
     mask(w.t0);
-    stage_begin(w.t0);
 #pragma unroll
-    for (int i = 0; i < 24; ++i) {
+    for (int i = 0; i < 29; ++i) {
       soften(i, 0);
-      if (i < 2 * NL) stage(i, after(cur));
+      stage(i, after(cur));
     }
     __syncthreads();
 #pragma unroll
@@ -1240,10 +1299,10 @@ void attend_wide_kernel(AttendParams p) {
       cur = after(cur);
       scores(tl, before);
       mask(tl);
-      stage_begin(tl);
       out_begin(before, par ^ 1, holes_before);
       out(before, par ^ 1, after(cur), std::true_type{});
     }
+    cutw = (uint32_t)uniform((int32_t)cuts);
     const int32_t last = (w.t1 - 1 - w.t0) & 1;
 #pragma unroll
     for (int i = 0; i < 4; ++i) out_ahead(i, cur, last);
