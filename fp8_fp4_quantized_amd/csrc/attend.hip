@@ -361,6 +361,7 @@ struct Query {
   int32_t lim;                 // rows below are visible ...
   uint64_t bits;               // ... and of the rows from base on those of bits
   float mx, sum, rsum;         // reference maximum (log2), sums of weights and rounded weights
+  float sink;                  // log2
 };
 
 __device__ __forceinline__ Query query_of(const AttendParams& p, int b, const SlotTokens& s, int32_t m) {
@@ -380,6 +381,7 @@ __device__ __forceinline__ Query query_of(const AttendParams& p, int b, const Sl
   }
   q.mx = kNegInf;
   q.sum = q.rsum = 0.0f;
+  q.sink = p.sink != nullptr ? p.sink[q.head] * kLog2e : kNegInf;
   return q;
 }
 
@@ -439,9 +441,7 @@ __device__ __forceinline__ float raise_max(Query& q, float tile_max) {
 struct Final {
   float f, lse;
 };
-__device__ __forceinline__ Final finish(const AttendParams& p, int32_t head, float mx, float sum,
-                                        float rsum) {
-  const float snk = p.sink != nullptr ? p.sink[head] * kLog2e : kNegInf;
+__device__ __forceinline__ Final finish(float snk, float mx, float sum, float rsum) {
   const float mm = fmaxf(mx, snk);
   const float e = mx == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(mx - mm);
   const float es = snk == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(snk - mm);
@@ -573,15 +573,28 @@ struct Walk {
   }
 };
 
+// sixteen accumulators out of the matrix registers here and not before: all of
+// them at once would not fit
+__device__ __forceinline__ f32x16 taken(f32x16 v) {
+  asm volatile("" : "+a"(v));
+  return v;
+}
+
 // The end of a piece: the sums of each query over the lanes and waves that
-// hold rows of it, then its outputs, or its partial sums for the join.
+// hold rows of it, then its outputs, or its partial sums for the join.  A lane
+// holds four dims of a query at a time: outputs are turned through LDS (area:
+// the tiles, 96 KB or more, three blocks of 32 queries) so that a wave writes whole rows; partial
+// sums are stored as they lie in the registers, a wave's
+// 1 KB at a time, in the order [query block][dim block][quad][wave][lane].
 template <int QB>
 __device__ __forceinline__ void end_piece(const AttendParams& p, const Walk& w, Query& q,
                                           const f32x16 (&o)[4][QB], int qb, int nb,
                                           float (*ssum)[32 * QB], float (*srsum)[32 * QB],
-                                          float* sfac) {
+                                          float* sfac, lds_ptr area) {
   constexpr int NB = 4 / QB, QT = 32 * QB;
-  const int lane = lane_id(), wave = uniform((int)(threadIdx.x >> 6));
+  int lane = lane_id();
+  asm volatile("" : "+v"(lane));              // nothing of the end is worked out before the tiles
+  const int wave = uniform((int)(threadIdx.x >> 6));
   const int ql = lane & 31, h = lane >> 5, qi = qb * 32 + ql;
   q.sum = sum_halves(q.sum);
   q.rsum = sum_halves(q.rsum);
@@ -595,34 +608,78 @@ __device__ __forceinline__ void end_piece(const AttendParams& p, const Walk& w, 
 #pragma unroll
     for (int x = 1; x < NB; ++x) { sum += ssum[x][qi]; rsum += srsum[x][qi]; }
     if (whole) {
-      const Query me = query_of(p, w.b, w.s, w.ub * QT + qi);
-      const Final f = finish(p, me.head, q.mx, sum, rsum);
+      const int32_t m = w.ub * QT + qi;
+      float snk = q.sink;
+      if constexpr (QB == 4) {                // a register that the wide kernel's tiles need
+        const int32_t mc = min(m, w.s.n * p.heads - 1);
+        snk = p.sink != nullptr
+                  ? p.sink[mc - (int32_t)udiv_magic((uint32_t)mc, p.head_div.m, p.head_div.sh1,
+                                                    p.head_div.sh2) * p.heads] * kLog2e
+                  : kNegInf;
+      }
+      const Final f = finish(snk, q.mx, sum, rsum);
       sfac[qi] = f.f;
-      if (p.lse != nullptr && me.ok) p.lse[(int64_t)(w.s.first + me.tok) * p.heads + me.head] = f.lse;
+      if (p.lse != nullptr && m < w.s.n * p.heads) p.lse[(int64_t)w.s.first * p.heads + m] = f.lse;
     } else {
       p.part_ml[part + qi] = make_float4(q.mx, sum, rsum, 0.0f);
     }
   }
-  __syncthreads();
+  if (!whole) {
+    float* const pp = p.part_o + part * kDim + 256 * wave + 4 * lane;
 #pragma unroll
-  for (int x = 0; x < QB; ++x) {
-    const Query y = query_of(p, w.b, w.s, w.ub * QT + x * 32 + ql);
-    if (!y.ok) continue;
-    uint16_t* op = p.out + (int64_t)(w.s.first + y.tok) * p.out_stride + (int64_t)y.head * p.out_hstride;
-    float* pp = p.part_o + (part + x * 32 + ql) * kDim;
-    const float f = whole ? sfac[x * 32 + ql] : 1.0f;
+    for (int x = 0; x < QB; ++x)
 #pragma unroll
-    for (int d = 0; d < 4; ++d)
+      for (int d = 0; d < 4; ++d) {
+        const f32x16 v = taken(o[d][x]);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int dim = 128 * wave + 32 * d + 8 * j + 4 * h;
-        const float a0 = o[d][x][4 * j], a1 = o[d][x][4 * j + 1], a2 = o[d][x][4 * j + 2],
-                    a3 = o[d][x][4 * j + 3];
-        if (whole)
-          *(u32x2*)(op + dim) = u32x2{pack_bf16(a0 * f, a1 * f), pack_bf16(a2 * f, a3 * f)};
-        else
-          *(f32x4*)(pp + dim) = f32x4{a0, a1, a2, a3};
+        for (int j = 0; j < 4; ++j)
+          *(f32x4*)(pp + ((x * 4 + d) * 4 + j) * 1024) =
+              f32x4{v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]};
       }
+    return;
+  }
+  __syncthreads();
+  const int32_t nq = w.s.n * p.heads;
+  constexpr int R = QB < 3 ? QB : 3;          // blocks of 32 queries that the area holds
+#pragma unroll
+  for (int x0 = 0; x0 < QB; x0 += R) {
+    if (x0 > 0) __syncthreads();
+#pragma unroll
+    for (int x = x0; x < min(x0 + R, QB); ++x) {
+      const float f = sfac[x * 32 + ql];
+      const lds_ptr row = area + (x - x0) * 32768 + ql * 1024 + 8 * h;
+#pragma unroll
+      for (int d = 0; d < 4; ++d) {
+        const f32x16 v = taken(o[d][x]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {           // chunk 16 wave + 4 d + j, permuted by the row
+          const uint32_t at = ((16 * wave + 4 * d + j) ^ (ql & 15)) << 4;
+          *(__attribute__((address_space(3))) u32x2*)(row + at) =
+              u32x2{pack_bf16(v[4 * j] * f, v[4 * j + 1] * f),
+                    pack_bf16(v[4 * j + 2] * f, v[4 * j + 3] * f)};
+        }
+      }
+    }
+    __syncthreads();
+    for (int x = x0; x < min(x0 + R, QB); ++x) {
+      // the wave's 8 rows: its first one's place, then from head to head
+      const int32_t m = w.ub * QT + x * 32 + wave * 8;
+      int32_t tok = (int32_t)udiv_magic((uint32_t)m, p.head_div.m, p.head_div.sh1, p.head_div.sh2);
+      int32_t head = m - tok * p.heads;
+      const int rows = min(8, nq - m);
+      uint16_t* op = p.out + (int64_t)(w.s.first + tok) * p.out_stride + (int64_t)head * p.out_hstride;
+      for (int i = 0; i < rows; ++i) {
+        const int r = wave * 8 + i;
+        const u32x4 v = *(const __attribute__((address_space(3))) u32x4*)(
+            area + (x - x0) * 32768 + r * 1024 + ((lane ^ (r & 15)) << 4));
+        *(u32x4*)(op + 8 * lane) = v;
+        op += p.out_hstride;
+        if (++head == p.heads) {
+          head = 0;
+          op += p.out_stride - p.heads * p.out_hstride;
+        }
+      }
+    }
   }
 }
 
@@ -789,13 +846,24 @@ void attend_kernel(AttendParams p) {
           load_all();
           __syncthreads();
         }
-      } else {
-        note_valid(par ^ 1);
-        locate(tl + 2, page);
-        page = entry(tl + 3);
       }
-      // ---- scores of this wave's 32 rows and 32 queries; with two buffers, tile
-      // tl + 1 is expanded into the other one between, tile tl + 2 requested
+      // With two buffers, tile tl + 1 is expanded into the other one in steps
+      // between the products (conversions, their write a step later, and the
+      // load for tile tl + 2 in the registers that are free then): the first
+      // half between the score products, the rest between O's.
+      constexpr int PARTS = L == kV4 ? 9 : 2 * NL;      // of a group
+      constexpr int HALF = (G * PARTS + 1) / 2;
+      uint4 put_v = make_uint4(0, 0, 0, 0);
+      auto stage = [&](int part, int step) {  // part: over all groups
+        const int g = part / PARTS, r = part % PARTS, k = r >> 1, j = r & 1;
+        if (g >= G) return;
+        if (step == 0) put_v = gr[g].expand(k, j);
+        else if (step == 1)
+          Group<L>::write(tiles3 + (cur ^ TB) + (row0 + 8 * g) * 1024,
+                          G > 1 ? place ^ (32 * (g & 1)) : place, lane, k, j, put_v);
+        else if (j == Group<L>::parts(k) - 1) load(g, k);
+      };
+      // ---- scores of this wave's 32 rows and 32 queries
       f32x16 sc;
       {
         constexpr int LA = 6;
@@ -805,24 +873,18 @@ void attend_kernel(AttendParams p) {
         };
 #pragma unroll
         for (int k = 0; k < LA; ++k) x[k] = rows16(k);
-        int g = 0, ld = 0, in_load = 0;       // constants after unrolling
 #pragma unroll
         for (int k = 0; k < 32; ++k) {
           score_mfma(sc, x[k % LA], qv[k], k == 0);
           if (k + LA < 32) x[k % LA] = rows16(k + LA);
           if constexpr (BUF == 2) {
-            if (k % 3 != 0 && g < G) {
-              put(cur ^ TB, g, ld, in_load);
-              if (++in_load == Group<L>::parts(ld)) {
-                load(g, ld);
-                in_load = 0;
-                if (++ld == NL) ld = 0, ++g;
-              }
-            }
+            if (k == 1) note_valid(par ^ 1);
+            if (k == 2) locate(tl + 2, page);
+            if (k == 4) page = entry(tl + 3);
+            if (k >= 5 && (k - 5) / 3 < HALF) stage((k - 5) / 3, (k - 5) % 3);
           }
           __builtin_amdgcn_sched_barrier(0);
         }
-        if constexpr (BUF == 2) okm = okm_next;
       }
       scores_done(sc);
       // ---- mask (only a tile that some query does not see whole)
@@ -835,12 +897,12 @@ void attend_kernel(AttendParams p) {
         if (lane == 0) snf[wave] = any;
       }
       // ---- the block's maximum
-      float tm = max3(sc[0], sc[1], sc[2]);
-#pragma unroll
-      for (int i = 3; i < 15; i += 2) tm = max3(tm, sc[i], sc[i + 1]);
-      tm = max_halves(max3(tm, sc[15], sc[15])) * c2;
+      float tm = max3(max3(max3(sc[0], sc[1], sc[2]), sc[3], sc[4]),
+                      max3(max3(sc[5], sc[6], sc[7]), sc[8], sc[9]),
+                      max3(max3(sc[10], sc[11], sc[12]), max3(sc[13], sc[14], sc[15]), sc[15]));
+      tm = max_halves(tm) * c2;
       smax[nb][qi] = tm;                      // (both halves of the wave write the same)
-      float mine = QB == 1 || qb == 0 ? ref[0] : ref[QB - 1];
+      const float mine = QB == 1 || qb == 0 ? ref[0] : ref[QB - 1];
       const bool jump = __ballot(tm > mine + 16.0f) != 0;
       if (lane == 0) sjump[wave] = jump;
       // ---- weights, their sums, and their bf16 to LDS
@@ -848,40 +910,68 @@ void attend_kernel(AttendParams p) {
       float ts, tr;
       auto weigh = [&](float at) {
         const float base = at == kNegInf ? 0.0f : at;
-        ts = tr = 0.0f;
+        float e[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) e[i] = __builtin_fmaf(sc[i], c2, -base);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) e[i] = __builtin_amdgcn_exp2f(e[i]);
+        float t[4] = {};
+        tr = 0.0f;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          float e[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            e[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[4 * j + i], c2, -base));
-            ts += e[i];
-          }
-          const uint32_t w0 = pack_bf16(e[0], e[1]), w1 = pack_bf16(e[2], e[3]);
-          tr = add_pair(add_pair(tr, w0), w1);
+          for (int i = 0; i < 4; ++i) t[i] += e[4 * j + i];
+          const uint32_t w0 = pack_bf16(e[4 * j], e[4 * j + 1]), w1 = pack_bf16(e[4 * j + 2], e[4 * j + 3]);
           *(u32x2*)(wrow + 8 * j) = u32x2{w0, w1};
+          tr = add_pair(add_pair(tr, w0), w1);
         }
+        ts = (t[0] + t[1]) + (t[2] + t[3]);
       };
       weigh(mine);
       __syncthreads();
-      // ---- the tile's maxima over the waves of each query
-      float top[QB];
+      // ---- the tile's maxima over the waves of each query, and what the waves noted
+      union Frag { s16x4 half[2]; bf16x8 v; };
+      auto dims = [&](int i) {                // dim block i & 3, rows 16 (i >> 2) ..
+        Frag f;
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          f.half[e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+              (trp)(tiles3 + cur + vp[e][i & 3] + 16384 * (i >> 2)));
+        return f.v;
+      };
+      auto weights = [&](int k, int x) {
+        return __builtin_bit_cast(bf16x8, *(const u32x4*)(wts + (x * 32 + ql) * PS + 16 * k + 8 * h));
+      };
+      const int32_t jumps = *(const int32_t*)sjump, bad = *(const int32_t*)snf;
+      float top[QB], part[QB][NB];
+#pragma unroll
+      for (int x = 0; x < QB; ++x)
+#pragma unroll
+        for (int y = 0; y < NB; ++y) part[x][y] = smax[y][x * 32 + ql];
+      constexpr int N = NT / 4;               // dim blocks times 16-row steps
+      bf16x8 xv[3], wv[2][QB];
+      auto first_frags = [&]() {
+#pragma unroll
+        for (int x = 0; x < QB; ++x) wv[0][x] = weights(0, x);
+#pragma unroll
+        for (int i = 0; i < 3; ++i) xv[i] = dims(i);
+      };
+      first_frags();
 #pragma unroll
       for (int x = 0; x < QB; ++x) {
-        top[x] = smax[0][x * 32 + ql];
+        top[x] = part[x][0];
 #pragma unroll
-        for (int y = 1; y < NB; ++y) top[x] = fmaxf(top[x], smax[y][x * 32 + ql]);
+        for (int y = 1; y < NB; ++y) top[x] = fmaxf(top[x], part[x][y]);
       }
-      const bool again = uniform(*(const int32_t*)sjump) != 0;
-      const bool dirty = holes && uniform(*(const int32_t*)snf) != 0;
+      const bool again = uniform(jumps) != 0, dirty = holes && uniform(bad) != 0;
       // raises the references passed by more than 8 and rescales what was summed
       auto raise = [&]() {
 #pragma unroll
         for (int x = 0; x < QB; ++x) {
+          if (__ballot(top[x] > ref[x] + 8.0f) == 0) continue;
           const float old = ref[x];
           if (top[x] > old + 8.0f) ref[x] = top[x];
           const float alpha = ref[x] == old ? 1.0f : __builtin_amdgcn_exp2f(old - ref[x]);
-          if (__ballot(alpha != 1.0f) == 0) continue;
           if (x == qb) {
             q.sum *= alpha;
             q.rsum *= alpha;
@@ -893,48 +983,35 @@ void attend_kernel(AttendParams p) {
           }
         }
       };
-      if (again) {
-        raise();
-        weigh(QB == 1 || qb == 0 ? ref[0] : ref[QB - 1]);
+      if (again || dirty) {
+        if (again) {
+          raise();
+          weigh(QB == 1 || qb == 0 ? ref[0] : ref[QB - 1]);
+        }
+        // a NaN or an infinity in a row that some query does not see: its weight
+        // there is 0, and 0 times it would not be
+        if (dirty) zero_not_finite<TB>(tiles3 + cur);
+        __syncthreads();
+        first_frags();
       }
-      // a NaN or an infinity in a row that some query does not see: its weight
-      // there is 0, and 0 times it would not be
-      if (dirty) zero_not_finite<TB>(tiles3 + cur);
-      if (again || dirty) __syncthreads();
       q.sum += ts;
       q.rsum += tr;
       // ---- O += X^T P^T on dims [128 wave, 128 wave + 128)
-      {
-        union Frag { s16x4 half[2]; bf16x8 v; };
-        auto dims = [&](int i) {              // dim block i & 3, rows 16 (i >> 2) ..
-          Frag f;
 #pragma unroll
-          for (int e = 0; e < 2; ++e)
-            f.half[e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                (trp)(tiles3 + cur + vp[e][i & 3] + 16384 * (i >> 2)));
-          return f.v;
-        };
-        auto weights = [&](int k, int x) {
-          return __builtin_bit_cast(bf16x8, *(const u32x4*)(wts + (x * 32 + ql) * PS + 16 * k + 8 * h));
-        };
-        constexpr int N = NT / 4;             // dim blocks times 16-row steps
-        bf16x8 xv[3], wv[2][QB];
+      for (int i = 0; i < N; ++i) {
 #pragma unroll
-        for (int x = 0; x < QB; ++x) wv[0][x] = weights(0, x);
-#pragma unroll
-        for (int i = 0; i < 3; ++i) xv[i] = dims(i);
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-#pragma unroll
-          for (int x = 0; x < QB; ++x) out_mfma(o[i & 3][x], xv[i % 3], wv[(i >> 2) & 1][x]);
-          if (i + 3 < N) xv[i % 3] = dims(i + 3);
-          if ((i & 3) == 1 && i + 4 < N) {
-#pragma unroll
-            for (int x = 0; x < QB; ++x) wv[((i >> 2) + 1) & 1][x] = weights((i >> 2) + 1, x);
+        for (int x = 0; x < QB; ++x) {
+          out_mfma(o[i & 3][x], xv[i % 3], wv[(i >> 2) & 1][x]);
+          if (x == QB - 1 && i + 3 < N) xv[i % 3] = dims(i + 3);
+          if ((i & 3) == 1 && i + 4 < N) wv[((i >> 2) + 1) & 1][x] = weights((i >> 2) + 1, x);
+          if constexpr (BUF == 2) {
+            const int step = i * QB + x;
+            stage(HALF + step / 3, step % 3);
           }
           __builtin_amdgcn_sched_barrier(0);
         }
       }
+      if constexpr (BUF == 2) okm = okm_next;
       if (!again) raise();
       __syncthreads();                        // the tile, the weights and the maxima are free
     }
@@ -943,7 +1020,7 @@ void attend_kernel(AttendParams p) {
 #pragma unroll
       for (int x = 0; x < QB; ++x) out_done(o[d][x]);
     q.mx = QB == 1 || qb == 0 ? ref[0] : ref[QB - 1];
-    end_piece<QB>(p, w, q, o, qb, nb, ssum, srsum, sfac);
+    end_piece<QB>(p, w, q, o, qb, nb, ssum, srsum, sfac, tiles3);
     __syncthreads();
   } while (w.next(p, QT, NT));
 }
@@ -1312,74 +1389,78 @@ void attend_wide_kernel(AttendParams p) {
     for (int d = 0; d < 4; ++d)
 #pragma unroll
       for (int y = 0; y < QB; ++y) out_done(o[d][y]);
-    end_piece<QB>(p, w, q, o, wave, 0, ssum, srsum, sfac);
+    end_piece<QB>(p, w, q, o, wave, 0, ssum, srsum, sfac, tiles3);
     __syncthreads();
   } while (w.next(p, QT, NT));
 }
 
 // ------------------------------------------------------------------ join
-// One workgroup per query of a unit that was cut: the parts are dealt to the
-// four waves (8 dims a lane), each scaled to the common maximum, and the
-// waves' sums added.
+// One workgroup per 8 queries and 128 dims (the dims of one wave) of a unit
+// that was cut, 8 threads of neighbouring queries on 128 bytes of a part: the
+// parts' weights against the common maximum into LDS, then the weighted sum of
+// the parts, four dims a thread.
 __global__ __launch_bounds__(256) void attend_join_kernel(AttendParams p, int qt) {
-  __shared__ float acc[3][kDim];
+  __shared__ float weight[kAttendGrid][8];
+  __shared__ float red[3][4][8];
   if (p.plan_units == 0 && (int)blockIdx.x >= p.head->nsplit) return;
   const AttendSplit sp = p.splits[blockIdx.x];
   if (sp.parts < 2) return;
   int32_t none = 0;
   const SlotTokens s = slot_tokens(p, sp.slot, &none);
-  const int qi = blockIdx.y;
-  const int32_t m = sp.unit * qt + qi;
-  if (m >= s.n * p.heads) return;
-  const int lane = lane_id(), wave = uniform((int)(threadIdx.x >> 6));
+  const int q8 = threadIdx.x & 7, piece = threadIdx.x >> 3, wave = uniform((int)(threadIdx.x >> 6));
+  const int32_t m0 = sp.unit * qt + blockIdx.y * 8;
+  if (m0 >= s.n * p.heads) return;
+  const int qi = blockIdx.y * 8 + q8;         // of the unit
   // part k lies with workgroup wg0 + k: its second place for the first part
   // (which began at the unit's first tile), its first place for the others
-  auto place = [&](int k) -> int64_t { return ((int64_t)(sp.wg0 + k) * 2 + (k == 0 ? 1 : 0)) * qt + qi; };
-  float mx = kNegInf;
-  for (int k = lane; k < sp.parts; k += kLanes) mx = fmaxf(mx, p.part_ml[place(k)].x);
+  auto place = [&](int k) -> int64_t { return ((int64_t)(sp.wg0 + k) * 2 + (k == 0 ? 1 : 0)) * qt; };
+  // over the 32 threads of a query
+  auto reduce = [&](float v, int slot, bool maximum) {
 #pragma unroll
-  for (int d = 1; d < kLanes; d <<= 1) mx = fmaxf(mx, __shfl_xor(mx, d));
+    for (int d = 8; d < kLanes; d <<= 1) {
+      const float y = __shfl_xor(v, d);
+      v = maximum ? fmaxf(v, y) : v + y;
+    }
+    if ((threadIdx.x & 63) < 8) red[slot][wave][q8] = v;
+    __syncthreads();
+    float r = red[slot][0][q8];
+#pragma unroll
+    for (int w = 1; w < 4; ++w) r = maximum ? fmaxf(r, red[slot][w][q8]) : r + red[slot][w][q8];
+    return r;
+  };
+  float mx = kNegInf;
+  for (int k = piece; k < sp.parts; k += 32) mx = fmaxf(mx, p.part_ml[place(k) + qi].x);
+  mx = reduce(mx, 0, true);
   float sum = 0.0f, rsum = 0.0f;
-  for (int k = lane; k < sp.parts; k += kLanes) {
-    const float4 v = p.part_ml[place(k)];
+  for (int k = piece; k < sp.parts; k += 32) {
+    const float4 v = p.part_ml[place(k) + qi];
     const float e = v.x == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(v.x - mx);
+    weight[k][q8] = e;
     sum += v.y * e;
     rsum += v.z * e;
   }
-  sum = wave_sum_f32(sum);
-  rsum = wave_sum_f32(rsum);
-  float a[8] = {};
-  for (int k = wave; k < sp.parts; k += 4) {
-    const int64_t at = place(k);
-    const float4 v = p.part_ml[at];
-    if (v.y == 0.0f) continue;                // a part that saw nothing
-    const float e = v.x == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(v.x - mx);
-    const f32x4 x = *(const f32x4*)(p.part_o + at * kDim + 8 * lane);
-    const f32x4 y = *(const f32x4*)(p.part_o + at * kDim + 8 * lane + 4);
+  sum = reduce(sum, 1, false);
+  rsum = reduce(rsum, 2, false);              // (its barrier covers weight)
+  // piece = dim block * 8 + quad * 2 + half, as the parts are laid out
+  const int x = qi >> 5, ql = qi & 31, w = blockIdx.z;
+  const float* const src = p.part_o + (x * 16 + (piece >> 1)) * 1024 + 256 * w + ((piece & 1) * 32 + ql) * 4;
+  f32x4 a = {};
+#pragma unroll 8
+  for (int k = 0; k < sp.parts; ++k) {
+    const f32x4 v = *(const f32x4*)(src + place(k) * kDim);
+    const float e = weight[k][q8];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      a[i] = __builtin_fmaf(x[i], e, a[i]);
-      a[4 + i] = __builtin_fmaf(y[i], e, a[4 + i]);
-    }
+    for (int i = 0; i < 4; ++i) a[i] = __builtin_fmaf(v[i], e, a[i]);
   }
-  if (wave > 0) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) acc[wave - 1][8 * lane + i] = a[i];
-  }
-  __syncthreads();
-  if (wave > 0) return;
-#pragma unroll
-  for (int w = 0; w < 3; ++w)
-#pragma unroll
-    for (int i = 0; i < 8; ++i) a[i] += acc[w][8 * lane + i];
+  const int32_t m = m0 + q8;
+  if (m >= s.n * p.heads) return;
   const int32_t tok = (int32_t)udiv_magic((uint32_t)m, p.head_div.m, p.head_div.sh1, p.head_div.sh2);
   const int32_t head = m - tok * p.heads;
-  const Final fin = finish(p, head, mx, sum, rsum);
-  const float f = fin.f;
-  uint16_t* op = p.out + (int64_t)(s.first + tok) * p.out_stride + (int64_t)head * p.out_hstride;
-  st_u4(op + 8 * lane, make_uint4(pack_bf16(a[0] * f, a[1] * f), pack_bf16(a[2] * f, a[3] * f),
-                                  pack_bf16(a[4] * f, a[5] * f), pack_bf16(a[6] * f, a[7] * f)));
-  if (p.lse != nullptr && lane == 0)
+  const Final fin = finish(p.sink != nullptr ? p.sink[head] * kLog2e : kNegInf, mx, sum, rsum);
+  uint16_t* const op = p.out + (int64_t)(s.first + tok) * p.out_stride + (int64_t)head * p.out_hstride;
+  *(u32x2*)(op + 128 * w + 4 * piece) =
+      u32x2{pack_bf16(a[0] * fin.f, a[1] * fin.f), pack_bf16(a[2] * fin.f, a[3] * fin.f)};
+  if (p.lse != nullptr && w == 0 && piece == 0)
     p.lse[(int64_t)(s.first + tok) * p.heads + head] = fin.lse;
 }
 
@@ -1418,8 +1499,8 @@ hipError_t launch_attend(const AttendParams& p, int qblocks, hipStream_t stream)
   // one boundary between two workgroups
   const int64_t splits = p.plan_units > 0 ? (int64_t)p.num_slots * p.plan_units
                                           : min(p.units_max, (int64_t)kAttendGrid - 1);
-  hipLaunchKernelGGL(attend_join_kernel, dim3((unsigned)splits, (unsigned)qt), dim3(256), 0, stream,
-                     p, qt);
+  hipLaunchKernelGGL(attend_join_kernel, dim3((unsigned)splits, (unsigned)(qt / 8), 4), dim3(256), 0,
+                     stream, p, qt);
   return hipGetLastError();
 }
 

@@ -151,7 +151,7 @@ struct SlotMapParams {
 // the fewest cache rows a workgroup takes (a call with fewer rows to read
 // uses fewer workgroups: each costs its share of the join).
 constexpr int kAttendWorkgroups = 256;
-constexpr int kAttendLeastRows = 256;
+constexpr int kAttendLeastRows = 128;
 
 // A unit's begin and end (its queries in, its outputs out), as the rows that
 // take the same time: 30,000 to 40,000 cycles beside 4,100 for a 32-row tile.
