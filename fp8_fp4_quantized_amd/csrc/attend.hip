@@ -456,99 +456,114 @@ struct Walk {
   int b, ub;
   int32_t t0, t1, tiles, rows;
   int eb, eub, et;             // the end: slot, unit, tile
-  int64_t at, quota;           // (plan_here) cost before the unit, cost per workgroup
+  int32_t parts;               // (plan_here) workgroups from this one on in the end's unit
   SlotTokens s;
 
   __device__ __forceinline__ void piece(const AttendParams& p, int qt, int nt) {
-    rows = unit_rows(p, s, ub * qt, qt);
+    rows = uniform(unit_rows(p, s, ub * qt, qt));
     tiles = unit_tiles(rows, nt);
-    t1 = b == eb && ub == eub ? et : tiles;
+    t1 = uniform(b == eb && ub == eub ? et : tiles);
     // plan_here: the workgroup with a unit's first tile tells the join how many
     // workgroups share it
-    if (p.plan_units > 0 && t0 == 0 && threadIdx.x == 0) {
-      int32_t parts = 1;
-      if (t1 < tiles)
-        parts += (int32_t)((at + unit_cost(nt) + tiles - 1) / quota - (at + unit_cost(nt)) / quota);
-      p.splits[b * p.plan_units + ub] = AttendSplit{b, ub, (int32_t)blockIdx.x, parts};
-    }
+    if (p.plan_units > 0 && t0 == 0 && threadIdx.x == 0)
+      p.splits[b * p.plan_units + ub] = AttendSplit{b, ub, (int32_t)blockIdx.x, t1 < tiles ? parts : 1};
+  }
+  __device__ __forceinline__ void take_slot(const AttendParams& p) {
+    int32_t none = 0;
+    const SlotTokens c = slot_tokens(p, b, &none);
+    s = SlotTokens{uniform(c.first), uniform(c.n), uniform(c.pos)};
   }
   __device__ __forceinline__ bool begin(const AttendParams& p, int qt, int nt) {
-    int32_t none = 0;
     if (p.plan_units > 0) {
       if (!plan_here(p, qt, nt)) return false;
     } else {
       const AttendStart st = p.starts[blockIdx.x], en = p.starts[blockIdx.x + 1];
       b = uniform(st.slot), ub = uniform(st.unit), t0 = uniform(st.tile);
       eb = uniform(en.slot), eub = uniform(en.unit), et = uniform(en.tile);
+      if (b < p.num_slots) take_slot(p);
     }
     if (b >= p.num_slots || (b == eb && ub == eub && t0 == et)) return false;
-    s = slot_tokens(p, b, &none);
     piece(p, qt, nt);
     return true;
   }
-  // The plan without a launch of its own, for few units that each workgroup
-  // can sum by itself (plan_units units in every active slot): a share of the
-  // slots per thread, a prefix sum of their costs, and the two threads whose
-  // slots hold this workgroup's start and end write them down.
+  // The plan without a launch of its own, for few units: each wave sums all of
+  // them for itself (plan_units places in every slot, those of a share of
+  // consecutive ones per lane), and the lanes whose places hold this
+  // workgroup's start and end say so.
   __device__ __forceinline__ bool plan_here(const AttendParams& p, int qt, int nt) {
-    __shared__ int64_t buf[kAttendBlock / kLanes];
-    __shared__ AttendStart ends[2];
-    __shared__ int64_t before;
-    const int tid = threadIdx.x, lane = lane_id(), wave = tid >> 6, U = p.plan_units;
-    const int per = (p.num_slots + kAttendBlock - 1) / kAttendBlock;
-    const int ba = min(p.num_slots, tid * per), bz = min(p.num_slots, ba + per);
-    int32_t bad = 0;
+    constexpr int kShare = kAttendPlanUnits / kLanes;
+    int lane = lane_id();
+    asm volatile("" : "+v"(lane));            // nothing of the plan is kept over the tiles
+    const int U = p.plan_units, N = p.num_slots * U, per = (N + kLanes - 1) / kLanes;
+    const bool first = blockIdx.x == 0 && threadIdx.x < kLanes;
+    SlotTokens c[kShare];
+    int32_t cost[kShare], slot[kShare], unit[kShare], bad = 0;
     int64_t mine = 0;
-    for (int i = ba; i < bz; ++i) {
-      const SlotTokens c = slot_tokens(p, i, &bad);
-      for (int k = 0; k < U; ++k) {
-        if (c.n > 0) mine += unit_tiles(unit_rows(p, c, k * qt, qt), nt) + unit_cost(nt);
-        else if (blockIdx.x == 0) p.splits[i * U + k] = AttendSplit{i, k, 0, 0};
-      }
-    }
-    if (bad != 0 && blockIdx.x == 0 && p.status != nullptr) atomicOr(p.status, bad);
-    int64_t x = mine;
+    slot[0] = (int32_t)udiv_magic((uint32_t)(lane * per), p.plan_div.m, p.plan_div.sh1, p.plan_div.sh2);
+    unit[0] = lane * per - slot[0] * U;
 #pragma unroll
-    for (int d = 1; d < kLanes; d <<= 1) {
+    for (int j = 0; j < kShare; ++j) {
+      if (j > 0) {
+        const bool wrap = unit[j - 1] + 1 == U;
+        slot[j] = slot[j - 1] + (wrap ? 1 : 0);
+        unit[j] = wrap ? 0 : unit[j - 1] + 1;
+      }
+      const bool in = j < per && slot[j] < p.num_slots;
+      c[j] = slot_tokens(p, min(slot[j], p.num_slots - 1), &bad);
+      const bool has = in && unit[j] < units_of(p, c[j].n, qt);
+      cost[j] = has ? unit_tiles(unit_rows(p, c[j], unit[j] * qt, qt), nt) + unit_cost(nt) : 0;
+      mine += cost[j];
+      if (first && in && !has) p.splits[slot[j] * U + unit[j]] = AttendSplit{slot[j], unit[j], 0, 0};
+    }
+    if (bad != 0 && first && p.status != nullptr) atomicOr(p.status, bad);
+    int64_t x = mine;
+    for (int d = 1; d * per < N; d <<= 1) {
       const int64_t y = __shfl_up(x, d);
       if (lane >= d) x += y;
     }
-    if (lane == kLanes - 1) buf[wave] = x;
-    if (tid < 2) ends[tid] = AttendStart{p.num_slots, 0, 0, 0};
-    __syncthreads();
-    int64_t total = 0;
-    for (int i = 0; i < kAttendBlock / kLanes; ++i) {
-      if (i == wave) x += total;
-      total += buf[i];
-    }
-    quota = max((total + kAttendGrid - 1) / kAttendGrid, (int64_t)(kAttendLeastRows / nt));
-    int64_t c = x - mine;
+    auto lane64 = [](int64_t v, int l) {
+      return (int64_t)((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int32_t)(v >> 32), l) << 32 |
+                       (uint32_t)__builtin_amdgcn_readlane((int32_t)v, l));
+    };
+    const int64_t total = lane64(x, (N - 1) / per);
+    const int64_t quota = max((total + kAttendGrid - 1) / kAttendGrid, (int64_t)(kAttendLeastRows / nt));
     const int64_t goal0 = blockIdx.x * quota, goal1 = goal0 + quota;
     if (goal0 >= total) return false;
-    if (mine > 0 && goal1 >= c && goal0 < c + mine) {
-      for (int i = ba; i < bz; ++i) {
-        const SlotTokens sl = slot_tokens(p, i, &bad);
-        for (int k = 0; k < U && sl.n > 0; ++k) {
-          const int64_t end = c + unit_cost(nt) + unit_tiles(unit_rows(p, sl, k * qt, qt), nt);
-          if (goal0 >= c && goal0 < end) {
-            ends[0] = AttendStart{i, k, (int32_t)max(goal0 - c - unit_cost(nt), (int64_t)0), 0};
-            before = c;
-          }
-          if (goal1 >= c && goal1 < end)
-            ends[1] = AttendStart{i, k, (int32_t)max(goal1 - c - unit_cost(nt), (int64_t)0), 0};
-          c = end;
-        }
+    bool h0 = false, h1 = false;
+    int32_t b0 = 0, u0 = 0, x0 = 0, b1 = 0, u1 = 0, x1 = 0;
+    int64_t k = x - mine, last = 0;
+    SlotTokens c0{};
+#pragma unroll
+    for (int j = 0; j < kShare; ++j) {
+      const int64_t end = k + cost[j];
+      if (goal0 >= k && goal0 < end) {
+        h0 = true, b0 = slot[j], u0 = unit[j], c0 = c[j];
+        x0 = (int32_t)max(goal0 - k - unit_cost(nt), (int64_t)0);
       }
+      if (goal1 >= k && goal1 < end) {
+        h1 = true, b1 = slot[j], u1 = unit[j], last = end - 1;
+        x1 = (int32_t)max(goal1 - k - unit_cost(nt), (int64_t)0);
+      }
+      k = end;
     }
-    __syncthreads();
-    b = uniform(ends[0].slot), ub = uniform(ends[0].unit), t0 = uniform(ends[0].tile);
-    eb = uniform(ends[1].slot), eub = uniform(ends[1].unit), et = uniform(ends[1].tile);
-    at = uniform64(before);
+    const int l0 = __builtin_ctzll(__ballot(h0));
+    b = __builtin_amdgcn_readlane(b0, l0), ub = __builtin_amdgcn_readlane(u0, l0);
+    t0 = __builtin_amdgcn_readlane(x0, l0);
+    s.first = __builtin_amdgcn_readlane(c0.first, l0), s.n = __builtin_amdgcn_readlane(c0.n, l0);
+    s.pos = __builtin_amdgcn_readlane(c0.pos, l0);
+    const uint64_t m1 = __ballot(h1);
+    const int l1 = m1 != 0 ? __builtin_ctzll(m1) : 0;
+    eb = uniform(m1 != 0 ? __builtin_amdgcn_readlane(b1, l1) : p.num_slots);
+    eub = uniform(m1 != 0 ? __builtin_amdgcn_readlane(u1, l1) : 0);
+    et = uniform(m1 != 0 ? __builtin_amdgcn_readlane(x1, l1) : 0);
+    // (its last tile lies with workgroup last / quota)
+    const uint64_t z = lane64(last, l1);
+    parts = uniform(1 - (int32_t)blockIdx.x +
+                    (int32_t)(z >> 32 == 0 ? (uint32_t)z / (uint32_t)quota : z / (uint64_t)quota));
     return true;
   }
   __device__ __forceinline__ bool next(const AttendParams& p, int qt, int nt) {
     if (b == eb && ub == eub) return false;
-    at += unit_cost(nt) + tiles;
     t0 = 0;
     ++ub;
     if ((int64_t)ub * qt >= (int64_t)s.n * p.heads) {
@@ -565,7 +580,7 @@ struct Walk {
           break;
         }
       }
-      s = slot_tokens(p, b, &none);
+      take_slot(p);
     }
     if (b == eb && ub == eub && et == 0) return false;
     piece(p, qt, nt);
@@ -1414,44 +1429,63 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendParams p, int qt
   // part k lies with workgroup wg0 + k: its second place for the first part
   // (which began at the unit's first tile), its first place for the others
   auto place = [&](int k) -> int64_t { return ((int64_t)(sp.wg0 + k) * 2 + (k == 0 ? 1 : 0)) * qt; };
-  // over the 32 threads of a query
-  auto reduce = [&](float v, int slot, bool maximum) {
-#pragma unroll
-    for (int d = 8; d < kLanes; d <<= 1) {
-      const float y = __shfl_xor(v, d);
-      v = maximum ? fmaxf(v, y) : v + y;
-    }
-    if ((threadIdx.x & 63) < 8) red[slot][wave][q8] = v;
-    __syncthreads();
-    float r = red[slot][0][q8];
-#pragma unroll
-    for (int w = 1; w < 4; ++w) r = maximum ? fmaxf(r, red[slot][w][q8]) : r + red[slot][w][q8];
-    return r;
-  };
-  float mx = kNegInf;
-  for (int k = piece; k < sp.parts; k += 32) mx = fmaxf(mx, p.part_ml[place(k) + qi].x);
-  mx = reduce(mx, 0, true);
-  float sum = 0.0f, rsum = 0.0f;
-  for (int k = piece; k < sp.parts; k += 32) {
-    const float4 v = p.part_ml[place(k) + qi];
-    const float e = v.x == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(v.x - mx);
-    weight[k][q8] = e;
-    sum += v.y * e;
-    rsum += v.z * e;
-  }
-  sum = reduce(sum, 1, false);
-  rsum = reduce(rsum, 2, false);              // (its barrier covers weight)
+  // The first parts' sums are asked for at once, and all their statistics.
   // piece = dim block * 8 + quad * 2 + half, as the parts are laid out
+  constexpr int P = 8;
   const int x = qi >> 5, ql = qi & 31, w = blockIdx.z;
   const float* const src = p.part_o + (x * 16 + (piece >> 1)) * 1024 + 256 * w + ((piece & 1) * 32 + ql) * 4;
-  f32x4 a = {};
-#pragma unroll 8
-  for (int k = 0; k < sp.parts; ++k) {
-    const f32x4 v = *(const f32x4*)(src + place(k) * kDim);
-    const float e = weight[k][q8];
+  float4 ml[kAttendGrid / 32];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) a[i] = __builtin_fmaf(v[i], e, a[i]);
+  for (int i = 0; i < kAttendGrid / 32; ++i) {
+    const int k = piece + 32 * i;
+    ml[i] = make_float4(kNegInf, 0.0f, 0.0f, 0.0f);
+    if (k < sp.parts) ml[i] = p.part_ml[place(k) + qi];
   }
+  f32x4 v[P];
+#pragma unroll
+  for (int i = 0; i < P; ++i) v[i] = *(const f32x4*)(src + place(min(i, sp.parts - 1)) * kDim);
+  // over the 8 lanes of a query in each wave, then over the waves
+  auto spread = [&](float y, int slot, auto op) {
+#pragma unroll
+    for (int d = 8; d < kLanes; d <<= 1) y = op(y, __shfl_xor(y, d));
+    if ((threadIdx.x & 63) < 8) red[slot][wave][q8] = y;
+  };
+  auto gathered = [&](int slot, auto op) {
+    return op(op(red[slot][0][q8], red[slot][1][q8]), op(red[slot][2][q8], red[slot][3][q8]));
+  };
+  auto larger = [](float y, float z) { return fmaxf(y, z); };
+  auto plus = [](float y, float z) { return y + z; };
+  float mx = kNegInf;
+#pragma unroll
+  for (int i = 0; i < kAttendGrid / 32; ++i) mx = fmaxf(mx, ml[i].x);
+  spread(mx, 0, larger);
+  __syncthreads();
+  mx = gathered(0, larger);
+  float sum = 0.0f, rsum = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kAttendGrid / 32; ++i) {
+    const int k = piece + 32 * i;
+    if (k >= sp.parts) break;
+    const float e = ml[i].x == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(ml[i].x - mx);
+    weight[k][q8] = e;
+    sum += ml[i].y * e;
+    rsum += ml[i].z * e;
+  }
+  spread(sum, 1, plus);
+  spread(rsum, 2, plus);
+  __syncthreads();
+  sum = gathered(1, plus);
+  rsum = gathered(2, plus);
+  f32x4 a = {};
+  auto add = [&](const f32x4& y, float e) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) a[i] = __builtin_fmaf(y[i], e, a[i]);
+  };
+#pragma unroll
+  for (int i = 0; i < P; ++i)
+    if (i < sp.parts) add(v[i], weight[i][q8]);
+#pragma unroll 8
+  for (int k = P; k < sp.parts; ++k) add(*(const f32x4*)(src + place(k) * kDim), weight[k][q8]);
   const int32_t m = m0 + q8;
   if (m >= s.n * p.heads) return;
   const int32_t tok = (int32_t)udiv_magic((uint32_t)m, p.head_div.m, p.head_div.sh1, p.head_div.sh2);

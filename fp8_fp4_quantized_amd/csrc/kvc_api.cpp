@@ -176,9 +176,11 @@ int attend(const kvc_attend_args* a, bool tree, void* stream, const char* who) {
   int qblocks = attend_qblocks(a->num_slots, tokens, a->num_heads);
   if (a->cache.page_size < 8 && qblocks == 4) qblocks = 2;   // the wide kernel's pages hold 8 rows or more
   p.units_max = tokens * a->num_heads / (32 * qblocks) + a->num_slots;
-  if (tree) {
-    const int64_t units = ((int64_t)a->draft_len * a->num_heads + 32 * qblocks - 1) / (32 * qblocks);
-    if (units <= 8 && units * a->num_slots <= kvc::kAttendPlanUnits) p.plan_units = (int32_t)units;
+  const int64_t units =
+      ((tree ? a->draft_len : tokens) * a->num_heads + 32 * qblocks - 1) / (32 * qblocks);
+  if (units * a->num_slots <= kvc::kAttendPlanUnits) {
+    p.plan_units = (int32_t)units;
+    p.plan_div = kvc::div_magic((uint32_t)units);
   }
   uint8_t* w = static_cast<uint8_t*>(a->workspace);
   p.head = reinterpret_cast<kvc::AttendHead*>(w + at[0]);

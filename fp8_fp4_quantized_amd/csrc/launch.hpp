@@ -160,7 +160,7 @@ constexpr int kAttendUnitRows = 320;
 // Most units of a call whose workgroups plan for themselves (no launch for
 // the plan): beyond, the sums over them cost each workgroup more than the
 // launch.
-constexpr int kAttendPlanUnits = 1024;
+constexpr int kAttendPlanUnits = 256;
 
 struct AttendHead {            // written by the plan
   int32_t nsplit;              // units cut between workgroups
@@ -198,7 +198,8 @@ struct AttendParams {
   float* lse;                  // nullable
   int32_t* status;
   int64_t units_max;           // units the call can have at the most
-  int32_t plan_units;          // > 0: units per slot, and every workgroup plans for itself
+  int32_t plan_units;          // > 0: most units of a slot, and every workgroup plans for itself
+  DivMagic plan_div;           // division by plan_units
   // workspace
   AttendHead* head;
   AttendStart* starts;         // [kAttendWorkgroups + 1]
