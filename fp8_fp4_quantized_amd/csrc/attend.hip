@@ -7,13 +7,24 @@
 // and one staged tile of rows serves both products.
 //
 // The queries of a slot are its (token, head) pairs in that order, cut into
-// units of QT = 32 QB; a unit's rows are cut into tiles of NT = 128 / QB.
-// Three launches: attend_plan_kernel deals the tiles of all units evenly to
-// the workgroups of attend_kernel (one per compute unit, each a run of
-// consecutive tiles, crossing units as it comes), and attend_join_kernel
-// joins the units that were cut between workgroups.  The split follows the
-// lengths on the device, so a captured call adapts to refreshed lengths, and
-// it is a function of the lengths alone, so results repeat bit for bit.
+// units of QT = 32 QB; a unit's rows are cut into tiles of NT = 128 / QB.  The
+// tiles of all units are dealt evenly to the workgroups of attend_kernel (one
+// per compute unit, each a run of consecutive tiles, crossing units as it
+// comes) by attend_plan_kernel, or for few units by each workgroup itself, and
+// attend_join_kernel joins the units that were cut between workgroups.  The
+// split follows the lengths on the device, so a captured call adapts to
+// refreshed lengths, and it is a function of the lengths alone, so results
+// repeat bit for bit.
+//
+// What bounds it: a tile costs 2 * 2 * QT * NT * 512 flops and NT rows of 528
+// (V41), 288 (V41_FP4) or 584 (V4) bytes, so from 64 queries a unit up the
+// matrix units bound it (about 1.5 PFLOP/s: the clock falls to 1.6 GHz under
+// them) before HBM does; below, HBM.  What it reaches, in visible (query, row)
+// pairs * 2048 flops: 1.07 PFLOP/s on a prompt of 8,192 tokens with 128 heads
+// (V41, 8.2 ms), 0.68 on 16 prompts of some 2,000 tokens with 32 heads (V41_FP4,
+// 16 tiles a unit on average, 1.5 ms), 0.61 on 64 decodes with 64 heads
+// (V41_FP4, 124 us), 2.7 TB/s and 0.57 PFLOP/s on 128 chains of 4 with 16 heads
+// (V4, 127 us).
 #include <type_traits>
 
 #include "launch.hpp"
@@ -87,7 +98,8 @@ __device__ __forceinline__ int32_t unit_cost(int nt) { return kAttendUnitRows / 
 // ------------------------------------------------------------------ plan
 // One workgroup: a prefix sum of the slots' units, then each thread walks an
 // equal share of the units twice, to sum their tiles and to place the
-// boundaries between the workgroups of attend_kernel.
+// boundaries between the workgroups of attend_kernel.  Latency: 6 us for 32
+// units.
 __device__ __forceinline__ int64_t plan_excl_scan(int64_t v, int64_t* buf, int64_t* total) {
   const int lane = lane_id(), wave = threadIdx.x >> 6;
   int64_t x = v;
@@ -424,18 +436,6 @@ __device__ __forceinline__ void zero_not_finite(lds_ptr tile) {
   }
 }
 
-// The reference maximum moves only when it is passed by 8 (in log2): weights
-// up to 2^8 lose nothing in fp32, and O is rescaled rarely.  Returns the
-// factor for what was summed before.
-__device__ __forceinline__ float raise_max(Query& q, float tile_max) {
-  const float old = q.mx;
-  if (tile_max > old + 8.0f) q.mx = tile_max;
-  const float alpha = q.mx == old ? 1.0f : __builtin_amdgcn_exp2f(old - q.mx);
-  q.sum *= alpha;
-  q.rsum *= alpha;
-  return alpha;
-}
-
 // Out and lse factors of a query from its complete sums (or, with a cut unit,
 // the joined ones)
 struct Final {
@@ -711,12 +711,21 @@ __device__ __forceinline__ void end_piece(const AttendParams& p, const Walk& w, 
 //
 // This is the kernel for units of 32 (QB = 1) and 64 queries; a query's rows
 // are spread over NB waves, which agree on its reference maximum a tile late:
-// a tile's weights are taken against the maximum of the tiles before it, and
-// only where a score passes that by more than 16 (in log2; always in a piece's
-// first tile) are they taken again, after the waves have compared.  Two
-// barriers a tile then (QB = 1: three).  QB = 2 has two tile buffers and
-// expands the next tile between the score products; the 128-row tiles of
-// QB = 1 leave room for one.
+// a tile's weights are taken against the maximum of the tiles before it (which
+// moves only when it is passed by 8 in log2: weights up to 2^8 lose nothing in
+// fp32, and O is rescaled rarely), and only where a score passes that by more
+// than 16 (always in a piece's first tile) are they taken again, after the waves
+// have compared.  Two barriers a tile then (QB = 1: three).  QB = 2 has two tile
+// buffers and expands the next tile between the products of this one; the
+// 128-row tiles of QB = 1 leave room for one.
+//
+// A wave is alone on its SIMD (O, the queries' fragments and the rows in flight
+// take its 512 registers), so its issue slots are what it runs out of: on 64
+// decodes with 64 heads over V41_FP4 rows it issues in 53% of its cycles, of
+// which 34% are vector instructions (the expansion of the rows for the most),
+// and the matrix units work in 28%.  Deeper read-ahead of the tiles' fragments
+// (8 instead of 6 for the scores, 5 instead of 3 for O) measured slower: 127 and
+// 131 against 125.5 us.
 //
 // RUN: pages of 8 rows or more, so that an 8-row group lies in one page; smaller
 // pages look up every row.
@@ -1047,6 +1056,12 @@ void attend_kernel(AttendParams p) {
 // products, the softmax of this tile between the O products of the previous
 // one.  That takes three tile buffers and two of weights, and one barrier a
 // tile.  Pages of 8 rows or more.
+//
+// On a prompt of 8,192 tokens with 128 heads (V41) the matrix units work in
+// half of the cycles (64 products of 32 cycles in a tile's 4,000 or so), at 1.07
+// PFLOP/s.  The registers are full: a value more that lives over the tiles, or
+// accumulators that leave the matrix registers all at once, spills inside the
+// loop and cost 10% (9.2 against 8.2 ms).
 template <int L>
 __global__ __launch_bounds__(kAttendBlock) __attribute__((amdgpu_waves_per_eu(1, 1)))
 void attend_wide_kernel(AttendParams p) {
@@ -1291,7 +1306,8 @@ void attend_wide_kernel(AttendParams p) {
       }
       if (step == 7) tm = max3(tm, swapped, swapped) * c2;
       if (step == 8) {
-        // (raise_max, in pieces)
+        // the reference maximum moves only when it is passed by 8 (in log2): weights
+        // up to 2^8 lose nothing in fp32, and O is rescaled rarely
         alpha = q.mx;
         q.mx = tm > q.mx + 8.0f ? tm : q.mx;
       }
@@ -1413,7 +1429,9 @@ void attend_wide_kernel(AttendParams p) {
 // One workgroup per 8 queries and 128 dims (the dims of one wave) of a unit
 // that was cut, 8 threads of neighbouring queries on 128 bytes of a part: the
 // parts' weights against the common maximum into LDS, then the weighted sum of
-// the parts, four dims a thread.
+// the parts, four dims a thread.  Bound by the partial sums, 2 KB a query and
+// part, that it reads: 256 parts of 64 queries, 33 MB, take 14 us (2.4 TB/s);
+// 8 parts of 32 queries 4 us, which is latency.
 __global__ __launch_bounds__(256) void attend_join_kernel(AttendParams p, int qt) {
   __shared__ float weight[kAttendGrid][8];
   __shared__ float red[3][4][8];

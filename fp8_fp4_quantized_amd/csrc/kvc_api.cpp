@@ -85,7 +85,9 @@ bool page_size_ok(int32_t ps) { return ps >= 1 && ps <= 4096 && (ps & (ps - 1)) 
 
 // 32-query blocks per unit of the attention.  A unit's wider tiles cost fewer
 // reads of the staged rows per query, a wide unit half full costs its empty
-// half: slots of up to 32 or 64 queries take units of that size.
+// half: slots of up to 32 or 64 queries take units of that size.  Measured, a
+// token of 64 requests over V41_FP4 rows: 64 heads 123 us in units of 64, 172 in
+// units of 128; 32 heads 104 us in units of 32, 124 in units of 64.
 int attend_qblocks(int32_t slots, int64_t tokens, int32_t heads) {
   const int64_t per_slot = tokens * heads / (slots > 0 ? slots : 1);
   return per_slot <= 32 ? 1 : per_slot <= 64 ? 2 : 4;

@@ -427,6 +427,55 @@ def test_long_ragged_batch_cut_everywhere(kvc):
                   f"slot {b}")
 
 
+# at and past the units up to which workgroups plan for themselves
+@pytest.mark.parametrize("S,D,H", [(256, 1, 16), (257, 1, 40), (64, 4, 128), (65, 4, 128), (1, 64, 513)])
+def test_batches_around_the_planning_limit(kvc, S, D, H):
+    rng = random.Random(S + H)
+    starts = [rng.choice((-1, 0, 1, 62, 63, rng.randint(2, 150))) for _ in range(S)]
+    starts[0] = 150
+    f = Filled(kvc, "V41", 64, [max(0, s + D) if s >= 0 else 0 for s in starts], S)
+    q = queries(S * D, H, S)
+    out = torch.full((S * D, H, 512), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((S * D, H), 7.0, device="cuda")
+    kvc.kvc_attend_tree(f.cache, q.cuda(), torch.tensor(starts, dtype=torch.int32).cuda(),
+                        dev(f.table), out, scale=SCALE, draft_len=D, lse=lse)
+    out, lse = out.cpu(), lse.cpu()
+    for b, s in enumerate(starts):
+        t = slice(b * D, b * D + D)
+        if s < 0:
+            assert (out[t] == 7.0).all() and (lse[t] == 7.0).all()
+            continue
+        rows, _ = f.rows(b, s + D)
+        ref.check(out[t], lse[t], ref.attend(q[t].double(), rows, prefill_seen(s, D, 1, s + D), SCALE),
+                  f"slot {b}")
+
+
+@pytest.mark.parametrize("S,H,most", [(70, 100, 9), (200, 8, 3), (3, 16, 400)])
+def test_packed_batches_of_many_prompts(kvc, S, H, most):
+    rng = random.Random(S + H)
+    slots = [(rng.randint(0, 90), rng.choice((0, 1, rng.randint(0, most)))) for _ in range(S)]
+    slots[-1] = (17, most)
+    counts = [s + n for s, n in slots]
+    f = Filled(kvc, "V41_FP4", 32, counts, S)
+    T = sum(n for _, n in slots) + 5                     # and padded rows
+    q = queries(T, H, S)
+    first = np.cumsum([0] + [n for _, n in slots])[:-1]
+    off = torch.tensor(np.array([first, [n for _, n in slots]]), dtype=torch.int32).cuda()
+    out = torch.full((T, H, 512), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((T, H), 7.0, device="cuda")
+    kvc.kvc_attend_prefill(f.cache, q.cuda(), off, torch.tensor([s for s, _ in slots], dtype=torch.int32).cuda(),
+                           dev(f.table), out, scale=SCALE, lse=lse)
+    out, lse = out.cpu(), lse.cpu()
+    for b, (s, n) in enumerate(slots):
+        if n == 0:
+            continue
+        rows, _ = f.rows(b, s + n)
+        t = slice(int(first[b]), int(first[b]) + n)
+        ref.check(out[t], lse[t], ref.attend(q[t].double(), rows, prefill_seen(s, n, 1, s + n), SCALE),
+                  f"slot {b}")
+    assert (out[T - 5:] == 7.0).all() and (lse[T - 5:] == 7.0).all()
+
+
 def test_repeats_bit_for_bit_and_on_another_stream(kvc):
     starts = [1200, 30, 500]
     f = Filled(kvc, "V41", 64, [s + 4 for s in starts], 43)
