@@ -27,7 +27,7 @@
 // (V4, 127 us).
 #include <type_traits>
 
-#include "launch.hpp"
+#include "launch_attend.hpp"
 #include "row_ops.hpp"
 
 namespace kvc {

@@ -12,7 +12,7 @@
 #include <cstring>
 #include <string>
 
-#include "launch.hpp"
+#include "launch_attend.hpp"
 
 namespace {
 

@@ -82,7 +82,6 @@ enum : int32_t {
   kStPosRange = 16,
   kStReqRange = 32,
   kStTokenRange = 64,
-  kStNoPage = 128,
 };
 
 }  // namespace kvc

@@ -13,7 +13,7 @@
 // It is latency: two dependent loads, a scan and two more take 5 to 6 us for
 // 1,024 decodes as for 65,000 tokens of 300 requests; the bytes (0.8 MB there)
 // would take 0.2.
-#include "launch.hpp"
+#include "launch_attend.hpp"
 #include "layout.hpp"
 #include "wave.hpp"
 

@@ -8,7 +8,7 @@
 // in flight together; the grid strides over the rows.  The filter puts one
 // row of global ids on one wave.
 #include "launch.hpp"
-#include "row_load.hpp"
+#include "row_ops.hpp"
 
 namespace kvc {
 
@@ -214,15 +214,61 @@ template <int L, bool LARGE> constexpr int gather_unroll() { return LARGE && L !
 // workgroup of a large gather: 8 waves (0.6% faster than 4 on 262,144 V41
 // ids; 2 and 16 slower); a smaller gather keeps 4
 template <bool LARGE> constexpr int gather_block() { return LARGE ? 512 : kBlock; }
-// The codes' cache policy: a large gather reads each row once and loads them
-// non-temporally, so that the L2 keeps what the launch reads more than once --
-// the ids, the page-table entries and the scale lines (0.75 us faster on
-// 262,144 ids than cached loads); a small gather caches them, since the next
-// call may read the same rows again.
-template <bool LARGE> constexpr int gather_cpol() { return LARGE ? kCpolNtSc1 : kCpolSc1; }
 // most waves of a gather's grid (2^20 ids at 32 per batch); rows past them
 // take further turns
 constexpr int64_t kGatherMaxWaves = 32768;
+
+template <int L> struct LaneCodes;          // this lane's share of a row
+template <> struct LaneCodes<kV41> { uint2 codes; uint32_t scale; };
+template <> struct LaneCodes<kV41Fp4> { uint32_t codes; uint32_t scale; };
+template <> struct LaneCodes<kV4> { uint4 raw; uint32_t scale; };
+
+// Loads from the row's own base (the slot is the same on every lane).  A
+// row's scale part shares its cache line with the scale parts of the page's
+// other rows, so it is always a cached load (non-temporal: 6% slower on a
+// 262,144-id gather).  The codes take CPOL: a large gather reads each row
+// once and loads them non-temporally, so that the L2 keeps what the launch
+// reads more than once -- the ids, the page-table entries and the scale
+// lines (0.75 us faster on 262,144 ids than cached loads); a small gather
+// caches them, since the next call may read the same rows again.
+template <int L, int CPOL>
+__device__ __forceinline__ LaneCodes<L> load_lane(const PagedKV<L>& kv, int64_t slot, int lane) {
+  LaneCodes<L> r;
+  if constexpr (L == kV41) {
+    r.codes = ld_u2_buf<CPOL>(kv.data(slot), 8u * lane);
+    r.scale = ld_u8_dev(kv.scale(slot), (uint32_t)lane >> 2);
+  } else if constexpr (L == kV41Fp4) {
+    r.codes = ld_u32_buf<CPOL>(kv.data(slot), 4u * lane);
+    r.scale = ld_u8_dev(kv.scale(slot), (uint32_t)lane >> 1);
+  } else {
+    const uint8_t* d = kv.data(slot);
+    if (lane < kRopeLane0) {
+      const uint2 c = ld_u2_buf<CPOL>(d, 8u * lane);
+      r.raw = make_uint4(c.x, c.y, 0u, 0u);
+      r.scale = ld_u8_dev(kv.scale(slot), (uint32_t)lane >> 3);
+    } else {
+      r.raw = ld_u4_buf<CPOL>(d, kNope + 16u * (lane - kRopeLane0));
+      r.scale = 0;
+    }
+  }
+  return r;
+}
+
+template <int L>
+__device__ __forceinline__ uint4 decode_lane(const LaneCodes<L>& c, int lane);
+template <>
+__device__ __forceinline__ uint4 decode_lane<kV41>(const LaneCodes<kV41>& c, int) {
+  return dq_fp8x8(c.codes, c.scale);
+}
+template <>
+__device__ __forceinline__ uint4 decode_lane<kV41Fp4>(const LaneCodes<kV41Fp4>& c, int) {
+  return dq_fp4x8(c.codes, c.scale);
+}
+template <>
+__device__ __forceinline__ uint4 decode_lane<kV4>(const LaneCodes<kV4>& c, int lane) {
+  if (lane >= kRopeLane0) return c.raw;
+  return dq_fp8x8(make_uint2(c.raw.x, c.raw.y), c.scale);
+}
 
 // A wave takes the rows of the gather p.batch at a time: lane i reads id i
 // of the batch and resolves it to a physical slot (one vector load of ids,
@@ -237,7 +283,7 @@ constexpr int64_t kGatherMaxWaves = 32768;
 template <int L, bool LARGE>
 __global__ __launch_bounds__(gather_block<LARGE>()) __attribute__((amdgpu_waves_per_eu(8, 8)))
 void dequant_gather_kernel(GatherParams p) {
-  constexpr int CPOL = gather_cpol<LARGE>();
+  constexpr int CPOL = LARGE ? kCpolNtSc1 : kCpolSc1;
   constexpr int kWaves = gather_block<LARGE>() / kLanes;
   const PagedKV<L> kv = paged<L>(p.cache);
   const int lane = lane_id();
