@@ -99,7 +99,7 @@ __device__ __forceinline__ int32_t unit_cost(int nt) { return kAttendUnitRows / 
 // One workgroup: a prefix sum of the slots' units, then each thread walks an
 // equal share of the units twice, to sum their tiles and to place the
 // boundaries between the workgroups of attend_kernel.  Latency: 6 us for 32
-// units.
+// units, 16 to 18 for 8,192.
 __device__ __forceinline__ int64_t plan_excl_scan(int64_t v, int64_t* buf, int64_t* total) {
   const int lane = lane_id(), wave = threadIdx.x >> 6;
   int64_t x = v;
@@ -1430,7 +1430,7 @@ void attend_wide_kernel(AttendParams p) {
 // that was cut, 8 threads of neighbouring queries on 128 bytes of a part: the
 // parts' weights against the common maximum into LDS, then the weighted sum of
 // the parts, four dims a thread.  Bound by the partial sums, 2 KB a query and
-// part, that it reads: 256 parts of 64 queries, 33 MB, take 14 us (2.4 TB/s);
+// part, that it reads: some 260 parts of 64 queries, 34 MB, take 11 to 14 us;
 // 8 parts of 32 queries 4 us, which is latency.
 __global__ __launch_bounds__(256) void attend_join_kernel(AttendParams p, int qt) {
   __shared__ float weight[kAttendGrid][8];

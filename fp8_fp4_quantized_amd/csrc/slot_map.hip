@@ -10,8 +10,8 @@
 // page of a token that falls on a page taken in this call is looked up in
 // the free list, not in the page table.
 //
-// It is latency: two dependent loads, a scan and two more take 5 to 6 us for
-// 1,024 decodes as for 65,000 tokens of 300 requests; the bytes (0.8 MB there)
+// It is latency: two dependent loads, a scan and two more take 5.4 to 6.5 us for
+// 1,024 decodes as for the 60,000 tokens of 300 requests; the bytes (0.8 MB there)
 // would take 0.2.
 #include "launch_attend.hpp"
 #include "layout.hpp"
