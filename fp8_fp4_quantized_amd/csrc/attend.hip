@@ -1426,12 +1426,15 @@ void attend_wide_kernel(AttendParams p) {
 }
 
 // ------------------------------------------------------------------ join
-// One workgroup per 8 queries and 128 dims (the dims of one wave) of a unit
+// One workgroup per 8 queries and 256 dims (the dims of two waves) of a unit
 // that was cut, 8 threads of neighbouring queries on 128 bytes of a part: the
 // parts' weights against the common maximum into LDS, then the weighted sum of
-// the parts, four dims a thread.  Bound by the partial sums, 2 KB a query and
-// part, that it reads: some 260 parts of 64 queries, 34 MB, take 11 to 14 us;
-// 8 parts of 32 queries 4 us, which is latency.
+// the parts, four dims of each wave a thread.  Bound by the partial sums, 2 KB a
+// query and part, that it reads: some 260 parts of 64 queries, 34 MB, take 10 to
+// 12 us; 8 parts of 32 queries 4 us, which is latency.  (128 dims a workgroup: 128
+// chains of 4 128.5 instead of 125.2 us in all, one decode 21.3 instead of 21.6;
+// 512: 126.7 and 22.0.)
+constexpr int kJoinWaves = 2;
 __global__ __launch_bounds__(256) void attend_join_kernel(AttendParams p, int qt) {
   __shared__ float weight[kAttendGrid][8];
   __shared__ float red[3][4][8];
@@ -1449,9 +1452,9 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendParams p, int qt
   auto place = [&](int k) -> int64_t { return ((int64_t)(sp.wg0 + k) * 2 + (k == 0 ? 1 : 0)) * qt; };
   // The first parts' sums are asked for at once, and all their statistics.
   // piece = dim block * 8 + quad * 2 + half, as the parts are laid out
-  constexpr int P = 8;
-  const int x = qi >> 5, ql = qi & 31, w = blockIdx.z;
-  const float* const src = p.part_o + (x * 16 + (piece >> 1)) * 1024 + 256 * w + ((piece & 1) * 32 + ql) * 4;
+  constexpr int P = 4, W = kJoinWaves;
+  const int x = qi >> 5, ql = qi & 31, w0 = blockIdx.z * W;
+  const float* const src = p.part_o + (x * 16 + (piece >> 1)) * 1024 + 256 * w0 + ((piece & 1) * 32 + ql) * 4;
   float4 ml[kAttendGrid / 32];
 #pragma unroll
   for (int i = 0; i < kAttendGrid / 32; ++i) {
@@ -1459,9 +1462,13 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendParams p, int qt
     ml[i] = make_float4(kNegInf, 0.0f, 0.0f, 0.0f);
     if (k < sp.parts) ml[i] = p.part_ml[place(k) + qi];
   }
-  f32x4 v[P];
+  f32x4 v[P][W];
 #pragma unroll
-  for (int i = 0; i < P; ++i) v[i] = *(const f32x4*)(src + place(min(i, sp.parts - 1)) * kDim);
+  for (int i = 0; i < P; ++i) {
+    const float* const part = src + place(min(i, sp.parts - 1)) * kDim;
+#pragma unroll
+    for (int w = 0; w < W; ++w) v[i][w] = *(const f32x4*)(part + 256 * w);
+  }
   // over the 8 lanes of a query in each wave, then over the waves
   auto spread = [&](float y, int slot, auto op) {
 #pragma unroll
@@ -1494,25 +1501,33 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendParams p, int qt
   __syncthreads();
   sum = gathered(1, plus);
   rsum = gathered(2, plus);
-  f32x4 a = {};
-  auto add = [&](const f32x4& y, float e) {
+  f32x4 a[W] = {};
+  auto add = [&](f32x4& to, const f32x4& y, float e) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) a[i] = __builtin_fmaf(y[i], e, a[i]);
+    for (int i = 0; i < 4; ++i) to[i] = __builtin_fmaf(y[i], e, to[i]);
   };
 #pragma unroll
   for (int i = 0; i < P; ++i)
-    if (i < sp.parts) add(v[i], weight[i][q8]);
-#pragma unroll 8
-  for (int k = P; k < sp.parts; ++k) add(*(const f32x4*)(src + place(k) * kDim), weight[k][q8]);
+    if (i < sp.parts)
+#pragma unroll
+      for (int w = 0; w < W; ++w) add(a[w], v[i][w], weight[i][q8]);
+#pragma unroll 4
+  for (int k = P; k < sp.parts; ++k) {
+    const float* const part = src + place(k) * kDim;
+#pragma unroll
+    for (int w = 0; w < W; ++w) add(a[w], *(const f32x4*)(part + 256 * w), weight[k][q8]);
+  }
   const int32_t m = m0 + q8;
   if (m >= s.n * p.heads) return;
   const int32_t tok = (int32_t)udiv_magic((uint32_t)m, p.head_div.m, p.head_div.sh1, p.head_div.sh2);
   const int32_t head = m - tok * p.heads;
   const Final fin = finish(p.sink != nullptr ? p.sink[head] * kLog2e : kNegInf, mx, sum, rsum);
   uint16_t* const op = p.out + (int64_t)(s.first + tok) * p.out_stride + (int64_t)head * p.out_hstride;
-  *(u32x2*)(op + 128 * w + 4 * piece) =
-      u32x2{pack_bf16(a[0] * fin.f, a[1] * fin.f), pack_bf16(a[2] * fin.f, a[3] * fin.f)};
-  if (p.lse != nullptr && w == 0 && piece == 0)
+#pragma unroll
+  for (int w = 0; w < W; ++w)
+    *(u32x2*)(op + 128 * (w0 + w) + 4 * piece) =
+        u32x2{pack_bf16(a[w][0] * fin.f, a[w][1] * fin.f), pack_bf16(a[w][2] * fin.f, a[w][3] * fin.f)};
+  if (p.lse != nullptr && w0 == 0 && piece == 0)
     p.lse[(int64_t)(s.first + tok) * p.heads + head] = fin.lse;
 }
 
@@ -1551,8 +1566,8 @@ hipError_t launch_attend(const AttendParams& p, int qblocks, hipStream_t stream)
   // one boundary between two workgroups
   const int64_t splits = p.plan_units > 0 ? (int64_t)p.num_slots * p.plan_units
                                           : min(p.units_max, (int64_t)kAttendGrid - 1);
-  hipLaunchKernelGGL(attend_join_kernel, dim3((unsigned)splits, (unsigned)(qt / 8), 4), dim3(256), 0,
-                     stream, p, qt);
+  hipLaunchKernelGGL(attend_join_kernel, dim3((unsigned)splits, (unsigned)(qt / 8), 4 / kJoinWaves),
+                     dim3(256), 0, stream, p, qt);
   return hipGetLastError();
 }
 
