@@ -992,6 +992,10 @@ void attend_kernel(AttendParams p) {
       auto raise = [&]() {
 #pragma unroll
         for (int x = 0; x < QB; ++x) {
+          if (tl == w.t0) {                   // (nothing is summed yet)
+            ref[x] = top[x];
+            continue;
+          }
           if (__ballot(top[x] > ref[x] + 8.0f) == 0) continue;
           const float old = ref[x];
           if (top[x] > old + 8.0f) ref[x] = top[x];
