@@ -150,7 +150,8 @@ def _ptr(t) -> int | None:
     return None if t is None else t.data_ptr()
 
 
-_I32_T = (torch.int32,)
+_INT32 = torch.int32
+_I32_T = (_INT32,)
 _F32_T = (torch.float32,)
 _B16_T = (torch.bfloat16, torch.int16, torch.uint16)
 
@@ -462,6 +463,20 @@ def _i32(t, n: int, name: str) -> int | None:
     return _dense(t, _I32_T, name)
 
 
+def _i32_on(t, n: int, name: str, index: int) -> int | None:
+    """``_i32`` of a tensor that must be on the device of that index."""
+    if t is None:
+        return None
+    # (get_device: one call for being on a device and on which; a slot map's
+    # kernel is as short as these checks)
+    if (t.dtype is _INT32 and t.get_device() == index and t.is_contiguous()
+            and (n == 0 or t.numel() >= n)):
+        return t.data_ptr()
+    if index >= 0:
+        _one_device(torch.device("cuda", index), ((name, t),))
+    return _i32(t, n, name)
+
+
 def _pt_stride(page_table) -> int:
     """Entries between page-table rows (of a single row: its width, whatever
     stride the tensor carries)."""
@@ -497,26 +512,27 @@ def kvc_slot_map(*, ratio: int, page_size: int, num_pages: int, lens: torch.Tens
     ``token_to_req [max_tokens]``, ``totals [4]`` that are given.
     ``max_tokens`` defaults to the smallest per-token output."""
     S = lens.numel()
-    per_token = (out_loc, positions, token_to_req, depth)
+    per = max_tokens
     if max_tokens is None:
-        max_tokens = min((t.numel() for t in per_token if t is not None), default=S * token_stride)
-    dev = lens.device
-    _one_device(dev, (("new_lens", new_lens), ("depth", depth), ("page_table", page_table),
-                      ("free_pages", free_pages), ("offsets", offsets), ("start_pos", start_pos),
-                      ("out_loc", out_loc), ("positions", positions),
-                      ("token_to_req", token_to_req), ("totals", totals), ("status", status)))
-    _need(page_table.dim() == 2 and page_table.shape[0] >= S,
-          f"page_table: shape {tuple(page_table.shape)}, need {S} rows")
-    a = kvc_slot_map_args(
-        ratio, page_size, num_pages, S, token_stride, _i32(lens, S, "lens"),
-        _i32(new_lens, S, "new_lens"), _i32(depth, max_tokens, "depth"),
-        _rows(page_table, _I32_T, "page_table"), _pt_stride(page_table), page_table.shape[1],
-        _i32(free_pages, 0, "free_pages"), free_pages.numel(), max_tokens,
-        _i32(offsets, 2 * S, "offsets"), _i32(start_pos, S, "start_pos"),
-        _i32(out_loc, max_tokens, "out_loc"), _i32(positions, max_tokens, "positions"),
-        _i32(token_to_req, max_tokens, "token_to_req"), _i32(totals, 4, "totals"),
-        _i32(status, 1, "status"))
-    _call_on(dev, stream, lib().kvc_slot_map, a)
+        max_tokens = min([t.numel() for t in (out_loc, positions, token_to_req, depth)
+                          if t is not None], default=S * token_stride)
+        per = 0                               # (no per-token tensor is shorter)
+    on = lens.get_device()
+    lens_p = _i32(lens, S, "lens")            # (refuses one that is on no device)
+    if page_table.get_device() != on:
+        _one_device(lens.device, (("page_table", page_table),))
+    table_p = _rows(page_table, _I32_T, "page_table")
+    rows, width = page_table.shape
+    _need(rows >= S, f"page_table: shape {tuple(page_table.shape)}, need {S} rows")
+    _call_on(lens.device, stream, lib().kvc_slot_map, kvc_slot_map_args(
+        ratio, page_size, num_pages, S, token_stride, lens_p,
+        _i32_on(new_lens, S, "new_lens", on), _i32_on(depth, per, "depth", on), table_p,
+        page_table.stride(0) if rows > 1 else width, width,
+        _i32_on(free_pages, 0, "free_pages", on), free_pages.numel(), max_tokens,
+        _i32_on(offsets, 2 * S, "offsets", on), _i32_on(start_pos, S, "start_pos", on),
+        _i32_on(out_loc, per, "out_loc", on), _i32_on(positions, per, "positions", on),
+        _i32_on(token_to_req, per, "token_to_req", on), _i32_on(totals, 4, "totals", on),
+        _i32_on(status, 1, "status", on)))
 
 
 # ----------------------------------------------------------------- attention
