@@ -20,11 +20,11 @@
 // (V41), 288 (V41_FP4) or 584 (V4) bytes, so from 64 queries a unit up the
 // matrix units bound it (about 1.5 PFLOP/s: the clock falls to 1.6 GHz under
 // them) before HBM does; below, HBM.  What it reaches, in visible (query, row)
-// pairs * 2048 flops: 1.07 PFLOP/s on a prompt of 8,192 tokens with 128 heads
-// (V41, 8.2 ms), 0.68 on 16 prompts of some 2,000 tokens with 32 heads (V41_FP4,
+// pairs * 2048 flops: 1.08 PFLOP/s on a prompt of 8,192 tokens with 128 heads
+// (V41, 8.1 ms), 0.68 on 16 prompts of some 2,000 tokens with 32 heads (V41_FP4,
 // 16 tiles a unit on average, 1.5 ms), 0.61 on 64 decodes with 64 heads
-// (V41_FP4, 124 us), 2.7 TB/s and 0.57 PFLOP/s on 128 chains of 4 with 16 heads
-// (V4, 127 us).
+// (V41_FP4, 124 us), 2.75 TB/s and 0.59 PFLOP/s on 128 chains of 4 with 16 heads
+// (V4, 124 us).
 #include <type_traits>
 
 #include "launch_attend.hpp"
@@ -1062,7 +1062,7 @@ void attend_kernel(AttendParams p) {
 // tile.  Pages of 8 rows or more.
 //
 // On a prompt of 8,192 tokens with 128 heads (V41) the matrix units work in
-// half of the cycles (64 products of 32 cycles in a tile's 4,000 or so), at 1.07
+// half of the cycles (64 products of 32 cycles in a tile's 4,000 or so), at 1.08
 // PFLOP/s.  The registers are full: a value more that lives over the tiles, or
 // accumulators that leave the matrix registers all at once, spills inside the
 // loop and cost 10% (9.2 against 8.2 ms).

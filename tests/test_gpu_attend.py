@@ -476,6 +476,39 @@ def test_packed_batches_of_many_prompts(kvc, S, H, most):
     assert (out[T - 5:] == 7.0).all() and (lse[T - 5:] == 7.0).all()
 
 
+@pytest.mark.parametrize("packed", [False, True])
+def test_most_slots_few_of_them_active(kvc, packed):
+    S, H, D = 8191, 3, 2
+    rng = random.Random(67 + packed)
+    active = sorted(rng.sample(range(S), 40) + [0, S - 1])
+    starts, new = [-1] * S, [0] * S
+    for b in active:
+        starts[b], new[b] = rng.randint(0, 90), rng.randint(1, 5) if packed else D
+    counts = [s + n if s >= 0 else 0 for s, n in zip(starts, new)]
+    f = Filled(kvc, "V41", 64, counts, 67)
+    first = np.cumsum([0] + new)[:-1] if packed else np.arange(S) * D
+    T = sum(new) if packed else S * D
+    q = queries(T, H, 67)
+    out = torch.full((T, H, 512), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((T, H), 7.0, device="cuda")
+    start = torch.tensor(starts, dtype=torch.int32).cuda()
+    if packed:
+        off = torch.tensor(np.array([first, new]), dtype=torch.int32).cuda()
+        kvc.kvc_attend_prefill(f.cache, q.cuda(), off, start, dev(f.table), out, scale=SCALE, lse=lse)
+    else:
+        kvc.kvc_attend_tree(f.cache, q.cuda(), start, dev(f.table), out, scale=SCALE, draft_len=D, lse=lse)
+    out, lse = out.cpu(), lse.cpu()
+    rest = torch.ones(T, dtype=torch.bool)
+    for b in active:
+        s, n = starts[b], new[b]
+        rows, _ = f.rows(b, s + n)
+        t = slice(int(first[b]), int(first[b]) + n)
+        rest[t] = False
+        ref.check(out[t], lse[t], ref.attend(q[t].double(), rows, prefill_seen(s, n, 1, s + n), SCALE),
+                  f"slot {b}")
+    assert (out[rest] == 7.0).all() and (lse[rest] == 7.0).all()
+
+
 def test_repeats_bit_for_bit_and_on_another_stream(kvc):
     starts = [1200, 30, 500]
     f = Filled(kvc, "V41", 64, [s + 4 for s in starts], 43)
