@@ -586,6 +586,49 @@ def test_graph_replays_follow_refreshed_inputs(kvc):
                                                  SCALE), f"replay {k} slot {b}")
 
 
+def test_graph_replays_of_a_packed_batch_with_its_own_plan(kvc):
+    """A batch planned by a kernel of its own, captured once: every replay
+    follows the offsets and starts of its moment, eager calls in between."""
+    S, H, T = 40, 100, 150
+    f = Filled(kvc, "V4", 64, [300] * S, 71)
+    table = dev(f.table)
+    q = queries(T, H, 71)
+    qd = q.cuda()
+    off = torch.zeros(2, S, dtype=torch.int32).cuda()
+    start = torch.zeros(S, dtype=torch.int32).cuda()
+    out = torch.empty_like(qd)
+    other = torch.empty_like(qd)
+    lse = torch.empty(T, H, device="cuda")
+    kvc.kvc_attend_prefill(f.cache, qd, off, start, table, out, scale=SCALE, lse=lse)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        kvc.kvc_attend_prefill(f.cache, qd, off, start, table, out, scale=SCALE, lse=lse)
+    for k in range(4):
+        rng = random.Random(80 + k)
+        new = [rng.choice((0, 1, 3, 7)) for _ in range(S)]
+        while sum(new) > T:
+            new[new.index(max(new))] = 0
+        starts = [rng.randint(0, 290) for _ in range(S)]
+        if k == 2:
+            starts = [-1] * S                 # nothing to do
+        first = np.cumsum([0] + new)[:-1]
+        off.copy_(torch.tensor(np.array([first, new]), dtype=torch.int32))
+        start.copy_(torch.tensor(starts, dtype=torch.int32))
+        out.fill_(3.0)
+        other.fill_(3.0)
+        g.replay()
+        kvc.kvc_attend_prefill(f.cache, qd, off, start, table, other, scale=SCALE)
+        torch.cuda.synchronize()
+        assert torch.equal(out, other)
+        for b in [b for b in range(S) if new[b] and starts[b] >= 0][::7]:
+            rows, _ = f.rows(b, starts[b] + new[b])
+            t = slice(int(first[b]), int(first[b]) + new[b])
+            ref.check(out[t], lse[t], ref.attend(q[t].double(), rows,
+                                                 prefill_seen(starts[b], new[b], 1, starts[b] + new[b]),
+                                                 SCALE), f"replay {k} slot {b}")
+        assert (out[sum(new):] == 3.0).all()
+
+
 def test_zero_slots_and_zero_rows(kvc):
     f = Filled(kvc, "V41", 64, [64], 59)
     e = lambda *s: torch.empty(*s, dtype=torch.int32, device="cuda")
