@@ -326,18 +326,29 @@ struct Rows {
 // compiler gives every matrix-instruction result of a kernel of this size to
 // the accumulator file, which O fills (256 registers for 128 queries), and
 // moves O through the vector registers where it allocates it by itself.
-// A result feeding the next instruction's C operand needs no wait; s_nop 0
-// covers an operand that a vector instruction has just written.  scores_done
-// and out_done give the 16 wait states from a last result to a vector
-// instruction that reads it.
+// A result feeding the next instruction's C operand needs no wait; an operand
+// that a vector instruction has just written needs two wait states (WAIT: s_nop
+// 1, 2% on units of 64; where the operands come from LDS and from registers
+// that stay, none are needed, and a test reads the assembly for it).
+// scores_done and out_done give the 16 wait states from a last result to a
+// vector instruction that reads it.
+template <bool WAIT>
 __device__ __forceinline__ void score_mfma(f32x16& sc, bf16x8 x, bf16x8 q, bool first) {
-  if (first)
-    asm("s_nop 0\n\tv_mfma_f32_32x32x16_bf16 %0, %1, %2, 0" : "=&v"(sc) : "v"(x), "v"(q));
+  if (WAIT && first)
+    asm("s_nop 1\n\tv_mfma_f32_32x32x16_bf16 %0, %1, %2, 0" : "=&v"(sc) : "v"(x), "v"(q));
+  else if (WAIT)
+    asm("s_nop 1\n\tv_mfma_f32_32x32x16_bf16 %0, %1, %2, %0" : "+&v"(sc) : "v"(x), "v"(q));
+  else if (first)
+    asm("v_mfma_f32_32x32x16_bf16 %0, %1, %2, 0" : "=&v"(sc) : "v"(x), "v"(q));
   else
-    asm("s_nop 0\n\tv_mfma_f32_32x32x16_bf16 %0, %1, %2, %0" : "+&v"(sc) : "v"(x), "v"(q));
+    asm("v_mfma_f32_32x32x16_bf16 %0, %1, %2, %0" : "+&v"(sc) : "v"(x), "v"(q));
 }
+template <bool WAIT>
 __device__ __forceinline__ void out_mfma(f32x16& o, bf16x8 x, bf16x8 w) {
-  asm("s_nop 0\n\tv_mfma_f32_32x32x16_bf16 %0, %1, %2, %0" : "+a"(o) : "v"(x), "v"(w));
+  if (WAIT)
+    asm("s_nop 1\n\tv_mfma_f32_32x32x16_bf16 %0, %1, %2, %0" : "+a"(o) : "v"(x), "v"(w));
+  else
+    asm("v_mfma_f32_32x32x16_bf16 %0, %1, %2, %0" : "+a"(o) : "v"(x), "v"(w));
 }
 __device__ __forceinline__ void scores_done(f32x16& sc) { asm("s_nop 15" : "+v"(sc)); }
 __device__ __forceinline__ void out_done(f32x16& o) { asm("s_nop 15" : "+a"(o)); }
@@ -899,7 +910,7 @@ void attend_kernel(AttendParams p) {
         for (int k = 0; k < LA; ++k) x[k] = rows16(k);
 #pragma unroll
         for (int k = 0; k < 32; ++k) {
-          score_mfma(sc, x[k % LA], qv[k], k == 0);
+          score_mfma<true>(sc, x[k % LA], qv[k], k == 0);
           if (k + LA < 32) x[k % LA] = rows16(k + LA);
           if constexpr (BUF == 2) {
             if (k == 1) note_valid(par ^ 1);
@@ -1029,7 +1040,7 @@ void attend_kernel(AttendParams p) {
       for (int i = 0; i < N; ++i) {
 #pragma unroll
         for (int x = 0; x < QB; ++x) {
-          out_mfma(o[i & 3][x], xv[i % 3], wv[(i >> 2) & 1][x]);
+          out_mfma<true>(o[i & 3][x], xv[i % 3], wv[(i >> 2) & 1][x]);
           if (x == QB - 1 && i + 3 < N) xv[i % 3] = dims(i + 3);
           if ((i & 3) == 1 && i + 4 < N) wv[((i >> 2) + 1) & 1][x] = weights((i >> 2) + 1, x);
           if constexpr (BUF == 2) {
@@ -1260,7 +1271,7 @@ void attend_wide_kernel(AttendParams p) {
       bf16x8 qt[3];
 #pragma unroll
       for (int k = 0; k < 32; ++k) {
-        score_mfma(sc, x[k % 6], k < 32 - kTail ? qv[k < 32 - kTail ? k : 0] : qt[k % 3], k == 0);
+        score_mfma<false>(sc, x[k % 6], k < 32 - kTail ? qv[k < 32 - kTail ? k : 0] : qt[k % 3], k == 0);
         if (k + 3 >= 32 - kTail && k + 3 < 32) qt[k % 3] = query_tail(k + 3);
         if (k + 6 < 32) x[k % 6] = score_rows(k + 6);
         if (k >= 28) out_ahead(k - 28, before, ((tl - w.t0) & 1) ^ 1);
@@ -1375,7 +1386,7 @@ void attend_wide_kernel(AttendParams p) {
         const bf16x8 xi = xv[i & 1];
 #pragma unroll
         for (int y = 0; y < QB; ++y) {
-          out_mfma(o[i & 3][y], xi, wv[y]);
+          out_mfma<false>(o[i & 3][y], xi, wv[y]);
           if (y == 0 && i + 2 < 8) xv[i & 1] = out_dims(i + 2, at);
           if (i == 3) wv[y] = out_weights(1, y, par);
           if constexpr (with.value) {
