@@ -326,10 +326,12 @@ struct Rows {
 // compiler gives every matrix-instruction result of a kernel of this size to
 // the accumulator file, which O fills (256 registers for 128 queries), and
 // moves O through the vector registers where it allocates it by itself.
-// A result feeding the next instruction's C operand needs no wait; an operand
+// A result feeding the next instruction's C operand needs no wait.  An operand
 // that a vector instruction has just written needs two wait states (WAIT: s_nop
-// 1, 2% on units of 64; where the operands come from LDS and from registers
-// that stay, none are needed, and a test reads the assembly for it).
+// 1): the compiler keeps some of the queries of units of 32 and 64 in
+// accumulator registers and copies them over.  The other operands come from LDS
+// and from registers that stay, and need none (1 to 2% of the time); a test
+// reads the assembly for both.
 // scores_done and out_done give the 16 wait states from a last result to a
 // vector instruction that reads it.
 template <bool WAIT>
@@ -343,12 +345,8 @@ __device__ __forceinline__ void score_mfma(f32x16& sc, bf16x8 x, bf16x8 q, bool 
   else
     asm("v_mfma_f32_32x32x16_bf16 %0, %1, %2, %0" : "+&v"(sc) : "v"(x), "v"(q));
 }
-template <bool WAIT>
 __device__ __forceinline__ void out_mfma(f32x16& o, bf16x8 x, bf16x8 w) {
-  if (WAIT)
-    asm("s_nop 1\n\tv_mfma_f32_32x32x16_bf16 %0, %1, %2, %0" : "+a"(o) : "v"(x), "v"(w));
-  else
-    asm("v_mfma_f32_32x32x16_bf16 %0, %1, %2, %0" : "+a"(o) : "v"(x), "v"(w));
+  asm("v_mfma_f32_32x32x16_bf16 %0, %1, %2, %0" : "+a"(o) : "v"(x), "v"(w));
 }
 __device__ __forceinline__ void scores_done(f32x16& sc) { asm("s_nop 15" : "+v"(sc)); }
 __device__ __forceinline__ void out_done(f32x16& o) { asm("s_nop 15" : "+a"(o)); }
@@ -1040,7 +1038,7 @@ void attend_kernel(AttendParams p) {
       for (int i = 0; i < N; ++i) {
 #pragma unroll
         for (int x = 0; x < QB; ++x) {
-          out_mfma<true>(o[i & 3][x], xv[i % 3], wv[(i >> 2) & 1][x]);
+          out_mfma(o[i & 3][x], xv[i % 3], wv[(i >> 2) & 1][x]);
           if (x == QB - 1 && i + 3 < N) xv[i % 3] = dims(i + 3);
           if ((i & 3) == 1 && i + 4 < N) wv[((i >> 2) + 1) & 1][x] = weights((i >> 2) + 1, x);
           if constexpr (BUF == 2) {
@@ -1386,7 +1384,7 @@ void attend_wide_kernel(AttendParams p) {
         const bf16x8 xi = xv[i & 1];
 #pragma unroll
         for (int y = 0; y < QB; ++y) {
-          out_mfma<false>(o[i & 3][y], xi, wv[y]);
+          out_mfma(o[i & 3][y], xi, wv[y]);
           if (y == 0 && i + 2 < 8) xv[i & 1] = out_dims(i + 2, at);
           if (i == 3) wv[y] = out_weights(1, y, par);
           if constexpr (with.value) {
