@@ -366,13 +366,14 @@ __device__ __forceinline__ float sum_halves(float v) {
   const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
   return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
-// sum of a bf16 pair added to v
-__device__ __forceinline__ float add_pair(float v, uint32_t pair) {
+// the products of two bf16 pairs added to v
+__device__ __forceinline__ float dot_pair(float v, uint32_t a, uint32_t b) {
   typedef __bf16 bf16x2v __attribute__((ext_vector_type(2)));
-  const uint32_t ones = 0x3F803F80u;
-  return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2v, pair),
-                                         __builtin_bit_cast(bf16x2v, ones), v, false);
+  return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2v, a), __builtin_bit_cast(bf16x2v, b), v,
+                                         false);
 }
+// sum of a bf16 pair added to v
+__device__ __forceinline__ float add_pair(float v, uint32_t pair) { return dot_pair(v, pair, 0x3F803F80u); }
 
 // ------------------------------------------------------------------ a query
 // What a lane knows of its query, and the softmax state of it
@@ -430,19 +431,64 @@ __device__ __forceinline__ bool mask_scores(f32x16& sc, const Query& q, int32_t 
   return __ballot(nf) != 0;
 }
 
-// zeroes every NaN and infinity of a staged tile (BYTES long); all threads
-template <int BYTES>
-__device__ __forceinline__ void zero_not_finite(lds_ptr tile) {
+// A query that sees a row holding a NaN or an infinity is NaN, all of it and
+// its lse, wherever the row and the query lie.  A NaN gives a NaN weight and
+// does so by itself, and so does a score of +inf (inf - inf).  An infinity whose
+// score is -inf has the weight 0, and 0 times it makes NaN of its own dims:
+// end_piece widens them to the query.  Where that infinity was zeroed, for the
+// sake of a query that does not see the row, sees_bad says so.  (What either finds
+// goes to the sums by way of sfac, which is 0 otherwise.)
+// (A finite row whose score passes fp32 has the weight 0 and nothing else.)
+// FP4 rows hold no infinities: a code times its scale is at most 2,688.
+template <int L> constexpr bool kInfinities = L != kV41Fp4;
+constexpr float kNaN = __builtin_nanf("");
+
+// zeroes every NaN and infinity of a staged tile of ROWS rows and notes the rows
+// that held one, a bit each, in bad; all threads (a wave has consecutive rows),
+// with a barrier behind it
+template <int ROWS>
+__device__ __forceinline__ void zero_not_finite(lds_ptr tile, uint32_t* bad) {
   typedef __attribute__((address_space(3))) u32x4* vec;
-  for (int x = threadIdx.x; x < BYTES / 16; x += kAttendBlock) {
-    u32x4 v = *(vec)(tile + 16 * x);
+  typedef typename std::conditional<ROWS == 32, uint8_t,
+      typename std::conditional<ROWS == 64, uint16_t, uint32_t>::type>::type
+      Bits __attribute__((may_alias));
+  const int wave = uniform((int)(threadIdx.x >> 6)), lane = lane_id();
+  const lds_ptr rows = tile + wave * (ROWS / 4) * 1024 + 16 * lane;
+  constexpr int B = ROWS == 32 ? 8 : 16;      // rows read ahead
+  uint32_t found = 0;
+#pragma unroll 1
+  for (int r0 = 0; r0 < ROWS / 4; r0 += B) {
+    u32x4 v[B];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      if ((v[k] & 0x7F80u) == 0x7F80u) v[k] &= 0xFFFF0000u;
-      if ((v[k] & 0x7F800000u) == 0x7F800000u) v[k] &= 0xFFFFu;
+    for (int r = 0; r < B; ++r) v[r] = *(vec)(rows + 1024 * (r0 + r));
+#pragma unroll
+    for (int r = 0; r < B; ++r) {
+      bool any = false;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if ((v[r][k] & 0x7F80u) == 0x7F80u) v[r][k] &= 0xFFFF0000u, any = true;
+        if ((v[r][k] & 0x7F800000u) == 0x7F800000u) v[r][k] &= 0xFFFFu, any = true;
+      }
+      if (__ballot(any) == 0) continue;
+      *(vec)(rows + 1024 * (r0 + r)) = v[r];
+      found |= 1u << (r0 + r);
     }
-    *(vec)(tile + 16 * x) = v;
   }
+  if (lane == 0) ((Bits*)bad)[wave] = (Bits)found;
+  __syncthreads();
+}
+
+// whether the query sees one of the rows of bad, a bit each of the 32 from r0,
+// that lie in its lane (see mask_scores)
+__device__ __forceinline__ bool sees_bad(const Query& q, int32_t r0, int h, int32_t base, bool tree,
+                                         uint32_t bad) {
+  const int32_t below = min(max(q.lim - r0, 0), 32);
+  uint32_t seen = (uint32_t)((uint64_t(1) << below) - 1);
+  if (tree) {
+    const int32_t to = base - r0;             // where bit 0 of bits stands
+    seen |= (uint32_t)(to >= 0 ? q.bits << min(to, 63) : q.bits >> min(-to, 63) & (to > -64 ? ~0ull : 0));
+  }
+  return (seen & bad & (h != 0 ? 0xF0F0F0F0u : 0x0F0F0F0Fu)) != 0;
 }
 
 // Out and lse factors of a query from its complete sums (or, with a cut unit,
@@ -454,7 +500,8 @@ __device__ __forceinline__ Final finish(float snk, float mx, float sum, float rs
   const float mm = fmaxf(mx, snk);
   const float e = mx == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(mx - mm);
   const float es = snk == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(snk - mm);
-  return Final{e == 0.0f ? 0.0f : e / (rsum * e + es), mm + __builtin_log2f(sum * e + es)};
+  const float den = rsum * e + es;            // 0: no row and no sink
+  return Final{den == 0.0f ? 0.0f : e / den, mm + __builtin_log2f(sum * e + es)};
 }
 
 // ------------------------------------------------------------------ attend
@@ -597,6 +644,13 @@ struct Walk {
   }
 };
 
+// a barrier that orders LDS only: global stores before it are not waited for
+__device__ __forceinline__ void lds_barrier() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
 // sixteen accumulators out of the matrix registers here and not before: all of
 // them at once would not fit
 __device__ __forceinline__ f32x16 taken(f32x16 v) {
@@ -610,7 +664,8 @@ __device__ __forceinline__ f32x16 taken(f32x16 v) {
 // the tiles, 96 KB or more, three blocks of 32 queries) so that a wave writes whole rows; partial
 // sums are stored as they lie in the registers, a wave's
 // 1 KB at a time, in the order [query block][dim block][quad][wave][lane].
-template <int QB>
+// INF: a NaN among a query's dims makes NaN of them all (see kInfinities).
+template <int QB, bool INF>
 __device__ __forceinline__ void end_piece(const AttendParams& p, const Walk& w, Query& q,
                                           const f32x16 (&o)[4][QB], int qb, int nb,
                                           float (*ssum)[32 * QB], float (*srsum)[32 * QB],
@@ -623,14 +678,34 @@ __device__ __forceinline__ void end_piece(const AttendParams& p, const Walk& w, 
   q.sum = sum_halves(q.sum);
   q.rsum = sum_halves(q.rsum);
   if (h == 0) { ssum[nb][qi] = q.sum; srsum[nb][qi] = q.rsum; }
-  __syncthreads();
   const bool whole = w.t0 == 0 && w.t1 == w.tiles;
+  __syncthreads();
   // a part that began inside its unit lies in the workgroup's first place
   const int64_t part = ((int64_t)blockIdx.x * 2 + (w.t0 > 0 ? 0 : 1)) * QT;
+  if (!whole) {
+    float* const pp = p.part_o + part * kDim + 256 * wave + 4 * lane;
+#pragma unroll
+    for (int x = 0; x < QB; ++x) {
+      bool nan = false;
+#pragma unroll
+      for (int d = 0; d < 4; ++d) {
+        const f32x16 v = taken(o[d][x]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const f32x4 y = {v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]};
+          *(f32x4*)(pp + ((x * 4 + d) * 4 + j) * 1024) = y;
+          if constexpr (INF) nan |= __builtin_isunordered(y[0], y[1]) || __builtin_isunordered(y[2], y[3]);
+        }
+      }
+      if (INF && __builtin_expect(nan, false)) sfac[x * 32 + ql] = kNaN;
+    }
+    if constexpr (INF) lds_barrier();         // (the sums above are still being stored)
+  }
   if (nb == 0 && h == 0) {
     float sum = ssum[0][qi], rsum = srsum[0][qi];
 #pragma unroll
     for (int x = 1; x < NB; ++x) { sum += ssum[x][qi]; rsum += srsum[x][qi]; }
+    if constexpr (INF) sum += sfac[qi], rsum += sfac[qi];
     if (whole) {
       const int32_t m = w.ub * QT + qi;
       float snk = q.sink;
@@ -648,20 +723,7 @@ __device__ __forceinline__ void end_piece(const AttendParams& p, const Walk& w, 
       p.part_ml[part + qi] = make_float4(q.mx, sum, rsum, 0.0f);
     }
   }
-  if (!whole) {
-    float* const pp = p.part_o + part * kDim + 256 * wave + 4 * lane;
-#pragma unroll
-    for (int x = 0; x < QB; ++x)
-#pragma unroll
-      for (int d = 0; d < 4; ++d) {
-        const f32x16 v = taken(o[d][x]);
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          *(f32x4*)(pp + ((x * 4 + d) * 4 + j) * 1024) =
-              f32x4{v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]};
-      }
-    return;
-  }
+  if (!whole) return;
   __syncthreads();
   const int32_t nq = w.s.n * p.heads;
   constexpr int R = QB < 3 ? QB : 3;          // blocks of 32 queries that the area holds
@@ -692,15 +754,40 @@ __device__ __forceinline__ void end_piece(const AttendParams& p, const Walk& w, 
       int32_t head = m - tok * p.heads;
       const int rows = min(8, nq - m);
       uint16_t* op = p.out + (int64_t)(w.s.first + tok) * p.out_stride + (int64_t)head * p.out_hstride;
-      for (int i = 0; i < rows; ++i) {
+      // (a dot product with zeros is NaN where a value is not finite)
+      float probe = 0.0f;
+      auto turned = [&](int i) {
         const int r = wave * 8 + i;
-        const u32x4 v = *(const __attribute__((address_space(3))) u32x4*)(
+        return *(const __attribute__((address_space(3))) u32x4*)(
             area + (x - x0) * 32768 + r * 1024 + ((lane ^ (r & 15)) << 4));
+      };
+      auto write = [&](int i, u32x4 v) {
         *(u32x4*)(op + 8 * lane) = v;
         op += p.out_hstride;
         if (++head == p.heads) {
           head = 0;
           op += p.out_stride - p.heads * p.out_hstride;
+        }
+      };
+      for (int i = 0; i < rows; ++i) {
+        const u32x4 v = turned(i);
+        if constexpr (INF)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) probe = dot_pair(probe, v[k], 0);
+        write(i, v);
+      }
+      if (INF && __builtin_expect(__ballot(probe != probe) != 0, false)) {
+        // once more, row by row
+        op = p.out + (int64_t)(w.s.first + tok) * p.out_stride + (int64_t)(m - tok * p.heads) * p.out_hstride;
+        head = m - tok * p.heads;
+        for (int i = 0; i < rows; ++i) {
+          const u32x4 v = turned(i);
+          bool nan = false;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) nan |= (v[k] & 0x7FFFu) > 0x7F80u || (v[k] & 0x7FFF0000u) > 0x7F800000u;
+          const bool any = __ballot(nan) != 0;
+          write(i, any ? u32x4{0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u} : v);
+          if (any && lane == 0 && p.lse != nullptr) p.lse[(int64_t)w.s.first * p.heads + m + i] = kNaN;
         }
       }
     }
@@ -752,6 +839,7 @@ void attend_kernel(AttendParams p) {
   __shared__ float smax[NB][QT], ssum[NB][QT], srsum[NB][QT], sfac[QT];
   __shared__ __attribute__((aligned(16))) uint8_t svalid[BUF][16];
   __shared__ __attribute__((aligned(4))) uint8_t sjump[4], snf[4];
+  __shared__ uint32_t sbad[NB];               // rows of a tile that are not finite
   const int lane = lane_id(), wave = uniform((int)(threadIdx.x >> 6));
   const int ql = lane & 31, h = lane >> 5;
   const int qb = wave % QB, nb = wave / QB;
@@ -859,6 +947,7 @@ void attend_kernel(AttendParams p) {
     for (int d = 0; d < 4; ++d)
 #pragma unroll
       for (int x = 0; x < QB; ++x) o[d][x] = f32x16{};
+    if (kInfinities<L> && threadIdx.x < QT) sfac[threadIdx.x] = 0.0f;
     float ref[QB];                            // reference maxima of all the unit's queries ql, 32 + ql
 #pragma unroll
     for (int x = 0; x < QB; ++x) ref[x] = kNegInf;
@@ -1027,7 +1116,12 @@ void attend_kernel(AttendParams p) {
         }
         // a NaN or an infinity in a row that some query does not see: its weight
         // there is 0, and 0 times it would not be
-        if (dirty) zero_not_finite<TB>(tiles3 + cur);
+        if (__builtin_expect(dirty, false)) {
+          zero_not_finite<NT>(tiles3 + cur, sbad);
+          if (kInfinities<L> && sees_bad(q, tl * NT + nb * 32, h, w.s.pos, tree,
+                                         sbad[nb] & *(const uint32_t*)(svalid[par] + 4 * nb)))
+            sfac[qi] = kNaN;
+        }
         __syncthreads();
         first_frags();
       }
@@ -1057,7 +1151,7 @@ void attend_kernel(AttendParams p) {
 #pragma unroll
       for (int x = 0; x < QB; ++x) out_done(o[d][x]);
     q.mx = QB == 1 || qb == 0 ? ref[0] : ref[QB - 1];
-    end_piece<QB>(p, w, q, o, qb, nb, ssum, srsum, sfac, tiles3);
+    end_piece<QB, kInfinities<L>>(p, w, q, o, qb, nb, ssum, srsum, sfac, tiles3);
     __syncthreads();
   } while (w.next(p, QT, NT));
 }
@@ -1087,6 +1181,8 @@ void attend_wide_kernel(AttendParams p) {
   // a byte a wave: the tile's valid 8-row groups, the rescaled query blocks, the
   // blocks that met a score that is not finite where it is masked
   __shared__ __attribute__((aligned(4))) uint8_t svalid[2][4], sscale[2][4], snf[2][4];
+  // rows of a tile that are not finite, valid rows of a masked tile
+  __shared__ uint32_t sbad[1], smasked[2];
   const int lane = lane_id(), wave = uniform((int)(threadIdx.x >> 6));
   const int ql = lane & 31, h = lane >> 5;
   const int qi = wave * 32 + ql;
@@ -1166,6 +1262,7 @@ void attend_wide_kernel(AttendParams p) {
     for (int d = 0; d < 4; ++d)
 #pragma unroll
       for (int x = 0; x < QB; ++x) o[d][x] = f32x16{};
+    if (kInfinities<L> && threadIdx.x < QT) sfac[threadIdx.x] = 0.0f;
     __syncthreads();
 
     typedef const __attribute__((address_space(3))) u32x4* vec;
@@ -1283,6 +1380,7 @@ void attend_wide_kernel(AttendParams p) {
       scores_done(sc);
       const bool any = mask_scores(sc, q, tl * NT, h, w.s.pos, tree, okw);
       if (lane == 0) snf[(tl - w.t0) & 1][wave] = any;
+      if (kInfinities<L>) smasked[(tl - w.t0) & 1] = okw; // (the same of every wave)
     };
     // ---- tile tl + 1 expanded into the buffer at nxt, in steps of their own for
     // the conversions and the write that waits for them, and each load asked for
@@ -1352,13 +1450,13 @@ void attend_wide_kernel(AttendParams p) {
       }
       if (step >= 16 && step <= 28 && (step & 3) == 0) q.rsum = add_pair(add_pair(q.rsum, pair0), pair1);
     };
-    // ---- what must precede O's products over the tile at `at` (parity par)
-    auto out_begin = [&](uint32_t at, int32_t par, bool dirty) {
+    // ---- what must precede O's products over tile tl at `at` (parity par)
+    auto out_begin = [&](int32_t tl, uint32_t at, int32_t par, bool dirty) {
       // a NaN or an infinity in a row that some query does not see: its weight
       // there is 0, and 0 times it would not be
-      if (dirty && uniform(*(const int32_t*)snf[par]) != 0) {
-        zero_not_finite<TB>(tiles3 + at);
-        __syncthreads();
+      if (__builtin_expect(dirty && uniform(*(const int32_t*)snf[par]) != 0, false)) {
+        zero_not_finite<NT>(tiles3 + at, sbad);
+        if (kInfinities<L> && sees_bad(q, tl * NT, h, w.s.pos, tree, sbad[0] & smasked[par])) sfac[qi] = kNaN;
 #pragma unroll
         for (int i = 0; i < 4; ++i) out_ahead(i, at, par);
       }
@@ -1420,20 +1518,20 @@ void attend_wide_kernel(AttendParams p) {
       cur = after(cur);
       scores(tl, before);
       mask(tl);
-      out_begin(before, par ^ 1, holes_before);
+      out_begin(tl - 1, before, par ^ 1, holes_before);
       out(before, par ^ 1, after(cur), std::true_type{});
     }
     cutw = (uint32_t)uniform((int32_t)cuts);
     const int32_t last = (w.t1 - 1 - w.t0) & 1;
 #pragma unroll
     for (int i = 0; i < 4; ++i) out_ahead(i, cur, last);
-    out_begin(cur, last, holes);
+    out_begin(w.t1 - 1, cur, last, holes);
     out(cur, last, 0, std::false_type{});
 #pragma unroll
     for (int d = 0; d < 4; ++d)
 #pragma unroll
       for (int y = 0; y < QB; ++y) out_done(o[d][y]);
-    end_piece<QB>(p, w, q, o, wave, 0, ssum, srsum, sfac, tiles3);
+    end_piece<QB, kInfinities<L>>(p, w, q, o, wave, 0, ssum, srsum, sfac, tiles3);
     __syncthreads();
   } while (w.next(p, QT, NT));
 }

@@ -462,7 +462,9 @@ int kvc_slot_map(const kvc_slot_map_args* args, void* stream);
  * A row whose logical page is past pt_width (KVC_STATUS_PT_RANGE) or whose
  * page is outside the cache (KVC_STATUS_PAGE_RANGE) is left out, as if masked.
  * Rows that a query does not see do not reach it, whatever they hold; a row
- * holding a NaN makes NaN of the queries that see it.
+ * holding a NaN or an infinity makes NaN of the queries that see it, of all of
+ * out and of lse.  (A score past fp32 over finite rows and queries is that
+ * infinity: -inf weighs 0, +inf makes NaN.)
  *
  * workspace: kvc_attend_workspace bytes of device memory, 256-byte aligned,
  * written and read by the call (no state is kept in it); two calls that may
