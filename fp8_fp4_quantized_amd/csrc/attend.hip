@@ -499,7 +499,8 @@ struct Final {
 __device__ __forceinline__ Final finish(float snk, float mx, float sum, float rsum) {
   const float mm = fmaxf(mx, snk);
   const float e = mx == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(mx - mm);
-  const float es = snk == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(snk - mm);
+  // (an infinite sink outweighs every row: out is 0, lse infinite)
+  const float es = snk == kNegInf ? 0.0f : snk == mm ? 1.0f : __builtin_amdgcn_exp2f(snk - mm);
   const float den = rsum * e + es;            // 0: no row and no sink
   return Final{den == 0.0f ? 0.0f : e / den, mm + __builtin_log2f(sum * e + es)};
 }

@@ -438,7 +438,8 @@ int kvc_slot_map(const kvc_slot_map_args* args, void* stream);
  *   out = sum_r e^(s_r) x_r / (sum_r e^(s_r) + e^(sink)),
  *   lse = log2(sum_r e^(s_r) + e^(sink))        (no sink: e^(sink) is 0).
  * A query that sees no row gives out = 0 and lse = sink * log2(e), or -inf
- * without a sink.  Scores and sums are fp32; the weights e^(s_r) are rounded
+ * without a sink; a sink of +inf (or past fp32 times log2(e)) gives out = 0
+ * and lse = +inf.  Scores and sums are fp32; the weights e^(s_r) are rounded
  * to bf16 for the second product (and the sum out is divided by is that of
  * the rounded weights), out is rounded to bf16.
  *
