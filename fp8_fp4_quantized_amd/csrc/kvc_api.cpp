@@ -97,7 +97,7 @@ constexpr int64_t kMaxQueries = 0x7FFFFF00;   // query indices, rounded up to a 
 
 int64_t align256(int64_t n) { return (n + 255) & ~int64_t(255); }
 
-// places of the workspace's parts; returns its size
+// places of the workspace's parts; returns where they end
 int64_t attend_layout(int32_t slots, int64_t tokens, int32_t heads, int64_t (&at)[5]) {
   const int64_t parts = 2 * int64_t(kvc::kAttendWorkgroups) * 32 * attend_qblocks(slots, tokens, heads);
   int64_t n = 0;
@@ -107,6 +107,14 @@ int64_t attend_layout(int32_t slots, int64_t tokens, int32_t heads, int64_t (&at
   at[3] = n, n += align256(parts * 16);
   at[4] = n, n += align256(parts * 512 * 4);
   return n;
+}
+
+// bytes for `tokens` token rows whatever slots they are in: those of the widest
+// units they may take, one slot's (so that a workspace for the largest batch
+// serves the smaller ones, whose units may be wider)
+int64_t attend_bytes(int64_t tokens, int32_t heads) {
+  int64_t at[5];
+  return attend_layout(1, tokens, heads, at);
 }
 
 // the checks and the call shared by both attention entry points
@@ -148,8 +156,7 @@ int attend(const kvc_attend_args* a, bool tree, void* stream, const char* who) {
   if (!(a->scale > 0.0f) || !std::isfinite(a->scale))
     return fail(KVC_EINVAL, "%s: scale must be finite and > 0", who);
   const int64_t tokens = tree ? (int64_t)a->num_slots * a->draft_len : a->q_rows;
-  int64_t at[5];
-  const int64_t need = attend_layout(a->num_slots, tokens, a->num_heads, at);
+  const int64_t need = attend_bytes(tokens, a->num_heads);
   if (a->workspace == nullptr || ((uintptr_t)a->workspace & 255u) != 0 || a->workspace_bytes < need)
     return fail(KVC_EINVAL, "%s: workspace needs %lld bytes, 256-byte aligned", who, (long long)need);
   if (kvc::launch_attend == nullptr) return fail(KVC_ELAUNCH, "%s: built without kernels", who);
@@ -184,6 +191,8 @@ int attend(const kvc_attend_args* a, bool tree, void* stream, const char* who) {
     p.plan_units = (int32_t)units;
     p.plan_div = kvc::div_magic((uint32_t)units);
   }
+  int64_t at[5];
+  attend_layout(a->num_slots, tokens, a->num_heads, at);
   uint8_t* w = static_cast<uint8_t*>(a->workspace);
   p.head = reinterpret_cast<kvc::AttendHead*>(w + at[0]);
   p.starts = reinterpret_cast<kvc::AttendStart*>(w + at[1]);
@@ -564,8 +573,7 @@ int kvc_attend_workspace(int32_t num_slots, int64_t tokens, int32_t num_heads, i
   if (num_slots < 0 || num_slots > kvc::kMaxSlots || num_heads < 1 || num_heads > 1024 || tokens < 0 ||
       tokens > kMaxQueries / num_heads)
     return fail(KVC_EINVAL, "%s: sizes outside those of an attention call", who);
-  int64_t at[5];
-  *bytes = attend_layout(num_slots, tokens, num_heads, at);
+  *bytes = attend_bytes(tokens, num_heads);
   return ok();
 }
 
