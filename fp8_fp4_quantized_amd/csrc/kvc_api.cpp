@@ -153,8 +153,9 @@ int attend(const kvc_attend_args* a, bool tree, void* stream, const char* who) {
   if (a->page_table == nullptr || a->pt_width < 1 || a->pt_stride < a->pt_width)
     return fail(KVC_EINVAL, "%s: page table needs 1 <= pt_width <= pt_stride (%lld, %lld)", who,
                 (long long)a->pt_width, (long long)a->pt_stride);
-  if (!(a->scale > 0.0f) || !std::isfinite(a->scale))
-    return fail(KVC_EINVAL, "%s: scale must be finite and > 0", who);
+  p.scale_log2 = (float)((double)a->scale * 1.4426950408889634074);
+  if (!(a->scale > 0.0f) || !std::isfinite(p.scale_log2))
+    return fail(KVC_EINVAL, "%s: scale must be > 0, and scale * log2(e) finite", who);
   const int64_t tokens = tree ? (int64_t)a->num_slots * a->draft_len : a->q_rows;
   const int64_t need = attend_bytes(tokens, a->num_heads);
   if (a->workspace == nullptr || ((uintptr_t)a->workspace & 255u) != 0 || a->workspace_bytes < need)
@@ -175,7 +176,6 @@ int attend(const kvc_attend_args* a, bool tree, void* stream, const char* who) {
   p.pt_stride = a->pt_stride;
   p.pt_width = a->pt_width;
   p.tree = tree ? a->tree : nullptr;
-  p.scale_log2 = (float)((double)a->scale * 1.4426950408889634074);
   p.sink = a->sink;
   p.out = static_cast<uint16_t*>(a->out);
   p.out_stride = a->out_stride;

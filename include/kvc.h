@@ -485,7 +485,7 @@ typedef struct kvc_attend_args {
   int64_t pt_stride;
   int64_t pt_width;           /* 1 .. pt_stride */
   const uint64_t* tree;       /* device [S * D] or NULL, tree mode */
-  float scale;                /* finite, > 0 */
+  float scale;                /* > 0, finite times log2(e) too */
   const float* sink;          /* device fp32 [H] or NULL */
   void* out;                  /* device bf16, strides as q's; must not overlap an input */
   int64_t out_stride;
