@@ -483,6 +483,13 @@ def _pt_stride(page_table) -> int:
     return page_table.stride(0) if page_table.shape[0] > 1 else page_table.shape[1]
 
 
+def _rows_are(t, n: int, name: str) -> None:
+    """Refuses a tensor of rows (two dims) that are not of n entries each, whose
+    entries the library would take as rows of n; a flat one passes."""
+    if t is not None and t.dim() > 1 and (t.dim() != 2 or t.shape[1] != n):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, need rows of {n}")
+
+
 def _call_on(dev, stream, fn, args) -> None:
     """One call with ``dev`` as the current device, on ``stream`` (default:
     that device's current stream)."""
@@ -518,6 +525,11 @@ def kvc_slot_map(*, ratio: int, page_size: int, num_pages: int, lens: torch.Tens
                           if t is not None], default=S * token_stride)
         per = 0                               # (no per-token tensor is shorter)
     on = lens.get_device()
+    if offsets is not None:
+        _need(offsets.dim() < 2 or offsets.shape == (2, S),
+              f"offsets: shape {tuple(offsets.shape)}, need (2, {S})")
+    if depth is not None and token_stride > 0:
+        _rows_are(depth, token_stride, "depth")
     lens_p = _i32(lens, S, "lens")            # (refuses one that is on no device)
     if page_table.get_device() != on:
         _one_device(lens.device, (("page_table", page_table),))
@@ -593,6 +605,7 @@ def kvc_attend_prefill(cache: Cache, q: torch.Tensor, offsets: torch.Tensor,
     where it is not given)."""
     S = start_pos.numel()
     _need(offsets.numel() == 2 * S, f"offsets: expected [2, {S}] entries")
+    _rows_are(offsets, S, "offsets")
     _attend(lib().kvc_attend_prefill, cache, q, start_pos, page_table, out, slots=S,
             tokens=q.shape[0], ratio=ratio, scale=scale, sink=sink, lse=lse, workspace=workspace,
             status=status, stream=stream, offsets=offsets)
@@ -612,6 +625,7 @@ def kvc_attend_tree(cache: Cache, q: torch.Tensor, start_pos: torch.Tensor,
     _need(q.dim() == 3 and q.shape[0] >= S * draft_len,
           f"q: shape {tuple(q.shape)} for {S} slots x {draft_len} tokens")
     _need(tree is None or tree.numel() >= S * draft_len, f"tree: expected [{S}, {draft_len}] masks")
+    _rows_are(tree, draft_len, "tree")
     _attend(lib().kvc_attend_tree, cache, q, start_pos, page_table, out, slots=S,
             tokens=S * draft_len, ratio=ratio, scale=scale, sink=sink, lse=lse,
             workspace=workspace, status=status, stream=stream, draft_len=draft_len, tree=tree)
