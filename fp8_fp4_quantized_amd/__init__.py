@@ -525,9 +525,9 @@ def kvc_slot_map(*, ratio: int, page_size: int, num_pages: int, lens: torch.Tens
                           if t is not None], default=S * token_stride)
         per = 0                               # (no per-token tensor is shorter)
     on = lens.get_device()
-    if offsets is not None:
-        _need(offsets.dim() < 2 or offsets.shape == (2, S),
-              f"offsets: shape {tuple(offsets.shape)}, need (2, {S})")
+    # (messages are made only where they are raised: one takes as long as three checks)
+    if offsets is not None and offsets.dim() > 1 and offsets.shape != (2, S):
+        raise ValueError(f"offsets: shape {tuple(offsets.shape)}, need (2, {S})")
     if depth is not None and token_stride > 0:
         _rows_are(depth, token_stride, "depth")
     lens_p = _i32(lens, S, "lens")            # (refuses one that is on no device)
@@ -535,7 +535,8 @@ def kvc_slot_map(*, ratio: int, page_size: int, num_pages: int, lens: torch.Tens
         _one_device(lens.device, (("page_table", page_table),))
     table_p = _rows(page_table, _I32_T, "page_table")
     rows, width = page_table.shape
-    _need(rows >= S, f"page_table: shape {tuple(page_table.shape)}, need {S} rows")
+    if rows < S:
+        raise ValueError(f"page_table: shape {tuple(page_table.shape)}, need {S} rows")
     _call_on(lens.device, stream, lib().kvc_slot_map, kvc_slot_map_args(
         ratio, page_size, num_pages, S, token_stride, lens_p,
         _i32_on(new_lens, S, "new_lens", on), _i32_on(depth, per, "depth", on), table_p,
