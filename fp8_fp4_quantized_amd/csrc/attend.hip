@@ -330,8 +330,9 @@ struct Rows {
 // that a vector instruction has just written needs two wait states (WAIT: s_nop
 // 1): the compiler keeps some of the queries of units of 32 and 64 in
 // accumulator registers and copies them over.  The other operands come from LDS
-// and from registers that stay, and need none (1 to 2% of the time); a test
-// reads the assembly for both.
+// and from registers that stay, and need none (1 to 2% of the time).  That rests
+// on the registers the compiler allocates: the build reads the assembly and
+// stops where a wait state is missing.
 // scores_done and out_done give the 16 wait states from a last result to a
 // vector instruction that reads it.
 template <bool WAIT>
