@@ -143,10 +143,14 @@ int attend(const kvc_attend_args* a, bool tree, void* stream, const char* who) {
   if (a->num_slots == 0 || a->q_rows == 0) return ok();
   if (a->q == nullptr || !aligned16(a->q) || a->out == nullptr || !aligned16(a->out))
     return fail(KVC_EINVAL, "%s: q and out must be non-NULL and 16-byte aligned", who);
-  if (a->q_stride < 0 || a->q_head_stride < 0 || a->q_stride % 8 != 0 || a->q_head_stride % 8 != 0)
+  // (the stride of an axis of one entry is not used)
+  p.q_stride = a->q_rows > 1 ? a->q_stride : 0;
+  p.q_hstride = a->num_heads > 1 ? a->q_head_stride : 0;
+  p.out_stride = a->q_rows > 1 ? a->out_stride : 512;
+  p.out_hstride = a->num_heads > 1 ? a->out_head_stride : 512;
+  if (p.q_stride < 0 || p.q_hstride < 0 || p.q_stride % 8 != 0 || p.q_hstride % 8 != 0)
     return fail(KVC_EINVAL, "%s: q strides must be multiples of 8, >= 0", who);
-  if (a->out_stride % 8 != 0 || a->out_head_stride % 8 != 0 ||
-      (a->q_rows > 1 && a->out_stride < 512) || (a->num_heads > 1 && a->out_head_stride < 512))
+  if (p.out_stride % 8 != 0 || p.out_hstride % 8 != 0 || p.out_stride < 512 || p.out_hstride < 512)
     return fail(KVC_EINVAL, "%s: out strides must be multiples of 8, >= 512", who);
   if (a->start_pos == nullptr) return fail(KVC_EINVAL, "%s: start_pos is NULL", who);
   if (!tree && a->offsets == nullptr) return fail(KVC_EINVAL, "%s: offsets is NULL", who);
@@ -167,8 +171,6 @@ int attend(const kvc_attend_args* a, bool tree, void* stream, const char* who) {
   p.num_slots = a->num_slots;
   p.draft_len = tree ? a->draft_len : 0;
   p.q = static_cast<const uint16_t*>(a->q);
-  p.q_stride = a->q_stride;
-  p.q_hstride = a->q_head_stride;
   p.q_rows = a->q_rows;
   p.offsets = tree ? nullptr : a->offsets;
   p.start_pos = a->start_pos;
@@ -178,8 +180,6 @@ int attend(const kvc_attend_args* a, bool tree, void* stream, const char* who) {
   p.tree = tree ? a->tree : nullptr;
   p.sink = a->sink;
   p.out = static_cast<uint16_t*>(a->out);
-  p.out_stride = a->out_stride;
-  p.out_hstride = a->out_head_stride;
   p.lse = a->lse;
   p.status = a->status;
   int qblocks = attend_qblocks(a->num_slots, tokens, a->num_heads);

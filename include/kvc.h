@@ -476,7 +476,8 @@ typedef struct kvc_attend_args {
   int32_t num_slots;          /* S, 0..8191 */
   int32_t draft_len;          /* tree: D, 1..64 (prefill: ignored) */
   const void* q;              /* device bf16: token t, head h at q + t*q_stride + h*q_head_stride */
-  int64_t q_stride;           /* elements, multiples of 8; q 16-byte aligned */
+  int64_t q_stride;           /* elements, multiples of 8 (an axis of one entry: any); q
+                                 16-byte aligned */
   int64_t q_head_stride;
   int64_t q_rows;             /* token rows q, out and lse hold; q_rows * H <= 2^31 - 256 */
   const int32_t* offsets;     /* device int32 [2, S], prefill (tree: ignored) */
