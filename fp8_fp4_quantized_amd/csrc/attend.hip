@@ -17,14 +17,16 @@
 // repeat bit for bit.
 //
 // What bounds it: a tile costs 2 * 2 * QT * NT * 512 flops and NT rows of 528
-// (V41), 288 (V41_FP4) or 584 (V4) bytes, so from 64 queries a unit up the
-// matrix units bound it (about 1.5 PFLOP/s: the clock falls to 1.6 GHz under
-// them) before HBM does; below, HBM.  What it reaches, in visible (query, row)
-// pairs * 2048 flops: 1.08 PFLOP/s on a prompt of 8,192 tokens with 128 heads
-// (V41, 8.1 ms), 0.68 on 16 prompts of some 2,000 tokens with 32 heads (V41_FP4,
-// 16 tiles a unit on average, 1.5 ms), 0.61 on 64 decodes with 64 heads
-// (V41_FP4, 124 us), 2.75 TB/s and 0.59 PFLOP/s on 128 chains of 4 with 16 heads
-// (V4, 124 us).
+// (V41), 288 (V41_FP4) or 584 (V4) bytes.  At about 1.5 PFLOP/s (the clock falls
+// to 1.6 GHz under the matrix units) and 5.2 TB/s the two take the same time at 75
+// queries a unit for V41, 41 for V41_FP4 and 83 for V4: units of 128 are bound by
+// the matrix units, units of 64 by them for V41_FP4 and by HBM for the others,
+// units of 32 by HBM.  What it reaches, in visible (query, row) pairs * 2048
+// flops: 1.08 PFLOP/s on a prompt of 8,192 tokens with 128 heads (V41, 8.1 ms),
+// 0.69 on 16 prompts of some 2,000 tokens with 32 heads (V41_FP4, 16 tiles a unit
+// on average, 1.5 ms), 0.61 to 0.63 on 64 decodes with 64 heads (V41_FP4, 120 to
+// 125 us), 2.6 to 2.7 TB/s and 0.56 to 0.58 PFLOP/s on 128 chains of 4 with 16
+// heads (V4, 125 to 129 us), 3.0 TB/s on 64 decodes with 32 heads (V41, 101 us).
 #include <type_traits>
 
 #include "launch_attend.hpp"
@@ -819,9 +821,9 @@ __device__ __forceinline__ void end_piece(const AttendParams& p, const Walk& w, 
 //
 // A wave is alone on its SIMD (O, the queries' fragments and the rows in flight
 // take its 512 registers), so its issue slots are what it runs out of: on 64
-// decodes with 64 heads over V41_FP4 rows it issues in 53% of its cycles, of
-// which 34% are vector instructions (the expansion of the rows for the most),
-// and the matrix units work in 28%.  Deeper read-ahead of the tiles' fragments
+// decodes with 64 heads over V41_FP4 rows it issues in 53% of its cycles, in 33%
+// vector instructions (the expansion of the rows for the most), and the matrix
+// units work in 29%.  Deeper read-ahead of the tiles' fragments
 // (8 instead of 6 for the scores, 5 instead of 3 for O) measured slower: 127 and
 // 131 against 125.5 us.
 //

@@ -87,7 +87,11 @@ bool page_size_ok(int32_t ps) { return ps >= 1 && ps <= 4096 && (ps & (ps - 1)) 
 // reads of the staged rows per query, a wide unit half full costs its empty
 // half: slots of up to 32 or 64 queries take units of that size.  Measured, a
 // token of 64 requests over V41_FP4 rows: 64 heads 123 us in units of 64, 172 in
-// units of 128; 32 heads 104 us in units of 32, 124 in units of 64.
+// units of 128; 32 heads 104 us in units of 32, 124 in units of 64.  The rule sees
+// the call's sizes, not the lengths, which are on the device: a packed step of a
+// 2,048-token prompt and 200 single tokens with 16 heads averages 180 queries a
+// slot and takes units of 128, 304 us where the prompt alone takes 114 and the
+// tokens alone 131.
 int attend_qblocks(int32_t slots, int64_t tokens, int32_t heads) {
   const int64_t per_slot = tokens * heads / (slots > 0 ? slots : 1);
   return per_slot <= 32 ? 1 : per_slot <= 64 ? 2 : 4;

@@ -39,8 +39,13 @@ struct SlotMapParams {
 
 // Workgroups of the attention kernel, one per compute unit of an MI355X, and
 // the fewest cache rows a workgroup takes (a call with fewer rows to read
-// uses fewer workgroups: each costs its share of the join).  One decode over
-// 1,000 rows and the other small calls measure the same with 64.
+// uses fewer workgroups: each costs its share of the join).  In tiles that is 1 of
+// units of 32, 2 of 64, 4 of 128.  Measured for one request, us a call with 64 /
+// 128 / 256 rows: a token of 16 heads over 1,000 rows 21.1 / 21.1 / 23.8 (64 and
+// 128 are a tile both), over 8,000 27.9 / 27.9 / 23.7; of 64 heads over 1,000 21.4
+// / 21.2 / 25.6, over 4,000 28.5 / 26.1 / 29.1, over 30,000 61.8 / 61.9 / 47.3 (the
+// join reads a part of every workgroup); 8 drafts of 16 heads over 2,000 29.1 /
+// 29.1 / 33.4, 64 drafts over 1,000 35.9 / 40.0 / 40.5.
 constexpr int kAttendWorkgroups = 256;
 constexpr int kAttendLeastRows = 128;
 

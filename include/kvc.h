@@ -442,6 +442,8 @@ int kvc_slot_map(const kvc_slot_map_args* args, void* stream);
  * and lse = +inf.  Scores and sums are fp32; the weights e^(s_r) are rounded
  * to bf16 for the second product (and the sum out is divided by is that of
  * the rounded weights), out is rounded to bf16.
+ * A merge of the parts of one query's rows (across ranks, say) counts the sink
+ * of every part whose lse holds it: give the sink to one of them.
  *
  * kvc_attend_prefill (packed tokens of different lengths, whole prompts or
  *   extends): slot b's tokens are rows offsets[b] .. + count - 1 of q, at
@@ -449,8 +451,10 @@ int kvc_slot_map(const kvc_slot_map_args* args, void* stream);
  *   at position p sees the compressed rows r < (p + 1) / ratio -- its request's
  *   rows up to the one it completes, which the caller has stored.  start_pos <
  *   0 or count <= 0: no tokens; rows outside [0, q_rows) skip the slot with
- *   KVC_STATUS_TOKEN_RANGE.  Slots' token rows must not overlap.  (Either
- *   call: positions past 2^31 - 257 skip the slot with KVC_STATUS_POS_RANGE.)
+ *   KVC_STATUS_TOKEN_RANGE.  Slots' token rows must not overlap.  (A long
+ *   prompt and many single tokens are faster in a call each: the work is cut
+ *   for q_rows * heads / num_slots queries a slot.)  (Either call: positions
+ *   past 2^31 - 257 skip the slot with KVC_STATUS_POS_RANGE.)
  * kvc_attend_tree (D = draft_len tokens per slot, rows b*D .. b*D + D - 1; D = 1
  *   is plain decode): tree = NULL: a chain, token j is at position start_pos[b]
  *   + j and sees as in prefill.  tree given (ratio 1): token j sees the rows
