@@ -14,9 +14,9 @@ from __future__ import annotations
 import glob
 import importlib.util
 import os
+import shutil
 import subprocess
 import sys
-import tempfile
 import concurrent.futures as cf
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -44,7 +44,9 @@ def _wait_states():
 def _compile(src: str, obj: str, verbose: bool, waits: bool = False) -> None:
     """One object; waits: its device assembly is read before it is put there."""
     if waits:
-        with tempfile.TemporaryDirectory() as tmp:
+        tmp = obj + ".parts"                      # (its name ends up in the object)
+        os.makedirs(tmp, exist_ok=True)
+        try:
             made = os.path.join(tmp, os.path.basename(obj))
             _hipcc(src, made, verbose, ["-save-temps=obj"])
             (text,) = glob.glob(os.path.join(tmp, f"*-{ARCH}.s"))
@@ -53,8 +55,9 @@ def _compile(src: str, obj: str, verbose: bool, waits: bool = False) -> None:
             if found:
                 raise RuntimeError(f"{src}: {len(found)} missing wait states at {count} matrix "
                                    f"instructions, the first: {found[:3]}")
-            with open(made, "rb") as fh, open(obj, "wb") as to:
-                to.write(fh.read())
+            os.replace(made, obj)
+        finally:
+            shutil.rmtree(tmp)
     else:
         _hipcc(src, obj, verbose, [])
 
