@@ -28,6 +28,8 @@ STATUS_ID_RANGE, STATUS_PAGE_RANGE, STATUS_PT_RANGE = 1, 2, 4
 STATUS_LATENT_RANGE, STATUS_POS_RANGE, STATUS_REQ_RANGE = 8, 16, 32
 STATUS_TOKEN_RANGE = 64
 STATUS_NO_PAGE = 128
+ROPE_SCALING = {"none": 0, "linear": 1, "base": 2, "parts": 3}
+WEIGH_FEW = 128        # (token, head) pairs a slot may have without a workspace
 
 
 class KvcError(RuntimeError):
@@ -94,6 +96,70 @@ class kvc_attend_args(C.Structure):
     ]
 
 
+class kvc_rope_table_args(C.Structure):
+    _fields_ = [
+        ("freqs", C.c_void_p), ("n", C.c_int64), ("first", C.c_int64), ("rot_dim", C.c_int32),
+        ("scaling", C.c_int32), ("base", C.c_double), ("factor", C.c_double),
+        ("original", C.c_double), ("beta_fast", C.c_double), ("beta_slow", C.c_double),
+        ("mscale", C.c_double),
+    ]
+
+
+class kvc_rope_args(C.Structure):
+    _fields_ = [
+        ("dtype", C.c_int32), ("num_heads", C.c_int32), ("head_dim", C.c_int32),
+        ("rot_dim", C.c_int32), ("offset", C.c_int32), ("half", C.c_int32),
+        ("transpose", C.c_int32), ("tokens", C.c_int64),
+        ("x", C.c_void_p), ("x_stride", C.c_int64), ("x_head_stride", C.c_int64),
+        ("out", C.c_void_p), ("out_stride", C.c_int64), ("out_head_stride", C.c_int64),
+        ("positions", C.c_void_p), ("freqs", C.c_void_p), ("max_pos", C.c_int64),
+        ("status", C.c_void_p),
+    ]
+
+
+class kvc_weigh_args(C.Structure):
+    _fields_ = [
+        ("ratio", C.c_int32), ("num_heads", C.c_int32), ("num_slots", C.c_int32),
+        ("draft_len", C.c_int32),
+        ("q", C.c_void_p), ("q_stride", C.c_int64), ("q_head_stride", C.c_int64),
+        ("q_rows", C.c_int64), ("lse", C.c_void_p),
+        ("offsets", C.c_void_p), ("start_pos", C.c_void_p),
+        ("page_table", C.c_void_p), ("pt_stride", C.c_int64), ("pt_width", C.c_int64),
+        ("tree", C.c_void_p), ("scale", C.c_float), ("decay", C.c_float),
+        ("prev", C.c_void_p), ("prev_stride", C.c_int64),
+        ("weights", C.c_void_p), ("w_stride", C.c_int64), ("w_width", C.c_int64),
+        ("cache", kvc_cache),
+        ("workspace", C.c_void_p), ("workspace_bytes", C.c_int64), ("status", C.c_void_p),
+    ]
+
+
+class kvc_evict_args(C.Structure):
+    _fields_ = [
+        ("ratio", C.c_int32), ("num_slots", C.c_int32), ("lens", C.c_void_p),
+        ("weights", C.c_void_p), ("w_stride", C.c_int64), ("w_width", C.c_int64),
+        ("budget", C.c_int32), ("first", C.c_int32), ("recent", C.c_int32),
+        ("budgets", C.c_void_p),
+        ("kept", C.c_void_p), ("kept_stride", C.c_int64), ("kept_width", C.c_int64),
+        ("counts", C.c_void_p), ("kept_weights", C.c_void_p), ("kw_stride", C.c_int64),
+        ("workspace", C.c_void_p), ("workspace_bytes", C.c_int64), ("status", C.c_void_p),
+    ]
+
+
+class kvc_compact_args(C.Structure):
+    _fields_ = [
+        ("ratio", C.c_int32), ("num_slots", C.c_int32), ("lens", C.c_void_p),
+        ("kept", C.c_void_p), ("kept_stride", C.c_int64), ("kept_width", C.c_int64),
+        ("counts", C.c_void_p),
+        ("page_table", C.c_void_p), ("pt_stride", C.c_int64), ("pt_width", C.c_int64),
+        ("free_pages", C.c_void_p), ("n_free", C.c_int64),
+        ("new_table", C.c_void_p), ("nt_stride", C.c_int64), ("new_lens", C.c_void_p),
+        ("kept_weights", C.c_void_p), ("kw_stride", C.c_int64),
+        ("weights", C.c_void_p), ("w_stride", C.c_int64), ("w_width", C.c_int64),
+        ("freed", C.c_void_p), ("freed_cap", C.c_int64), ("totals", C.c_void_p),
+        ("cache", kvc_cache), ("status", C.c_void_p),
+    ]
+
+
 # symbol -> (restype, argtypes); the same list as include/kvc.h
 _VP, _I32, _I64 = C.c_void_p, C.c_int32, C.c_int64
 SIGNATURES = {
@@ -115,6 +181,14 @@ SIGNATURES = {
     "kvc_attend_workspace": (C.c_int, [_I32, _I64, _I32, C.POINTER(_I64)]),
     "kvc_attend_prefill": (C.c_int, [C.POINTER(kvc_attend_args), _VP]),
     "kvc_attend_tree": (C.c_int, [C.POINTER(kvc_attend_args), _VP]),
+    "kvc_rope_table": (C.c_int, [C.POINTER(kvc_rope_table_args), _VP]),
+    "kvc_rope_rows": (C.c_int, [C.POINTER(kvc_rope_args), _VP]),
+    "kvc_weigh_workspace": (C.c_int, [C.POINTER(_I64)]),
+    "kvc_weigh_prefill": (C.c_int, [C.POINTER(kvc_weigh_args), _VP]),
+    "kvc_weigh_tree": (C.c_int, [C.POINTER(kvc_weigh_args), _VP]),
+    "kvc_evict_workspace": (C.c_int, [_I32, _I64, C.POINTER(_I64)]),
+    "kvc_evict_select": (C.c_int, [C.POINTER(kvc_evict_args), _VP]),
+    "kvc_cache_compact": (C.c_int, [C.POINTER(kvc_compact_args), _VP]),
     "kvc_last_error": (C.c_char_p, []),
     "kvc_version": (C.c_int, []),
 }
@@ -630,3 +704,246 @@ def kvc_attend_tree(cache: Cache, q: torch.Tensor, start_pos: torch.Tensor,
     _attend(lib().kvc_attend_tree, cache, q, start_pos, page_table, out, slots=S,
             tokens=S * draft_len, ratio=ratio, scale=scale, sink=sink, lse=lse,
             workspace=workspace, status=status, stream=stream, draft_len=draft_len, tree=tree)
+
+
+# -------------------------------------------------------------------- rotary
+_DTYPES = {torch.bfloat16: 0, torch.int16: 0, torch.uint16: 0, torch.float16: 1, torch.float32: 2}
+
+
+def kvc_rope_table(out: torch.Tensor, *, first: int = 0, base: float = 10000.0,
+                   scaling: str = "none", factor: float = 1.0, original: float = 0.0,
+                   beta_fast: float = 32.0, beta_slow: float = 1.0, mscale: float = 1.0,
+                   stream=None) -> None:
+    """The rotary table of positions ``first ..`` into ``out [n, rot_dim]``
+    (fp32, (cos, sin) pairs).  ``scaling``: "none", "linear", "base" or
+    "parts" (by ``factor``; "parts" from an ``original`` context, between
+    ``beta_fast`` and ``beta_slow`` turns); ``mscale`` multiplies the
+    entries."""
+    _need(out.dim() == 2, f"out: expected [positions, rot_dim], got shape {tuple(out.shape)}")
+    _need(scaling in ROPE_SCALING, f"scaling: {scaling!r}, one of {sorted(ROPE_SCALING)}")
+    a = kvc_rope_table_args(_dense(out, _F32_T, "out"), out.shape[0], first, out.shape[1],
+                            ROPE_SCALING[scaling], base, factor, original, beta_fast, beta_slow,
+                            mscale)
+    _call_on(out.device, stream, lib().kvc_rope_table, a)
+
+
+def kvc_rope_rows(x: torch.Tensor, positions: torch.Tensor, freqs: torch.Tensor,
+                  out: torch.Tensor | None = None, *, offset: int | None = None,
+                  half: bool = False, transpose: bool = False,
+                  status: torch.Tensor | None = None, stream=None) -> None:
+    """Rotate ``x [T, H, D]`` or ``[T, D]`` (bf16, fp16 or fp32) at
+    ``positions [T]`` by the table ``freqs [max_pos, rot_dim]`` into ``out``
+    (default: in place).  The rotated dims are ``offset ..`` (default: the
+    last ``rot_dim``), pairs of neighbours or of ``half``s; ``transpose`` is
+    the inverse rotation, which is also the rotation's backward pass."""
+    if out is None:
+        out = x
+    for name, t in (("x", x), ("out", out)):
+        _need(t.is_cuda and t.dtype in _DTYPES and t.dim() in (2, 3) and
+              (t.stride(-1) == 1 or t.shape[-1] == 1),
+              f"{name}: expected a [tokens, heads, dims] or [tokens, dims] device tensor of bf16, fp16 "
+              f"or fp32 with contiguous rows, got {t.dtype} {tuple(t.shape)} strides {t.stride()}")
+    _need(out.shape == x.shape and out.dtype == x.dtype,
+          f"out: {out.dtype} {tuple(out.shape)}, x is {x.dtype} {tuple(x.shape)}")
+    T, D = x.shape[0], x.shape[-1]
+    H = x.shape[1] if x.dim() == 3 else 1
+    _one_device(x.device, (("out", out), ("positions", positions), ("freqs", freqs),
+                           ("status", status)))
+    _need(freqs.dim() == 2, f"freqs: shape {tuple(freqs.shape)}, expected [max_pos, rot_dim]")
+    if T == 0 or H == 0:
+        return
+    x0, o0 = x.stride(0), out.stride(0)
+    x1, o1 = (x.stride(1), out.stride(1)) if x.dim() == 3 else (0, 0)
+    # a written row must be its own
+    _need(T <= 1 or H <= 1 or o0 >= (H - 1) * o1 + D or o1 >= (T - 1) * o0 + D,
+          f"out: overlapping rows (strides {out.stride()})")
+    apart = out.data_ptr() - x.data_ptr()
+    _need(apart == 0 or x.stride() != out.stride() or abs(apart) >= D * x.element_size(),
+          "out: overlaps x without being x")
+    rot = freqs.shape[1]
+    a = kvc_rope_args(_DTYPES[x.dtype], H, D, rot, D - rot if offset is None else offset, half,
+                      transpose, T, x.data_ptr(), x0, x1, out.data_ptr(), o0, o1,
+                      _i32(positions, T, "positions"), _dense(freqs, _F32_T, "freqs"),
+                      freqs.shape[0], _i32(status, 1, "status"))
+    _call_on(x.device, stream, lib().kvc_rope_rows, a)
+
+
+# ------------------------------------------------------------------ eviction
+def _table(t, types, rows: int, width: int, name: str):
+    """Pointer, row stride of a 2-D device tensor of at least ``rows`` rows of
+    ``width`` entries, or (None, 0) for None."""
+    if t is None:
+        return None, 0
+    at = _rows(t, types, name)
+    if t.shape[0] < rows or t.shape[1] < width:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, need at least [{rows}, {width}]")
+    return at, _pt_stride(t)
+
+
+def _scratch(n: int, dev, stream):
+    """Workspace of n bytes, of the stream the call runs on (the allocator then
+    reuses it in order)."""
+    with torch.cuda.device(dev), torch.cuda.stream(stream):
+        return torch.empty(n, dtype=torch.uint8, device=dev)
+
+
+_weigh_bytes = None
+
+
+def kvc_weigh_workspace() -> int:
+    """Workspace bytes of a kvc_weigh_* call that needs one (a slot with more
+    than ``WEIGH_FEW`` (token, head) pairs)."""
+    global _weigh_bytes
+    if _weigh_bytes is None:
+        n = C.c_int64(0)
+        _check(lib().kvc_weigh_workspace(C.byref(n)))
+        _weigh_bytes = n.value
+    return _weigh_bytes
+
+
+def _weigh(fn, cache: Cache, q, lse, start_pos, page_table, weights, *, slots, pairs, ratio, scale,
+           prev, decay, workspace, status, stream, offsets=None, draft_len=0, tree=None) -> None:
+    _need(q.is_cuda and q.dtype in _B16_T and q.dim() == 3 and q.shape[2] == 512 and q.stride(2) == 1,
+          f"q: expected a [tokens, heads, 512] bf16 device tensor with contiguous rows, got {q.dtype} "
+          f"{tuple(q.shape)} strides {q.stride()}")
+    T, H, _ = q.shape
+    dev = q.device
+    _one_device(dev, (("cache", cache.data), ("lse", lse), ("start_pos", start_pos),
+                      ("page_table", page_table), ("offsets", offsets), ("tree", tree),
+                      ("weights", weights), ("prev", prev), ("workspace", workspace),
+                      ("status", status)))
+    _need(tuple(lse.shape) == (T, H), f"lse: shape {tuple(lse.shape)}, expected [{T}, {H}]")
+    _need(weights.dim() == 2, f"weights: shape {tuple(weights.shape)}, expected [slots, rows]")
+    table, pt_stride = _table(page_table, _I32_T, slots, 0, "page_table")
+    W = weights.shape[1]
+    w, w_stride = _table(weights, _F32_T, slots, 0, "weights")
+    old, old_stride = _table(prev, _F32_T, slots, W, "prev")
+    if pairs > WEIGH_FEW and workspace is None:
+        workspace = _scratch(kvc_weigh_workspace(), dev, stream)
+    a = kvc_weigh_args(
+        ratio, H, slots, draft_len, q.data_ptr(), q.stride(0), q.stride(1), T,
+        _dense(lse, _F32_T, "lse"), _i32(offsets, 2 * slots, "offsets"),
+        _i32(start_pos, slots, "start_pos"), table, pt_stride, page_table.shape[1],
+        _opt(tree, _dense, (torch.int64, torch.uint64), "tree"), scale, decay, old, old_stride,
+        w, w_stride, W, cache.desc(), _opt(workspace, _dense, (torch.uint8,), "workspace"),
+        0 if workspace is None else workspace.numel(), _i32(status, 1, "status"))
+    _call_on(dev, stream, fn, a)
+
+
+def kvc_weigh_prefill(cache: Cache, q: torch.Tensor, lse: torch.Tensor, offsets: torch.Tensor,
+                      start_pos: torch.Tensor, page_table: torch.Tensor, weights: torch.Tensor, *,
+                      scale: float, ratio: int = 1, prev: torch.Tensor | None = None,
+                      decay: float = 1.0, workspace: torch.Tensor | None = None,
+                      status: torch.Tensor | None = None, stream=None) -> None:
+    """Attention weight that the cached rows collect from packed tokens: for
+    every row its tokens see, ``weights [S, rows]`` becomes ``decay`` times
+    ``prev`` (default: 0; may be ``weights``) plus the sum of the weights that
+    ``kvc_attend_prefill`` gave the row, whose ``q [T, H, 512]`` and
+    ``lse [T, H]`` these are.  ``workspace``: a uint8 tensor of
+    ``kvc_weigh_workspace`` bytes (allocated per call where it is needed and
+    not given)."""
+    S = start_pos.numel()
+    _need(offsets.numel() == 2 * S, f"offsets: expected [2, {S}] entries")
+    _rows_are(offsets, S, "offsets")
+    _weigh(lib().kvc_weigh_prefill, cache, q, lse, start_pos, page_table, weights, slots=S,
+           pairs=q.shape[0] * q.shape[1] if q.dim() == 3 else 0, ratio=ratio, scale=scale, prev=prev,
+           decay=decay, workspace=workspace, status=status, stream=stream, offsets=offsets)
+
+
+def kvc_weigh_tree(cache: Cache, q: torch.Tensor, lse: torch.Tensor, start_pos: torch.Tensor,
+                   page_table: torch.Tensor, weights: torch.Tensor, *, scale: float,
+                   draft_len: int = 1, tree: torch.Tensor | None = None, ratio: int = 1,
+                   prev: torch.Tensor | None = None, decay: float = 1.0,
+                   workspace: torch.Tensor | None = None, status: torch.Tensor | None = None,
+                   stream=None) -> None:
+    """kvc_weigh_prefill for ``draft_len`` tokens per slot, ``q [S *
+    draft_len, H, 512]`` and the ``lse`` that ``kvc_attend_tree`` gave: a
+    chain, a tree of ancestor masks, or single tokens."""
+    S = start_pos.numel()
+    _need(q.dim() == 3 and q.shape[0] >= S * draft_len,
+          f"q: shape {tuple(q.shape)} for {S} slots x {draft_len} tokens")
+    _need(tree is None or tree.numel() >= S * draft_len, f"tree: expected [{S}, {draft_len}] masks")
+    _rows_are(tree, draft_len, "tree")
+    _weigh(lib().kvc_weigh_tree, cache, q, lse, start_pos, page_table, weights, slots=S,
+           pairs=draft_len * q.shape[1], ratio=ratio, scale=scale, prev=prev, decay=decay,
+           workspace=workspace, status=status, stream=stream, draft_len=draft_len, tree=tree)
+
+
+def kvc_evict_workspace(num_slots: int, w_width: int) -> int:
+    """Workspace bytes of kvc_evict_select over ``num_slots`` rows of
+    ``w_width`` weights."""
+    n = C.c_int64(0)
+    _check(lib().kvc_evict_workspace(num_slots, w_width, C.byref(n)))
+    return n.value
+
+
+def kvc_evict_select(lens: torch.Tensor, weights: torch.Tensor, kept: torch.Tensor,
+                     counts: torch.Tensor, *, budget: int | None = None, ratio: int = 1,
+                     first: int = 0, recent: int = 0, budgets: torch.Tensor | None = None,
+                     kept_weights: torch.Tensor | None = None,
+                     workspace: torch.Tensor | None = None, status: torch.Tensor | None = None,
+                     stream=None) -> None:
+    """The rows that stay of slots of ``lens [S]`` tokens: at most ``budget``
+    (default: as many as ``kept`` holds) or ``budgets [S]`` rows, the
+    ``first`` and the ``recent`` ones and, of the others, those with the
+    greatest ``weights [S, rows]``.  Their numbers go to ``kept [S, K]``
+    (ascending, then -1), their count to ``counts [S]`` (-1: an inactive or
+    refused slot), their weights to ``kept_weights [S, K]``."""
+    S = lens.numel()
+    on = lens.get_device()
+    lens_p = _i32(lens, S, "lens")            # (refuses one that is on no device)
+    _one_device(lens.device, (("weights", weights), ("kept", kept), ("kept_weights", kept_weights),
+                              ("workspace", workspace)))
+    w, w_stride = _table(weights, _F32_T, S, 0, "weights")
+    k, k_stride = _table(kept, _I32_T, S, 0, "kept")
+    K = kept.shape[1]
+    kw, kw_stride = _table(kept_weights, _F32_T, S, K, "kept_weights")
+    W = weights.shape[1]
+    if workspace is None and S > 0 and W > 0:
+        n = kvc_evict_workspace(S, W)
+        if n > 0:
+            workspace = _scratch(n, lens.device, stream)
+    a = kvc_evict_args(
+        ratio, S, lens_p, w, w_stride, W, K if budget is None else budget, first, recent,
+        _i32_on(budgets, S, "budgets", on), k, k_stride, K, _i32_on(counts, S, "counts", on), kw,
+        kw_stride, _opt(workspace, _dense, (torch.uint8,), "workspace"),
+        0 if workspace is None else workspace.numel(), _i32_on(status, 1, "status", on))
+    _call_on(lens.device, stream, lib().kvc_evict_select, a)
+
+
+def kvc_cache_compact(cache: Cache, lens: torch.Tensor, kept: torch.Tensor, counts: torch.Tensor,
+                      page_table: torch.Tensor, free_pages: torch.Tensor, new_table: torch.Tensor,
+                      new_lens: torch.Tensor, *, ratio: int = 1,
+                      kept_weights: torch.Tensor | None = None,
+                      weights: torch.Tensor | None = None, freed: torch.Tensor | None = None,
+                      totals: torch.Tensor | None = None, status: torch.Tensor | None = None,
+                      stream=None) -> None:
+    """Move the rows ``kept [S, K]`` (``counts [S]`` of them) of slots that drop
+    some to pages of ``free_pages``: ``new_table [S, pages]`` and ``new_lens
+    [S]`` say where the slots are afterwards, ``freed`` lists the pages given
+    back, ``kept_weights [S, K]`` goes to the front of ``weights [S, rows]``,
+    and ``totals [4]`` counts pages taken, pages given back, rows dropped and
+    slots refused."""
+    S = lens.numel()
+    on = lens.get_device()
+    lens_p = _i32(lens, S, "lens")            # (refuses one that is on no device)
+    _one_device(lens.device, (("cache", cache.data), ("kept", kept), ("page_table", page_table),
+                              ("new_table", new_table), ("kept_weights", kept_weights),
+                              ("weights", weights)))
+    k, k_stride = _table(kept, _I32_T, S, 0, "kept")
+    K = kept.shape[1]
+    table, pt_stride = _table(page_table, _I32_T, S, 0, "page_table")
+    width = page_table.shape[1]
+    new, nt_stride = _table(new_table, _I32_T, S, width, "new_table")
+    kw, kw_stride = _table(kept_weights, _F32_T, S, K, "kept_weights")
+    w, w_stride = _table(weights, _F32_T, S, 0, "weights")
+    # (an empty tensor has no address: the library would take it as none given)
+    _need(freed is None or freed.numel() > 0 or S == 0, "freed: holds no page")
+    a = kvc_compact_args(
+        ratio, S, lens_p, k, k_stride, K, _i32_on(counts, S, "counts", on), table, pt_stride, width,
+        _i32_on(free_pages, 0, "free_pages", on), free_pages.numel(), new, nt_stride,
+        _i32_on(new_lens, S, "new_lens", on), kw, kw_stride, w, w_stride,
+        0 if weights is None else weights.shape[1], _i32_on(freed, 0, "freed", on),
+        0 if freed is None else freed.numel(), _i32_on(totals, 4, "totals", on), cache.desc(),
+        _i32_on(status, 1, "status", on))
+    _call_on(lens.device, stream, lib().kvc_cache_compact, a)

@@ -12,7 +12,7 @@
 #include <cstring>
 #include <string>
 
-#include "launch_attend.hpp"
+#include "launch_evict.hpp"
 
 namespace {
 
@@ -204,6 +204,126 @@ int attend(const kvc_attend_args* a, bool tree, void* stream, const char* who) {
   p.part_ml = reinterpret_cast<float4*>(w + at[3]);
   p.part_o = reinterpret_cast<float*>(w + at[4]);
   return launched(kvc::launch_attend(p, qblocks, static_cast<hipStream_t>(stream)), who);
+}
+
+// ------------------------------------------------------------------ rotary
+// pair index that makes `turns` turns over the original context
+double pair_of_turns(const kvc_rope_table_args* a, double turns) {
+  return a->rot_dim * std::log(a->original / (turns * 6.283185307179586477)) / (2.0 * std::log(a->base));
+}
+
+// speeds as half turns a position
+void rope_speeds(const kvc_rope_table_args* a, double* speed) {
+  const int R = a->rot_dim;
+  const double base = a->scaling == KVC_ROPE_BASE ? a->base * std::pow(a->factor, double(R) / (R - 2)) : a->base;
+  double lo = 0.0, hi = 0.0;
+  if (a->scaling == KVC_ROPE_PARTS) {
+    lo = std::fmax(std::floor(pair_of_turns(a, a->beta_fast)), 0.0);
+    hi = std::fmin(std::ceil(pair_of_turns(a, a->beta_slow)), double(R - 1));
+  }
+  for (int j = 0; j < R / 2; ++j) {
+    double w = std::pow(base, -2.0 * j / R);
+    if (a->scaling == KVC_ROPE_LINEAR) {
+      w /= a->factor;
+    } else if (a->scaling == KVC_ROPE_PARTS) {
+      const double r = std::fmin(std::fmax((j - lo) / std::fmax(hi - lo, 0.001), 0.0), 1.0);
+      w = w * (1.0 - r) + w / a->factor * r;
+    }
+    speed[j] = w / 3.141592653589793238;
+  }
+}
+
+bool positive(double v) { return v > 0.0 && std::isfinite(v); }
+
+// ------------------------------------------------------------------ weights
+constexpr int64_t kWeighSplitBytes = kvc::kWeighWorkgroups * (int64_t)sizeof(kvc::WeighSplit);
+constexpr int64_t kWeighBytes = kWeighSplitBytes + 2 * kvc::kWeighWorkgroups * kvc::kWeighRows * (int64_t)sizeof(float);
+
+int weigh(const kvc_weigh_args* a, bool tree, void* stream, const char* who) {
+  if (a == nullptr) return fail(KVC_EINVAL, "%s: args is NULL", who);
+  kvc::WeighParams p{};
+  int rc = check_cache(&a->cache, &p.cache, who);
+  if (rc) return rc;
+  if (a->ratio != 1 && a->ratio != 2) return fail(KVC_EUNSUPPORTED, "%s: ratio %d (1 or 2)", who, a->ratio);
+  if (a->num_heads < 1 || a->num_heads > 1024)
+    return fail(KVC_EINVAL, "%s: num_heads %d outside [1, 1024]", who, a->num_heads);
+  if (a->num_slots < 0 || a->num_slots > kvc::kMaxSlots)
+    return fail(KVC_EINVAL, "%s: num_slots %d outside [0, %d]", who, a->num_slots, kvc::kMaxSlots);
+  if (a->q_rows < 0 || a->q_rows > kMaxQueries / a->num_heads)
+    return fail(KVC_EINVAL, "%s: q_rows %lld: q_rows * num_heads must not pass 2^31 - 256", who,
+                (long long)a->q_rows);
+  if (tree) {
+    if (a->draft_len < 1 || a->draft_len > 64)
+      return fail(KVC_EINVAL, "%s: draft_len %d outside [1, 64]", who, a->draft_len);
+    if (a->tree != nullptr && a->ratio != 1)
+      return fail(KVC_EUNSUPPORTED, "%s: a tree needs ratio 1 (a cached row per drafted token)", who);
+    if (a->q_rows < (int64_t)a->num_slots * a->draft_len)
+      return fail(KVC_EINVAL, "%s: q_rows %lld, need num_slots * draft_len = %lld", who,
+                  (long long)a->q_rows, (long long)a->num_slots * a->draft_len);
+  }
+  if (!(a->decay >= 0.0f) || !std::isfinite(a->decay))
+    return fail(KVC_EINVAL, "%s: decay must be finite, >= 0", who);
+  p.scale_log2 = (float)((double)a->scale * 1.4426950408889634074);
+  if (!(a->scale > 0.0f) || !std::isfinite(p.scale_log2))
+    return fail(KVC_EINVAL, "%s: scale must be > 0, and scale * log2(e) finite", who);
+  if (a->num_slots == 0 || a->q_rows == 0) return ok();
+  if (a->q == nullptr || !aligned16(a->q)) return fail(KVC_EINVAL, "%s: q must be non-NULL and 16-byte aligned", who);
+  // (the stride of an axis of one entry is not used)
+  p.q_stride = a->q_rows > 1 ? a->q_stride : 0;
+  p.q_hstride = a->num_heads > 1 ? a->q_head_stride : 0;
+  if (p.q_stride < 0 || p.q_hstride < 0 || p.q_stride % 8 != 0 || p.q_hstride % 8 != 0)
+    return fail(KVC_EINVAL, "%s: q strides must be multiples of 8, >= 0", who);
+  if (a->lse == nullptr || a->start_pos == nullptr || (!tree && a->offsets == nullptr))
+    return fail(KVC_EINVAL, "%s: NULL lse, start_pos or offsets", who);
+  if (a->page_table == nullptr || a->pt_width < 1 || a->pt_stride < a->pt_width)
+    return fail(KVC_EINVAL, "%s: page table needs 1 <= pt_width <= pt_stride (%lld, %lld)", who,
+                (long long)a->pt_width, (long long)a->pt_stride);
+  if (a->weights == nullptr || a->w_width < 1 || a->w_stride < a->w_width)
+    return fail(KVC_EINVAL, "%s: weights need 1 <= w_width <= w_stride (%lld, %lld)", who,
+                (long long)a->w_width, (long long)a->w_stride);
+  if (a->prev != nullptr && a->prev_stride < a->w_width)
+    return fail(KVC_EINVAL, "%s: prev_stride %lld below w_width %lld", who, (long long)a->prev_stride,
+                (long long)a->w_width);
+  if (a->prev == a->weights && a->prev_stride != a->w_stride)
+    return fail(KVC_EINVAL, "%s: prev is weights, with another stride", who);
+  if (a->weights == a->lse) return fail(KVC_EINVAL, "%s: weights must not be an input", who);
+  const int64_t slot_queries = (tree ? (int64_t)a->draft_len : a->q_rows) * a->num_heads;
+  if (slot_queries > kvc::kWeighFew &&
+      (a->workspace == nullptr || ((uintptr_t)a->workspace & 255u) != 0 || a->workspace_bytes < kWeighBytes))
+    return fail(KVC_EINVAL, "%s: workspace needs %lld bytes, 256-byte aligned", who, (long long)kWeighBytes);
+  if (kvc::launch_weigh == nullptr) return fail(KVC_ELAUNCH, "%s: built without kernels", who);
+  p.ratio = a->ratio;
+  p.heads = a->num_heads;
+  p.head_div = kvc::div_magic((uint32_t)a->num_heads);
+  p.num_slots = a->num_slots;
+  p.draft_len = tree ? a->draft_len : 0;
+  p.q = static_cast<const uint16_t*>(a->q);
+  p.q_rows = a->q_rows;
+  p.lse = a->lse;
+  p.offsets = tree ? nullptr : a->offsets;
+  p.start_pos = a->start_pos;
+  p.page_table = a->page_table;
+  p.pt_stride = a->pt_stride;
+  p.pt_width = a->pt_width;
+  p.tree = tree ? a->tree : nullptr;
+  p.decay = a->decay;
+  p.prev = a->prev;
+  p.prev_stride = a->prev_stride;
+  p.weights = a->weights;
+  p.w_stride = a->w_stride;
+  p.w_width = a->w_width;
+  p.status = a->status;
+  if (slot_queries > kvc::kWeighFew) {
+    p.splits = static_cast<kvc::WeighSplit*>(a->workspace);
+    p.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(a->workspace) + kWeighSplitBytes);
+  }
+  return launched(kvc::launch_weigh(p, slot_queries, static_cast<hipStream_t>(stream)), who);
+}
+
+// ------------------------------------------------------------------ eviction
+int64_t evict_bytes(int32_t slots, int64_t width) {
+  (void)slots, (void)width;
+  return 0;
 }
 
 }  // namespace
@@ -587,6 +707,222 @@ int kvc_attend_prefill(const kvc_attend_args* args, void* stream) {
 
 int kvc_attend_tree(const kvc_attend_args* args, void* stream) {
   return attend(args, true, stream, "kvc_attend_tree");
+}
+
+// ----------------------------------------------------------------- rotary
+int kvc_rope_table(const kvc_rope_table_args* a, void* stream) {
+  const char* who = "kvc_rope_table";
+  if (a == nullptr) return fail(KVC_EINVAL, "%s: args is NULL", who);
+  if (a->scaling < KVC_ROPE_NONE || a->scaling > KVC_ROPE_PARTS)
+    return fail(KVC_EUNSUPPORTED, "%s: scaling %d", who, a->scaling);
+  const int least = a->scaling == KVC_ROPE_BASE ? 4 : 2;
+  if (a->rot_dim < least || a->rot_dim > 2 * kvc::kRopeMaxPairs || a->rot_dim % 2 != 0)
+    return fail(KVC_EINVAL, "%s: rot_dim %d must be even, in [%d, %d]", who, a->rot_dim, least,
+                2 * kvc::kRopeMaxPairs);
+  const int64_t end = (int64_t)1 << 31;
+  if (a->n < 0 || a->first < 0 || a->first > end || a->n > end - a->first)
+    return fail(KVC_EINVAL, "%s: first and n must be >= 0, first + n at most 2^31", who);
+  if (!(a->base > 1.0) || !std::isfinite(a->base)) return fail(KVC_EINVAL, "%s: base must be > 1", who);
+  if (a->scaling != KVC_ROPE_NONE && !positive(a->factor))
+    return fail(KVC_EINVAL, "%s: factor must be > 0", who);
+  if (a->scaling == KVC_ROPE_PARTS &&
+      (!positive(a->original) || !positive(a->beta_slow) || !(a->beta_fast >= a->beta_slow) ||
+       !std::isfinite(a->beta_fast)))
+    return fail(KVC_EINVAL, "%s: scaling by parts needs original > 0 and beta_fast >= beta_slow > 0", who);
+  if (!positive(a->mscale)) return fail(KVC_EINVAL, "%s: mscale must be > 0", who);
+  if (a->n == 0) return ok();
+  if (a->freqs == nullptr || !aligned16(a->freqs))
+    return fail(KVC_EINVAL, "%s: freqs must be non-NULL, 16-byte aligned", who);
+  kvc::RopeTableParams p{};
+  rope_speeds(a, p.speed);
+  for (int j = 0; j < a->rot_dim / 2; ++j)
+    if (!std::isfinite(p.speed[j])) return fail(KVC_EINVAL, "%s: base and factor give no finite speeds", who);
+  if (kvc::launch_rope_table == nullptr) return fail(KVC_ELAUNCH, "%s: built without kernels", who);
+  p.freqs = a->freqs;
+  p.n = a->n;
+  p.first = a->first;
+  p.pairs = a->rot_dim / 2;
+  p.mscale = a->mscale;
+  return launched(kvc::launch_rope_table(p, static_cast<hipStream_t>(stream)), who);
+}
+
+int kvc_rope_rows(const kvc_rope_args* a, void* stream) {
+  const char* who = "kvc_rope_rows";
+  if (a == nullptr) return fail(KVC_EINVAL, "%s: args is NULL", who);
+  if (a->dtype < KVC_BF16 || a->dtype > KVC_FP32) return fail(KVC_EUNSUPPORTED, "%s: dtype %d", who, a->dtype);
+  if (a->num_heads < 1 || a->num_heads > 1024)
+    return fail(KVC_EINVAL, "%s: num_heads %d outside [1, 1024]", who, a->num_heads);
+  if (a->head_dim < 2 || a->head_dim > 8192)
+    return fail(KVC_EINVAL, "%s: head_dim %d outside [2, 8192]", who, a->head_dim);
+  if (a->rot_dim < 2 || a->rot_dim > a->head_dim || a->rot_dim % 2 != 0)
+    return fail(KVC_EINVAL, "%s: rot_dim %d must be even, in [2, head_dim]", who, a->rot_dim);
+  if (a->offset < 0 || a->offset > a->head_dim - a->rot_dim)
+    return fail(KVC_EINVAL, "%s: offset %d outside [0, head_dim - rot_dim]", who, a->offset);
+  if (a->tokens < 0 || a->tokens > 0x7FFFFFFF) return fail(KVC_EINVAL, "%s: tokens outside [0, 2^31)", who);
+  if (a->max_pos < 1) return fail(KVC_EINVAL, "%s: max_pos must be >= 1", who);
+  if (a->tokens == 0) return ok();
+  const uintptr_t size = a->dtype == KVC_FP32 ? 4 : 2;
+  if (a->x == nullptr || a->out == nullptr || (uintptr_t)a->x % size != 0 || (uintptr_t)a->out % size != 0)
+    return fail(KVC_EINVAL, "%s: x and out must be non-NULL and aligned to their type", who);
+  kvc::RopeRowsParams p{};
+  // (the stride of an axis of one entry is not used)
+  p.x_stride = a->tokens > 1 ? a->x_stride : 0;
+  p.x_hstride = a->num_heads > 1 ? a->x_head_stride : 0;
+  p.out_stride = a->tokens > 1 ? a->out_stride : 0;
+  p.out_hstride = a->num_heads > 1 ? a->out_head_stride : 0;
+  if (p.x_stride < 0 || p.x_hstride < 0) return fail(KVC_EINVAL, "%s: x strides must be >= 0", who);
+  if ((a->tokens > 1 && p.out_stride < a->head_dim) || (a->num_heads > 1 && p.out_hstride < a->head_dim))
+    return fail(KVC_EINVAL, "%s: out strides must be >= head_dim", who);
+  p.in_place = a->x == a->out;
+  if (p.in_place && (p.x_stride != p.out_stride || p.x_hstride != p.out_hstride))
+    return fail(KVC_EINVAL, "%s: out is x, with other strides", who);
+  if (a->positions == nullptr || a->freqs == nullptr || (uintptr_t)a->freqs % 8 != 0)
+    return fail(KVC_EINVAL, "%s: NULL positions or freqs, or freqs not 8-byte aligned", who);
+  if (kvc::launch_rope_rows == nullptr) return fail(KVC_ELAUNCH, "%s: built without kernels", who);
+  p.x = a->x;
+  p.out = a->out;
+  p.tokens = a->tokens;
+  p.heads = a->num_heads;
+  p.dim = a->head_dim;
+  p.rot = a->rot_dim;
+  p.offset = a->offset;
+  p.type = a->dtype;
+  p.half = a->half != 0;
+  p.transpose = a->transpose != 0;
+  p.positions = a->positions;
+  p.freqs = a->freqs;
+  p.max_pos = a->max_pos;
+  p.status = a->status;
+  return launched(kvc::launch_rope_rows(p, static_cast<hipStream_t>(stream)), who);
+}
+
+// --------------------------------------------------------------- eviction
+int kvc_weigh_workspace(int64_t* bytes) {
+  if (bytes == nullptr) return fail(KVC_EINVAL, "kvc_weigh_workspace: bytes is NULL");
+  *bytes = kWeighBytes;
+  return ok();
+}
+
+int kvc_weigh_prefill(const kvc_weigh_args* args, void* stream) {
+  return weigh(args, false, stream, "kvc_weigh_prefill");
+}
+
+int kvc_weigh_tree(const kvc_weigh_args* args, void* stream) {
+  return weigh(args, true, stream, "kvc_weigh_tree");
+}
+
+int kvc_evict_workspace(int32_t num_slots, int64_t w_width, int64_t* bytes) {
+  const char* who = "kvc_evict_workspace";
+  if (bytes == nullptr) return fail(KVC_EINVAL, "%s: bytes is NULL", who);
+  if (num_slots < 0 || num_slots > kvc::kMaxSlots || w_width < 1)
+    return fail(KVC_EINVAL, "%s: sizes outside those of a call", who);
+  *bytes = evict_bytes(num_slots, w_width);
+  return ok();
+}
+
+int kvc_evict_select(const kvc_evict_args* a, void* stream) {
+  const char* who = "kvc_evict_select";
+  if (a == nullptr) return fail(KVC_EINVAL, "%s: args is NULL", who);
+  if (a->ratio != 1 && a->ratio != 2) return fail(KVC_EUNSUPPORTED, "%s: ratio %d (1 or 2)", who, a->ratio);
+  if (a->num_slots < 0 || a->num_slots > kvc::kMaxSlots)
+    return fail(KVC_EINVAL, "%s: num_slots %d outside [0, %d]", who, a->num_slots, kvc::kMaxSlots);
+  if (a->first < 0 || a->recent < 0) return fail(KVC_EINVAL, "%s: first and recent must be >= 0", who);
+  if (a->num_slots == 0) return ok();
+  if (a->lens == nullptr || a->counts == nullptr || a->counts == a->lens)
+    return fail(KVC_EINVAL, "%s: NULL lens or counts, or counts is lens", who);
+  if (a->weights == nullptr || a->w_width < 1 || a->w_stride < a->w_width)
+    return fail(KVC_EINVAL, "%s: weights need 1 <= w_width <= w_stride (%lld, %lld)", who,
+                (long long)a->w_width, (long long)a->w_stride);
+  if (a->kept == nullptr || a->kept_width < 1 || a->kept_width > 0x7FFFFFFF || a->kept_stride < a->kept_width)
+    return fail(KVC_EINVAL, "%s: kept needs 1 <= kept_width <= kept_stride (%lld, %lld)", who,
+                (long long)a->kept_width, (long long)a->kept_stride);
+  if (a->kept_weights != nullptr && (a->kw_stride < a->kept_width || a->kept_weights == a->weights))
+    return fail(KVC_EINVAL, "%s: kept_weights needs a stride >= kept_width, and is not weights", who);
+  const int64_t need = evict_bytes(a->num_slots, a->w_width);
+  if (need > 0 && (a->workspace == nullptr || ((uintptr_t)a->workspace & 255u) != 0 || a->workspace_bytes < need))
+    return fail(KVC_EINVAL, "%s: workspace needs %lld bytes, 256-byte aligned", who, (long long)need);
+  if (kvc::launch_select == nullptr) return fail(KVC_ELAUNCH, "%s: built without kernels", who);
+  kvc::SelectParams p{};
+  p.ratio = a->ratio;
+  p.num_slots = a->num_slots;
+  p.lens = a->lens;
+  p.weights = a->weights;
+  p.w_stride = a->w_stride;
+  p.w_width = a->w_width;
+  p.budget = a->budget;
+  p.budgets = a->budgets;
+  p.first = a->first;
+  p.recent = a->recent;
+  p.kept = a->kept;
+  p.kept_stride = a->kept_stride;
+  p.kept_width = (int32_t)a->kept_width;
+  p.counts = a->counts;
+  p.kept_weights = a->kept_weights;
+  p.kw_stride = a->kw_stride;
+  p.status = a->status;
+  return launched(kvc::launch_select(p, static_cast<hipStream_t>(stream)), who);
+}
+
+int kvc_cache_compact(const kvc_compact_args* a, void* stream) {
+  const char* who = "kvc_cache_compact";
+  if (a == nullptr) return fail(KVC_EINVAL, "%s: args is NULL", who);
+  kvc::CompactParams p{};
+  int rc = check_cache(&a->cache, &p.cache, who);
+  if (rc) return rc;
+  if (a->ratio != 1 && a->ratio != 2) return fail(KVC_EUNSUPPORTED, "%s: ratio %d (1 or 2)", who, a->ratio);
+  if (a->num_slots < 0 || a->num_slots > kvc::kMaxSlots)
+    return fail(KVC_EINVAL, "%s: num_slots %d outside [0, %d]", who, a->num_slots, kvc::kMaxSlots);
+  if (a->n_free < 0 || a->n_free >= 0x7FFFFFFF || a->freed_cap < 0 || a->freed_cap >= 0x7FFFFFFF)
+    return fail(KVC_EINVAL, "%s: n_free and freed_cap must lie in [0, 2^31 - 2]", who);
+  if (a->num_slots == 0) return ok();
+  if (a->lens == nullptr || a->counts == nullptr || a->new_lens == nullptr)
+    return fail(KVC_EINVAL, "%s: NULL lens, counts or new_lens", who);
+  if (a->new_lens == a->lens || a->new_lens == a->counts)
+    return fail(KVC_EINVAL, "%s: new_lens must not be an input", who);
+  if (a->kept == nullptr || a->kept_width < 1 || a->kept_width > 0x7FFFFFFF || a->kept_stride < a->kept_width)
+    return fail(KVC_EINVAL, "%s: kept needs 1 <= kept_width <= kept_stride (%lld, %lld)", who,
+                (long long)a->kept_width, (long long)a->kept_stride);
+  if (a->page_table == nullptr || a->pt_width < 1 || a->pt_stride < a->pt_width)
+    return fail(KVC_EINVAL, "%s: page table needs 1 <= pt_width <= pt_stride (%lld, %lld)", who,
+                (long long)a->pt_width, (long long)a->pt_stride);
+  if (a->new_table == nullptr || a->nt_stride < a->pt_width || a->new_table == a->page_table)
+    return fail(KVC_EINVAL, "%s: new_table needs a stride >= pt_width, and is not page_table", who);
+  if (a->n_free > 0 && a->free_pages == nullptr)
+    return fail(KVC_EINVAL, "%s: free_pages is NULL with n_free > 0", who);
+  if (a->freed != nullptr && a->freed == a->free_pages)
+    return fail(KVC_EINVAL, "%s: freed must not be free_pages", who);
+  if ((a->kept_weights == nullptr) != (a->weights == nullptr))
+    return fail(KVC_EINVAL, "%s: kept_weights and weights come together", who);
+  if (a->weights != nullptr && (a->kw_stride < a->kept_width || a->w_width < 1 || a->w_stride < a->w_width ||
+                                a->weights == a->kept_weights))
+    return fail(KVC_EINVAL, "%s: weights need 1 <= w_width <= w_stride, kept_weights a stride >= kept_width, "
+                            "and memory of its own", who);
+  if (kvc::launch_compact == nullptr) return fail(KVC_ELAUNCH, "%s: built without kernels", who);
+  p.ratio = a->ratio;
+  p.num_slots = a->num_slots;
+  p.lens = a->lens;
+  p.kept = a->kept;
+  p.kept_stride = a->kept_stride;
+  p.kept_width = (int32_t)a->kept_width;
+  p.counts = a->counts;
+  p.page_table = a->page_table;
+  p.pt_stride = a->pt_stride;
+  p.pt_width = a->pt_width;
+  p.free_pages = a->free_pages;
+  p.n_free = a->n_free;
+  p.new_table = a->new_table;
+  p.nt_stride = a->nt_stride;
+  p.new_lens = a->new_lens;
+  p.kept_weights = a->kept_weights;
+  p.kw_stride = a->kw_stride;
+  p.weights = a->weights;
+  p.w_stride = a->w_stride;
+  p.w_width = a->w_width;
+  p.freed = a->freed;
+  p.freed_cap = a->freed_cap;
+  p.totals = a->totals;
+  p.status = a->status;
+  return launched(kvc::launch_compact(p, static_cast<hipStream_t>(stream)), who);
 }
 
 }  // extern "C"

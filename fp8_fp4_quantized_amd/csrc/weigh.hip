@@ -1,0 +1,625 @@
+// weigh.hip -- attention weight that cached rows collect (gfx950): for every row
+// r of a slot, over the (token, head) pairs m of the slot that see it,
+//   sum_m 2^(s_mr - lse_m),   s_mr = scale * log2(e) * (q_m . x_r),
+// added to decay times what the row had.  lse is the attention's, so a pair's
+// weights over its rows sum to 1 (less with a sink).
+//
+// Scores are products of matrix instructions with the queries as rows and the
+// cached rows as columns of the result: a lane then holds 16 scores of one
+// cached row, and the sum over the queries stays in its registers.  A lane reads
+// the codes of its row straight from the page into the operand's place (dims in
+// the order the codes come in; the queries are read from LDS in the same order),
+// so pages of any size are alike and nothing of a row passes through LDS.
+#include <algorithm>
+
+#include "launch_evict.hpp"
+#include "row_ops.hpp"
+
+namespace kvc {
+
+namespace {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+constexpr float kNegInf = -__builtin_inff();
+
+// tokens of slot b, the position of its first one and the rows they may see; n =
+// 0 for a slot that has none or is skipped
+struct SlotTokens {
+  int32_t first, n, pos, rows;
+};
+__device__ __forceinline__ SlotTokens slot_tokens(const WeighParams& p, int b, int32_t* bad) {
+  SlotTokens s;
+  s.pos = p.start_pos[b];
+  if (p.offsets == nullptr) {
+    s.first = b * p.draft_len;
+    s.n = p.draft_len;
+  } else {
+    s.first = p.offsets[b];
+    s.n = p.offsets[p.num_slots + b];
+    if (s.n < 0) s.n = 0;
+    if (s.pos >= 0 && s.n > 0 && (s.first < 0 || (int64_t)s.first + s.n > p.q_rows)) {
+      s.n = 0;
+      *bad |= kStTokenRange;
+    }
+  }
+  if (s.pos < 0) s.n = 0;
+  // row indices stay in int32
+  if (s.n > 0 && (int64_t)s.pos + s.n > 0x7FFFFFFF - 256) {
+    s.n = 0;
+    *bad |= kStPosRange;
+  }
+  s.rows = s.n > 0 ? (s.pos + s.n) >> (p.ratio - 1) : 0;
+  // rows past the table or the weights' row are left out
+  const int64_t most = min(p.pt_width << p.cache.page_bits, p.w_width);
+  if (s.rows > most) {
+    s.rows = (int32_t)most;
+    *bad |= kStPtRange;
+  }
+  return s;
+}
+
+// first token of the slot that sees row r
+__device__ __forceinline__ int32_t first_token(const WeighParams& p, const SlotTokens& s, int32_t r) {
+  if (p.tree != nullptr) return 0;
+  const int64_t t = (int64_t)(r + 1) * p.ratio - 1 - s.pos;
+  return t > 0 ? (int32_t)t : 0;
+}
+
+// rows below which every token of the slot sees all
+__device__ __forceinline__ int32_t first_limit(const WeighParams& p, const SlotTokens& s) {
+  return p.tree != nullptr ? s.pos : (s.pos + 1) >> (p.ratio - 1);
+}
+
+// ------------------------------------------------------------------ a row
+// The codes of a lane's row, its half of each 64 (FP4) or 32 dims: lane l has
+// row l % 32 of the wave's and half h = l / 32.  Step j of the product (16 dims,
+// 8 a half) takes the dims of chunk(j) + 8-dim chunks of the half:
+//   V41      dims 32 (j / 2) + 16 h + 8 (j % 2): load j / 2, scale byte j / 2
+//   V41_FP4  dims 64 (j / 4) + 32 h + 8 (j % 4): load j / 4, scale byte 4 (j / 4) + 2 h + j % 4 / 2
+//   V4       as V41 (scale byte j / 4) up to j = 27, then rope dims 448 + 16 (j - 28) + 8 h
+template <int L> struct CodesShape;
+template <> struct CodesShape<kV41> { static constexpr int kLoads = 16, kScales = 4; };
+template <> struct CodesShape<kV41Fp4> { static constexpr int kLoads = 8, kScales = 8; };
+template <> struct CodesShape<kV4> { static constexpr int kLoads = 18, kScales = 2; };
+
+template <int L>
+struct Codes {
+  static constexpr int N = CodesShape<L>::kLoads;
+  u32x4 code[N];
+  uint32_t scale[CodesShape<L>::kScales];
+
+  // data: the row's data part + 16 h; scale parts whole
+  __device__ __forceinline__ void load_code(const uint8_t* data, int i) { code[i] = *(const u32x4*)(data + 32 * i); }
+  __device__ __forceinline__ void load_scale(const uint8_t* sc) {
+    if constexpr (L == kV4) {
+      const u32x2 v = *(const u32x2*)sc;
+      scale[0] = v.x, scale[1] = v.y;
+    } else {
+#pragma unroll
+      for (int k = 0; k < CodesShape<L>::kScales / 4; ++k) {
+        const u32x4 v = *(const u32x4*)(sc + 16 * k);
+        scale[4 * k] = v.x, scale[4 * k + 1] = v.y, scale[4 * k + 2] = v.z, scale[4 * k + 3] = v.w;
+      }
+    }
+  }
+  // load of step j (of its last one, the code is done with)
+  static constexpr int load_of(int j) { return L == kV41Fp4 ? j >> 2 : L == kV4 && j >= 28 ? j - 14 : j >> 1; }
+  static constexpr bool last_of(int j) { return L == kV41Fp4 ? (j & 3) == 3 : L == kV4 && j >= 28 ? true : (j & 1) != 0; }
+  __device__ __forceinline__ bf16x8 expand(int j, int h) const {
+    uint4 v;
+    if constexpr (L == kV41Fp4) {
+      const uint32_t pair = scale[j >> 2] >> (16 * h);
+      v = dq_fp4x8(code[j >> 2][j & 3], (j & 2) ? pair >> 8 & 0xFFu : pair & 0xFFu);
+    } else if (L == kV4 && j >= 28) {
+      const u32x4 c = code[j - 14];
+      v = make_uint4(c.x, c.y, c.z, c.w);
+    } else {
+      const int g = L == kV4 ? j >> 2 : j >> 1;
+      const u32x4 c = code[j >> 1];
+      v = dq_fp8x8((j & 1) ? make_uint2(c.z, c.w) : make_uint2(c.x, c.y), scale[g >> 2] >> (8 * (g & 3)) & 0xFFu);
+    }
+    return __builtin_bit_cast(bf16x8, u32x4{v.x, v.y, v.z, v.w});
+  }
+  // 8-dim chunk of step j in a row of queries: that of half 0, and how far half 1 is
+  static constexpr int chunk(int j) {
+    return L == kV41Fp4 ? 8 * (j >> 2) + (j & 3) : L == kV4 && j >= 28 ? 56 + 2 * (j - 28) : 4 * (j >> 1) + (j & 1);
+  }
+  static constexpr int half_chunks(int j) { return L == kV41Fp4 ? 4 : L == kV4 && j >= 28 ? 1 : 2; }
+};
+
+// where a lane's row lies; a row that is none is read at row 0 of page 0
+struct Place {
+  const uint8_t* data;
+  const uint8_t* scale;
+  bool ok;
+};
+template <int L>
+__device__ __forceinline__ Place place_of(const WeighParams& p, int64_t b, int32_t r, int32_t rows) {
+  Place a;
+  const int pb = p.cache.page_bits;
+  int32_t page = 0;
+  a.ok = r < rows;
+  if (a.ok) {
+    page = p.page_table[b * p.pt_stride + (r >> pb)];
+    if (page < 0 || page >= p.cache.num_pages) {
+      a.ok = false;
+      page = 0;
+      if (p.status != nullptr) atomicOr(p.status, kStPageRange);
+    }
+  }
+  const int64_t in = a.ok ? r & ((1 << pb) - 1) : 0;
+  const uint8_t* base = p.cache.base + page * p.cache.page_stride;
+  a.data = base + in * LayoutTraits<L>::kData + 16 * (lane_id() >> 5);
+  a.scale = base + ((int64_t)LayoutTraits<L>::kData << pb) + in * LayoutTraits<L>::kScale;
+  return a;
+}
+
+// The weight of row r after the call: a row that this call's tokens complete
+// begins at 0; a row that is not finite (its sum is not either) collects nothing.
+__device__ __forceinline__ void put_weight(const WeighParams& p, int64_t b, const SlotTokens& s, int32_t r,
+                                           float sum) {
+  float old = 0.0f;
+  if (p.prev != nullptr && r < s.pos >> (p.ratio - 1)) old = p.prev[b * p.prev_stride + r];
+  if (!(sum < __builtin_inff())) sum = 0.0f;
+  p.weights[b * p.w_stride + r] = __builtin_fmaf(p.decay, old, sum);
+}
+
+__device__ __forceinline__ float sum_halves(float v) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+// ------------------------------------------------------------------ queries
+// 32 queries of a slot in LDS: row m's 16-byte chunk c at place c ^ (m % 16) of
+// its 1024 bytes (16 consecutive rows' chunks then lie in all banks), and of each
+// query -lse, the rows below which all are seen, and a tree's mask.  A query past
+// the end, or one whose lse is not finite (it has no rows, or no answer), has
+// -lse = -inf and zeros: its weights are 0.
+struct QueryRows {
+  float neg_lse[32];
+  int32_t limit[32];
+  uint64_t mask[32];
+};
+
+// tree mask of a token
+__device__ __forceinline__ uint64_t mask_of(const WeighParams& p, int64_t b, const SlotTokens& s, int32_t tok) {
+  const uint64_t m = p.tree[b * p.draft_len + tok];
+  return s.n < 64 ? m & ((uint64_t(1) << s.n) - 1) : m;
+}
+
+// A lane's query m of the slot's flat (token, head) list; end: of the queries
+struct LaneQuery {
+  const uint16_t* at;
+  float neg_lse;
+  int32_t limit;
+  uint64_t mask;
+};
+__device__ __forceinline__ LaneQuery lane_query(const WeighParams& p, int64_t b, const SlotTokens& s, int64_t m,
+                                                int64_t end) {
+  LaneQuery q{p.q, kNegInf, 0, 0};
+  if (m >= end) return q;
+  const int32_t tok = (int32_t)udiv_magic((uint32_t)m, p.head_div.m, p.head_div.sh1, p.head_div.sh2);
+  const int32_t head = (int32_t)m - tok * p.heads;
+  const int64_t row = (int64_t)s.first + tok;
+  q.at = p.q + row * p.q_stride + head * p.q_hstride;
+  const float lse = p.lse[row * p.heads + head];
+  if (__builtin_fabsf(lse) < __builtin_inff()) q.neg_lse = -lse;
+  q.limit = p.tree != nullptr ? s.pos : (s.pos + tok + 1) >> (p.ratio - 1);
+  if (p.tree != nullptr) q.mask = mask_of(p, b, s, tok);
+  return q;
+}
+
+// whether a query with that limit and mask sees row r; base: the row of mask bit 0
+__device__ __forceinline__ bool sees(int32_t r, int32_t limit, bool tree, uint64_t mask, int32_t base) {
+  bool see = r < limit;
+  if (tree) {
+    const uint32_t x = (uint32_t)(r - base);
+    see |= x < 64u && (mask >> (x & 63u) & 1) != 0;
+  }
+  return see;
+}
+
+// Adds a lane's 16 weights of a 32 x 32 result to v.  masked: some of the
+// queries may not see some of the rows.
+__device__ __forceinline__ float add_weights(float v, const f32x16& s, float scale, const QueryRows& q, int h,
+                                             bool masked, int32_t r, bool tree, int32_t base) {
+#pragma unroll
+  for (int a = 0; a < 4; ++a) {
+    const f32x4 nl = *(const f32x4*)&q.neg_lse[8 * a + 4 * h];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float w = __builtin_amdgcn_exp2f(__builtin_fmaf(s[4 * a + i], scale, nl[i]));
+      if (masked) {
+        const int m = 8 * a + 4 * h + i;
+        if (!sees(r, q.limit[m], tree, tree ? q.mask[m] : 0, base)) w = 0.0f;
+      }
+      v += w;
+    }
+  }
+  return v;
+}
+
+// ------------------------------------------------------------------ batch
+// Sums over the slots in LDS: of a call's blocks of rows, or of its cost.
+template <int BLOCK>
+__device__ __forceinline__ int64_t block_scan64(int64_t v, int64_t* buf, int64_t* total) {
+  const int lane = lane_id(), wave = threadIdx.x >> 6;
+  int64_t x = v;
+#pragma unroll
+  for (int d = 1; d < kLanes; d <<= 1) {
+    const int64_t o = __shfl_up(x, d);
+    if (lane >= d) x += o;
+  }
+  __syncthreads();
+  if (lane == kLanes - 1) buf[wave] = x;
+  __syncthreads();
+  int64_t t = 0;
+  for (int w = 0; w < BLOCK / kLanes; ++w) {
+    if (w == wave) x += t;
+    t += buf[w];
+  }
+  *total = t;
+  return x;
+}
+
+// last slot whose sum before it is <= at (slots that add nothing share the start
+// of the next one)
+template <typename T>
+__device__ __forceinline__ int slot_at(const T* before, int n, T at) {
+  int lo = 0, hi = n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (before[mid] <= at) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
+// ------------------------------------------------------------------ few queries
+// Slots of up to 32 NC queries each: they stay in LDS while 8 waves go over the
+// slot's rows, 32 at a time.
+constexpr int kFewBlock = 512;
+constexpr int kFewWaves = kFewBlock / kLanes;
+constexpr int kFewGrid = 256;
+
+template <int L, int NC, int SLOTS>
+__global__ __launch_bounds__(kFewBlock) void weigh_few_kernel(WeighParams p) {
+  __shared__ __attribute__((aligned(16))) uint8_t rows[NC * 32 * 1024];
+  __shared__ QueryRows info[NC];
+  // blocks of 32 rows before each second slot
+  __shared__ uint32_t before[SLOTS / 2];
+  __shared__ int64_t buf[kFewWaves];
+  const int S = p.num_slots, tid = threadIdx.x, lane = lane_id(), wave = uniform(tid >> 6);
+  const int h = lane >> 5;
+  int32_t bad = 0;
+  int64_t carry = 0;
+  for (int b0 = 0; b0 < S; b0 += 2 * kFewBlock) {
+    const int b = b0 + 2 * tid;
+    int64_t n0 = 0, n1 = 0, total;
+    if (b < S) n0 = (slot_tokens(p, b, &bad).rows + 31) >> 5;
+    if (b + 1 < S) n1 = (slot_tokens(p, b + 1, &bad).rows + 31) >> 5;
+    const int64_t end = block_scan64<kFewBlock>(n0 + n1, buf, &total) + carry;
+    if (b < S) before[b >> 1] = (uint32_t)(end - n0 - n1);
+    carry += total;
+  }
+  if (blockIdx.x == 0 && bad != 0 && p.status != nullptr) atomicOr(p.status, bad);
+  __syncthreads();
+  const uint32_t all = (uint32_t)carry;
+  const uint32_t quota = (all + gridDim.x - 1) / gridDim.x;
+  uint32_t at = min(all, quota * blockIdx.x);
+  const uint32_t to = min(all, at + quota);
+  while (at < to) {
+    // the slot of block `at`
+    int b = 2 * slot_at(before, (S + 1) >> 1, at);
+    uint32_t first = before[b >> 1];
+    int32_t none = 0;
+    SlotTokens s = slot_tokens(p, b, &none);
+    uint32_t blocks = (uint32_t)(s.rows + 31) >> 5;
+    if (at - first >= blocks) {
+      first += blocks;
+      ++b;
+      s = slot_tokens(p, b, &none);
+      blocks = (uint32_t)(s.rows + 31) >> 5;
+    }
+    b = uniform(b);
+    s = SlotTokens{uniform(s.first), uniform(s.n), uniform(s.pos), uniform(s.rows)};
+    const uint32_t k0 = uniform((int32_t)(at - first)), k1 = min((uint32_t)uniform((int32_t)blocks), to - uniform((int32_t)first));
+    // its queries
+    const int64_t nq = (int64_t)s.n * p.heads;
+    __syncthreads();
+    for (int m0 = 8 * wave; m0 < 32 * NC; m0 += 8 * kFewWaves) {
+      const LaneQuery q = lane_query(p, b, s, m0 + (lane & 7), nq);
+      if (lane < 8) {
+        QueryRows& i = info[m0 >> 5];
+        i.neg_lse[(m0 & 31) + lane] = q.neg_lse;
+        i.limit[(m0 & 31) + lane] = q.limit;
+        i.mask[(m0 & 31) + lane] = q.mask;
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int64_t from = uniform64(__shfl((int64_t)(uintptr_t)q.at, k));
+        const bool real = __shfl(q.neg_lse, k) != kNegInf;
+        u32x4 v = *(const u32x4*)((const uint8_t*)(uintptr_t)from + 16 * lane);
+        if (!real) v = u32x4{0, 0, 0, 0};
+        const int m = m0 + k;
+        *(u32x4*)(rows + m * 1024 + 16 * (lane ^ (m & 15))) = v;
+      }
+    }
+    __syncthreads();
+    // its rows
+    const int32_t clear = first_limit(p, s);
+    for (uint32_t k = k0 + wave; k < k1; k += kFewWaves) {
+      const int32_t r = (int32_t)(32 * k) + (lane & 31);
+      // (the queries' fragments are read again for every block: kept over the
+      // loop they would not fit)
+      int row_base = (lane & 31) * 1024, low = lane & 15;
+      asm volatile("" : "+v"(row_base), "+v"(low));
+      const Place pl = place_of<L>(p, b, r, s.rows);
+      Codes<L> c;
+#pragma unroll
+      for (int i = 0; i < Codes<L>::N; ++i) c.load_code(pl.data, i);
+      c.load_scale(pl.scale);
+      f32x16 acc[NC];
+#pragma unroll
+      for (int n = 0; n < NC; ++n) acc[n] = f32x16{};
+#pragma unroll
+      for (int j = 0; j < 32; ++j) {
+        const bf16x8 x = c.expand(j, h);
+        const uint32_t at_row = row_base + 16 * ((Codes<L>::chunk(j) + Codes<L>::half_chunks(j) * h) ^ low);
+#pragma unroll
+        for (int n = 0; n < NC; ++n) {
+          const bf16x8 a = *(const bf16x8*)(rows + n * 32 * 1024 + at_row);
+          acc[n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, x, acc[n], 0, 0, 0);
+        }
+      }
+      const bool masked = (int32_t)(32 * k) + 32 > clear;
+      float v = 0.0f;
+#pragma unroll
+      for (int n = 0; n < NC; ++n)
+        v = masked ? add_weights(v, acc[n], p.scale_log2, info[n], h, true, r, p.tree != nullptr, s.pos)
+                   : add_weights(v, acc[n], p.scale_log2, info[n], h, false, r, false, 0);
+      v = sum_halves(v);
+      if (lane < 32 && r < s.rows) put_weight(p, b, s, r, pl.ok ? v : 0.0f);
+    }
+    at = uniform((int32_t)(first + k1));
+  }
+}
+
+// ------------------------------------------------------------------ many queries
+// Blocks of 256 rows, 64 a wave, whose operands stay in registers while the
+// queries that see them pass through LDS, 32 at a time.  The work of all blocks
+// is dealt evenly to the workgroups, a run each of the blocks' tokens in order;
+// what a workgroup has of a block that it does not have whole goes to the
+// workspace, and weigh_join_kernel adds the parts in order.
+constexpr int kManyBlock = 256;
+constexpr int kManyRowBits = 8;
+static_assert(kWeighRows == 1 << kManyRowBits, "rows of a block");
+
+// A block's begin, its rows fetched and expanded, as the queries that take the
+// same time
+constexpr int kBlockQueries = 128;
+
+__device__ __forceinline__ int32_t blocks_of(const SlotTokens& s) {
+  return (int32_t)(((int64_t)s.rows + kWeighRows - 1) >> kManyRowBits);
+}
+
+// Cost of the first k blocks of a slot: their (token, head) pairs, the tokens of
+// block i being those from first_token of its first row on -- 0, or growing by
+// rows * ratio a block.
+__device__ __forceinline__ int64_t cost_before(const WeighParams& p, const SlotTokens& s, int64_t k) {
+  int64_t tokens = s.n * k;
+  if (p.tree == nullptr) {
+    const int step = kManyRowBits + p.ratio - 1;
+    const int64_t c = p.ratio - 1 - (int64_t)s.pos;            // first_token of block i: (i << step) + c, or 0
+    const int64_t i1 = c > 0 ? 0 : (-c >> step) + 1;
+    if (k > i1) tokens -= (k - i1) * (((i1 + k - 1) << step) + 2 * c) / 2;
+  }
+  return tokens * p.heads + k * kBlockQueries;
+}
+
+template <int SLOTS>
+struct Deal {
+  int64_t before[SLOTS];       // cost of the slots before each one
+};
+
+// a slot's block, and where it begins in the call's cost
+struct BlockAt {
+  int b;
+  SlotTokens s;
+  int32_t k;
+  int64_t at, end;
+};
+template <int SLOTS>
+__device__ __forceinline__ BlockAt block_at(const WeighParams& p, const Deal<SLOTS>& d, int64_t at) {
+  BlockAt x;
+  x.b = uniform(slot_at(d.before, p.num_slots, at));
+  int32_t none = 0;
+  const SlotTokens s = slot_tokens(p, x.b, &none);
+  x.s = SlotTokens{uniform(s.first), uniform(s.n), uniform(s.pos), uniform(s.rows)};
+  const int64_t in = at - uniform64(d.before[x.b]);
+  int32_t lo = 0, hi = blocks_of(x.s) - 1;
+  while (lo < hi) {
+    const int32_t mid = (int32_t)(((int64_t)lo + hi + 1) >> 1);
+    if (cost_before(p, x.s, mid) <= in) lo = mid;
+    else hi = mid - 1;
+  }
+  x.k = uniform(lo);
+  x.at = uniform64(d.before[x.b]) + cost_before(p, x.s, x.k);
+  x.end = uniform64(d.before[x.b]) + cost_before(p, x.s, x.k + 1);
+  return x;
+}
+// token of a block where place `at` of the call's cost falls
+__device__ __forceinline__ int32_t token_at(const WeighParams& p, const BlockAt& x, int32_t first, int64_t at) {
+  const int64_t in = at - x.at - kBlockQueries;
+  return in <= 0 ? first : first + (int32_t)udiv_magic((uint32_t)in, p.head_div.m, p.head_div.sh1, p.head_div.sh2);
+}
+
+// 8 of a chunk's 32 queries, on their way to LDS
+struct Staged {
+  u32x4 v[8];
+  LaneQuery q;
+};
+__device__ __forceinline__ void stage_load(Staged& g, const WeighParams& p, int64_t b, const SlotTokens& s,
+                                           int64_t m0, int64_t end, int wave, int lane) {
+  g.q = lane_query(p, b, s, m0 + 8 * wave + (lane & 7), end);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const int64_t from = uniform64(__shfl((int64_t)(uintptr_t)g.q.at, k));
+    g.v[k] = *(const u32x4*)((const uint8_t*)(uintptr_t)from + 16 * lane);
+  }
+}
+__device__ __forceinline__ void stage_store(const Staged& g, uint8_t* rows, QueryRows& info, int wave, int lane) {
+  if (lane < 8) {
+    info.neg_lse[8 * wave + lane] = g.q.neg_lse;
+    info.limit[8 * wave + lane] = g.q.limit;
+    info.mask[8 * wave + lane] = g.q.mask;
+  }
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const bool real = __shfl(g.q.neg_lse, k) != kNegInf;
+    const int m = 8 * wave + k;
+    *(u32x4*)(rows + m * 1024 + 16 * (lane ^ (m & 15))) = real ? g.v[k] : u32x4{0, 0, 0, 0};
+  }
+}
+
+template <int L, int SLOTS>
+__global__ __launch_bounds__(kManyBlock) void weigh_many_kernel(WeighParams p) {
+  __shared__ __attribute__((aligned(16))) uint8_t rows[2][32 * 1024];
+  __shared__ QueryRows info[2];
+  __shared__ Deal<SLOTS> deal;
+  __shared__ int64_t buf[kManyBlock / kLanes];
+  const int S = p.num_slots, tid = threadIdx.x, lane = lane_id(), wave = uniform(tid >> 6);
+  const int h = lane >> 5, wg = blockIdx.x;
+  int32_t bad = 0;
+  int64_t carry = 0;
+  for (int b0 = 0; b0 < S; b0 += kManyBlock) {
+    const int b = b0 + tid;
+    int64_t cost = 0, total;
+    if (b < S) {
+      const SlotTokens s = slot_tokens(p, b, &bad);
+      cost = cost_before(p, s, blocks_of(s));
+    }
+    const int64_t end = block_scan64<kManyBlock>(cost, buf, &total) + carry;
+    if (b < S) deal.before[b] = end - cost;
+    carry += total;
+  }
+  __syncthreads();
+  if (wg == 0 && bad != 0 && p.status != nullptr) atomicOr(p.status, bad);
+  // (a share holds a block's begin and a token, so that no part of a block is empty)
+  const int64_t quota = max((carry + kWeighWorkgroups - 1) / kWeighWorkgroups,
+                            (int64_t)kBlockQueries + max(p.heads, 256));
+  const int64_t goal0 = quota * wg, goal1 = min(goal0 + quota, carry);
+  WeighSplit split{0, 0, 0, 0};
+  int64_t at = goal0;
+  while (at < goal1) {
+    const BlockAt x = block_at<SLOTS>(p, deal, at);
+    at = x.end;
+    const SlotTokens& s = x.s;
+    const int32_t first = first_token(p, s, x.k << kManyRowBits);
+    const int32_t ta = x.at >= goal0 ? first : token_at(p, x, first, goal0);
+    const int32_t tb = x.end <= goal1 ? s.n : token_at(p, x, first, goal1);
+    if (ta >= tb) continue;
+    const bool whole = ta == first && tb == s.n;
+    if (ta == first && tb < s.n) {
+      const uint64_t last = (uint64_t)(x.end - 1) / (uint64_t)quota;
+      split = WeighSplit{x.b, x.k, (int32_t)last - wg + 1, 0};
+    }
+    // its rows
+    const int32_t r0 = (x.k << kManyRowBits) + 64 * wave;
+    bf16x8 xf[2][32];
+    bool ok[2];
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+      const Place pl = place_of<L>(p, x.b, r0 + 32 * n + (lane & 31), s.rows);
+      ok[n] = pl.ok;
+      Codes<L> c;
+#pragma unroll
+      for (int i = 0; i < Codes<L>::N; ++i) c.load_code(pl.data, i);
+      c.load_scale(pl.scale);
+#pragma unroll
+      for (int j = 0; j < 32; ++j) xf[n][j] = c.expand(j, h);
+    }
+    // the queries
+    const int64_t end = (int64_t)tb * p.heads;
+    int64_t m0 = (int64_t)ta * p.heads;
+    Staged g;
+    stage_load(g, p, x.b, s, m0, end, wave, lane);
+    stage_store(g, rows[0], info[0], wave, lane);
+    __syncthreads();
+    float v[2] = {0.0f, 0.0f};
+    for (int turn = 0; m0 < end; m0 += 32, turn ^= 1) {
+      const bool more = m0 + 32 < end;
+      if (more) stage_load(g, p, x.b, s, m0 + 32, end, wave, lane);
+      f32x16 acc[2] = {f32x16{}, f32x16{}};
+#pragma unroll
+      for (int j = 0; j < 32; ++j) {
+        const uint32_t at_row = (lane & 31) * 1024 + 16 * ((Codes<L>::chunk(j) + Codes<L>::half_chunks(j) * h) ^ (lane & 15));
+        const bf16x8 a = *(const bf16x8*)(rows[turn] + at_row);
+        acc[0] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, xf[0][j], acc[0], 0, 0, 0);
+        acc[1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, xf[1][j], acc[1], 0, 0, 0);
+      }
+      const bool masked = r0 + 64 > uniform(info[turn].limit[0]);
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+        v[n] = masked ? add_weights(v[n], acc[n], p.scale_log2, info[turn], h, true, r0 + 32 * n + (lane & 31),
+                                    p.tree != nullptr, s.pos)
+                      : add_weights(v[n], acc[n], p.scale_log2, info[turn], h, false, 0, false, 0);
+      if (more) stage_store(g, rows[turn ^ 1], info[turn ^ 1], wave, lane);
+      __syncthreads();
+    }
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+      const float both = sum_halves(v[n]), sum = ok[n] ? both : 0.0f;
+      const int32_t r = r0 + 32 * n + (lane & 31);
+      if (lane < 32) {
+        if (!whole) p.parts[((int64_t)2 * wg + (ta > first ? 0 : 1)) * kWeighRows + 64 * wave + 32 * n + lane] = sum;
+        else if (r < s.rows) put_weight(p, x.b, s, r, sum);
+      }
+    }
+  }
+  if (tid == 0) p.splits[wg] = split;
+}
+
+__global__ __launch_bounds__(kWeighRows) void weigh_join_kernel(WeighParams p) {
+  const int wg = blockIdx.x;
+  const WeighSplit x = p.splits[wg];
+  if (x.parts == 0) return;
+  int32_t none = 0;
+  const SlotTokens s = slot_tokens(p, x.slot, &none);
+  float v = p.parts[((int64_t)2 * wg + 1) * kWeighRows + threadIdx.x];
+  for (int i = 1; i < x.parts; ++i) v += p.parts[((int64_t)2 * (wg + i)) * kWeighRows + threadIdx.x];
+  const int32_t r = (x.block << kManyRowBits) + (int32_t)threadIdx.x;
+  if (r < s.rows) put_weight(p, x.slot, s, r, v);
+}
+
+template <int L, int NC>
+void launch_few(const WeighParams& p, hipStream_t stream) {
+  if (p.num_slots <= 1024) weigh_few_kernel<L, NC, 1024><<<kFewGrid, kFewBlock, 0, stream>>>(p);
+  else weigh_few_kernel<L, NC, kMaxSlots + 1><<<kFewGrid, kFewBlock, 0, stream>>>(p);
+}
+
+template <int L>
+void launch_weigh_as(const WeighParams& p, int64_t slot_queries, hipStream_t stream) {
+  if (slot_queries <= 32) return launch_few<L, 1>(p, stream);
+  if (slot_queries <= 64) return launch_few<L, 2>(p, stream);
+  if (slot_queries <= kWeighFew) return launch_few<L, 4>(p, stream);
+  if (p.num_slots <= 1024) weigh_many_kernel<L, 1024><<<kWeighWorkgroups, kManyBlock, 0, stream>>>(p);
+  else weigh_many_kernel<L, kMaxSlots + 1><<<kWeighWorkgroups, kManyBlock, 0, stream>>>(p);
+  weigh_join_kernel<<<kWeighWorkgroups, kWeighRows, 0, stream>>>(p);
+}
+
+}  // namespace
+
+hipError_t launch_weigh(const WeighParams& p, int64_t slot_queries, hipStream_t stream) {
+  switch (p.cache.layout) {
+    case kV4: launch_weigh_as<kV4>(p, slot_queries, stream); break;
+    case kV41: launch_weigh_as<kV41>(p, slot_queries, stream); break;
+    default: launch_weigh_as<kV41Fp4>(p, slot_queries, stream); break;
+  }
+  return hipGetLastError();
+}
+
+}  // namespace kvc

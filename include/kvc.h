@@ -511,6 +511,245 @@ int kvc_attend_workspace(int32_t num_slots, int64_t tokens, int32_t num_heads, i
 int kvc_attend_prefill(const kvc_attend_args* args, void* stream);
 int kvc_attend_tree(const kvc_attend_args* args, void* stream);
 
+/* ---------------------------------------------------------------- rotary
+ * The rotary table that the stores, the compressor and kvc_rope_rows read:
+ * row i, for position first + i, holds
+ *   freqs[i][2j] = mscale * cos(a), freqs[i][2j + 1] = mscale * sin(a),
+ *   a = (first + i) * w_j,   j = 0 .. rot_dim / 2 - 1,
+ * with w_j = base^(-2j / rot_dim), changed for contexts longer than those the
+ * base was made for (f = factor):
+ *   KVC_ROPE_LINEAR  w_j / f
+ *   KVC_ROPE_BASE    those of base * f^(rot_dim / (rot_dim - 2))
+ *   KVC_ROPE_PARTS   w_j (1 - r_j) + (w_j / f) r_j, r_j = (j - lo) / (hi - lo)
+ *                    clamped to [0, 1]: pairs up to lo keep their speed, those
+ *                    from hi on are slowed, lo and hi being the pairs that make
+ *                    beta_fast and beta_slow turns over `original` positions,
+ *                      j(turns) = rot_dim ln(original / (2 pi turns)) / (2 ln base),
+ *                    rounded down and up, at least 0 and at most rot_dim - 1
+ *                    (hi - lo at least 0.001).
+ * Speeds and angles are 64 bits; each entry is rounded to fp32 once. */
+typedef enum kvc_rope_scaling {
+  KVC_ROPE_NONE = 0,
+  KVC_ROPE_LINEAR = 1,
+  KVC_ROPE_BASE = 2,
+  KVC_ROPE_PARTS = 3
+} kvc_rope_scaling;
+
+typedef struct kvc_rope_table_args {
+  float* freqs;               /* device fp32 [n, rot_dim], 16-byte aligned */
+  int64_t n;                  /* rows, >= 0; first + n <= 2^31 */
+  int64_t first;              /* position of the first row, >= 0 */
+  int32_t rot_dim;            /* even, 2..512 (BASE: 4..512) */
+  int32_t scaling;            /* kvc_rope_scaling */
+  double base;                /* > 1, finite */
+  double factor;              /* > 0, finite; not looked at without scaling */
+  double original;            /* PARTS: positions of the original context, > 0 */
+  double beta_fast;           /* PARTS: turns, beta_fast >= beta_slow > 0 */
+  double beta_slow;
+  double mscale;              /* > 0, finite */
+} kvc_rope_table_args;
+
+int kvc_rope_table(const kvc_rope_table_args* args, void* stream);
+
+/* Rotates heads at their tokens' positions: queries before the attention, and
+ * (transpose) the rope dims of its outputs, which are sums of rotated rows.  Of
+ * every token t and head h the dims offset .. offset + rot_dim - 1 are taken in
+ * pairs, (offset + 2j, offset + 2j + 1), or with `half` (offset + j, offset +
+ * rot_dim / 2 + j); a pair (a, b) becomes
+ *   (a c - b s, a s + b c),   transpose: (a c + b s, b c - a s),
+ * (c, s) = (freqs[p][2j], freqs[p][2j + 1]), p = positions[t].  transpose is the
+ * inverse rotation (mscale 1) and the backward pass of the rotation: the
+ * gradient of x is the transposed rotation of the gradient of out.  The other
+ * dims are copied; where out is x (same pointer and strides) they are not
+ * touched.  Computed in fp32, rounded once to the type.  A position < 0 or >=
+ * max_pos leaves the token's rows of out as they are, with
+ * KVC_STATUS_POS_RANGE.  out and x must be the same memory or not overlap. */
+typedef enum kvc_dtype {
+  KVC_BF16 = 0,
+  KVC_FP16 = 1,
+  KVC_FP32 = 2
+} kvc_dtype;
+
+typedef struct kvc_rope_args {
+  int32_t dtype;              /* kvc_dtype of x and out */
+  int32_t num_heads;          /* H, 1..1024 */
+  int32_t head_dim;           /* 2..8192 */
+  int32_t rot_dim;            /* even, 2..head_dim */
+  int32_t offset;             /* 0 .. head_dim - rot_dim */
+  int32_t half;               /* pairs of halves, not of neighbours */
+  int32_t transpose;
+  int64_t tokens;             /* T >= 0 */
+  const void* x;              /* device: token t, head h at x + t*x_stride + h*x_head_stride */
+  int64_t x_stride;           /* elements, >= 0 */
+  int64_t x_head_stride;
+  void* out;                  /* device, strides as x's (>= head_dim for an axis of
+                                 more than one entry) */
+  int64_t out_stride;
+  int64_t out_head_stride;
+  const int32_t* positions;   /* device int32 [T] */
+  const float* freqs;         /* device fp32 [max_pos, rot_dim], 8-byte aligned */
+  int64_t max_pos;            /* >= 1 */
+  int32_t* status;            /* device int32 or NULL */
+} kvc_rope_args;
+
+int kvc_rope_rows(const kvc_rope_args* args, void* stream);
+
+/* ---------------------------------------------------------------- eviction
+ * A request whose rows pass what it may hold keeps the ones that its tokens have
+ * given most attention: kvc_weigh_* collects that attention per cached row,
+ * kvc_evict_select chooses the rows, kvc_cache_compact moves them to pages of
+ * their own.
+ *
+ * kvc_weigh_prefill / kvc_weigh_tree: the queries, forms, masks, page tables and
+ *   rows are those of kvc_attend_prefill / kvc_attend_tree, lse what that call
+ *   gave (base 2).  With x_r the dequantized row r of slot b, over the tokens t
+ *   and heads h of the slot that see r,
+ *     weights[b][r] = decay * prev[b][r] + sum_th 2^(scale log2(e) (q_th . x_r) - lse_th)
+ *   for every row r < (start_pos[b] + count) / ratio; weights past these, and
+ *   those of skipped slots, are left as they are.  prev counts as 0 for the rows
+ *   r >= start_pos[b] / ratio, which the call's tokens complete (they need no
+ *   preparation), and everywhere where it is NULL; it may be weights itself.
+ *   A query whose lse is not finite adds nothing; a row that is not finite
+ *   collects nothing, and neither does a row whose page is outside the cache
+ *   (KVC_STATUS_PAGE_RANGE).  Rows past pt_width pages or w_width entries are
+ *   left out with KVC_STATUS_PT_RANGE.  Scores and sums are fp32; the order of a
+ *   sum depends on the call's sizes and lengths alone, so results repeat.
+ *   workspace: kvc_weigh_workspace bytes, 256-byte aligned, as the attention's;
+ *   not needed (may be NULL) where no slot can have more than 128 (token, head)
+ *   pairs: draft_len * H, or q_rows * H for kvc_weigh_prefill, up to 128. */
+typedef struct kvc_weigh_args {
+  int32_t ratio;              /* 1 or 2 */
+  int32_t num_heads;          /* H, 1..1024 */
+  int32_t num_slots;          /* S, 0..8191 */
+  int32_t draft_len;          /* tree: D, 1..64 (prefill: ignored) */
+  const void* q;              /* as kvc_attend_args */
+  int64_t q_stride;
+  int64_t q_head_stride;
+  int64_t q_rows;             /* token rows q and lse hold; q_rows * H <= 2^31 - 256 */
+  const float* lse;           /* device fp32 [q_rows, H] */
+  const int32_t* offsets;     /* device int32 [2, S], prefill (tree: ignored) */
+  const int32_t* start_pos;   /* device int32 [S] */
+  const int32_t* page_table;  /* device int32 [S, pt_stride] */
+  int64_t pt_stride;
+  int64_t pt_width;           /* 1 .. pt_stride */
+  const uint64_t* tree;       /* device [S * D] or NULL, tree mode */
+  float scale;                /* > 0, finite times log2(e) too */
+  float decay;                /* finite, >= 0 */
+  const float* prev;          /* device fp32 [S, prev_stride], w_width valid entries a row, or NULL */
+  int64_t prev_stride;        /* >= w_width */
+  float* weights;             /* device fp32 [S, w_stride]; no other input */
+  int64_t w_stride;           /* >= w_width */
+  int64_t w_width;            /* entries per row, >= 1 */
+  kvc_cache cache;
+  void* workspace;
+  int64_t workspace_bytes;
+  int32_t* status;            /* device int32 or NULL */
+} kvc_weigh_args;
+
+/* Workspace bytes of a call that needs one, whatever its sizes.  Host only. */
+int kvc_weigh_workspace(int64_t* bytes);
+
+int kvc_weigh_prefill(const kvc_weigh_args* args, void* stream);
+int kvc_weigh_tree(const kvc_weigh_args* args, void* stream);
+
+/* Which rows stay.  Slot b has R = lens[b] / ratio rows and may keep B =
+ * budgets[b] (or budget; negative or past kept_width: kept_width).  R <= B: all of
+ * them.  Otherwise B: the first f = min(first, B), the last g = min(recent, B -
+ * f), and of the rows between those the B - f - g with the greatest weights,
+ * equal ones the lower row first (-0 is 0, a NaN is below everything).
+ *   kept         the rows kept, ascending, then -1 up to kept_width
+ *   counts       their number; -1 for a slot that is inactive (lens[b] < 0) or
+ *                whose rows pass w_width (KVC_STATUS_PT_RANGE): its kept are -1
+ *   kept_weights their weights, then 0, or NULL
+ * workspace: kvc_evict_workspace bytes, 256-byte aligned, as the attention's (0
+ *   bytes: may be NULL). */
+typedef struct kvc_evict_args {
+  int32_t ratio;              /* 1 or 2 */
+  int32_t num_slots;          /* S, 0..8191 */
+  const int32_t* lens;        /* device int32 [S]: tokens */
+  const float* weights;       /* device fp32 [S, w_stride] */
+  int64_t w_stride;           /* >= w_width */
+  int64_t w_width;            /* >= 1 */
+  int32_t budget;             /* rows a slot keeps */
+  int32_t first;              /* >= 0 */
+  int32_t recent;             /* >= 0 */
+  const int32_t* budgets;     /* device int32 [S] or NULL */
+  int32_t* kept;              /* device int32 [S, kept_stride] */
+  int64_t kept_stride;        /* >= kept_width */
+  int64_t kept_width;         /* 1 .. 2^31 - 1 */
+  int32_t* counts;            /* device int32 [S] */
+  float* kept_weights;        /* device fp32 [S, kw_stride] or NULL */
+  int64_t kw_stride;          /* >= kept_width */
+  void* workspace;
+  int64_t workspace_bytes;
+  int32_t* status;            /* device int32 or NULL */
+} kvc_evict_args;
+
+/* Workspace bytes of a call of num_slots slots and w_width weights a row.  A call
+ * of no more of either takes no more.  Host only. */
+int kvc_evict_workspace(int32_t num_slots, int64_t w_width, int64_t* bytes);
+
+int kvc_evict_select(const kvc_evict_args* args, void* stream);
+
+/* Moves the rows of slots that drop some: with R = lens[b] / ratio rows, pages of
+ * page_size P and 0 <= counts[b] = C < R, row kept[b][i] of the slot becomes row i
+ * (i < C; any order, any repetition) of ceil(C / P) pages taken from the front of
+ * free_pages, slots in order, and the slot's ceil(R / P) old pages are listed in
+ * freed, slots in order.  A slot with C < 0 or C >= R stays as it is.  Old pages,
+ * the old table, lens, kept and counts are read only: the call can be captured
+ * and gives the same when it is repeated, rows shared with another request stay
+ * that request's, and the pages in freed may be used again once no request has
+ * them.
+ *   new_table    [S, nt_stride], pt_width entries a row: the slot's pages after
+ *                the call, then 0; must not overlap page_table
+ *   new_lens     C * ratio + lens[b] % ratio, or lens[b] of a slot that stays: the
+ *                lens of the next kvc_slot_map, the start_pos of the next
+ *                attention.  (Positions for the rotation are the request's own:
+ *                rows keep those they were stored with.)
+ *   kept_weights with weights (both or neither): entry i of a moved slot's row of
+ *                kept_weights becomes entry i of its row of weights
+ *   freed        [freed_cap] or NULL
+ *   totals       [4] or NULL: pages taken, pages given back, rows dropped
+ *                (at most 2^31 - 1), slots refused
+ * A slot is refused, and stays as it is, when its rows pass pt_width pages or its
+ * count kept_width or w_width (KVC_STATUS_PT_RANGE), or when the pages asked for
+ * or given back up to and including it pass n_free (or num_pages - 1) or
+ * freed_cap (KVC_STATUS_NO_PAGE; every later slot with rows to drop is refused
+ * with it).  A kept row outside the slot (KVC_STATUS_ID_RANGE) or on a page
+ * outside the cache (KVC_STATUS_PAGE_RANGE) gives a row of zero bytes; a row
+ * whose new page is below 1 or outside the cache is not written
+ * (KVC_STATUS_PAGE_RANGE).  free_pages must hold no page that a slot still has.
+ * Outputs must not overlap inputs or each other. */
+typedef struct kvc_compact_args {
+  int32_t ratio;              /* 1 or 2 */
+  int32_t num_slots;          /* S, 0..8191 */
+  const int32_t* lens;        /* device int32 [S] */
+  const int32_t* kept;        /* device int32 [S, kept_stride] */
+  int64_t kept_stride;        /* >= kept_width */
+  int64_t kept_width;         /* 1 .. 2^31 - 1 */
+  const int32_t* counts;      /* device int32 [S] */
+  const int32_t* page_table;  /* device int32 [S, pt_stride] */
+  int64_t pt_stride;
+  int64_t pt_width;           /* 1 .. pt_stride */
+  const int32_t* free_pages;  /* device int32 [n_free] (NULL when n_free is 0) */
+  int64_t n_free;             /* 0 .. 2^31 - 2 */
+  int32_t* new_table;
+  int64_t nt_stride;          /* >= pt_width */
+  int32_t* new_lens;          /* device int32 [S] */
+  const float* kept_weights;  /* device fp32 [S, kw_stride] or NULL */
+  int64_t kw_stride;          /* >= kept_width */
+  float* weights;             /* device fp32 [S, w_stride] or NULL */
+  int64_t w_stride;           /* >= w_width */
+  int64_t w_width;            /* >= 1 */
+  int32_t* freed;
+  int64_t freed_cap;          /* 0 .. 2^31 - 2 */
+  int32_t* totals;
+  kvc_cache cache;
+  int32_t* status;            /* device int32 or NULL */
+} kvc_compact_args;
+
+int kvc_cache_compact(const kvc_compact_args* args, void* stream);
+
 /* ---------------------------------------------------------------- misc */
 /* Message of the last failed call on this thread ("" if none). */
 const char* kvc_last_error(void);
