@@ -30,6 +30,7 @@ STATUS_TOKEN_RANGE = 64
 STATUS_NO_PAGE = 128
 ROPE_SCALING = {"none": 0, "linear": 1, "base": 2, "parts": 3}
 WEIGH_FEW = 128        # (token, head) pairs a slot may have without a workspace
+SELECT_NO_WORKSPACE = 16384   # weights a row may hold without a workspace
 
 
 class KvcError(RuntimeError):
@@ -727,6 +728,16 @@ def kvc_rope_table(out: torch.Tensor, *, first: int = 0, base: float = 10000.0,
     _call_on(out.device, stream, lib().kvc_rope_table, a)
 
 
+def _heads(t, name: str) -> None:
+    """Refuses what is not a [tokens, heads, dims] or [tokens, dims] device
+    tensor of heads."""
+    if not (t.is_cuda and t.dtype in _DTYPES and t.dim() in (2, 3) and
+            (t.stride(-1) == 1 or t.shape[-1] == 1)):
+        raise ValueError(f"{name}: expected a [tokens, heads, dims] or [tokens, dims] device tensor of "
+                         f"bf16, fp16 or fp32 with contiguous rows, got {t.dtype} {tuple(t.shape)} "
+                         f"strides {t.stride()}")
+
+
 def kvc_rope_rows(x: torch.Tensor, positions: torch.Tensor, freqs: torch.Tensor,
                   out: torch.Tensor | None = None, *, offset: int | None = None,
                   half: bool = False, transpose: bool = False,
@@ -736,48 +747,71 @@ def kvc_rope_rows(x: torch.Tensor, positions: torch.Tensor, freqs: torch.Tensor,
     (default: in place).  The rotated dims are ``offset ..`` (default: the
     last ``rot_dim``), pairs of neighbours or of ``half``s; ``transpose`` is
     the inverse rotation, which is also the rotation's backward pass."""
+    _heads(x, "x")
+    on = x.get_device()
+    shape, strides, at = x.shape, x.stride(), x.data_ptr()
+    if len(shape) == 3:
+        T, H, D = shape
+        x0, x1, _ = strides
+    else:
+        (T, D), H, x0, x1 = shape, 1, strides[0], 0
     if out is None:
-        out = x
-    for name, t in (("x", x), ("out", out)):
-        _need(t.is_cuda and t.dtype in _DTYPES and t.dim() in (2, 3) and
-              (t.stride(-1) == 1 or t.shape[-1] == 1),
-              f"{name}: expected a [tokens, heads, dims] or [tokens, dims] device tensor of bf16, fp16 "
-              f"or fp32 with contiguous rows, got {t.dtype} {tuple(t.shape)} strides {t.stride()}")
-    _need(out.shape == x.shape and out.dtype == x.dtype,
-          f"out: {out.dtype} {tuple(out.shape)}, x is {x.dtype} {tuple(x.shape)}")
-    T, D = x.shape[0], x.shape[-1]
-    H = x.shape[1] if x.dim() == 3 else 1
-    _one_device(x.device, (("out", out), ("positions", positions), ("freqs", freqs),
-                           ("status", status)))
-    _need(freqs.dim() == 2, f"freqs: shape {tuple(freqs.shape)}, expected [max_pos, rot_dim]")
+        o0, o1, to = x0, x1, at
+    else:
+        _heads(out, "out")
+        if out.shape != shape or out.dtype != x.dtype:
+            raise ValueError(f"out: {out.dtype} {tuple(out.shape)}, x is {x.dtype} {tuple(shape)}")
+        if out.get_device() != on:
+            _one_device(x.device, (("out", out),))
+        to = out.data_ptr()
+        o0, o1 = out.stride(0), out.stride(1) if len(shape) == 3 else 0
+        if to != at and out.stride() == strides and abs(to - at) < D * x.element_size():
+            raise ValueError("out: overlaps x without being x")
+    # a written row must be its own
+    if T > 1 and H > 1 and o0 < (H - 1) * o1 + D and o1 < (T - 1) * o0 + D:
+        raise ValueError(f"out: overlapping rows (strides {o0}, {o1})")
+    if freqs.dim() != 2 or freqs.get_device() != on:
+        _one_device(x.device, (("freqs", freqs),))
+        raise ValueError(f"freqs: shape {tuple(freqs.shape)}, expected [max_pos, rot_dim]")
+    max_pos, rot = freqs.shape
+    pos = _i32_on(positions, T, "positions", on)
+    table = _dense(freqs, _F32_T, "freqs")
+    flag = _i32_on(status, 1, "status", on)
     if T == 0 or H == 0:
         return
-    x0, o0 = x.stride(0), out.stride(0)
-    x1, o1 = (x.stride(1), out.stride(1)) if x.dim() == 3 else (0, 0)
-    # a written row must be its own
-    _need(T <= 1 or H <= 1 or o0 >= (H - 1) * o1 + D or o1 >= (T - 1) * o0 + D,
-          f"out: overlapping rows (strides {out.stride()})")
-    apart = out.data_ptr() - x.data_ptr()
-    _need(apart == 0 or x.stride() != out.stride() or abs(apart) >= D * x.element_size(),
-          "out: overlaps x without being x")
-    rot = freqs.shape[1]
-    a = kvc_rope_args(_DTYPES[x.dtype], H, D, rot, D - rot if offset is None else offset, half,
-                      transpose, T, x.data_ptr(), x0, x1, out.data_ptr(), o0, o1,
-                      _i32(positions, T, "positions"), _dense(freqs, _F32_T, "freqs"),
-                      freqs.shape[0], _i32(status, 1, "status"))
-    _call_on(x.device, stream, lib().kvc_rope_rows, a)
+    _call_on(x.device, stream, lib().kvc_rope_rows, kvc_rope_args(
+        _DTYPES[x.dtype], H, D, rot, D - rot if offset is None else offset, half, transpose, T, at,
+        x0, x1, to, o0, o1, pos, table, max_pos, flag))
 
 
 # ------------------------------------------------------------------ eviction
-def _table(t, types, rows: int, width: int, name: str):
-    """Pointer, row stride of a 2-D device tensor of at least ``rows`` rows of
-    ``width`` entries, or (None, 0) for None."""
+def _table(t, types, rows: int, width: int, name: str, index: int):
+    """Pointer, row stride of a 2-D tensor of at least ``rows`` rows of ``width``
+    entries on the device of that index, or (None, 0) for None."""
     if t is None:
         return None, 0
+    if t.get_device() != index and index >= 0:
+        _one_device(torch.device("cuda", index), ((name, t),))
     at = _rows(t, types, name)
-    if t.shape[0] < rows or t.shape[1] < width:
+    n, w = t.shape
+    if n < rows or w < width:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, need at least [{rows}, {width}]")
-    return at, _pt_stride(t)
+    return at, t.stride(0) if n > 1 else w
+
+
+def _bytes(workspace, name: str, index: int):
+    """Pointer, size of a workspace on the device of that index."""
+    if workspace is None:
+        return None, 0
+    if workspace.get_device() != index:
+        _one_device(torch.device("cuda", index), ((name, workspace),))
+    return _dense(workspace, (torch.uint8,), name), workspace.numel()
+
+
+def _cache_on(cache: Cache, index: int):
+    if cache.data.get_device() != index:
+        _one_device(torch.device("cuda", index), (("cache", cache.data),))
+    return cache.desc()
 
 
 def _scratch(n: int, dev, stream):
@@ -803,31 +837,29 @@ def kvc_weigh_workspace() -> int:
 
 def _weigh(fn, cache: Cache, q, lse, start_pos, page_table, weights, *, slots, pairs, ratio, scale,
            prev, decay, workspace, status, stream, offsets=None, draft_len=0, tree=None) -> None:
-    _need(q.is_cuda and q.dtype in _B16_T and q.dim() == 3 and q.shape[2] == 512 and q.stride(2) == 1,
-          f"q: expected a [tokens, heads, 512] bf16 device tensor with contiguous rows, got {q.dtype} "
-          f"{tuple(q.shape)} strides {q.stride()}")
+    if not (q.is_cuda and q.dtype in _B16_T and q.dim() == 3 and q.shape[2] == 512 and q.stride(2) == 1):
+        raise ValueError(f"q: expected a [tokens, heads, 512] bf16 device tensor with contiguous rows, got "
+                         f"{q.dtype} {tuple(q.shape)} strides {q.stride()}")
     T, H, _ = q.shape
-    dev = q.device
-    _one_device(dev, (("cache", cache.data), ("lse", lse), ("start_pos", start_pos),
-                      ("page_table", page_table), ("offsets", offsets), ("tree", tree),
-                      ("weights", weights), ("prev", prev), ("workspace", workspace),
-                      ("status", status)))
-    _need(tuple(lse.shape) == (T, H), f"lse: shape {tuple(lse.shape)}, expected [{T}, {H}]")
-    _need(weights.dim() == 2, f"weights: shape {tuple(weights.shape)}, expected [slots, rows]")
-    table, pt_stride = _table(page_table, _I32_T, slots, 0, "page_table")
+    q0, q1, _ = q.stride()
+    on = q.get_device()
+    if lse.get_device() != on or (tree is not None and tree.get_device() != on):
+        _one_device(q.device, (("lse", lse), ("tree", tree)))
+    if lse.shape != (T, H):
+        raise ValueError(f"lse: shape {tuple(lse.shape)}, expected [{T}, {H}]")
+    table, pt_stride = _table(page_table, _I32_T, slots, 0, "page_table", on)
+    w, w_stride = _table(weights, _F32_T, slots, 0, "weights", on)
     W = weights.shape[1]
-    w, w_stride = _table(weights, _F32_T, slots, 0, "weights")
-    old, old_stride = _table(prev, _F32_T, slots, W, "prev")
+    old, old_stride = _table(prev, _F32_T, slots, W, "prev", on)
     if pairs > WEIGH_FEW and workspace is None:
-        workspace = _scratch(kvc_weigh_workspace(), dev, stream)
-    a = kvc_weigh_args(
-        ratio, H, slots, draft_len, q.data_ptr(), q.stride(0), q.stride(1), T,
-        _dense(lse, _F32_T, "lse"), _i32(offsets, 2 * slots, "offsets"),
-        _i32(start_pos, slots, "start_pos"), table, pt_stride, page_table.shape[1],
-        _opt(tree, _dense, (torch.int64, torch.uint64), "tree"), scale, decay, old, old_stride,
-        w, w_stride, W, cache.desc(), _opt(workspace, _dense, (torch.uint8,), "workspace"),
-        0 if workspace is None else workspace.numel(), _i32(status, 1, "status"))
-    _call_on(dev, stream, fn, a)
+        workspace = _scratch(kvc_weigh_workspace(), q.device, stream)
+    space, size = _bytes(workspace, "workspace", on)
+    _call_on(q.device, stream, fn, kvc_weigh_args(
+        ratio, H, slots, draft_len, q.data_ptr(), q0, q1, T, _dense(lse, _F32_T, "lse"),
+        _i32_on(offsets, 2 * slots, "offsets", on), _i32_on(start_pos, slots, "start_pos", on), table,
+        pt_stride, page_table.shape[1], _opt(tree, _dense, (torch.int64, torch.uint64), "tree"), scale,
+        decay, old, old_stride, w, w_stride, W, _cache_on(cache, on), space, size,
+        _i32_on(status, 1, "status", on)))
 
 
 def kvc_weigh_prefill(cache: Cache, q: torch.Tensor, lse: torch.Tensor, offsets: torch.Tensor,
@@ -843,7 +875,8 @@ def kvc_weigh_prefill(cache: Cache, q: torch.Tensor, lse: torch.Tensor, offsets:
     ``kvc_weigh_workspace`` bytes (allocated per call where it is needed and
     not given)."""
     S = start_pos.numel()
-    _need(offsets.numel() == 2 * S, f"offsets: expected [2, {S}] entries")
+    if offsets.numel() != 2 * S:
+        raise ValueError(f"offsets: shape {tuple(offsets.shape)}, expected [2, {S}]")
     _rows_are(offsets, S, "offsets")
     _weigh(lib().kvc_weigh_prefill, cache, q, lse, start_pos, page_table, weights, slots=S,
            pairs=q.shape[0] * q.shape[1] if q.dim() == 3 else 0, ratio=ratio, scale=scale, prev=prev,
@@ -860,9 +893,10 @@ def kvc_weigh_tree(cache: Cache, q: torch.Tensor, lse: torch.Tensor, start_pos: 
     draft_len, H, 512]`` and the ``lse`` that ``kvc_attend_tree`` gave: a
     chain, a tree of ancestor masks, or single tokens."""
     S = start_pos.numel()
-    _need(q.dim() == 3 and q.shape[0] >= S * draft_len,
-          f"q: shape {tuple(q.shape)} for {S} slots x {draft_len} tokens")
-    _need(tree is None or tree.numel() >= S * draft_len, f"tree: expected [{S}, {draft_len}] masks")
+    if q.dim() != 3 or q.shape[0] < S * draft_len:
+        raise ValueError(f"q: shape {tuple(q.shape)} for {S} slots x {draft_len} tokens")
+    if tree is not None and tree.numel() < S * draft_len:
+        raise ValueError(f"tree: shape {tuple(tree.shape)}, expected [{S}, {draft_len}] masks")
     _rows_are(tree, draft_len, "tree")
     _weigh(lib().kvc_weigh_tree, cache, q, lse, start_pos, page_table, weights, slots=S,
            pairs=draft_len * q.shape[1], ratio=ratio, scale=scale, prev=prev, decay=decay,
@@ -892,23 +926,17 @@ def kvc_evict_select(lens: torch.Tensor, weights: torch.Tensor, kept: torch.Tens
     S = lens.numel()
     on = lens.get_device()
     lens_p = _i32(lens, S, "lens")            # (refuses one that is on no device)
-    _one_device(lens.device, (("weights", weights), ("kept", kept), ("kept_weights", kept_weights),
-                              ("workspace", workspace)))
-    w, w_stride = _table(weights, _F32_T, S, 0, "weights")
-    k, k_stride = _table(kept, _I32_T, S, 0, "kept")
-    K = kept.shape[1]
-    kw, kw_stride = _table(kept_weights, _F32_T, S, K, "kept_weights")
-    W = weights.shape[1]
-    if workspace is None and S > 0 and W > 0:
-        n = kvc_evict_workspace(S, W)
-        if n > 0:
-            workspace = _scratch(n, lens.device, stream)
-    a = kvc_evict_args(
+    w, w_stride = _table(weights, _F32_T, S, 0, "weights", on)
+    k, k_stride = _table(kept, _I32_T, S, 0, "kept", on)
+    K, W = kept.shape[1], weights.shape[1]
+    kw, kw_stride = _table(kept_weights, _F32_T, S, K, "kept_weights", on)
+    if workspace is None and W > SELECT_NO_WORKSPACE and S > 0:
+        workspace = _scratch(kvc_evict_workspace(S, W), lens.device, stream)
+    space, size = _bytes(workspace, "workspace", on)
+    _call_on(lens.device, stream, lib().kvc_evict_select, kvc_evict_args(
         ratio, S, lens_p, w, w_stride, W, K if budget is None else budget, first, recent,
         _i32_on(budgets, S, "budgets", on), k, k_stride, K, _i32_on(counts, S, "counts", on), kw,
-        kw_stride, _opt(workspace, _dense, (torch.uint8,), "workspace"),
-        0 if workspace is None else workspace.numel(), _i32_on(status, 1, "status", on))
-    _call_on(lens.device, stream, lib().kvc_evict_select, a)
+        kw_stride, space, size, _i32_on(status, 1, "status", on)))
 
 
 def kvc_cache_compact(cache: Cache, lens: torch.Tensor, kept: torch.Tensor, counts: torch.Tensor,
@@ -927,23 +955,20 @@ def kvc_cache_compact(cache: Cache, lens: torch.Tensor, kept: torch.Tensor, coun
     S = lens.numel()
     on = lens.get_device()
     lens_p = _i32(lens, S, "lens")            # (refuses one that is on no device)
-    _one_device(lens.device, (("cache", cache.data), ("kept", kept), ("page_table", page_table),
-                              ("new_table", new_table), ("kept_weights", kept_weights),
-                              ("weights", weights)))
-    k, k_stride = _table(kept, _I32_T, S, 0, "kept")
+    k, k_stride = _table(kept, _I32_T, S, 0, "kept", on)
     K = kept.shape[1]
-    table, pt_stride = _table(page_table, _I32_T, S, 0, "page_table")
+    table, pt_stride = _table(page_table, _I32_T, S, 0, "page_table", on)
     width = page_table.shape[1]
-    new, nt_stride = _table(new_table, _I32_T, S, width, "new_table")
-    kw, kw_stride = _table(kept_weights, _F32_T, S, K, "kept_weights")
-    w, w_stride = _table(weights, _F32_T, S, 0, "weights")
+    new, nt_stride = _table(new_table, _I32_T, S, width, "new_table", on)
+    kw, kw_stride = _table(kept_weights, _F32_T, S, K, "kept_weights", on)
+    w, w_stride = _table(weights, _F32_T, S, 0, "weights", on)
     # (an empty tensor has no address: the library would take it as none given)
-    _need(freed is None or freed.numel() > 0 or S == 0, "freed: holds no page")
-    a = kvc_compact_args(
+    if freed is not None and freed.numel() == 0 and S > 0:
+        raise ValueError("freed: holds no page")
+    _call_on(lens.device, stream, lib().kvc_cache_compact, kvc_compact_args(
         ratio, S, lens_p, k, k_stride, K, _i32_on(counts, S, "counts", on), table, pt_stride, width,
         _i32_on(free_pages, 0, "free_pages", on), free_pages.numel(), new, nt_stride,
         _i32_on(new_lens, S, "new_lens", on), kw, kw_stride, w, w_stride,
         0 if weights is None else weights.shape[1], _i32_on(freed, 0, "freed", on),
-        0 if freed is None else freed.numel(), _i32_on(totals, 4, "totals", on), cache.desc(),
-        _i32_on(status, 1, "status", on))
-    _call_on(lens.device, stream, lib().kvc_cache_compact, a)
+        0 if freed is None else freed.numel(), _i32_on(totals, 4, "totals", on),
+        _cache_on(cache, on), _i32_on(status, 1, "status", on)))

@@ -3,9 +3,8 @@
 //
 // Choice: of a slot's R rows the first `first` and the last `recent` stay, and of
 // those between them the ones with the greatest weights, ties to the lower row.
-// The weights are ordered as 32-bit keys; three passes over them count the
-// keys' digits (11, 11 and 10 bits) and leave the key of the last row that is
-// kept, a fourth writes the rows in order.  One workgroup a slot.
+// The weights are ordered as 32-bit keys, and the key of the last row that is kept
+// is found digit by digit.
 //
 // Move: row i of a slot's list goes to row i of pages taken from the free list,
 // in slot order.  Every workgroup scans all slots into LDS, as the slot map
@@ -20,9 +19,25 @@ namespace kvc {
 
 namespace {
 
+// ------------------------------------------------------------------ choice
+// The key of the last row kept is found digit by digit (12, 10 and 10 bits) from
+// histograms of the candidates' keys, and the rows are then written in order.
+//   select_registers_kernel  rows of weights of up to kSelectRegisterRows: one
+//                            workgroup a slot, the keys in registers, read once
+//   select_count / select_write  longer ones of up to kSelectSegmentSlots slots: a slot's
+//                            rows in segments, one workgroup each; a launch a digit
+//                            and one that writes.  A segment's histogram lies in
+//                            the workspace, and each workgroup of the next launch
+//                            adds the slot's for itself -- no atomics in memory,
+//                            nothing to clear -- together with those of the
+//                            segments before its own, which say where it writes.
+//   select_stream_kernel     longer ones of more slots, which fill the card with a
+//                            workgroup each: the keys are read once a digit
 constexpr int kSelectBlock = 1024;
 constexpr int kSelectWaves = kSelectBlock / kLanes;
-constexpr int kBins = 2048;
+constexpr int kTopBits = 12, kLowBits = 10;
+constexpr int kTopBins = 1 << kTopBits, kLowBins = 1 << kLowBits;
+constexpr int kShift[3] = {20, 10, 0};
 
 // Order of the weights as unsigned keys: NaN below everything, -0 as 0.
 __device__ __forceinline__ uint32_t weight_key(float w) {
@@ -32,7 +47,7 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
 }
 
 // inclusive sum over the workgroup's threads, *total of all; buf: kSelectWaves
-// words that no thread still reads, and none may write before the next barrier
+// words that no thread still reads
 __device__ __forceinline__ int32_t block_scan(int32_t v, int32_t* buf, int32_t* total) {
   const int lane = lane_id(), wave = uniform((int)(threadIdx.x >> 6));
   v = wave_incl_scan_i32(v);
@@ -48,98 +63,336 @@ struct Choice {
   int32_t rows, keep;          // rows it has, rows kept (-1: inactive or refused)
   int32_t lo, hi;              // rows [lo, hi) compete for ...
   int32_t take;                // ... so many places
+  bool all;                    // none does
 };
-__device__ __forceinline__ Choice choice_of(const SelectParams& p, int b) {
+__device__ __forceinline__ Choice choice_of(const SelectParams& p, int b, bool report) {
   Choice c{};
   const int32_t len = p.lens[b];
   c.keep = -1;
+  c.all = true;
   if (len < 0) return c;
   c.rows = len >> (p.ratio - 1);
   if (c.rows > p.w_width) {
-    if (threadIdx.x == 0 && p.status != nullptr) atomicOr(p.status, kStPtRange);
+    if (report && threadIdx.x == 0 && p.status != nullptr) atomicOr(p.status, kStPtRange);
     return c;
   }
   int32_t budget = p.budgets != nullptr ? p.budgets[b] : p.budget;
   if (budget < 0 || budget > p.kept_width) budget = p.kept_width;
-  if (c.rows <= budget) {                     // every row stays
-    c.keep = c.rows;
-    return c;
-  }
-  c.keep = budget;
+  c.keep = min(c.rows, budget);
+  if (c.rows <= budget) return c;
   c.lo = min(p.first, budget);
   const int32_t recent = min(p.recent, budget - c.lo);
   c.hi = c.rows - recent;
   c.take = budget - c.lo - recent;
+  c.all = c.take == 0;
   return c;
 }
 
-__global__ __launch_bounds__(kSelectBlock) void select_kernel(SelectParams p) {
-  __shared__ uint32_t hist[kBins];
-  __shared__ int32_t buf[2][kSelectWaves];
-  __shared__ int32_t found[2];                // digit, places left for it
-  const int b = blockIdx.x, tid = threadIdx.x;
-  const Choice c = choice_of(p, b);
-  const float* w = p.weights + b * p.w_stride;
-  int32_t* kept = p.kept + b * p.kept_stride;
-  float* kw = p.kept_weights != nullptr ? p.kept_weights + b * p.kw_stride : nullptr;
-  const bool all = c.keep < 0 || c.keep == c.rows;
-  if (tid == 0) p.counts[b] = c.keep;
-  // rows kept whatever their weight, and what follows the list
-  for (int32_t i = tid; i < p.kept_width; i += kSelectBlock) {
-    const bool mid = !all && i >= c.lo && i < c.lo + c.take;
-    if (mid) continue;
-    const int32_t r = i >= c.keep ? -1 : all || i < c.lo ? i : c.rows - (c.keep - i);
+// A slot's lists and what of them does not depend on the weights: the count, the
+// rows that stay whatever theirs, and what follows the list.  The slot's
+// workgroups, `of` of them, take a share each.
+struct Lists {
+  const float* w;
+  int32_t* kept;
+  float* kw;
+  __device__ __forceinline__ Lists(const SelectParams& p, int64_t b)
+      : w(p.weights + b * p.w_stride), kept(p.kept + b * p.kept_stride),
+        kw(p.kept_weights != nullptr ? p.kept_weights + b * p.kw_stride : nullptr) {}
+  __device__ __forceinline__ void put(int32_t i, int32_t r, float v) const {
     kept[i] = r;
-    if (kw != nullptr) kw[i] = r >= 0 ? w[r] : 0.0f;
+    if (kw != nullptr) kw[i] = v;
   }
-  if (all || c.take == 0) return;
+  __device__ __forceinline__ void begin(const SelectParams& p, int b, const Choice& c, int part, int of) const {
+    if (threadIdx.x == 0 && part == 0) p.counts[b] = c.keep;
+    // (all rows kept: lo and take are 0 or the first rows and none, and row i is i
+    // up to lo, then counted from the end)
+    const bool whole = c.keep == c.rows;
+    for (int64_t i = part * kSelectBlock + threadIdx.x; i < p.kept_width; i += of * kSelectBlock) {
+      if (i >= c.lo && i < c.lo + c.take) continue;
+      const int32_t r = i >= c.keep ? -1 : whole || i < c.lo ? (int32_t)i : c.rows - (c.keep - (int32_t)i);
+      put((int32_t)i, r, r >= 0 ? w[r] : 0.0f);
+    }
+  }
+};
 
-  // the digits of the last kept row's key, from the top
-  uint32_t prefix = 0;                        // key bits above `shift + bits`
-  int32_t left = c.take;                      // places for keys with that prefix
-  int shift = 21;
+// Of N bins a thread, n[k] keys in the k-th from the greatest down (thread 0 has
+// the greatest): the bin that holds the left-th greatest key, and which of that
+// bin's it is.  found: 2 words that no thread still reads.
+struct Digit {
+  uint32_t bin;
+  int32_t left;
+};
+template <int N>
+__device__ __forceinline__ Digit find_digit(const int32_t (&n)[N], int32_t left, int32_t* buf, int32_t* found) {
+  int32_t sum = 0, total;
+#pragma unroll
+  for (int k = 0; k < N; ++k) sum += n[k];
+  int32_t above = block_scan(sum, buf, &total) - sum;
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    if (above < left && above + n[k] >= left) {
+      found[0] = N * kSelectBlock - 1 - N * (int)threadIdx.x - k;
+      found[1] = left - above;
+    }
+    above += n[k];
+  }
+  __syncthreads();
+  return Digit{(uint32_t)found[0], found[1]};
+}
+template <int N>
+__device__ __forceinline__ void bins_of(const uint32_t* hist, int32_t (&n)[N]) {
+#pragma unroll
+  for (int k = 0; k < N; ++k) n[k] = (int32_t)hist[N * kSelectBlock - 1 - N * (int)threadIdx.x - k];
+}
+
+// lanes below this one in m
+__device__ __forceinline__ int32_t lanes_before(uint64_t m) {
+  return (int32_t)__builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0u));
+}
+
+// Writes the kept ones of 64 rows, a lane each, and moves the counts past them.
+// key: of the last row kept, of whose equals the first `left` are kept.
+struct Written {
+  int32_t above, equal;        // rows before these that are greater, equal
+};
+__device__ __forceinline__ void write_rows(const Lists& l, const Choice& c, Written& at, uint32_t key, int32_t left,
+                                           int32_t r, float v, bool in) {
+  const uint32_t k = weight_key(v);
+  const uint64_t gt = __ballot(in && k > key), eq = __ballot(in && k == key);
+  const int32_t g = at.above + lanes_before(gt), e = at.equal + lanes_before(eq);
+  if (in && (k > key || (k == key && e < left))) l.put(c.lo + g + min(e, left), r, v);
+  at.above += __builtin_popcountll(gt);
+  at.equal += __builtin_popcountll(eq);
+}
+
+// E * 64 rows a wave
+template <int E>
+__global__ __launch_bounds__(kSelectBlock) void select_registers_kernel(SelectParams p) {
+  __shared__ uint32_t hist[kTopBins];
+  __shared__ int32_t buf[2][kSelectWaves], found[3][2];
+  __shared__ int32_t counts[kSelectWaves][2];
+  const int b = blockIdx.x, tid = threadIdx.x, lane = lane_id(), wave = uniform(tid >> 6);
+  const Choice c = choice_of(p, b, true);
+  const Lists l(p, b);
+  const int32_t r0 = c.lo + wave * E * kLanes + lane;
+  float v[E];
+  if (!c.all) {
+#pragma unroll
+    for (int i = 0; i < E; ++i) v[i] = r0 + i * kLanes < c.hi ? l.w[r0 + i * kLanes] : 0.0f;
+  }
+  l.begin(p, b, c, 0, 1);
+  if (c.all) return;
+  Digit d{0, c.take};
+  uint32_t key = 0;
+#pragma unroll
   for (int pass = 0; pass < 3; ++pass) {
-    const int bits = pass < 2 ? 11 : 10;
-    for (int i = tid; i < kBins; i += kSelectBlock) hist[i] = 0;
+    for (int i = tid; i < (pass == 0 ? kTopBins : kLowBins); i += kSelectBlock) hist[i] = 0;
     __syncthreads();
-    for (int32_t r = c.lo + tid; r < c.hi; r += kSelectBlock) {
-      const uint32_t k = weight_key(w[r]);
-      if (pass == 0 || k >> (shift + bits) == prefix) atomicAdd(&hist[k >> shift & ((1u << bits) - 1)], 1u);
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      const uint32_t k = weight_key(v[i]);
+      if (r0 + i * kLanes < c.hi && (pass == 0 || k >> (kShift[pass] + kLowBits) == key))
+        atomicAdd(&hist[pass == 0 ? k >> kShift[0] : k >> kShift[pass] & (kLowBins - 1)], 1u);
     }
     __syncthreads();
-    // bins from the greatest down, two a thread
-    const int top = (1 << bits) - 1 - 2 * tid;
-    const int32_t n0 = top >= 0 ? (int32_t)hist[top] : 0, n1 = top >= 1 ? (int32_t)hist[top - 1] : 0;
-    int32_t total;
-    const int32_t end = block_scan(n0 + n1, buf[pass & 1], &total);
-    const int32_t at = end - n0 - n1;         // keys in greater bins
-    if (at < left && at + n0 >= left) found[0] = top, found[1] = left - at;
-    else if (at + n0 < left && end >= left) found[0] = top - 1, found[1] = left - at - n0;
-    __syncthreads();
-    prefix = pass == 0 ? (uint32_t)found[0] : prefix << bits | (uint32_t)found[0];
-    left = found[1];
-    shift = pass == 0 ? 10 : 0;
+    if (pass == 0) {
+      int32_t n[kTopBins / kSelectBlock];
+      bins_of(hist, n);
+      d = find_digit(n, d.left, buf[0], found[0]);
+      key = d.bin;
+    } else {
+      int32_t n[1];
+      bins_of(hist, n);
+      d = find_digit(n, d.left, buf[pass & 1], found[pass]);
+      key = key << kLowBits | d.bin;
+    }
   }
-  // keys above `prefix` are kept, and the first `left` equal to it
+  Written at{0, 0};
+#pragma unroll
+  for (int i = 0; i < E; ++i) {
+    const uint32_t k = weight_key(v[i]);
+    const bool in = r0 + i * kLanes < c.hi;
+    at.above += __builtin_popcountll(__ballot(in && k > key));
+    at.equal += __builtin_popcountll(__ballot(in && k == key));
+  }
+  if (lane == 0) counts[wave][0] = at.above, counts[wave][1] = at.equal;
+  __syncthreads();
+  at = Written{0, 0};
+  for (int w = 0; w < wave; ++w) at.above += counts[w][0], at.equal += counts[w][1];
+#pragma unroll
+  for (int i = 0; i < E; ++i)
+    write_rows(l, c, at, key, d.left, r0 + i * kLanes, v[i], r0 + i * kLanes < c.hi);
+}
+
+__global__ __launch_bounds__(kSelectBlock) void select_stream_kernel(SelectParams p) {
+  __shared__ uint32_t hist[kTopBins];
+  __shared__ int32_t buf[2][kSelectWaves], found[3][2];
+  const int b = blockIdx.x, tid = threadIdx.x;
+  const Choice c = choice_of(p, b, true);
+  const Lists l(p, b);
+  l.begin(p, b, c, 0, 1);
+  if (c.all) return;
+  Digit d{0, c.take};
+  uint32_t key = 0;
+  for (int pass = 0; pass < 3; ++pass) {
+    for (int i = tid; i < (pass == 0 ? kTopBins : kLowBins); i += kSelectBlock) hist[i] = 0;
+    __syncthreads();
+    for (int64_t r = (int64_t)c.lo + tid; r < c.hi; r += kSelectBlock) {
+      const uint32_t k = weight_key(l.w[r]);
+      if (pass == 0) atomicAdd(&hist[k >> kShift[0]], 1u);
+      else if (k >> (kShift[pass] + kLowBits) == key) atomicAdd(&hist[k >> kShift[pass] & (kLowBins - 1)], 1u);
+    }
+    __syncthreads();
+    if (pass == 0) {
+      int32_t n[kTopBins / kSelectBlock];
+      bins_of(hist, n);
+      d = find_digit(n, d.left, buf[0], found[0]);
+      key = d.bin;
+    } else {
+      int32_t n[1];
+      bins_of(hist, n);
+      d = find_digit(n, d.left, buf[pass & 1], found[pass]);
+      key = key << kLowBits | d.bin;
+    }
+  }
   int32_t above = 0, equal = 0;               // of the rows before this turn's
   int turn = 0;
-  for (int32_t r0 = c.lo; r0 < c.hi; r0 += kSelectBlock, turn ^= 1) {
-    const int32_t r = r0 + tid;
-    const float v = r < c.hi ? w[r] : 0.0f;
+  for (int64_t t0 = c.lo; t0 < c.hi; t0 += kSelectBlock, turn ^= 1) {
+    const int64_t r = t0 + tid;
+    const float v = r < c.hi ? l.w[r] : 0.0f;
     const uint32_t k = weight_key(v);
-    const bool gt = r < c.hi && k > prefix, eq = r < c.hi && k == prefix;
+    const bool gt = r < c.hi && k > key, eq = r < c.hi && k == key;
     int32_t total;
     // (both counts of a turn fit 16 bits)
     const int32_t end = block_scan((gt ? 1 : 0) | (eq ? 1 << 16 : 0), buf[turn], &total);
-    const int32_t before_gt = above + (end & 0xFFFF) - (gt ? 1 : 0);
-    const int32_t before_eq = equal + (end >> 16) - (eq ? 1 : 0);
-    if (gt || (eq && before_eq < left)) {
-      const int32_t i = c.lo + before_gt + min(before_eq, left);
-      kept[i] = r;
-      if (kw != nullptr) kw[i] = v;
-    }
+    const int32_t g = above + (end & 0xFFFF) - (gt ? 1 : 0), e = equal + (end >> 16) - (eq ? 1 : 0);
+    if (gt || (eq && e < d.left)) l.put(c.lo + g + min(e, d.left), (int32_t)r, v);
     above += total & 0xFFFF;
     equal += total >> 16;
+  }
+}
+
+// ---- segments
+// The keys of segment s of a slot that begin with the digits found so far, counted
+// by their next one; `pass` digits are found, the last of them in this launch.
+struct Found {
+  uint32_t key;                // digits found, the last in the low bits
+  int32_t left;                // of the rows with them, so many are kept
+  Written before;              // in the segments before this one: rows kept for certain; (equal: used at the end)
+};
+
+// The digit that the histograms of the last launch give, from the slot's sums
+template <int BINS>
+__device__ __forceinline__ Found next_digit(const SelectParams& p, Found f, const uint32_t* hists, int s, int32_t* buf,
+                                            int32_t* found, int32_t* sums) {
+  constexpr int N = BINS / kSelectBlock;
+  const int top = N * kSelectBlock - N - N * (int)threadIdx.x;   // the thread's least bin
+  int32_t n[N], before[N];
+#pragma unroll
+  for (int k = 0; k < N; ++k) n[k] = before[k] = 0;
+#pragma unroll 8
+  for (int t = 0; t < p.segments; ++t) {
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      const int32_t h = (int32_t)hists[(int64_t)t * BINS + top + N - 1 - k];
+      n[k] += h;
+      if (t < s) before[k] += h;
+    }
+  }
+  const Digit d = find_digit(n, f.left, buf, found);
+  // rows in the segments before this one whose digit is greater, and that have it
+  int32_t above = 0;
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    const uint32_t bin = (uint32_t)(top + N - 1 - k);
+    if (bin > d.bin) above += before[k];
+    if (bin == d.bin) sums[0] = before[k];
+  }
+  int32_t total;
+  block_scan(above, buf + kSelectWaves, &total);
+  f.key = f.key << (BINS == kTopBins ? 0 : kLowBits) | d.bin;
+  f.left = d.left;
+  f.before.above += total;
+  f.before.equal = sums[0];
+  return f;
+}
+
+template <int PASS>
+__global__ __launch_bounds__(kSelectBlock) void select_count_kernel(SelectParams p) {
+  constexpr int BINS = PASS == 0 ? kTopBins : kLowBins;
+  __shared__ uint32_t hist[BINS];
+  __shared__ int32_t buf[2 * kSelectWaves], found[2], sums[1];
+  const int s = blockIdx.x, b = blockIdx.y, tid = threadIdx.x;
+  const Choice c = choice_of(p, b, PASS == 0 && s == 0);
+  const Lists l(p, b);
+  if (PASS == 0) l.begin(p, b, c, s, p.segments);
+  if (c.all) return;
+  const int64_t seg = (int64_t)b * p.segments + s;
+  Found f{0, c.take, {0, 0}};
+  if constexpr (PASS == 1) {
+    f = next_digit<kTopBins>(p, f, p.top_hists + (int64_t)b * p.segments * kTopBins, s, buf, found, sums);
+  } else if constexpr (PASS == 2) {
+    const int32_t* st = p.states + 4 * seg;
+    f = Found{(uint32_t)st[0], st[1], {st[2], 0}};
+    f = next_digit<kLowBins>(p, f, p.low_hists + (int64_t)b * p.segments * kLowBins, s, buf, found, sums);
+  }
+  for (int i = tid; i < BINS; i += kSelectBlock) hist[i] = 0;
+  __syncthreads();
+  const int64_t begin = c.lo + s * p.segment_rows, end = min((int64_t)c.hi, begin + p.segment_rows);
+#pragma unroll 4
+  for (int64_t r = begin + tid; r < end; r += kSelectBlock) {
+    const uint32_t k = weight_key(l.w[r]);
+    if (PASS == 0) atomicAdd(&hist[k >> kShift[0]], 1u);
+    else if (k >> (kShift[PASS] + kLowBits) == f.key) atomicAdd(&hist[k >> kShift[PASS] & (kLowBins - 1)], 1u);
+  }
+  __syncthreads();
+  uint32_t* out = PASS == 0 ? p.top_hists + seg * kTopBins
+                            : p.low_hists + ((int64_t)(PASS - 1) * p.num_slots * p.segments + seg) * kLowBins;
+  for (int i = tid; i < BINS; i += kSelectBlock) out[i] = hist[i];
+  if (PASS > 0 && tid == 0) {
+    int32_t* st = p.states + 4 * seg;
+    st[0] = (int32_t)f.key, st[1] = f.left, st[2] = f.before.above;
+  }
+}
+
+__global__ __launch_bounds__(kSelectBlock) void select_write_kernel(SelectParams p) {
+  __shared__ int32_t buf[2 * kSelectWaves], found[2], sums[1];
+  __shared__ int32_t counts[2][kSelectWaves][2];
+  const int s = blockIdx.x, b = blockIdx.y, lane = lane_id(), wave = uniform((int)(threadIdx.x >> 6));
+  const Choice c = choice_of(p, b, false);
+  if (c.all) return;
+  const Lists l(p, b);
+  const int64_t seg = (int64_t)b * p.segments + s;
+  const int32_t* st = p.states + 4 * seg;
+  Found f{(uint32_t)st[0], st[1], {st[2], 0}};
+  f = next_digit<kLowBins>(p, f, p.low_hists + (int64_t)(p.num_slots + b) * p.segments * kLowBins, s, buf, found, sums);
+  // turns of 16 waves of 256 rows
+  constexpr int E = 4;
+  const int64_t begin = c.lo + s * p.segment_rows, end = min((int64_t)c.hi, begin + p.segment_rows);
+  int turn = 0;
+  for (int64_t t0 = begin; t0 < end; t0 += kSelectBlock * E, turn ^= 1) {
+    const int64_t r0 = t0 + wave * E * kLanes + lane;
+    float v[E];
+    Written at{0, 0};
+#pragma unroll
+    for (int i = 0; i < E; ++i) v[i] = r0 + i * kLanes < end ? l.w[r0 + i * kLanes] : 0.0f;
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      const uint32_t k = weight_key(v[i]);
+      const bool in = r0 + i * kLanes < end;
+      at.above += __builtin_popcountll(__ballot(in && k > f.key));
+      at.equal += __builtin_popcountll(__ballot(in && k == f.key));
+    }
+    if (lane == 0) counts[turn][wave][0] = at.above, counts[turn][wave][1] = at.equal;
+    __syncthreads();
+    at = f.before;
+    for (int w = 0; w < kSelectWaves; ++w) {
+      if (w < wave) at.above += counts[turn][w][0], at.equal += counts[turn][w][1];
+      f.before.above += counts[turn][w][0], f.before.equal += counts[turn][w][1];
+    }
+#pragma unroll
+    for (int i = 0; i < E; ++i)
+      write_rows(l, c, at, f.key, f.left, (int32_t)(r0 + i * kLanes), v[i], r0 + i * kLanes < end);
   }
 }
 
@@ -394,7 +647,22 @@ void launch_compact_as(const CompactParams& p, hipStream_t stream) {
 }  // namespace
 
 hipError_t launch_select(const SelectParams& p, hipStream_t stream) {
-  select_kernel<<<dim3((uint32_t)p.num_slots), kSelectBlock, 0, stream>>>(p);
+  const dim3 slots((uint32_t)p.num_slots);
+  if (p.segments > 0) {
+    const dim3 grid((uint32_t)p.segments, (uint32_t)p.num_slots);
+    select_count_kernel<0><<<grid, kSelectBlock, 0, stream>>>(p);
+    select_count_kernel<1><<<grid, kSelectBlock, 0, stream>>>(p);
+    select_count_kernel<2><<<grid, kSelectBlock, 0, stream>>>(p);
+    select_write_kernel<<<grid, kSelectBlock, 0, stream>>>(p);
+  } else if (p.w_width <= kSelectBlock) {
+    select_registers_kernel<1><<<slots, kSelectBlock, 0, stream>>>(p);
+  } else if (p.w_width <= 4 * kSelectBlock) {
+    select_registers_kernel<4><<<slots, kSelectBlock, 0, stream>>>(p);
+  } else if (p.w_width <= kSelectRegisterRows) {
+    select_registers_kernel<kSelectRegisterRows / kSelectBlock><<<slots, kSelectBlock, 0, stream>>>(p);
+  } else {
+    select_stream_kernel<<<slots, kSelectBlock, 0, stream>>>(p);
+  }
   return hipGetLastError();
 }
 

@@ -321,9 +321,22 @@ int weigh(const kvc_weigh_args* a, bool tree, void* stream, const char* who) {
 }
 
 // ------------------------------------------------------------------ eviction
+// segments of a slot's row of weights, 0 where it is not cut
+int32_t evict_segments(int32_t slots, int64_t width) {
+  if (width <= kvc::kSelectRegisterRows || slots < 1 || slots > kvc::kSelectSegmentSlots) return 0;
+  const int64_t most = kvc::kSelectSegments / slots;
+  const int64_t n = (width + kvc::kSelectSegmentRows - 1) / kvc::kSelectSegmentRows;
+  return (int32_t)(n < most ? n : most);
+}
+
+// Bytes for calls of up to that many slots and weights a row, whatever cut
+// they take: a shorter row, or fewer slots, may be cut into more segments in
+// all, up to the most there are.
 int64_t evict_bytes(int32_t slots, int64_t width) {
-  (void)slots, (void)width;
-  return 0;
+  if (width <= kvc::kSelectRegisterRows) return 0;
+  const int64_t n = (width + kvc::kSelectSegmentRows - 1) / kvc::kSelectSegmentRows * slots;
+  const int64_t segments = n < kvc::kSelectSegments ? n : kvc::kSelectSegments;
+  return segments * (kvc::kSelectTopWords + 2 * kvc::kSelectLowWords + 4) * 4;
 }
 
 }  // namespace
@@ -838,7 +851,9 @@ int kvc_evict_select(const kvc_evict_args* a, void* stream) {
                 (long long)a->kept_width, (long long)a->kept_stride);
   if (a->kept_weights != nullptr && (a->kw_stride < a->kept_width || a->kept_weights == a->weights))
     return fail(KVC_EINVAL, "%s: kept_weights needs a stride >= kept_width, and is not weights", who);
-  const int64_t need = evict_bytes(a->num_slots, a->w_width);
+  const int32_t segments = evict_segments(a->num_slots, a->w_width);
+  const int64_t all = (int64_t)segments * a->num_slots;
+  const int64_t need = all * (kvc::kSelectTopWords + 2 * kvc::kSelectLowWords + 4) * 4;
   if (need > 0 && (a->workspace == nullptr || ((uintptr_t)a->workspace & 255u) != 0 || a->workspace_bytes < need))
     return fail(KVC_EINVAL, "%s: workspace needs %lld bytes, 256-byte aligned", who, (long long)need);
   if (kvc::launch_select == nullptr) return fail(KVC_ELAUNCH, "%s: built without kernels", who);
@@ -860,6 +875,13 @@ int kvc_evict_select(const kvc_evict_args* a, void* stream) {
   p.kept_weights = a->kept_weights;
   p.kw_stride = a->kw_stride;
   p.status = a->status;
+  if (segments > 0) {
+    p.segments = segments;
+    p.segment_rows = (a->w_width + segments - 1) / segments;
+    p.top_hists = static_cast<uint32_t*>(a->workspace);
+    p.low_hists = p.top_hists + all * kvc::kSelectTopWords;
+    p.states = reinterpret_cast<int32_t*>(p.low_hists + 2 * all * kvc::kSelectLowWords);
+  }
   return launched(kvc::launch_select(p, static_cast<hipStream_t>(stream)), who);
 }
 

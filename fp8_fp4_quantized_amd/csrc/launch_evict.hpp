@@ -80,6 +80,16 @@ struct WeighParams {
 };
 
 // ---------------------------------------------------------------- choice
+// Rows of weights that one workgroup keeps in registers; of longer ones of up to
+// kSelectSegmentSlots slots, a slot's rows are cut into segments of at least
+// kSelectSegmentRows, kSelectSegments for all slots together at the most.
+constexpr int kSelectRegisterRows = 16384;
+constexpr int kSelectSegmentSlots = 256;
+constexpr int kSelectSegmentRows = 16384;
+constexpr int kSelectSegments = 512;
+// words of a segment in the workspace: histograms of 12, 10 and 10 bits, a state of 4
+constexpr int kSelectTopWords = 4096, kSelectLowWords = 1024;
+
 struct SelectParams {
   int32_t ratio;
   int32_t num_slots;
@@ -96,6 +106,12 @@ struct SelectParams {
   float* kept_weights;         // nullable
   int64_t kw_stride;
   int32_t* status;
+  // segments a slot (0: none), their rows, and the workspace
+  int32_t segments;
+  int64_t segment_rows;
+  uint32_t* top_hists;         // [slots][segments][kSelectTopWords]
+  uint32_t* low_hists;         // [2][slots][segments][kSelectLowWords]
+  int32_t* states;             // [slots][segments][4]
 };
 
 // ---------------------------------------------------------------- move

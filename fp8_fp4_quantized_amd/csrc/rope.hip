@@ -12,6 +12,8 @@
 //   (a c - b s, a s + b c), transposed (a c + b s, b c - a s),
 // in fp32, rounded once to the heads' type.  Bound by HBM; in place only the
 // rotated dims move.
+#include <type_traits>
+
 #include "launch_evict.hpp"
 #include "layout.hpp"
 #include "row_ops.hpp"
@@ -151,6 +153,230 @@ hipError_t launch_elements(RopeRowsParams p, hipStream_t stream) {
   return hipGetLastError();
 }
 
+// By 16 bytes, E dims: a unit is 16 bytes of a head -- with pairs of halves, the
+// 16 bytes of either half that belong together.  A thread takes kUnits of them, all
+// loads issued before the first store.
+constexpr int kUnits = 4;
+
+template <int T>
+struct Vec {
+  static constexpr int E = T == kRopeF32 ? 4 : 8;
+  float f[E];
+  __device__ __forceinline__ explicit Vec(u32x4 v) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      if constexpr (T == kRopeF32) f[e] = __uint_as_float(v[e]);
+      else f[e] = Elem<T>::get((uint16_t)(v[e / 2] >> (16 * (e & 1))));
+    }
+  }
+  __device__ __forceinline__ u32x4 bits() const {
+    u32x4 v;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if constexpr (T == kRopeF32) v[k] = __float_as_uint(f[k]);
+      else if constexpr (T == kRopeBf16) v[k] = pack_bf16(f[2 * k], f[2 * k + 1]);
+      else v[k] = (uint32_t)Elem<T>::put(f[2 * k]) | (uint32_t)Elem<T>::put(f[2 * k + 1]) << 16;
+    }
+    return v;
+  }
+};
+
+// (a table's rows begin at multiples of 8 bytes)
+typedef float f32x4_8 __attribute__((ext_vector_type(4), aligned(8)));
+
+template <int T, bool HALF>
+__global__ __launch_bounds__(kRopeBlock) void rope_vectors_kernel(RopeRowsParams p) {
+  constexpr int E = Vec<T>::E, size = 16 / E;
+  const int64_t u0 = (int64_t)blockIdx.x * (kRopeBlock * kUnits);
+  const int64_t token0 = u0 / p.token_units;
+  const uint32_t rem0 = (uint32_t)(u0 - token0 * p.token_units) + threadIdx.x;
+  const int pair_units = HALF ? p.rot / 2 / E : 0;
+  u32x4 a[kUnits], b[kUnits];
+  uint8_t* out[kUnits];
+  int32_t pos[kUnits], d[kUnits];             // d: first dim of the unit (of its half)
+  bool pair[kUnits];                          // HALF: a unit of two
+#pragma unroll
+  for (int i = 0; i < kUnits; ++i) {
+    out[i] = nullptr;
+    if (u0 + i * kRopeBlock + threadIdx.x >= p.units) continue;
+    const Unit u = unit_at(p, token0, rem0 + i * kRopeBlock);
+    pos[i] = p.positions[u.token];
+    pair[i] = HALF && u.k < pair_units;
+    if constexpr (HALF) {
+      const int c = (u.k - pair_units) * E;   // dims that are copied
+      d[i] = pair[i] ? p.offset + u.k * E : c < p.offset ? c : c + p.rot;
+    } else {
+      d[i] = ((p.in_place ? p.offset / E : 0) + u.k) * E;
+    }
+    const uint8_t* x = (const uint8_t*)p.x + (u.token * p.x_stride + u.head * p.x_hstride + d[i]) * size;
+    out[i] = (uint8_t*)p.out + (u.token * p.out_stride + u.head * p.out_hstride + d[i]) * size;
+    a[i] = *(const u32x4*)x;
+    if (HALF && pair[i]) b[i] = *(const u32x4*)(x + p.rot / 2 * size);
+  }
+#pragma unroll
+  for (int i = 0; i < kUnits; ++i) {
+    if (out[i] == nullptr || !position_ok(p, pos[i])) continue;
+    const float* f = p.freqs + (int64_t)pos[i] * p.rot;
+    if constexpr (HALF) {
+      if (pair[i]) {
+        Vec<T> va(a[i]), vb(b[i]);
+#pragma unroll
+        for (int e = 0; e < E; e += 2) {
+          const f32x4_8 t = *(const f32x4_8*)(f + 2 * (d[i] - p.offset + e));
+          const Turned r0 = turn(va.f[e], vb.f[e], t[0], p.transpose ? -t[1] : t[1]);
+          const Turned r1 = turn(va.f[e + 1], vb.f[e + 1], t[2], p.transpose ? -t[3] : t[3]);
+          va.f[e] = r0.a, vb.f[e] = r0.b, va.f[e + 1] = r1.a, vb.f[e + 1] = r1.b;
+        }
+        a[i] = va.bits();
+        *(u32x4*)(out[i] + p.rot / 2 * size) = vb.bits();
+      }
+    } else {
+      const int at = d[i] - p.offset;         // (even)
+      if (at >= 0 && at + E <= p.rot) {
+        Vec<T> v(a[i]);
+#pragma unroll
+        for (int e = 0; e < E; e += 4) {
+          const f32x4_8 t = *(const f32x4_8*)(f + at + e);
+          const Turned r0 = turn(v.f[e], v.f[e + 1], t[0], p.transpose ? -t[1] : t[1]);
+          const Turned r1 = turn(v.f[e + 2], v.f[e + 3], t[2], p.transpose ? -t[3] : t[3]);
+          v.f[e] = r0.a, v.f[e + 1] = r0.b, v.f[e + 2] = r1.a, v.f[e + 3] = r1.b;
+        }
+        a[i] = v.bits();
+      } else if (at + E > 0 && at < p.rot) {
+        // the rotated dims begin or end in the unit
+        Vec<T> v(a[i]);
+#pragma unroll
+        for (int e = 0; e < E; e += 2) {
+          if (at + e < 0 || at + e >= p.rot) continue;
+          const f32x2 t = *(const f32x2*)(f + at + e);
+          const Turned r = turn(v.f[e], v.f[e + 1], t[0], p.transpose ? -t[1] : t[1]);
+          v.f[e] = r.a, v.f[e + 1] = r.b;
+        }
+        a[i] = v.bits();
+      }
+    }
+    *(u32x4*)out[i] = a[i];
+  }
+}
+
+// 16 bytes at an address of any element
+typedef uint32_t u32x4_2 __attribute__((ext_vector_type(4), aligned(2)));
+typedef uint32_t u32x4_4 __attribute__((ext_vector_type(4), aligned(4)));
+
+// The same for any offset, dims, strides and addresses, into another place than
+// x: every unit makes its own E dims (the last unit of a head ends with it and may
+// overlap the one before, which writes the same), whose partners it has, or
+// fetches one by one.  Addresses need not be multiples of 16: loads and stores of
+// 16 bytes take any.
+template <int T>
+__global__ __launch_bounds__(kRopeBlock) void rope_any_kernel(RopeRowsParams p) {
+  typedef typename Elem<T>::type Ty;
+  typedef typename std::conditional<T == kRopeF32, u32x4_4, u32x4_2>::type u32x4_any;
+  constexpr int E = Vec<T>::E;
+  const int64_t u0 = (int64_t)blockIdx.x * (kRopeBlock * kUnits);
+  const int64_t token0 = u0 / p.token_units;
+  const uint32_t rem0 = (uint32_t)(u0 - token0 * p.token_units) + threadIdx.x;
+  const int apart = p.rot / 2;
+  u32x4 v[kUnits];
+  const Ty* x[kUnits];
+  Ty* out[kUnits];
+  int32_t pos[kUnits], rel[kUnits];           // rel: first dim of the unit from the first rotated one
+#pragma unroll
+  for (int i = 0; i < kUnits; ++i) {
+    out[i] = nullptr;
+    if (u0 + i * kRopeBlock + threadIdx.x >= p.units) continue;
+    const Unit u = unit_at(p, token0, rem0 + i * kRopeBlock);
+    pos[i] = p.positions[u.token];
+    const int d = min(u.k * E, p.dim - E);
+    rel[i] = d - p.offset;
+    x[i] = (const Ty*)p.x + u.token * p.x_stride + u.head * p.x_hstride + d;
+    out[i] = (Ty*)p.out + u.token * p.out_stride + u.head * p.out_hstride + d;
+    v[i] = *(const u32x4_any*)x[i];
+  }
+#pragma unroll
+  for (int i = 0; i < kUnits; ++i) {
+    if (out[i] == nullptr || !position_ok(p, pos[i])) continue;
+    if (rel[i] + E > 0 && rel[i] < p.rot) {
+      const f32x2* f = (const f32x2*)(p.freqs + (int64_t)pos[i] * p.rot);
+      const Vec<T> own(v[i]);
+      Vec<T> made = own;
+      // partners: in the unit but for one at either end, or half the rotated dims away
+      float other[E];
+      if (!p.half) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) other[e] = ((rel[i] + e) & 1) != 0 ? own.f[max(e - 1, 0)] : own.f[min(e + 1, E - 1)];
+        if ((rel[i] & 1) != 0) {
+          if (rel[i] > 0) other[0] = Elem<T>::get(x[i][-1]);
+          if (rel[i] + E < p.rot) other[E - 1] = Elem<T>::get(x[i][E]);
+        }
+      } else if (rel[i] >= 0 && rel[i] + E <= apart) {
+        const Vec<T> w(*(const u32x4_any*)(x[i] + apart));
+#pragma unroll
+        for (int e = 0; e < E; ++e) other[e] = w.f[e];
+      } else if (rel[i] >= apart && rel[i] + E <= p.rot) {
+        const Vec<T> w(*(const u32x4_any*)(x[i] - apart));
+#pragma unroll
+        for (int e = 0; e < E; ++e) other[e] = w.f[e];
+      } else {
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          const int r = rel[i] + e;
+          other[e] = r >= 0 && r < p.rot ? Elem<T>::get(x[i][r < apart ? e + apart : e - apart]) : 0.0f;
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const int r = min(max(rel[i] + e, 0), p.rot - 1);
+        const bool second = p.half ? r >= apart : (r & 1) != 0;
+        const f32x2 t = f[p.half ? (second ? r - apart : r) : r >> 1];
+        const float sn = p.transpose ? -t[1] : t[1];
+        const float y = second ? turn(other[e], own.f[e], t[0], sn).b : turn(own.f[e], other[e], t[0], sn).a;
+        if (r == rel[i] + e) made.f[e] = y;
+      }
+      v[i] = made.bits();
+    }
+    *(u32x4_any*)out[i] = v[i];
+  }
+}
+
+template <int T>
+hipError_t launch_any(RopeRowsParams p, hipStream_t stream) {
+  constexpr int E = Vec<T>::E;
+  p.head_units = (p.dim + E - 1) / E;
+  p.token_units = p.head_units * p.heads;
+  p.head_div = div_magic((uint32_t)p.head_units);
+  p.token_div = div_magic((uint32_t)p.token_units);
+  p.units = p.tokens * p.token_units;
+  const dim3 grid((uint32_t)((p.units + kRopeBlock * kUnits - 1) / (kRopeBlock * kUnits)));
+  rope_any_kernel<T><<<grid, kRopeBlock, 0, stream>>>(p);
+  return hipGetLastError();
+}
+
+template <int T>
+hipError_t launch_vectors(RopeRowsParams p, hipStream_t stream) {
+  constexpr int E = Vec<T>::E;
+  if (p.half) p.head_units = p.rot / 2 / E + (p.in_place ? 0 : (p.dim - p.rot) / E);
+  else if (p.in_place) p.head_units = (p.offset + p.rot + E - 1) / E - p.offset / E;
+  else p.head_units = p.dim / E;
+  p.token_units = p.head_units * p.heads;
+  p.head_div = div_magic((uint32_t)p.head_units);
+  p.token_div = div_magic((uint32_t)p.token_units);
+  p.units = p.tokens * p.token_units;
+  const dim3 grid((uint32_t)((p.units + kRopeBlock * kUnits - 1) / (kRopeBlock * kUnits)));
+  if (p.half) rope_vectors_kernel<T, true><<<grid, kRopeBlock, 0, stream>>>(p);
+  else rope_vectors_kernel<T, false><<<grid, kRopeBlock, 0, stream>>>(p);
+  return hipGetLastError();
+}
+
+// Whether heads can be taken by 16 bytes: addresses, strides and dims of whole
+// ones, pairs inside one of them (or their halves at whole ones).
+bool by_vectors(const RopeRowsParams& p) {
+  const int E = p.type == kRopeF32 ? 4 : 8;
+  const int64_t strides = p.x_stride | p.x_hstride | p.out_stride | p.out_hstride | p.dim;
+  if (strides % E != 0 || (((uintptr_t)p.x | (uintptr_t)p.out) & 15u) != 0) return false;
+  return p.half ? p.offset % E == 0 && p.rot / 2 % E == 0 : p.offset % 2 == 0;
+}
+
 }  // namespace
 
 hipError_t launch_rope_table(const RopeTableParams& p, hipStream_t stream) {
@@ -162,6 +388,21 @@ hipError_t launch_rope_table(const RopeTableParams& p, hipStream_t stream) {
   return hipGetLastError();
 }
 
-hipError_t launch_rope_rows(const RopeRowsParams& p, hipStream_t stream) { return launch_elements(p, stream); }
+hipError_t launch_rope_rows(const RopeRowsParams& p, hipStream_t stream) {
+  if (!by_vectors(p)) {
+    // in place a unit's partners would be another's to write
+    if (p.in_place || p.dim < (p.type == kRopeF32 ? 4 : 8)) return launch_elements(p, stream);
+    switch (p.type) {
+      case kRopeBf16: return launch_any<kRopeBf16>(p, stream);
+      case kRopeF16: return launch_any<kRopeF16>(p, stream);
+      default: return launch_any<kRopeF32>(p, stream);
+    }
+  }
+  switch (p.type) {
+    case kRopeBf16: return launch_vectors<kRopeBf16>(p, stream);
+    case kRopeF16: return launch_vectors<kRopeF16>(p, stream);
+    default: return launch_vectors<kRopeF32>(p, stream);
+  }
+}
 
 }  // namespace kvc
