@@ -24,7 +24,7 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libkvc.so")
 SOURCES = ["kvc_api.cpp", "store_gather.hip", "compress.hip", "slot_map.hip", "attend.hip",
            "rope.hip", "weigh.hip", "evict.hip"]
-WAITS = {"attend.hip"}                        # matrix instructions written out
+WAITS = {"attend.hip", "weigh.hip"}           # matrix instructions written out
 CEILING_LIB = os.path.join(HERE, "libkvc_ceiling.so")
 CEILING_SOURCES = ["ceiling.hip"]
 ARCH = "gfx950"

@@ -22,6 +22,10 @@ namespace {
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
+
+typedef const __attribute__((address_space(3))) uint8_t* lds_cptr;
+typedef __attribute__((address_space(3))) uint8_t* lds_ptr;
 
 constexpr float kNegInf = -__builtin_inff();
 
@@ -176,8 +180,8 @@ __device__ __forceinline__ float sum_halves(float v) {
 // 32 queries of a slot in LDS: row m's 16-byte chunk c at place c ^ (m % 16) of
 // its 1024 bytes (16 consecutive rows' chunks then lie in all banks), and of each
 // query -lse, the rows below which all are seen, and a tree's mask.  A query past
-// the end, or one whose lse is not finite (it has no rows, or no answer), has
-// -lse = -inf and zeros: its weights are 0.
+// the end, or one whose lse is not finite (it has no rows, or no answer), gives
+// nothing and has -lse = -inf.
 struct QueryRows {
   float neg_lse[32];
   int32_t limit[32];
@@ -193,20 +197,21 @@ __device__ __forceinline__ uint64_t mask_of(const WeighParams& p, int64_t b, con
 // A lane's query m of the slot's flat (token, head) list; end: of the queries
 struct LaneQuery {
   const uint16_t* at;
-  float neg_lse;
+  float lse;                   // as it is in memory: waited for where neg_lse is called
   int32_t limit;
   uint64_t mask;
+  __device__ __forceinline__ float neg_lse() const { return __builtin_fabsf(lse) < __builtin_inff() ? -lse : kNegInf; }
 };
 __device__ __forceinline__ LaneQuery lane_query(const WeighParams& p, int64_t b, const SlotTokens& s, int64_t m,
                                                 int64_t end) {
   LaneQuery q{p.q, kNegInf, 0, 0};
   if (m >= end) return q;
+  // (no wait in here: what is loaded is looked at by the caller)
   const int32_t tok = (int32_t)udiv_magic((uint32_t)m, p.head_div.m, p.head_div.sh1, p.head_div.sh2);
   const int32_t head = (int32_t)m - tok * p.heads;
   const int64_t row = (int64_t)s.first + tok;
   q.at = p.q + row * p.q_stride + head * p.q_hstride;
-  const float lse = p.lse[row * p.heads + head];
-  if (__builtin_fabsf(lse) < __builtin_inff()) q.neg_lse = -lse;
+  q.lse = p.lse[row * p.heads + head];
   q.limit = p.tree != nullptr ? s.pos : (s.pos + tok + 1) >> (p.ratio - 1);
   if (p.tree != nullptr) q.mask = mask_of(p, b, s, tok);
   return q;
@@ -222,8 +227,11 @@ __device__ __forceinline__ bool sees(int32_t r, int32_t limit, bool tree, uint64
   return see;
 }
 
+// wait states from a last product to what reads, or overwrites, its result
+__device__ __forceinline__ void scores_done(f32x16& sc) { asm("s_nop 15" : "+v"(sc)); }
+
 // Adds a lane's 16 weights of a 32 x 32 result to v.  masked: some of the
-// queries may not see some of the rows.
+// queries may not see some of the rows, or give nothing.
 __device__ __forceinline__ float add_weights(float v, const f32x16& s, float scale, const QueryRows& q, int h,
                                              bool masked, int32_t r, bool tree, int32_t base) {
 #pragma unroll
@@ -234,7 +242,7 @@ __device__ __forceinline__ float add_weights(float v, const f32x16& s, float sca
       float w = __builtin_amdgcn_exp2f(__builtin_fmaf(s[4 * a + i], scale, nl[i]));
       if (masked) {
         const int m = 8 * a + 4 * h + i;
-        if (!sees(r, q.limit[m], tree, tree ? q.mask[m] : 0, base)) w = 0.0f;
+        if (nl[i] == kNegInf || !sees(r, q.limit[m], tree, tree ? q.mask[m] : 0, base)) w = 0.0f;
       }
       v += w;
     }
@@ -334,14 +342,14 @@ __global__ __launch_bounds__(kFewBlock) void weigh_few_kernel(WeighParams p) {
       const LaneQuery q = lane_query(p, b, s, m0 + (lane & 7), nq);
       if (lane < 8) {
         QueryRows& i = info[m0 >> 5];
-        i.neg_lse[(m0 & 31) + lane] = q.neg_lse;
+        i.neg_lse[(m0 & 31) + lane] = q.neg_lse();
         i.limit[(m0 & 31) + lane] = q.limit;
         i.mask[(m0 & 31) + lane] = q.mask;
       }
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         const int64_t from = uniform64(__shfl((int64_t)(uintptr_t)q.at, k));
-        const bool real = __shfl(q.neg_lse, k) != kNegInf;
+        const bool real = __shfl(q.neg_lse(), k) != kNegInf;
         u32x4 v = *(const u32x4*)((const uint8_t*)(uintptr_t)from + 16 * lane);
         if (!real) v = u32x4{0, 0, 0, 0};
         const int m = m0 + k;
@@ -375,6 +383,8 @@ __global__ __launch_bounds__(kFewBlock) void weigh_few_kernel(WeighParams p) {
           acc[n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, x, acc[n], 0, 0, 0);
         }
       }
+#pragma unroll
+      for (int n = 0; n < NC; ++n) scores_done(acc[n]);
       const bool masked = (int32_t)(32 * k) + 32 > clear;
       float v = 0.0f;
 #pragma unroll
@@ -464,31 +474,113 @@ struct Staged {
 };
 __device__ __forceinline__ void stage_load(Staged& g, const WeighParams& p, int64_t b, const SlotTokens& s,
                                            int64_t m0, int64_t end, int wave, int lane) {
+  typedef const __attribute__((address_space(1))) uint8_t* global_ptr;
   g.q = lane_query(p, b, s, m0 + 8 * wave + (lane & 7), end);
+  const uint64_t at = (uint64_t)(uintptr_t)g.q.at;
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
-    const int64_t from = uniform64(__shfl((int64_t)(uintptr_t)g.q.at, k));
-    g.v[k] = *(const u32x4*)((const uint8_t*)(uintptr_t)from + 16 * lane);
+    const uint64_t from = (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(at >> 32), k) << 32 |
+                          (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)at, k);
+    g.v[k] = *(const __attribute__((address_space(1))) u32x4*)((global_ptr)from + 16 * lane);
   }
 }
-__device__ __forceinline__ void stage_store(const Staged& g, uint8_t* rows, QueryRows& info, int wave, int lane) {
+// (the rows of queries that give nothing are as they come: see `plain` below)
+__device__ __forceinline__ void stage_store(const Staged& g, lds_ptr rows, QueryRows& info, int wave, int lane) {
   if (lane < 8) {
-    info.neg_lse[8 * wave + lane] = g.q.neg_lse;
-    info.limit[8 * wave + lane] = g.q.limit;
+    const float nl = g.q.neg_lse();
+    info.neg_lse[8 * wave + lane] = nl;
+    info.limit[8 * wave + lane] = nl == kNegInf ? 0 : g.q.limit;
     info.mask[8 * wave + lane] = g.q.mask;
   }
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const bool real = __shfl(g.q.neg_lse, k) != kNegInf;
-    const int m = 8 * wave + k;
-    *(u32x4*)(rows + m * 1024 + 16 * (lane ^ (m & 15))) = real ? g.v[k] : u32x4{0, 0, 0, 0};
-  }
+  for (int k = 0; k < 8; ++k)
+    *(__attribute__((address_space(3))) u32x4*)(rows + (8 * wave + k) * 1024 + 16 * (lane ^ (8 * (wave & 1) + k))) = g.v[k];
 }
+
+// The products are written out so that the rows stay in the 256 accumulator
+// registers and the scores in the vector registers their sums work in.  Their
+// operands come from LDS and from registers that stay; a result that feeds the next
+// product's C operand needs no wait.  The build reads the assembly for the wait
+// states and stops where one is missing.
+__device__ __forceinline__ void score_mfma(f32x16& sc, bf16x8 q, const bf16x8& x, bool first) {
+  if (first) asm("v_mfma_f32_32x32x16_bf16 %0, %1, %2, 0" : "=&v"(sc) : "v"(q), "a"(x));
+  else asm("v_mfma_f32_32x32x16_bf16 %0, %1, %2, %0" : "+&v"(sc) : "v"(q), "a"(x));
+}
+
+// a lane's place in a staged row of step j's queries
+template <int L>
+__device__ __forceinline__ uint32_t query_at(int j, int lane) {
+  const int c = Codes<L>::chunk(j);
+  const uint32_t base = (lane & 31) * 1024 + 16 * ((Codes<L>::half_chunks(j) * (lane >> 5)) ^ (lane & 15));
+  return (base ^ (16 * (c & 15))) + 256 * (c >> 4);
+}
+
+constexpr int kAhead = 4;        // fragments of queries read ahead
+
+// The scores of a chunk of 32 queries with the wave's 64 rows.  SUM 1: the weights
+// of the chunk before (scores prev, queries of) are added to part meanwhile, one a
+// step, their three instructions a step apart; 2: those of rows below the queries'
+// limits (r: the lane's first row).
+template <int L, int SUM>
+__device__ __forceinline__ void scores_of(f32x16 (&sc)[2], const bf16x8 (&x)[2][32], lds_cptr rows, int lane,
+                                          const f32x16 (&prev)[2], const QueryRows& of, int32_t r, float scale,
+                                          float (&part)[2]) {
+  bf16x8 q[kAhead];
+  float arg = 0.0f, w = 0.0f;
+  const int h = lane >> 5;
+  f32x4 nl[4];
+  i32x4 lim[4];
+  if constexpr (SUM > 0) {
+#pragma unroll
+    for (int a = 0; a < 4; ++a) nl[a] = *(const f32x4*)&of.neg_lse[8 * a + 4 * h];
+  }
+  if constexpr (SUM == 2) {
+#pragma unroll
+    for (int a = 0; a < 4; ++a) lim[a] = *(const i32x4*)&of.limit[8 * a + 4 * h];
+  }
+  // weight of step j: of scores prev[j % 2], element j / 2
+  auto kept = [&](float v, int j) {
+    if constexpr (SUM == 2) return r + 32 * (j & 1) < lim[j >> 3][j >> 1 & 3] ? v : 0.0f;
+    return v;
+  };
+#pragma unroll
+  for (int j = 0; j < kAhead; ++j) q[j] = *(const __attribute__((address_space(3))) bf16x8*)(rows + query_at<L>(j, lane));
+#pragma unroll
+  for (int j = 0; j < 32; ++j) {
+    score_mfma(sc[0], q[j % kAhead], x[0][j], j == 0);
+    score_mfma(sc[1], q[j % kAhead], x[1][j], j == 0);
+    if (j + kAhead < 32)
+      q[j % kAhead] = *(const __attribute__((address_space(3))) bf16x8*)(rows + query_at<L>(j + kAhead, lane));
+    if constexpr (SUM > 0) {
+      if (j > 1) part[j & 1] += kept(w, j - 2);
+      if (j > 0) w = __builtin_amdgcn_exp2f(arg);
+      arg = __builtin_fmaf(prev[j & 1][j >> 1], scale, nl[j >> 3][j >> 1 & 3]);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  if constexpr (SUM > 0) {
+    part[0] += kept(w, 30);
+    part[1] += kept(__builtin_amdgcn_exp2f(arg), 31);
+  }
+  scores_done(sc[0]);
+  scores_done(sc[1]);
+}
+
+// A sum with the rounding errors of its additions carried along (a slot's queries
+// may be a million)
+struct Total {
+  float sum, low;
+  __device__ __forceinline__ void add(float v) {
+    const float y = v - low, t = sum + y;
+    low = (t - sum) - y;
+    sum = t;
+  }
+};
 
 template <int L, int SLOTS>
 __global__ __launch_bounds__(kManyBlock) void weigh_many_kernel(WeighParams p) {
   __shared__ __attribute__((aligned(16))) uint8_t rows[2][32 * 1024];
-  __shared__ QueryRows info[2];
+  __shared__ QueryRows info[3];
   __shared__ Deal<SLOTS> deal;
   __shared__ int64_t buf[kManyBlock / kLanes];
   const int S = p.num_slots, tid = threadIdx.x, lane = lane_id(), wave = uniform(tid >> 6);
@@ -515,70 +607,99 @@ __global__ __launch_bounds__(kManyBlock) void weigh_many_kernel(WeighParams p) {
   WeighSplit split{0, 0, 0, 0};
   int64_t at = goal0;
   while (at < goal1) {
-    const BlockAt x = block_at<SLOTS>(p, deal, at);
-    at = x.end;
-    const SlotTokens& s = x.s;
-    const int32_t first = first_token(p, s, x.k << kManyRowBits);
-    const int32_t ta = x.at >= goal0 ? first : token_at(p, x, first, goal0);
-    const int32_t tb = x.end <= goal1 ? s.n : token_at(p, x, first, goal1);
+    const BlockAt blk = block_at<SLOTS>(p, deal, at);
+    at = blk.end;
+    const SlotTokens& s = blk.s;
+    const int32_t first = first_token(p, s, blk.k << kManyRowBits);
+    const int32_t ta = blk.at >= goal0 ? first : token_at(p, blk, first, goal0);
+    const int32_t tb = blk.end <= goal1 ? s.n : token_at(p, blk, first, goal1);
     if (ta >= tb) continue;
     const bool whole = ta == first && tb == s.n;
     if (ta == first && tb < s.n) {
-      const uint64_t last = (uint64_t)(x.end - 1) / (uint64_t)quota;
-      split = WeighSplit{x.b, x.k, (int32_t)last - wg + 1, 0};
+      const uint64_t last = (uint64_t)(blk.end - 1) / (uint64_t)quota;
+      split = WeighSplit{blk.b, blk.k, (int32_t)last - wg + 1, 0};
     }
+    const int64_t end = (int64_t)tb * p.heads;
+    int64_t m0 = (int64_t)ta * p.heads;
+    Staged g;
+    stage_load(g, p, blk.b, s, m0, end, wave, lane);
     // its rows
-    const int32_t r0 = (x.k << kManyRowBits) + 64 * wave;
-    bf16x8 xf[2][32];
+    const int32_t r0 = (blk.k << kManyRowBits) + 64 * wave;
+    bf16x8 x[2][32];
     bool ok[2];
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
-      const Place pl = place_of<L>(p, x.b, r0 + 32 * n + (lane & 31), s.rows);
+      const Place pl = place_of<L>(p, blk.b, r0 + 32 * n + (lane & 31), s.rows);
       ok[n] = pl.ok;
       Codes<L> c;
 #pragma unroll
       for (int i = 0; i < Codes<L>::N; ++i) c.load_code(pl.data, i);
       c.load_scale(pl.scale);
 #pragma unroll
-      for (int j = 0; j < 32; ++j) xf[n][j] = c.expand(j, h);
-    }
-    // the queries
-    const int64_t end = (int64_t)tb * p.heads;
-    int64_t m0 = (int64_t)ta * p.heads;
-    Staged g;
-    stage_load(g, p, x.b, s, m0, end, wave, lane);
-    stage_store(g, rows[0], info[0], wave, lane);
-    __syncthreads();
-    float v[2] = {0.0f, 0.0f};
-    for (int turn = 0; m0 < end; m0 += 32, turn ^= 1) {
-      const bool more = m0 + 32 < end;
-      if (more) stage_load(g, p, x.b, s, m0 + 32, end, wave, lane);
-      f32x16 acc[2] = {f32x16{}, f32x16{}};
-#pragma unroll
       for (int j = 0; j < 32; ++j) {
-        const uint32_t at_row = (lane & 31) * 1024 + 16 * ((Codes<L>::chunk(j) + Codes<L>::half_chunks(j) * h) ^ (lane & 15));
-        const bf16x8 a = *(const bf16x8*)(rows[turn] + at_row);
-        acc[0] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, xf[0][j], acc[0], 0, 0, 0);
-        acc[1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, xf[1][j], acc[1], 0, 0, 0);
+        x[n][j] = c.expand(j, h);
+        asm volatile("" : "+a"(x[n][j]));     // (to stay there)
       }
-      const bool masked = r0 + 64 > uniform(info[turn].limit[0]);
+    }
+    stage_store(g, (lds_ptr)rows[0], info[0], wave, lane);
+    __syncthreads();
+    // The queries, 32 a turn, the weights of a turn's scores added in the next one.
+    // plain: every query of the chunk gives weights to every row of the wave; a
+    // tree's others are added by themselves, each with its conditions.
+    Total total[2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};
+    f32x16 sc[2][2];
+    bool waiting = false, plain = false;
+    int now = 0;                              // of info's three
+    auto add_chunk = [&](f32x16 (&of)[2], const QueryRows& q) {
 #pragma unroll
       for (int n = 0; n < 2; ++n)
-        v[n] = masked ? add_weights(v[n], acc[n], p.scale_log2, info[turn], h, true, r0 + 32 * n + (lane & 31),
-                                    p.tree != nullptr, s.pos)
-                      : add_weights(v[n], acc[n], p.scale_log2, info[turn], h, false, 0, false, 0);
-      if (more) stage_store(g, rows[turn ^ 1], info[turn ^ 1], wave, lane);
+        total[n].add(add_weights(0.0f, of[n], p.scale_log2, q, h, true, r0 + 32 * n + (lane & 31), p.tree != nullptr,
+                                 s.pos));
+    };
+    auto step = [&](f32x16 (&cur)[2], f32x16 (&prev)[2], lds_ptr here, lds_ptr there) {
+      const bool more = m0 + 32 < end;
+      if (more) stage_load(g, p, blk.b, s, m0 + 32, end, wave, lane);
+      const QueryRows& before = info[now == 0 ? 2 : now - 1];
+      float part[2] = {0.0f, 0.0f};
+      if (waiting && plain) {
+        scores_of<L, 1>(cur, x, here, lane, prev, before, 0, p.scale_log2, part);
+      } else if (waiting && p.tree == nullptr) {
+        scores_of<L, 2>(cur, x, here, lane, prev, before, r0 + (lane & 31), p.scale_log2, part);
+      } else {
+        if (waiting) add_chunk(prev, before);
+        scores_of<L, 0>(cur, x, here, lane, prev, before, 0, 0.0f, part);
+      }
+      total[0].add(part[0]);
+      total[1].add(part[1]);
+      plain = __ballot(r0 + 64 > info[now].limit[lane & 31]) == 0;
+      waiting = true;
+      now = now == 2 ? 0 : now + 1;
+      if (more) stage_store(g, there, info[now], wave, lane);
       __syncthreads();
+      m0 += 32;
+    };
+    while (true) {
+      step(sc[0], sc[1], (lds_ptr)rows[0], (lds_ptr)rows[1]);
+      if (m0 >= end) {
+        add_chunk(sc[0], info[now == 0 ? 2 : now - 1]);
+        break;
+      }
+      step(sc[1], sc[0], (lds_ptr)rows[1], (lds_ptr)rows[0]);
+      if (m0 >= end) {
+        add_chunk(sc[1], info[now == 0 ? 2 : now - 1]);
+        break;
+      }
     }
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
-      const float both = sum_halves(v[n]), sum = ok[n] ? both : 0.0f;
+      const float both = sum_halves(total[n].sum), sum = ok[n] ? both : 0.0f;
       const int32_t r = r0 + 32 * n + (lane & 31);
       if (lane < 32) {
         if (!whole) p.parts[((int64_t)2 * wg + (ta > first ? 0 : 1)) * kWeighRows + 64 * wave + 32 * n + lane] = sum;
-        else if (r < s.rows) put_weight(p, x.b, s, r, sum);
+        else if (r < s.rows) put_weight(p, blk.b, s, r, sum);
       }
     }
+    __syncthreads();                          // info and rows are free
   }
   if (tid == 0) p.splits[wg] = split;
 }
