@@ -236,8 +236,8 @@ void rope_speeds(const kvc_rope_table_args* a, double* speed) {
 bool positive(double v) { return v > 0.0 && std::isfinite(v); }
 
 // ------------------------------------------------------------------ weights
-constexpr int64_t kWeighSplitBytes = kvc::kWeighWorkgroups * (int64_t)sizeof(kvc::WeighSplit);
-constexpr int64_t kWeighBytes = kWeighSplitBytes + 2 * kvc::kWeighWorkgroups * kvc::kWeighRows * (int64_t)sizeof(float);
+constexpr int64_t kWeighBytes =
+    (int64_t)sizeof(kvc::WeighHead) + kvc::kWeighParts * kvc::kWeighRows * (int64_t)sizeof(float);
 
 int weigh(const kvc_weigh_args* a, bool tree, void* stream, const char* who) {
   if (a == nullptr) return fail(KVC_EINVAL, "%s: args is NULL", who);
@@ -314,8 +314,8 @@ int weigh(const kvc_weigh_args* a, bool tree, void* stream, const char* who) {
   p.w_width = a->w_width;
   p.status = a->status;
   if (slot_queries > kvc::kWeighFew) {
-    p.splits = static_cast<kvc::WeighSplit*>(a->workspace);
-    p.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(a->workspace) + kWeighSplitBytes);
+    p.head = static_cast<kvc::WeighHead*>(a->workspace);
+    p.parts = reinterpret_cast<float*>(p.head + 1);
   }
   return launched(kvc::launch_weigh(p, slot_queries, static_cast<hipStream_t>(stream)), who);
 }

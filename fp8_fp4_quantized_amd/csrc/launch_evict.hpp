@@ -47,8 +47,12 @@ struct RopeRowsParams {
 constexpr int kWeighWorkgroups = 256;
 constexpr int kWeighRows = 256;       // rows of a block of it: 4 waves of 64
 
-struct WeighSplit {            // a block of rows cut between workgroups, by the one that has its first part
-  int32_t slot, block, parts, pad;
+// Places for the sums of slots that are cut into segments (256 floats each)
+constexpr int kWeighParts = 16384;
+
+struct WeighHead {             // written by the kernel, for the one that joins its sums
+  int32_t cut;                 // segments of 2^cut tokens
+  int32_t pad[63];
 };
 
 struct WeighParams {
@@ -75,8 +79,8 @@ struct WeighParams {
   int64_t w_stride, w_width;
   int32_t* status;
   // workspace of the kernel for many queries
-  WeighSplit* splits;          // [kWeighWorkgroups]
-  float* parts;                // [2 * kWeighWorkgroups][kWeighRows]
+  WeighHead* head;
+  float* parts;                // [kWeighParts][kWeighRows]
 };
 
 // ---------------------------------------------------------------- choice

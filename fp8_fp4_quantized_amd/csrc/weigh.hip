@@ -400,26 +400,30 @@ __global__ __launch_bounds__(kFewBlock) void weigh_few_kernel(WeighParams p) {
 
 // ------------------------------------------------------------------ many queries
 // Blocks of 256 rows, 64 a wave, whose operands stay in registers while the
-// queries that see them pass through LDS, 32 at a time.  The work of all blocks
-// is dealt evenly to the workgroups, a run each of the blocks' tokens in order;
-// what a workgroup has of a block that it does not have whole goes to the
-// workspace, and weigh_join_kernel adds the parts in order.
+// queries that see them pass through LDS, 32 at a time.  A slot's tokens are cut
+// into segments of 2^cut tokens; a part is a segment's queries with one of the
+// blocks that they see.  Parts are numbered segment by segment, an eighth of them
+// goes to the workgroups of each XCD, which take them in turn: those that run at
+// the same time share a segment, and its queries come from their L2 (a prompt of
+// 8,192 tokens with 128 heads is 1 GB of queries, each seen by 16 blocks on
+// average).  The sums of a slot of several segments go to the workspace, and
+// weigh_join_kernel adds them in order.
 constexpr int kManyBlock = 256;
 constexpr int kManyRowBits = 8;
 static_assert(kWeighRows == 1 << kManyRowBits, "rows of a block");
-
-// A block's begin, its rows fetched and expanded, as the queries that take the
-// same time
-constexpr int kBlockQueries = 128;
+constexpr int kXcds = 8;
 
 __device__ __forceinline__ int32_t blocks_of(const SlotTokens& s) {
   return (int32_t)(((int64_t)s.rows + kWeighRows - 1) >> kManyRowBits);
 }
+__device__ __forceinline__ int32_t segments_of(const SlotTokens& s, int cut) {
+  return (int32_t)(((int64_t)s.n + (int64_t(1) << cut) - 1) >> cut);
+}
 
-// Cost of the first k blocks of a slot: their (token, head) pairs, the tokens of
-// block i being those from first_token of its first row on -- 0, or growing by
-// rows * ratio a block.
-__device__ __forceinline__ int64_t cost_before(const WeighParams& p, const SlotTokens& s, int64_t k) {
+// (token, head) pairs of all blocks of a slot with the tokens that see their
+// first row: those from first_token on, which is 0 or grows by rows * ratio a block
+__device__ __forceinline__ int64_t work_of(const WeighParams& p, const SlotTokens& s) {
+  const int64_t k = blocks_of(s);
   int64_t tokens = s.n * k;
   if (p.tree == nullptr) {
     const int step = kManyRowBits + p.ratio - 1;
@@ -427,44 +431,115 @@ __device__ __forceinline__ int64_t cost_before(const WeighParams& p, const SlotT
     const int64_t i1 = c > 0 ? 0 : (-c >> step) + 1;
     if (k > i1) tokens -= (k - i1) * (((i1 + k - 1) << step) + 2 * c) / 2;
   }
-  return tokens * p.heads + k * kBlockQueries;
+  return tokens * p.heads;
 }
 
+// sum of i >> d over i < n
+__device__ __forceinline__ int64_t sum_shifted(int64_t n, int d) {
+  const int64_t q = n >> d, r = n & ((int64_t(1) << d) - 1);
+  return (q * (q - 1) / 2 << d) + r * q;
+}
+
+// Parts of the first g segments of a slot: the blocks that their last tokens see.
+// The last token of segment i sees (pos + (i + 1) 2^cut) >> (ratio - 1) rows, in
+// (y + i 2^cut) >> s blocks, y and s as below; the slot's last segment, and a
+// segment past the rows there are, see all of them.
+__device__ __forceinline__ int64_t parts_before(const WeighParams& p, const SlotTokens& s, int cut, int64_t g) {
+  const int64_t all = blocks_of(s);
+  if (p.tree != nullptr) return g * all;
+  const int64_t G = segments_of(s, cut), few = min(g, G - 1);
+  const int sh = kManyRowBits + p.ratio - 1;
+  const int64_t y = (int64_t)s.pos + (int64_t(1) << cut) + ((int64_t)(kWeighRows - 1) << (p.ratio - 1));
+  // segments that see fewer than all
+  const int64_t reach = (all << sh) - y;      // y + i 2^cut < all 2^s
+  const int64_t part = min(few, reach > 0 ? (reach + (int64_t(1) << cut) - 1) >> cut : 0);
+  const int64_t sum = cut >= sh ? part * (y >> sh) + ((part * (part - 1) / 2) << (cut - sh))
+                                : sum_shifted((y >> cut) + part, sh - cut) - sum_shifted(y >> cut, sh - cut);
+  return sum + (g - part) * all;
+}
+__device__ __forceinline__ int64_t parts_of(const WeighParams& p, const SlotTokens& s, int cut) {
+  return s.n > 0 ? parts_before(p, s, cut, segments_of(s, cut)) : 0;
+}
+
+// The first cut tried: segments of `share` queries, a sixteenth of a
+// workgroup's share of the work, but 2,048 or the whole share where it is less.
+__device__ __forceinline__ int first_cut(const WeighParams& p, int64_t work) {
+  const int64_t each = (work + kWeighWorkgroups - 1) / kWeighWorkgroups;
+  const int64_t share = max(each / 16, min(each, (int64_t)2048));
+  int cut = 0;
+  while ((int64_t)p.heads << (cut + 1) <= share && cut < 30) ++cut;
+  return cut;
+}
+
+// Sums over the slots before each second one: of their parts, and of those of
+// them that go to the workspace.
 template <int SLOTS>
 struct Deal {
-  int64_t before[SLOTS];       // cost of the slots before each one
+  uint32_t parts[SLOTS / 2], stored[SLOTS / 2];
 };
-
-// a slot's block, and where it begins in the call's cost
-struct BlockAt {
-  int b;
-  SlotTokens s;
-  int32_t k;
-  int64_t at, end;
+// fills it for a cut; returns the totals to every thread
+struct Totals {
+  int64_t parts, stored;
 };
 template <int SLOTS>
-__device__ __forceinline__ BlockAt block_at(const WeighParams& p, const Deal<SLOTS>& d, int64_t at) {
-  BlockAt x;
-  x.b = uniform(slot_at(d.before, p.num_slots, at));
+__device__ __forceinline__ Totals deal_parts(const WeighParams& p, int cut, Deal<SLOTS>& d, int64_t* buf) {
+  Totals t{0, 0};
+  for (int b0 = 0; b0 < p.num_slots; b0 += 2 * kManyBlock) {
+    const int b = b0 + 2 * (int)threadIdx.x;
+    int64_t n = 0, m = 0, total;
+    int32_t none = 0;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if (b + i >= p.num_slots) continue;
+      const SlotTokens s = slot_tokens(p, b + i, &none);
+      const int64_t parts = parts_of(p, s, cut);
+      n += parts;
+      m += segments_of(s, cut) > 1 ? parts : 0;
+    }
+    const int64_t ne = block_scan64<kManyBlock>(n, buf, &total) + t.parts;
+    t.parts += total;
+    const int64_t me = block_scan64<kManyBlock>(m, buf, &total) + t.stored;
+    t.stored += total;
+    if (b < p.num_slots) d.parts[b >> 1] = (uint32_t)(ne - n), d.stored[b >> 1] = (uint32_t)(me - m);
+  }
+  __syncthreads();
+  return t;
+}
+
+// A part: its slot, segment and block, and its place in the workspace (-1: the
+// slot has one segment).
+struct Part {
+  int b;
+  SlotTokens s;
+  int32_t g, k;
+  int64_t stored;
+};
+template <int SLOTS>
+__device__ __forceinline__ Part part_at(const WeighParams& p, const Deal<SLOTS>& d, int cut, uint32_t at) {
+  Part x;
+  x.b = 2 * slot_at(d.parts, (p.num_slots + 1) >> 1, at);
+  int64_t in = at - d.parts[x.b >> 1], base = d.stored[x.b >> 1];
   int32_t none = 0;
-  const SlotTokens s = slot_tokens(p, x.b, &none);
+  SlotTokens s = slot_tokens(p, x.b, &none);
+  const int64_t mine = parts_of(p, s, cut);
+  if (in >= mine) {
+    in -= mine;
+    if (segments_of(s, cut) > 1) base += mine;
+    s = slot_tokens(p, ++x.b, &none);
+  }
+  x.b = uniform(x.b);
   x.s = SlotTokens{uniform(s.first), uniform(s.n), uniform(s.pos), uniform(s.rows)};
-  const int64_t in = at - uniform64(d.before[x.b]);
-  int32_t lo = 0, hi = blocks_of(x.s) - 1;
+  const int32_t G = segments_of(x.s, cut);
+  int32_t lo = 0, hi = G - 1;
   while (lo < hi) {
-    const int32_t mid = (int32_t)(((int64_t)lo + hi + 1) >> 1);
-    if (cost_before(p, x.s, mid) <= in) lo = mid;
+    const int32_t mid = (lo + hi + 1) >> 1;
+    if (parts_before(p, x.s, cut, mid) <= in) lo = mid;
     else hi = mid - 1;
   }
-  x.k = uniform(lo);
-  x.at = uniform64(d.before[x.b]) + cost_before(p, x.s, x.k);
-  x.end = uniform64(d.before[x.b]) + cost_before(p, x.s, x.k + 1);
+  x.g = uniform(lo);
+  x.k = uniform((int32_t)(in - parts_before(p, x.s, cut, lo)));
+  x.stored = G > 1 ? uniform64(base + in) : -1;
   return x;
-}
-// token of a block where place `at` of the call's cost falls
-__device__ __forceinline__ int32_t token_at(const WeighParams& p, const BlockAt& x, int32_t first, int64_t at) {
-  const int64_t in = at - x.at - kBlockQueries;
-  return in <= 0 ? first : first + (int32_t)udiv_magic((uint32_t)in, p.head_div.m, p.head_div.sh1, p.head_div.sh2);
 }
 
 // 8 of a chunk's 32 queries, on their way to LDS
@@ -548,14 +623,17 @@ __device__ __forceinline__ void scores_of(f32x16 (&sc)[2], const bf16x8 (&x)[2][
 #pragma unroll
   for (int j = 0; j < 32; ++j) {
     score_mfma(sc[0], q[j % kAhead], x[0][j], j == 0);
-    score_mfma(sc[1], q[j % kAhead], x[1][j], j == 0);
-    if (j + kAhead < 32)
-      q[j % kAhead] = *(const __attribute__((address_space(3))) bf16x8*)(rows + query_at<L>(j + kAhead, lane));
+    __builtin_amdgcn_sched_barrier(0);
     if constexpr (SUM > 0) {
       if (j > 1) part[j & 1] += kept(w, j - 2);
       if (j > 0) w = __builtin_amdgcn_exp2f(arg);
-      arg = __builtin_fmaf(prev[j & 1][j >> 1], scale, nl[j >> 3][j >> 1 & 3]);
     }
+    __builtin_amdgcn_sched_barrier(0);
+    score_mfma(sc[1], q[j % kAhead], x[1][j], j == 0);
+    __builtin_amdgcn_sched_barrier(0);
+    if (j + kAhead < 32)
+      q[j % kAhead] = *(const __attribute__((address_space(3))) bf16x8*)(rows + query_at<L>(j + kAhead, lane));
+    if constexpr (SUM > 0) arg = __builtin_fmaf(prev[j & 1][j >> 1], scale, nl[j >> 3][j >> 1 & 3]);
     __builtin_amdgcn_sched_barrier(0);
   }
   if constexpr (SUM > 0) {
@@ -584,41 +662,24 @@ __global__ __launch_bounds__(kManyBlock) void weigh_many_kernel(WeighParams p) {
   __shared__ Deal<SLOTS> deal;
   __shared__ int64_t buf[kManyBlock / kLanes];
   const int S = p.num_slots, tid = threadIdx.x, lane = lane_id(), wave = uniform(tid >> 6);
-  const int h = lane >> 5, wg = blockIdx.x;
+  const int h = lane >> 5;
   int32_t bad = 0;
-  int64_t carry = 0;
-  for (int b0 = 0; b0 < S; b0 += kManyBlock) {
-    const int b = b0 + tid;
-    int64_t cost = 0, total;
-    if (b < S) {
-      const SlotTokens s = slot_tokens(p, b, &bad);
-      cost = cost_before(p, s, blocks_of(s));
-    }
-    const int64_t end = block_scan64<kManyBlock>(cost, buf, &total) + carry;
-    if (b < S) deal.before[b] = end - cost;
-    carry += total;
-  }
-  __syncthreads();
-  if (wg == 0 && bad != 0 && p.status != nullptr) atomicOr(p.status, bad);
-  // (a share holds a block's begin and a token, so that no part of a block is empty)
-  const int64_t quota = max((carry + kWeighWorkgroups - 1) / kWeighWorkgroups,
-                            (int64_t)kBlockQueries + max(p.heads, 256));
-  const int64_t goal0 = quota * wg, goal1 = min(goal0 + quota, carry);
-  WeighSplit split{0, 0, 0, 0};
-  int64_t at = goal0;
-  while (at < goal1) {
-    const BlockAt blk = block_at<SLOTS>(p, deal, at);
-    at = blk.end;
+  int64_t work = 0;
+  for (int b = tid; b < S; b += kManyBlock) work += work_of(p, slot_tokens(p, b, &bad));
+  block_scan64<kManyBlock>(work, buf, &work);
+  if (blockIdx.x == 0 && bad != 0 && p.status != nullptr) atomicOr(p.status, bad);
+  // (longer segments where there would be more parts than places for them)
+  int cut = first_cut(p, uniform64(work));
+  Totals all = deal_parts(p, cut, deal, buf);
+  while (all.stored > kWeighParts) all = deal_parts(p, ++cut, deal, buf);
+  if (blockIdx.x == 0 && tid == 0) p.head->cut = cut;
+  const int64_t count = uniform64(all.parts);
+  const uint32_t xcd = blockIdx.x % kXcds, to = (uint32_t)(count * (xcd + 1) / kXcds);
+  for (uint32_t at = (uint32_t)(count * xcd / kXcds) + blockIdx.x / kXcds; at < to; at += kWeighWorkgroups / kXcds) {
+    const Part blk = part_at(p, deal, cut, at);
     const SlotTokens& s = blk.s;
-    const int32_t first = first_token(p, s, blk.k << kManyRowBits);
-    const int32_t ta = blk.at >= goal0 ? first : token_at(p, blk, first, goal0);
-    const int32_t tb = blk.end <= goal1 ? s.n : token_at(p, blk, first, goal1);
-    if (ta >= tb) continue;
-    const bool whole = ta == first && tb == s.n;
-    if (ta == first && tb < s.n) {
-      const uint64_t last = (uint64_t)(blk.end - 1) / (uint64_t)quota;
-      split = WeighSplit{blk.b, blk.k, (int32_t)last - wg + 1, 0};
-    }
+    const int32_t ta = max(first_token(p, s, blk.k << kManyRowBits), blk.g << cut);
+    const int32_t tb = (int32_t)min((int64_t)s.n, (int64_t)(blk.g + 1) << cut);
     const int64_t end = (int64_t)tb * p.heads;
     int64_t m0 = (int64_t)ta * p.heads;
     Staged g;
@@ -657,8 +718,7 @@ __global__ __launch_bounds__(kManyBlock) void weigh_many_kernel(WeighParams p) {
                                  s.pos));
     };
     auto step = [&](f32x16 (&cur)[2], f32x16 (&prev)[2], lds_ptr here, lds_ptr there) {
-      const bool more = m0 + 32 < end;
-      if (more) stage_load(g, p, blk.b, s, m0 + 32, end, wave, lane);
+      stage_load(g, p, blk.b, s, m0 + 32, end, wave, lane);
       const QueryRows& before = info[now == 0 ? 2 : now - 1];
       float part[2] = {0.0f, 0.0f};
       if (waiting && plain) {
@@ -674,7 +734,7 @@ __global__ __launch_bounds__(kManyBlock) void weigh_many_kernel(WeighParams p) {
       plain = __ballot(r0 + 64 > info[now].limit[lane & 31]) == 0;
       waiting = true;
       now = now == 2 ? 0 : now + 1;
-      if (more) stage_store(g, there, info[now], wave, lane);
+      stage_store(g, there, info[now], wave, lane);
       __syncthreads();
       m0 += 32;
     };
@@ -695,25 +755,70 @@ __global__ __launch_bounds__(kManyBlock) void weigh_many_kernel(WeighParams p) {
       const float both = sum_halves(total[n].sum), sum = ok[n] ? both : 0.0f;
       const int32_t r = r0 + 32 * n + (lane & 31);
       if (lane < 32) {
-        if (!whole) p.parts[((int64_t)2 * wg + (ta > first ? 0 : 1)) * kWeighRows + 64 * wave + 32 * n + lane] = sum;
+        if (blk.stored >= 0) p.parts[blk.stored * kWeighRows + 64 * wave + 32 * n + lane] = sum;
         else if (r < s.rows) put_weight(p, blk.b, s, r, sum);
       }
     }
     __syncthreads();                          // info and rows are free
   }
-  if (tid == 0) p.splits[wg] = split;
 }
 
-__global__ __launch_bounds__(kWeighRows) void weigh_join_kernel(WeighParams p) {
-  const int wg = blockIdx.x;
-  const WeighSplit x = p.splits[wg];
-  if (x.parts == 0) return;
+// The sums of the slots that have several segments: a workgroup a block of rows,
+// its parts dealt to four groups of threads and added in order.
+constexpr int kJoinBlock = 1024;
+constexpr int kJoinGroups = kJoinBlock / kWeighRows;
+
+template <int SLOTS>
+__global__ __launch_bounds__(kJoinBlock) void weigh_join_kernel(WeighParams p) {
+  __shared__ uint32_t blocks[SLOTS / 2], stored[SLOTS / 2];
+  __shared__ int64_t buf[kJoinBlock / kLanes];
+  __shared__ float sums[kJoinGroups][kWeighRows];
+  const int cut = uniform(p.head->cut), S = p.num_slots;
+  int64_t count = 0, places = 0;
   int32_t none = 0;
-  const SlotTokens s = slot_tokens(p, x.slot, &none);
-  float v = p.parts[((int64_t)2 * wg + 1) * kWeighRows + threadIdx.x];
-  for (int i = 1; i < x.parts; ++i) v += p.parts[((int64_t)2 * (wg + i)) * kWeighRows + threadIdx.x];
-  const int32_t r = (x.block << kManyRowBits) + (int32_t)threadIdx.x;
-  if (r < s.rows) put_weight(p, x.slot, s, r, v);
+  for (int b0 = 0; b0 < S; b0 += 2 * kJoinBlock) {
+    const int b = b0 + 2 * (int)threadIdx.x;
+    int64_t n = 0, m = 0, total;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if (b + i >= S) continue;
+      const SlotTokens s = slot_tokens(p, b + i, &none);
+      if (segments_of(s, cut) > 1) n += blocks_of(s), m += parts_of(p, s, cut);
+    }
+    const int64_t ne = block_scan64<kJoinBlock>(n, buf, &total) + count;
+    count += total;
+    const int64_t me = block_scan64<kJoinBlock>(m, buf, &total) + places;
+    places += total;
+    if (b < S) blocks[b >> 1] = (uint32_t)(ne - n), stored[b >> 1] = (uint32_t)(me - m);
+  }
+  __syncthreads();
+  const int row = threadIdx.x % kWeighRows, group = threadIdx.x / kWeighRows;
+  for (uint32_t at = blockIdx.x; at < (uint32_t)count; at += gridDim.x) {
+    int b = 2 * slot_at(blocks, (S + 1) >> 1, at);
+    int64_t k = at - blocks[b >> 1], base = stored[b >> 1];
+    SlotTokens s = slot_tokens(p, b, &none);
+    const int64_t mine = segments_of(s, cut) > 1 ? blocks_of(s) : 0;
+    if (k >= mine) {
+      if (mine > 0) base += parts_of(p, s, cut);
+      k -= mine;
+      s = slot_tokens(p, ++b, &none);
+    }
+    // the block's parts: of the segments from the one of the first token that sees it
+    const int32_t G = segments_of(s, cut), g0 = first_token(p, s, (int32_t)k << kManyRowBits) >> cut;
+    float v = 0.0f;
+#pragma unroll 4
+    for (int32_t g = g0 + group; g < G; g += kJoinGroups)
+      v += p.parts[(base + parts_before(p, s, cut, g) + k) * kWeighRows + row];
+    sums[group][row] = v;
+    __syncthreads();
+    const int32_t r = ((int32_t)k << kManyRowBits) + row;
+    if (group == 0 && r < s.rows) {
+#pragma unroll
+      for (int i = 1; i < kJoinGroups; ++i) v += sums[i][row];
+      put_weight(p, b, s, r, v);
+    }
+    __syncthreads();
+  }
 }
 
 template <int L, int NC>
@@ -727,9 +832,13 @@ void launch_weigh_as(const WeighParams& p, int64_t slot_queries, hipStream_t str
   if (slot_queries <= 32) return launch_few<L, 1>(p, stream);
   if (slot_queries <= 64) return launch_few<L, 2>(p, stream);
   if (slot_queries <= kWeighFew) return launch_few<L, 4>(p, stream);
-  if (p.num_slots <= 1024) weigh_many_kernel<L, 1024><<<kWeighWorkgroups, kManyBlock, 0, stream>>>(p);
-  else weigh_many_kernel<L, kMaxSlots + 1><<<kWeighWorkgroups, kManyBlock, 0, stream>>>(p);
-  weigh_join_kernel<<<kWeighWorkgroups, kWeighRows, 0, stream>>>(p);
+  if (p.num_slots <= 1024) {
+    weigh_many_kernel<L, 1024><<<kWeighWorkgroups, kManyBlock, 0, stream>>>(p);
+    weigh_join_kernel<1024><<<kWeighWorkgroups, kJoinBlock, 0, stream>>>(p);
+  } else {
+    weigh_many_kernel<L, kMaxSlots + 1><<<kWeighWorkgroups, kManyBlock, 0, stream>>>(p);
+    weigh_join_kernel<kMaxSlots + 1><<<kWeighWorkgroups, kJoinBlock, 0, stream>>>(p);
+  }
 }
 
 }  // namespace
