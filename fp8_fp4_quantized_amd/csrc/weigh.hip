@@ -194,28 +194,68 @@ __device__ __forceinline__ uint64_t mask_of(const WeighParams& p, int64_t b, con
   return s.n < 64 ? m & ((uint64_t(1) << s.n) - 1) : m;
 }
 
-// A lane's query m of the slot's flat (token, head) list; end: of the queries
+// A lane's query m of the slot's flat (token, head) list, which ends at `end`: where
+// it lies (one past the end: where the last one does), and what is known of it.
+// lse is as it is in memory, waited for where put is called.
 struct LaneQuery {
   const uint16_t* at;
-  float lse;                   // as it is in memory: waited for where neg_lse is called
+  float lse;
   int32_t limit;
   uint64_t mask;
-  __device__ __forceinline__ float neg_lse() const { return __builtin_fabsf(lse) < __builtin_inff() ? -lse : kNegInf; }
+  bool real;
+
+  __device__ __forceinline__ void locate(const WeighParams& p, const SlotTokens& s, int64_t m, int64_t end,
+                                         int64_t* token, int64_t* entry) {
+    real = m < end;
+    const uint32_t n = (uint32_t)min(m, end - 1);
+    const uint32_t tok = udiv_magic(n, p.head_div.m, p.head_div.sh1, p.head_div.sh2);
+    const uint32_t head = n - tok * p.heads;
+    const int64_t row = (int64_t)s.first + tok;
+    at = p.q + row * p.q_stride + head * p.q_hstride;
+    limit = p.tree != nullptr ? s.pos : (int32_t)((uint32_t)s.pos + tok + 1) >> (p.ratio - 1);
+    *token = tok;
+    *entry = row * p.heads + head;
+  }
+  __device__ __forceinline__ void fetch(const WeighParams& p, int64_t b, const SlotTokens& s, int64_t token,
+                                        int64_t entry) {
+    lse = p.lse[entry];
+    mask = p.tree != nullptr ? mask_of(p, b, s, (int32_t)token) : 0;
+  }
+  __device__ __forceinline__ float neg_lse() const {
+    return real && __builtin_fabsf(lse) < __builtin_inff() ? -lse : kNegInf;
+  }
+  __device__ __forceinline__ void put(QueryRows& info, int m) const {
+    const float v = neg_lse();
+    info.neg_lse[m] = v;
+    info.limit[m] = v == kNegInf ? 0 : limit;
+    info.mask[m] = v == kNegInf ? 0 : mask;
+  }
 };
-__device__ __forceinline__ LaneQuery lane_query(const WeighParams& p, int64_t b, const SlotTokens& s, int64_t m,
-                                                int64_t end) {
-  LaneQuery q{p.q, kNegInf, 0, 0};
-  if (m >= end) return q;
-  // (no wait in here: what is loaded is looked at by the caller)
-  const int32_t tok = (int32_t)udiv_magic((uint32_t)m, p.head_div.m, p.head_div.sh1, p.head_div.sh2);
-  const int32_t head = (int32_t)m - tok * p.heads;
-  const int64_t row = (int64_t)s.first + tok;
-  q.at = p.q + row * p.q_stride + head * p.q_hstride;
-  q.lse = p.lse[row * p.heads + head];
-  q.limit = p.tree != nullptr ? s.pos : (s.pos + tok + 1) >> (p.ratio - 1);
-  if (p.tree != nullptr) q.mask = mask_of(p, b, s, tok);
-  return q;
-}
+
+// 8 queries of a wave on their way to LDS, 8 lanes each: load i takes their i-th 128
+// bytes.  m: the lane's query among those staged (8 * wave + lane / 8 + a multiple of 32).
+struct Staged {
+  u32x4 v[8];
+  LaneQuery q;
+  int64_t token, entry;
+
+  __device__ __forceinline__ void locate(const WeighParams& p, const SlotTokens& s, int64_t m, int64_t end) {
+    q.locate(p, s, m, end, &token, &entry);
+  }
+  __device__ __forceinline__ void load(int i) {
+    typedef const __attribute__((address_space(1))) u32x4* vec;
+    v[i] = *(vec)((uint64_t)(uintptr_t)q.at + 128 * i + 16 * (lane_id() & 7));
+  }
+  static __device__ __forceinline__ uint32_t place(int m) {
+    return m * 1024 + 16 * ((lane_id() & 7) ^ (m & 15));
+  }
+  __device__ __forceinline__ void store(lds_ptr rows, int m, int i) const {
+    *(__attribute__((address_space(3))) u32x4*)(rows + (place(m) ^ (128 * (i & 1))) + 256 * (i >> 1)) = v[i];
+  }
+  __device__ __forceinline__ void put(QueryRows& info, int m) const {
+    if ((lane_id() & 7) == 0) q.put(info, m);
+  }
+};
 
 // whether a query with that limit and mask sees row r; base: the row of mask bit 0
 __device__ __forceinline__ bool sees(int32_t r, int32_t limit, bool tree, uint64_t mask, int32_t base) {
@@ -339,21 +379,20 @@ __global__ __launch_bounds__(kFewBlock) void weigh_few_kernel(WeighParams p) {
     const int64_t nq = (int64_t)s.n * p.heads;
     __syncthreads();
     for (int m0 = 8 * wave; m0 < 32 * NC; m0 += 8 * kFewWaves) {
-      const LaneQuery q = lane_query(p, b, s, m0 + (lane & 7), nq);
-      if (lane < 8) {
-        QueryRows& i = info[m0 >> 5];
-        i.neg_lse[(m0 & 31) + lane] = q.neg_lse();
-        i.limit[(m0 & 31) + lane] = q.limit;
-        i.mask[(m0 & 31) + lane] = q.mask;
-      }
+      Staged g;
+      const int m = m0 + (lane >> 3);
+      g.locate(p, s, m, nq);
+      g.q.fetch(p, b, s, g.token, g.entry);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const int64_t from = uniform64(__shfl((int64_t)(uintptr_t)q.at, k));
-        const bool real = __shfl(q.neg_lse(), k) != kNegInf;
-        u32x4 v = *(const u32x4*)((const uint8_t*)(uintptr_t)from + 16 * lane);
-        if (!real) v = u32x4{0, 0, 0, 0};
-        const int m = m0 + k;
-        *(u32x4*)(rows + m * 1024 + 16 * (lane ^ (m & 15))) = v;
+      for (int i = 0; i < 8; ++i) g.load(i);
+      g.put(info[m0 >> 5], m & 31);
+      // (zeros in place of a query that gives nothing: its weights are then 0 of
+      // themselves)
+      const bool gives = g.q.neg_lse() != kNegInf;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (!gives) g.v[i] = u32x4{0, 0, 0, 0};
+        g.store((lds_ptr)rows, m, i);
       }
     }
     __syncthreads();
@@ -542,36 +581,6 @@ __device__ __forceinline__ Part part_at(const WeighParams& p, const Deal<SLOTS>&
   return x;
 }
 
-// 8 of a chunk's 32 queries, on their way to LDS
-struct Staged {
-  u32x4 v[8];
-  LaneQuery q;
-};
-__device__ __forceinline__ void stage_load(Staged& g, const WeighParams& p, int64_t b, const SlotTokens& s,
-                                           int64_t m0, int64_t end, int wave, int lane) {
-  typedef const __attribute__((address_space(1))) uint8_t* global_ptr;
-  g.q = lane_query(p, b, s, m0 + 8 * wave + (lane & 7), end);
-  const uint64_t at = (uint64_t)(uintptr_t)g.q.at;
-#pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const uint64_t from = (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(at >> 32), k) << 32 |
-                          (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)at, k);
-    g.v[k] = *(const __attribute__((address_space(1))) u32x4*)((global_ptr)from + 16 * lane);
-  }
-}
-// (the rows of queries that give nothing are as they come: see `plain` below)
-__device__ __forceinline__ void stage_store(const Staged& g, lds_ptr rows, QueryRows& info, int wave, int lane) {
-  if (lane < 8) {
-    const float nl = g.q.neg_lse();
-    info.neg_lse[8 * wave + lane] = nl;
-    info.limit[8 * wave + lane] = nl == kNegInf ? 0 : g.q.limit;
-    info.mask[8 * wave + lane] = g.q.mask;
-  }
-#pragma unroll
-  for (int k = 0; k < 8; ++k)
-    *(__attribute__((address_space(3))) u32x4*)(rows + (8 * wave + k) * 1024 + 16 * (lane ^ (8 * (wave & 1) + k))) = g.v[k];
-}
-
 // The products are written out so that the rows stay in the 256 accumulator
 // registers and the scores in the vector registers their sums work in.  Their
 // operands come from LDS and from registers that stay; a result that feeds the next
@@ -582,12 +591,43 @@ __device__ __forceinline__ void score_mfma(f32x16& sc, bf16x8 q, const bf16x8& x
   else asm("v_mfma_f32_32x32x16_bf16 %0, %1, %2, %0" : "+&v"(sc) : "v"(q), "a"(x));
 }
 
-// a lane's place in a staged row of step j's queries
+// 32 queries in LDS, as loads bring them there by themselves, 64 consecutive
+// 16-byte places each: groups of 8 queries, of each its dims in pieces of 64, of
+// each piece the 8 queries' 128 bytes.  Which query and chunk a place holds is the
+// lane's choice of address: query m of the group is at row m ^ (group % 2), its chunk c
+// of the piece at c ^ m, so that 16 consecutive queries' chunks lie in all banks.
+constexpr int kChunkBytes = 32 * 1024;
+struct Staging {
+  LaneQuery q;
+  int32_t m;                   // the lane's query of a chunk
+
+  __device__ __forceinline__ Staging(int wave, int lane) : m(8 * wave + ((lane >> 3) ^ (wave & 1))) {}
+  // where the lane reads; the query itself, then its lse and mask
+  __device__ __forceinline__ void locate(const WeighParams& p, int64_t b, const SlotTokens& s, int64_t m0, int64_t end) {
+    int64_t token, entry;
+    q.locate(p, s, m0 + m, end, &token, &entry);
+    q.fetch(p, b, s, token, entry);
+    q.at += 8 * ((lane_id() & 7) ^ (m & 7));
+  }
+  // piece i, to the place `to` of LDS (below 64 KB) and the 1,023 bytes behind it
+  __device__ __forceinline__ void load(uint32_t to, int i) const {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(to), "v"(q.at + 64 * i)
+                 : "memory", "m0");
+  }
+  // all loads are there, and the lane's own of the lse
+  __device__ __forceinline__ void arrive(QueryRows& info) const {
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    if ((lane_id() & 7) == 0) q.put(info, m);
+  }
+};
+
+// a lane's place in a staged chunk of step j's queries
 template <int L>
 __device__ __forceinline__ uint32_t query_at(int j, int lane) {
-  const int c = Codes<L>::chunk(j);
-  const uint32_t base = (lane & 31) * 1024 + 16 * ((Codes<L>::half_chunks(j) * (lane >> 5)) ^ (lane & 15));
-  return (base ^ (16 * (c & 15))) + 256 * (c >> 4);
+  const int c = Codes<L>::chunk(j), m = lane & 31;
+  const uint32_t base = (m >> 3) * 8192 + ((m & 7) ^ (m >> 3 & 1)) * 128 +
+                        16 * ((Codes<L>::half_chunks(j) * (lane >> 5)) ^ (m & 7));
+  return (base ^ (16 * (c & 7))) + 1024 * (c >> 3);
 }
 
 constexpr int kAhead = 4;        // fragments of queries read ahead
@@ -595,11 +635,11 @@ constexpr int kAhead = 4;        // fragments of queries read ahead
 // The scores of a chunk of 32 queries with the wave's 64 rows.  SUM 1: the weights
 // of the chunk before (scores prev, queries of) are added to part meanwhile, one a
 // step, their three instructions a step apart; 2: those of rows below the queries'
-// limits (r: the lane's first row).
-template <int L, int SUM>
+// limits (r: the lane's first row).  beside(j) is done in step j.
+template <int L, int SUM, typename Beside>
 __device__ __forceinline__ void scores_of(f32x16 (&sc)[2], const bf16x8 (&x)[2][32], lds_cptr rows, int lane,
                                           const f32x16 (&prev)[2], const QueryRows& of, int32_t r, float scale,
-                                          float (&part)[2]) {
+                                          float (&part)[2], Beside&& beside) {
   bf16x8 q[kAhead];
   float arg = 0.0f, w = 0.0f;
   const int h = lane >> 5;
@@ -634,6 +674,7 @@ __device__ __forceinline__ void scores_of(f32x16 (&sc)[2], const bf16x8 (&x)[2][
     if (j + kAhead < 32)
       q[j % kAhead] = *(const __attribute__((address_space(3))) bf16x8*)(rows + query_at<L>(j + kAhead, lane));
     if constexpr (SUM > 0) arg = __builtin_fmaf(prev[j & 1][j >> 1], scale, nl[j >> 3][j >> 1 & 3]);
+    beside(j);
     __builtin_amdgcn_sched_barrier(0);
   }
   if constexpr (SUM > 0) {
@@ -657,33 +698,40 @@ struct Total {
 
 template <int L, int SLOTS>
 __global__ __launch_bounds__(kManyBlock) void weigh_many_kernel(WeighParams p) {
-  __shared__ __attribute__((aligned(16))) uint8_t rows[2][32 * 1024];
-  __shared__ QueryRows info[3];
-  __shared__ Deal<SLOTS> deal;
-  __shared__ int64_t buf[kManyBlock / kLanes];
+  // (one object, the chunks at its begin: the loads that fill them reach 64 KB)
+  __shared__ struct {
+    __attribute__((aligned(1024))) uint8_t rows[2][kChunkBytes];
+    QueryRows info[3];
+    Deal<SLOTS> deal;
+    int64_t buf[kManyBlock / kLanes];
+  } sh;
+  QueryRows* const info = sh.info;
   const int S = p.num_slots, tid = threadIdx.x, lane = lane_id(), wave = uniform(tid >> 6);
   const int h = lane >> 5;
   int32_t bad = 0;
   int64_t work = 0;
   for (int b = tid; b < S; b += kManyBlock) work += work_of(p, slot_tokens(p, b, &bad));
-  block_scan64<kManyBlock>(work, buf, &work);
+  block_scan64<kManyBlock>(work, sh.buf, &work);
   if (blockIdx.x == 0 && bad != 0 && p.status != nullptr) atomicOr(p.status, bad);
   // (longer segments where there would be more parts than places for them)
   int cut = first_cut(p, uniform64(work));
-  Totals all = deal_parts(p, cut, deal, buf);
-  while (all.stored > kWeighParts) all = deal_parts(p, ++cut, deal, buf);
+  Totals all = deal_parts(p, cut, sh.deal, sh.buf);
+  while (all.stored > kWeighParts) all = deal_parts(p, ++cut, sh.deal, sh.buf);
   if (blockIdx.x == 0 && tid == 0) p.head->cut = cut;
   const int64_t count = uniform64(all.parts);
   const uint32_t xcd = blockIdx.x % kXcds, to = (uint32_t)(count * (xcd + 1) / kXcds);
   for (uint32_t at = (uint32_t)(count * xcd / kXcds) + blockIdx.x / kXcds; at < to; at += kWeighWorkgroups / kXcds) {
-    const Part blk = part_at(p, deal, cut, at);
+    const Part blk = part_at(p, sh.deal, cut, at);
     const SlotTokens& s = blk.s;
     const int32_t ta = max(first_token(p, s, blk.k << kManyRowBits), blk.g << cut);
     const int32_t tb = (int32_t)min((int64_t)s.n, (int64_t)(blk.g + 1) << cut);
     const int64_t end = (int64_t)tb * p.heads;
     int64_t m0 = (int64_t)ta * p.heads;
-    Staged g;
-    stage_load(g, p, blk.b, s, m0, end, wave, lane);
+    Staging g(wave, lane);
+    g.locate(p, blk.b, s, m0, end);
+    const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_ptr)sh.rows[0] + 8192 * wave;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) g.load(lds0 + 1024 * i, i);
     // its rows
     const int32_t r0 = (blk.k << kManyRowBits) + 64 * wave;
     bf16x8 x[2][32];
@@ -702,7 +750,7 @@ __global__ __launch_bounds__(kManyBlock) void weigh_many_kernel(WeighParams p) {
         asm volatile("" : "+a"(x[n][j]));     // (to stay there)
       }
     }
-    stage_store(g, (lds_ptr)rows[0], info[0], wave, lane);
+    g.arrive(info[0]);
     __syncthreads();
     // The queries, 32 a turn, the weights of a turn's scores added in the next one.
     // plain: every query of the chunk gives weights to every row of the wave; a
@@ -717,34 +765,39 @@ __global__ __launch_bounds__(kManyBlock) void weigh_many_kernel(WeighParams p) {
         total[n].add(add_weights(0.0f, of[n], p.scale_log2, q, h, true, r0 + 32 * n + (lane & 31), p.tree != nullptr,
                                  s.pos));
     };
-    auto step = [&](f32x16 (&cur)[2], f32x16 (&prev)[2], lds_ptr here, lds_ptr there) {
-      stage_load(g, p, blk.b, s, m0 + 32, end, wave, lane);
+    auto step = [&](f32x16 (&cur)[2], f32x16 (&prev)[2], lds_cptr here, uint32_t there) {
+      // the next chunk is asked for between the first products
+      QueryRows& next = info[now == 2 ? 0 : now + 1];
+      auto beside = [&](int j) {
+        if (j == 0) g.locate(p, blk.b, s, m0 + 32, end);
+        else if (j <= 8) g.load(there + 1024 * (j - 1), j - 1);
+      };
       const QueryRows& before = info[now == 0 ? 2 : now - 1];
       float part[2] = {0.0f, 0.0f};
       if (waiting && plain) {
-        scores_of<L, 1>(cur, x, here, lane, prev, before, 0, p.scale_log2, part);
+        scores_of<L, 1>(cur, x, here, lane, prev, before, 0, p.scale_log2, part, beside);
       } else if (waiting && p.tree == nullptr) {
-        scores_of<L, 2>(cur, x, here, lane, prev, before, r0 + (lane & 31), p.scale_log2, part);
+        scores_of<L, 2>(cur, x, here, lane, prev, before, r0 + (lane & 31), p.scale_log2, part, beside);
       } else {
         if (waiting) add_chunk(prev, before);
-        scores_of<L, 0>(cur, x, here, lane, prev, before, 0, 0.0f, part);
+        scores_of<L, 0>(cur, x, here, lane, prev, before, 0, 0.0f, part, beside);
       }
       total[0].add(part[0]);
       total[1].add(part[1]);
       plain = __ballot(r0 + 64 > info[now].limit[lane & 31]) == 0;
       waiting = true;
       now = now == 2 ? 0 : now + 1;
-      stage_store(g, there, info[now], wave, lane);
+      g.arrive(next);
       __syncthreads();
       m0 += 32;
     };
     while (true) {
-      step(sc[0], sc[1], (lds_ptr)rows[0], (lds_ptr)rows[1]);
+      step(sc[0], sc[1], (lds_cptr)sh.rows[0], lds0 + kChunkBytes);
       if (m0 >= end) {
         add_chunk(sc[0], info[now == 0 ? 2 : now - 1]);
         break;
       }
-      step(sc[1], sc[0], (lds_ptr)rows[1], (lds_ptr)rows[0]);
+      step(sc[1], sc[0], (lds_cptr)sh.rows[1], lds0);
       if (m0 >= end) {
         add_chunk(sc[1], info[now == 0 ? 2 : now - 1]);
         break;
