@@ -271,8 +271,9 @@ int weigh(const kvc_weigh_args* a, bool tree, void* stream, const char* who) {
   // (the stride of an axis of one entry is not used)
   p.q_stride = a->q_rows > 1 ? a->q_stride : 0;
   p.q_hstride = a->num_heads > 1 ? a->q_head_stride : 0;
-  if (p.q_stride < 0 || p.q_hstride < 0 || p.q_stride % 8 != 0 || p.q_hstride % 8 != 0)
-    return fail(KVC_EINVAL, "%s: q strides must be multiples of 8, >= 0", who);
+  if (p.q_stride < 0 || p.q_hstride < 0 || p.q_stride % 8 != 0 || p.q_hstride % 8 != 0 ||
+      p.q_stride > 0x7FFFFFFF || p.q_hstride > 0x7FFFFFFF)
+    return fail(KVC_EINVAL, "%s: q strides must be multiples of 8 in [0, 2^31)", who);
   if (a->lse == nullptr || a->start_pos == nullptr || (!tree && a->offsets == nullptr))
     return fail(KVC_EINVAL, "%s: NULL lse, start_pos or offsets", who);
   if (a->page_table == nullptr || a->pt_width < 1 || a->pt_stride < a->pt_width)

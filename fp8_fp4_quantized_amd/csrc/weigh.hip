@@ -200,26 +200,24 @@ __device__ __forceinline__ uint64_t mask_of(const WeighParams& p, int64_t b, con
 struct LaneQuery {
   const uint16_t* at;
   float lse;
-  int32_t limit;
+  int32_t token, limit;
+  int64_t entry;               // of lse
   uint64_t mask;
   bool real;
 
-  __device__ __forceinline__ void locate(const WeighParams& p, const SlotTokens& s, int64_t m, int64_t end,
-                                         int64_t* token, int64_t* entry) {
+  __device__ __forceinline__ void locate(const WeighParams& p, const SlotTokens& s, int32_t m, int32_t end) {
     real = m < end;
     const uint32_t n = (uint32_t)min(m, end - 1);
-    const uint32_t tok = udiv_magic(n, p.head_div.m, p.head_div.sh1, p.head_div.sh2);
-    const uint32_t head = n - tok * p.heads;
-    const int64_t row = (int64_t)s.first + tok;
-    at = p.q + row * p.q_stride + head * p.q_hstride;
-    limit = p.tree != nullptr ? s.pos : (int32_t)((uint32_t)s.pos + tok + 1) >> (p.ratio - 1);
-    *token = tok;
-    *entry = row * p.heads + head;
+    token = (int32_t)udiv_magic(n, p.head_div.m, p.head_div.sh1, p.head_div.sh2);
+    const uint32_t head = n - (uint32_t)token * (uint32_t)p.heads, row = (uint32_t)(s.first + token);
+    // (strides are below 2^31)
+    at = p.q + ((uint64_t)row * (uint32_t)p.q_stride + (uint64_t)head * (uint32_t)p.q_hstride);
+    entry = (uint64_t)row * (uint32_t)p.heads + head;
+    limit = p.tree != nullptr ? s.pos : (s.pos + token + 1) >> (p.ratio - 1);
   }
-  __device__ __forceinline__ void fetch(const WeighParams& p, int64_t b, const SlotTokens& s, int64_t token,
-                                        int64_t entry) {
+  __device__ __forceinline__ void fetch(const WeighParams& p, int64_t b, const SlotTokens& s) {
     lse = p.lse[entry];
-    mask = p.tree != nullptr ? mask_of(p, b, s, (int32_t)token) : 0;
+    mask = p.tree != nullptr ? mask_of(p, b, s, token) : 0;
   }
   __device__ __forceinline__ float neg_lse() const {
     return real && __builtin_fabsf(lse) < __builtin_inff() ? -lse : kNegInf;
@@ -237,11 +235,7 @@ struct LaneQuery {
 struct Staged {
   u32x4 v[8];
   LaneQuery q;
-  int64_t token, entry;
 
-  __device__ __forceinline__ void locate(const WeighParams& p, const SlotTokens& s, int64_t m, int64_t end) {
-    q.locate(p, s, m, end, &token, &entry);
-  }
   __device__ __forceinline__ void load(int i) {
     typedef const __attribute__((address_space(1))) u32x4* vec;
     v[i] = *(vec)((uint64_t)(uintptr_t)q.at + 128 * i + 16 * (lane_id() & 7));
@@ -376,13 +370,13 @@ __global__ __launch_bounds__(kFewBlock) void weigh_few_kernel(WeighParams p) {
     s = SlotTokens{uniform(s.first), uniform(s.n), uniform(s.pos), uniform(s.rows)};
     const uint32_t k0 = uniform((int32_t)(at - first)), k1 = min((uint32_t)uniform((int32_t)blocks), to - uniform((int32_t)first));
     // its queries
-    const int64_t nq = (int64_t)s.n * p.heads;
+    const int32_t nq = s.n * p.heads;
     __syncthreads();
     for (int m0 = 8 * wave; m0 < 32 * NC; m0 += 8 * kFewWaves) {
       Staged g;
       const int m = m0 + (lane >> 3);
-      g.locate(p, s, m, nq);
-      g.q.fetch(p, b, s, g.token, g.entry);
+      g.q.locate(p, s, m, nq);
+      g.q.fetch(p, b, s);
 #pragma unroll
       for (int i = 0; i < 8; ++i) g.load(i);
       g.put(info[m0 >> 5], m & 31);
@@ -597,27 +591,23 @@ __device__ __forceinline__ void score_mfma(f32x16& sc, bf16x8 q, const bf16x8& x
 // lane's choice of address: query m of the group is at row m ^ (group % 2), its chunk c
 // of the piece at c ^ m, so that 16 consecutive queries' chunks lie in all banks.
 constexpr int kChunkBytes = 32 * 1024;
-struct Staging {
-  LaneQuery q;
-  int32_t m;                   // the lane's query of a chunk
-
-  __device__ __forceinline__ Staging(int wave, int lane) : m(8 * wave + ((lane >> 3) ^ (wave & 1))) {}
-  // where the lane reads; the query itself, then its lse and mask
-  __device__ __forceinline__ void locate(const WeighParams& p, int64_t b, const SlotTokens& s, int64_t m0, int64_t end) {
-    int64_t token, entry;
-    q.locate(p, s, m0 + m, end, &token, &entry);
-    q.fetch(p, b, s, token, entry);
-    q.at += 8 * ((lane_id() & 7) ^ (m & 7));
+struct Staging : LaneQuery {
+  // piece I, from the lane's part of its query (8 dims at 8 * part) to the place `to` of
+  // LDS, below 64 KB, + 1024 I
+  template <int I>
+  __device__ __forceinline__ void load(uint32_t to, int part) const {
+    asm volatile("s_add_u32 m0, %0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(to),
+                 "v"(at + 8 * part + 64 * I), "n"(1024 * I)
+                 : "memory", "m0", "scc");
   }
-  // piece i, to the place `to` of LDS (below 64 KB) and the 1,023 bytes behind it
-  __device__ __forceinline__ void load(uint32_t to, int i) const {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(to), "v"(q.at + 64 * i)
-                 : "memory", "m0");
+  __device__ __forceinline__ void load_all(uint32_t to, int part) const {
+    load<0>(to, part), load<1>(to, part), load<2>(to, part), load<3>(to, part);
+    load<4>(to, part), load<5>(to, part), load<6>(to, part), load<7>(to, part);
   }
-  // all loads are there, and the lane's own of the lse
-  __device__ __forceinline__ void arrive(QueryRows& info) const {
+  // all that was asked for is there
+  __device__ __forceinline__ void arrive(QueryRows& info, int m) const {
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    if ((lane_id() & 7) == 0) q.put(info, m);
+    if ((lane_id() & 7) == 0) put(info, m);
   }
 };
 
@@ -633,13 +623,13 @@ __device__ __forceinline__ uint32_t query_at(int j, int lane) {
 constexpr int kAhead = 4;        // fragments of queries read ahead
 
 // The scores of a chunk of 32 queries with the wave's 64 rows.  SUM 1: the weights
-// of the chunk before (scores prev, queries of) are added to part meanwhile, one a
-// step, their three instructions a step apart; 2: those of rows below the queries'
-// limits (r: the lane's first row).  beside(j) is done in step j.
+// of the chunk before (scores prev, queries of) are added up meanwhile, one a step,
+// their three instructions a step apart; 2: those of rows below each query's own
+// limit (r: the lane's first row).  beside(j) is done in step j.
 template <int L, int SUM, typename Beside>
 __device__ __forceinline__ void scores_of(f32x16 (&sc)[2], const bf16x8 (&x)[2][32], lds_cptr rows, int lane,
                                           const f32x16 (&prev)[2], const QueryRows& of, int32_t r, float scale,
-                                          float (&part)[2], Beside&& beside) {
+                                          float (&sum)[2], Beside&& beside) {
   bf16x8 q[kAhead];
   float arg = 0.0f, w = 0.0f;
   const int h = lane >> 5;
@@ -665,7 +655,7 @@ __device__ __forceinline__ void scores_of(f32x16 (&sc)[2], const bf16x8 (&x)[2][
     score_mfma(sc[0], q[j % kAhead], x[0][j], j == 0);
     __builtin_amdgcn_sched_barrier(0);
     if constexpr (SUM > 0) {
-      if (j > 1) part[j & 1] += kept(w, j - 2);
+      if (j > 1) sum[j & 1] += kept(w, j - 2);
       if (j > 0) w = __builtin_amdgcn_exp2f(arg);
     }
     __builtin_amdgcn_sched_barrier(0);
@@ -678,8 +668,8 @@ __device__ __forceinline__ void scores_of(f32x16 (&sc)[2], const bf16x8 (&x)[2][
     __builtin_amdgcn_sched_barrier(0);
   }
   if constexpr (SUM > 0) {
-    part[0] += kept(w, 30);
-    part[1] += kept(__builtin_amdgcn_exp2f(arg), 31);
+    sum[0] += kept(w, 30);
+    sum[1] += kept(__builtin_amdgcn_exp2f(arg), 31);
   }
   scores_done(sc[0]);
   scores_done(sc[1]);
@@ -725,13 +715,16 @@ __global__ __launch_bounds__(kManyBlock) void weigh_many_kernel(WeighParams p) {
     const SlotTokens& s = blk.s;
     const int32_t ta = max(first_token(p, s, blk.k << kManyRowBits), blk.g << cut);
     const int32_t tb = (int32_t)min((int64_t)s.n, (int64_t)(blk.g + 1) << cut);
-    const int64_t end = (int64_t)tb * p.heads;
-    int64_t m0 = (int64_t)ta * p.heads;
-    Staging g(wave, lane);
-    g.locate(p, blk.b, s, m0, end);
+    const int32_t end = tb * p.heads;
+    int32_t m0 = ta * p.heads;
+    // the lane's query of a chunk, when they are staged, and its part of it
+    const int mine = 8 * wave + ((lane >> 3) ^ (wave & 1)), part8 = (lane & 7) ^ (mine & 7);
+    Staging g[2];
+    g[0].locate(p, s, m0 + mine, end);
     const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_ptr)sh.rows[0] + 8192 * wave;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) g.load(lds0 + 1024 * i, i);
+    g[0].load_all(lds0, part8);
+    g[0].fetch(p, blk.b, s);
+    g[1].locate(p, s, m0 + 32 + mine, end);
     // its rows
     const int32_t r0 = (blk.k << kManyRowBits) + 64 * wave;
     bf16x8 x[2][32];
@@ -750,14 +743,16 @@ __global__ __launch_bounds__(kManyBlock) void weigh_many_kernel(WeighParams p) {
         asm volatile("" : "+a"(x[n][j]));     // (to stay there)
       }
     }
-    g.arrive(info[0]);
+    g[0].arrive(info[0], mine);
     __syncthreads();
     // The queries, 32 a turn, the weights of a turn's scores added in the next one.
-    // plain: every query of the chunk gives weights to every row of the wave; a
-    // tree's others are added by themselves, each with its conditions.
+    // Where the queries of a chunk all see the same rows (those of a token's heads do),
+    // a lane takes its sum or leaves it (`limit`); where they do not, each weight has
+    // its own condition, and a tree's are added by themselves.
     Total total[2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};
     f32x16 sc[2][2];
-    bool waiting = false, plain = false;
+    bool waiting = false, same = false;
+    int32_t limit = 0;                        // of the chunk before, where `same`
     int now = 0;                              // of info's three
     auto add_chunk = [&](f32x16 (&of)[2], const QueryRows& q) {
 #pragma unroll
@@ -765,44 +760,64 @@ __global__ __launch_bounds__(kManyBlock) void weigh_many_kernel(WeighParams p) {
         total[n].add(add_weights(0.0f, of[n], p.scale_log2, q, h, true, r0 + 32 * n + (lane & 31), p.tree != nullptr,
                                  s.pos));
     };
-    auto step = [&](f32x16 (&cur)[2], f32x16 (&prev)[2], lds_cptr here, uint32_t there) {
-      // the next chunk is asked for between the first products
-      QueryRows& next = info[now == 2 ? 0 : now + 1];
-      auto beside = [&](int j) {
-        if (j == 0) g.locate(p, blk.b, s, m0 + 32, end);
-        else if (j <= 8) g.load(there + 1024 * (j - 1), j - 1);
-      };
+    // (the running sums are added up in fp32 for 8 turns, then into the totals)
+    float part[2] = {0.0f, 0.0f};
+    int turns = 0;
+    auto step = [&](f32x16 (&cur)[2], f32x16 (&prev)[2], lds_cptr here, uint32_t there, Staging& next, Staging& after) {
       const QueryRows& before = info[now == 0 ? 2 : now - 1];
-      float part[2] = {0.0f, 0.0f};
-      if (waiting && plain) {
-        scores_of<L, 1>(cur, x, here, lane, prev, before, 0, p.scale_log2, part, beside);
+      const int32_t mine_sees = info[now].limit[lane & 31];
+      // the next chunk is asked for between the first products, the one after it
+      // located between the last
+      auto beside = [&](int j) {
+        if (j == 0) next.load<0>(there, part8), next.load<1>(there, part8);
+        if (j == 1) next.load<2>(there, part8), next.load<3>(there, part8);
+        if (j == 2) next.load<4>(there, part8), next.load<5>(there, part8);
+        if (j == 3) next.load<6>(there, part8), next.load<7>(there, part8);
+        if (j == 4) next.fetch(p, blk.b, s);
+        if (j == 20) after.locate(p, s, m0 + 64 + mine, end);
+      };
+      float sum[2] = {0.0f, 0.0f};
+      if (waiting && same) {
+        scores_of<L, 1>(cur, x, here, lane, prev, before, 0, p.scale_log2, sum, beside);
+#pragma unroll
+        for (int n = 0; n < 2; ++n) sum[n] = r0 + 32 * n + (lane & 31) < limit ? sum[n] : 0.0f;
       } else if (waiting && p.tree == nullptr) {
-        scores_of<L, 2>(cur, x, here, lane, prev, before, r0 + (lane & 31), p.scale_log2, part, beside);
+        scores_of<L, 2>(cur, x, here, lane, prev, before, r0 + (lane & 31), p.scale_log2, sum, beside);
       } else {
         if (waiting) add_chunk(prev, before);
-        scores_of<L, 0>(cur, x, here, lane, prev, before, 0, 0.0f, part, beside);
+        scores_of<L, 0>(cur, x, here, lane, prev, before, 0, 0.0f, sum, beside);
       }
-      total[0].add(part[0]);
-      total[1].add(part[1]);
-      plain = __ballot(r0 + 64 > info[now].limit[lane & 31]) == 0;
+      part[0] += sum[0];
+      part[1] += sum[1];
+      if ((++turns & 7) == 0) {
+        total[0].add(part[0]);
+        total[1].add(part[1]);
+        part[0] = part[1] = 0.0f;
+      }
+      // (the rows of the wave, all below every limit, or cut by the same one)
+      limit = uniform(mine_sees);
+      same = __ballot(mine_sees != limit) == 0 && (p.tree == nullptr || r0 + 64 <= limit);
+      if (__ballot(mine_sees < r0 + 64) == 0) same = true, limit = 0x7FFFFFFF;
       waiting = true;
       now = now == 2 ? 0 : now + 1;
-      g.arrive(next);
+      next.arrive(info[now], mine);
       __syncthreads();
       m0 += 32;
     };
     while (true) {
-      step(sc[0], sc[1], (lds_cptr)sh.rows[0], lds0 + kChunkBytes);
+      step(sc[0], sc[1], (lds_cptr)sh.rows[0], lds0 + kChunkBytes, g[1], g[0]);
       if (m0 >= end) {
         add_chunk(sc[0], info[now == 0 ? 2 : now - 1]);
         break;
       }
-      step(sc[1], sc[0], (lds_cptr)sh.rows[1], lds0);
+      step(sc[1], sc[0], (lds_cptr)sh.rows[1], lds0, g[0], g[1]);
       if (m0 >= end) {
         add_chunk(sc[1], info[now == 0 ? 2 : now - 1]);
         break;
       }
     }
+    total[0].add(part[0]);
+    total[1].add(part[1]);
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
       const float both = sum_halves(total[n].sum), sum = ok[n] ? both : 0.0f;

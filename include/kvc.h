@@ -622,7 +622,7 @@ typedef struct kvc_weigh_args {
   int32_t num_heads;          /* H, 1..1024 */
   int32_t num_slots;          /* S, 0..8191 */
   int32_t draft_len;          /* tree: D, 1..64 (prefill: ignored) */
-  const void* q;              /* as kvc_attend_args */
+  const void* q;              /* as kvc_attend_args, strides below 2^31 */
   int64_t q_stride;
   int64_t q_head_stride;
   int64_t q_rows;             /* token rows q and lse hold; q_rows * H <= 2^31 - 256 */
