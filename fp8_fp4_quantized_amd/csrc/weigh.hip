@@ -109,6 +109,10 @@ struct Codes {
       }
     }
   }
+  __device__ __forceinline__ void take_scale(const Codes& of) {
+#pragma unroll
+    for (int k = 0; k < CodesShape<L>::kScales; ++k) scale[k] = of.scale[k];
+  }
   // load of step j (of its last one, the code is done with)
   static constexpr int load_of(int j) { return L == kV41Fp4 ? j >> 2 : L == kV4 && j >= 28 ? j - 14 : j >> 1; }
   static constexpr bool last_of(int j) { return L == kV41Fp4 ? (j & 3) == 3 : L == kV4 && j >= 28 ? true : (j & 1) != 0; }
@@ -161,12 +165,13 @@ __device__ __forceinline__ Place place_of(const WeighParams& p, int64_t b, int32
   return a;
 }
 
-// The weight of row r after the call: a row that this call's tokens complete
-// begins at 0; a row that is not finite (its sum is not either) collects nothing.
-__device__ __forceinline__ void put_weight(const WeighParams& p, int64_t b, const SlotTokens& s, int32_t r,
-                                           float sum) {
-  float old = 0.0f;
-  if (p.prev != nullptr && r < s.pos >> (p.ratio - 1)) old = p.prev[b * p.prev_stride + r];
+// The weight of row r after the call: decay times what it had, and its sum.  A row
+// that this call's tokens complete begins at 0; a row that is not finite (its sum is
+// not either) collects nothing.
+__device__ __forceinline__ float old_weight(const WeighParams& p, int64_t b, const SlotTokens& s, int32_t r) {
+  return p.prev != nullptr && r < s.pos >> (p.ratio - 1) ? p.prev[b * p.prev_stride + r] : 0.0f;
+}
+__device__ __forceinline__ void put_weight(const WeighParams& p, int64_t b, int32_t r, float old, float sum) {
   if (!(sum < __builtin_inff())) sum = 0.0f;
   p.weights[b * p.w_stride + r] = __builtin_fmaf(p.decay, old, sum);
 }
@@ -327,11 +332,17 @@ constexpr int kFewBlock = 512;
 constexpr int kFewWaves = kFewBlock / kLanes;
 constexpr int kFewGrid = 256;
 
+// A slot's begin, its queries brought to LDS, as the blocks that take the same time
+constexpr uint32_t kSlotBlocks = 8;
+__device__ __forceinline__ uint32_t few_cost(int32_t rows) {
+  return rows > 0 ? (uint32_t)((rows + 31) >> 5) + kSlotBlocks : 0;
+}
+
 template <int L, int NC, int SLOTS>
 __global__ __launch_bounds__(kFewBlock) void weigh_few_kernel(WeighParams p) {
   __shared__ __attribute__((aligned(16))) uint8_t rows[NC * 32 * 1024];
   __shared__ QueryRows info[NC];
-  // blocks of 32 rows before each second slot
+  // cost of the slots before each second one
   __shared__ uint32_t before[SLOTS / 2];
   __shared__ int64_t buf[kFewWaves];
   const int S = p.num_slots, tid = threadIdx.x, lane = lane_id(), wave = uniform(tid >> 6);
@@ -341,8 +352,8 @@ __global__ __launch_bounds__(kFewBlock) void weigh_few_kernel(WeighParams p) {
   for (int b0 = 0; b0 < S; b0 += 2 * kFewBlock) {
     const int b = b0 + 2 * tid;
     int64_t n0 = 0, n1 = 0, total;
-    if (b < S) n0 = (slot_tokens(p, b, &bad).rows + 31) >> 5;
-    if (b + 1 < S) n1 = (slot_tokens(p, b + 1, &bad).rows + 31) >> 5;
+    if (b < S) n0 = few_cost(slot_tokens(p, b, &bad).rows);
+    if (b + 1 < S) n1 = few_cost(slot_tokens(p, b + 1, &bad).rows);
     const int64_t end = block_scan64<kFewBlock>(n0 + n1, buf, &total) + carry;
     if (b < S) before[b >> 1] = (uint32_t)(end - n0 - n1);
     carry += total;
@@ -354,21 +365,25 @@ __global__ __launch_bounds__(kFewBlock) void weigh_few_kernel(WeighParams p) {
   uint32_t at = min(all, quota * blockIdx.x);
   const uint32_t to = min(all, at + quota);
   while (at < to) {
-    // the slot of block `at`
+    // the slot at that place
     int b = 2 * slot_at(before, (S + 1) >> 1, at);
     uint32_t first = before[b >> 1];
     int32_t none = 0;
     SlotTokens s = slot_tokens(p, b, &none);
-    uint32_t blocks = (uint32_t)(s.rows + 31) >> 5;
-    if (at - first >= blocks) {
-      first += blocks;
+    if (at - first >= few_cost(s.rows)) {
+      first += few_cost(s.rows);
       ++b;
       s = slot_tokens(p, b, &none);
-      blocks = (uint32_t)(s.rows + 31) >> 5;
     }
     b = uniform(b);
+    first = uniform((int32_t)first);
     s = SlotTokens{uniform(s.first), uniform(s.n), uniform(s.pos), uniform(s.rows)};
-    const uint32_t k0 = uniform((int32_t)(at - first)), k1 = min((uint32_t)uniform((int32_t)blocks), to - uniform((int32_t)first));
+    // its blocks from k0 to k1
+    const uint32_t k0 = max(at, first + kSlotBlocks) - first - kSlotBlocks;
+    const uint32_t end = min(to, first + few_cost(s.rows));
+    const uint32_t k1 = max(end, first + kSlotBlocks) - first - kSlotBlocks;
+    at = end;
+    if (k0 >= k1) continue;
     // its queries
     const int32_t nq = s.n * p.heads;
     __syncthreads();
@@ -392,42 +407,55 @@ __global__ __launch_bounds__(kFewBlock) void weigh_few_kernel(WeighParams p) {
     __syncthreads();
     // its rows
     const int32_t clear = first_limit(p, s);
-    for (uint32_t k = k0 + wave; k < k1; k += kFewWaves) {
-      const int32_t r = (int32_t)(32 * k) + (lane & 31);
-      // (the queries' fragments are read again for every block: kept over the
-      // loop they would not fit)
-      int row_base = (lane & 31) * 1024, low = lane & 15;
-      asm volatile("" : "+v"(row_base), "+v"(low));
-      const Place pl = place_of<L>(p, b, r, s.rows);
+    // (a block's codes take the place of the one before as its products are done)
+    uint32_t k = k0 + wave;
+    if (k < k1) {
+      auto row_of = [&](uint32_t block) { return (int32_t)(32 * block) + (lane & 31); };
+      Place here = place_of<L>(p, b, row_of(k), s.rows);
       Codes<L> c;
 #pragma unroll
-      for (int i = 0; i < Codes<L>::N; ++i) c.load_code(pl.data, i);
-      c.load_scale(pl.scale);
-      f32x16 acc[NC];
+      for (int i = 0; i < Codes<L>::N; ++i) c.load_code(here.data, i);
+      c.load_scale(here.scale);
+      Place next = place_of<L>(p, b, row_of(k + kFewWaves), min(s.rows, (int32_t)(32 * k1)));
+      for (; k < k1; k += kFewWaves) {
+        // (the queries' fragments are read again for every block: kept over the
+        // loop they would not fit)
+        int row_base = (lane & 31) * 1024, low = lane & 15;
+        asm volatile("" : "+v"(row_base), "+v"(low));
+        const int32_t r = row_of(k);
+        const float old = old_weight(p, b, s, min(r, s.rows - 1));
+        Codes<L> after;                       // its scales
+        after.load_scale(next.scale);
+        const Place then = place_of<L>(p, b, row_of(k + 2 * kFewWaves), min(s.rows, (int32_t)(32 * k1)));
+        f32x16 acc[NC];
 #pragma unroll
-      for (int n = 0; n < NC; ++n) acc[n] = f32x16{};
+        for (int n = 0; n < NC; ++n) acc[n] = f32x16{};
 #pragma unroll
-      for (int j = 0; j < 32; ++j) {
-        const bf16x8 x = c.expand(j, h);
-        const uint32_t at_row = row_base + 16 * ((Codes<L>::chunk(j) + Codes<L>::half_chunks(j) * h) ^ low);
+        for (int j = 0; j < 32; ++j) {
+          const bf16x8 x = c.expand(j, h);
+          if (Codes<L>::last_of(j)) c.load_code(next.data, Codes<L>::load_of(j));
+          const uint32_t at_row = row_base + 16 * ((Codes<L>::chunk(j) + Codes<L>::half_chunks(j) * h) ^ low);
 #pragma unroll
-        for (int n = 0; n < NC; ++n) {
-          const bf16x8 a = *(const bf16x8*)(rows + n * 32 * 1024 + at_row);
-          acc[n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, x, acc[n], 0, 0, 0);
+          for (int n = 0; n < NC; ++n) {
+            const bf16x8 a = *(const bf16x8*)(rows + n * 32 * 1024 + at_row);
+            acc[n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, x, acc[n], 0, 0, 0);
+          }
         }
+#pragma unroll
+        for (int n = 0; n < NC; ++n) scores_done(acc[n]);
+        const bool masked = (int32_t)(32 * k) + 32 > clear;
+        float v = 0.0f;
+#pragma unroll
+        for (int n = 0; n < NC; ++n)
+          v = masked ? add_weights(v, acc[n], p.scale_log2, info[n], h, true, r, p.tree != nullptr, s.pos)
+                     : add_weights(v, acc[n], p.scale_log2, info[n], h, false, r, false, 0);
+        v = sum_halves(v);
+        if (lane < 32 && r < s.rows) put_weight(p, b, r, old, here.ok ? v : 0.0f);
+        here = next;
+        next = then;
+        c.take_scale(after);
       }
-#pragma unroll
-      for (int n = 0; n < NC; ++n) scores_done(acc[n]);
-      const bool masked = (int32_t)(32 * k) + 32 > clear;
-      float v = 0.0f;
-#pragma unroll
-      for (int n = 0; n < NC; ++n)
-        v = masked ? add_weights(v, acc[n], p.scale_log2, info[n], h, true, r, p.tree != nullptr, s.pos)
-                   : add_weights(v, acc[n], p.scale_log2, info[n], h, false, r, false, 0);
-      v = sum_halves(v);
-      if (lane < 32 && r < s.rows) put_weight(p, b, s, r, pl.ok ? v : 0.0f);
     }
-    at = uniform((int32_t)(first + k1));
   }
 }
 
@@ -824,7 +852,7 @@ __global__ __launch_bounds__(kManyBlock) void weigh_many_kernel(WeighParams p) {
       const int32_t r = r0 + 32 * n + (lane & 31);
       if (lane < 32) {
         if (blk.stored >= 0) p.parts[blk.stored * kWeighRows + 64 * wave + 32 * n + lane] = sum;
-        else if (r < s.rows) put_weight(p, blk.b, s, r, sum);
+        else if (r < s.rows) put_weight(p, blk.b, r, old_weight(p, blk.b, s, r), sum);
       }
     }
     __syncthreads();                          // info and rows are free
@@ -883,7 +911,7 @@ __global__ __launch_bounds__(kJoinBlock) void weigh_join_kernel(WeighParams p) {
     if (group == 0 && r < s.rows) {
 #pragma unroll
       for (int i = 1; i < kJoinGroups; ++i) v += sums[i][row];
-      put_weight(p, b, s, r, v);
+      put_weight(p, b, r, old_weight(p, b, s, r), v);
     }
     __syncthreads();
   }
