@@ -20,8 +20,9 @@ namespace kvc {
 namespace {
 
 // ------------------------------------------------------------------ choice
-// The key of the last row kept is found digit by digit (12, 10 and 10 bits) from
-// histograms of the candidates' keys, and the rows are then written in order.
+// The key of the last row kept is found digit by digit (12, 10 and 10 bits; in
+// segments 11, 11 and 10) from histograms of the candidates' keys, and the rows are
+// then written in order.
 //   select_registers_kernel  rows of weights of up to kSelectRegisterRows: one
 //                            workgroup a slot, the keys in registers, read once
 //   select_count / select_write  longer ones of up to kSelectSegmentSlots slots: a slot's
@@ -273,12 +274,16 @@ __global__ __launch_bounds__(kSelectBlock) void select_stream_kernel(SelectParam
 }
 
 // ---- segments
-// The keys of segment s of a slot that begin with the digits found so far, counted
-// by their next one; `pass` digits are found, the last of them in this launch.
+constexpr int kSegBits[3] = {11, 11, 10}, kSegShift[3] = {21, 10, 0};
+constexpr int kSegBins = kSelectWords;        // of the first two; the third has half as many
+static_assert(kSegBins == 1 << kSegBits[0] && kSegBins == 1 << kSegBits[1], "words of a histogram");
+constexpr int kTurn = 16;                     // rows a thread has in registers
+
+// A segment of a slot: what is known of the key, and of the segments before it
 struct Found {
   uint32_t key;                // digits found, the last in the low bits
   int32_t left;                // of the rows with them, so many are kept
-  Written before;              // in the segments before this one: rows kept for certain; (equal: used at the end)
+  Written before;              // in the segments before this one: rows kept for certain, rows with all digits
 };
 
 // The digit that the histograms of the last launch give, from the slot's sums
@@ -286,17 +291,18 @@ template <int BINS>
 __device__ __forceinline__ Found next_digit(const SelectParams& p, Found f, const uint32_t* hists, int s, int32_t* buf,
                                             int32_t* found, int32_t* sums) {
   constexpr int N = BINS / kSelectBlock;
+  typedef uint32_t bins_t __attribute__((ext_vector_type(N)));
   const int top = N * kSelectBlock - N - N * (int)threadIdx.x;   // the thread's least bin
   int32_t n[N], before[N];
 #pragma unroll
   for (int k = 0; k < N; ++k) n[k] = before[k] = 0;
-#pragma unroll 8
+#pragma unroll 16
   for (int t = 0; t < p.segments; ++t) {
+    const bins_t h = *(const bins_t*)(hists + (int64_t)t * kSegBins + top);
 #pragma unroll
     for (int k = 0; k < N; ++k) {
-      const int32_t h = (int32_t)hists[(int64_t)t * BINS + top + N - 1 - k];
-      n[k] += h;
-      if (t < s) before[k] += h;
+      n[k] += (int32_t)h[N - 1 - k];
+      before[k] += t < s ? (int32_t)h[N - 1 - k] : 0;
     }
   }
   const Digit d = find_digit(n, f.left, buf, found);
@@ -310,44 +316,54 @@ __device__ __forceinline__ Found next_digit(const SelectParams& p, Found f, cons
   }
   int32_t total;
   block_scan(above, buf + kSelectWaves, &total);
-  f.key = f.key << (BINS == kTopBins ? 0 : kLowBits) | d.bin;
+  f.key = f.key * BINS + d.bin;
   f.left = d.left;
   f.before.above += total;
   f.before.equal = sums[0];
   return f;
 }
 
+__device__ __forceinline__ uint32_t* hists_of(const SelectParams& p, int pass, int64_t seg) {
+  return p.hists + ((int64_t)pass * p.num_slots * p.segments + seg) * kSegBins;
+}
+
+// Counts the segment's keys that begin with the PASS digits found -- the last of them
+// found here -- by their next one.
 template <int PASS>
 __global__ __launch_bounds__(kSelectBlock) void select_count_kernel(SelectParams p) {
-  constexpr int BINS = PASS == 0 ? kTopBins : kLowBins;
+  constexpr int BINS = 1 << kSegBits[PASS];
   __shared__ uint32_t hist[BINS];
   __shared__ int32_t buf[2 * kSelectWaves], found[2], sums[1];
   const int s = blockIdx.x, b = blockIdx.y, tid = threadIdx.x;
   const Choice c = choice_of(p, b, PASS == 0 && s == 0);
   const Lists l(p, b);
+  const int64_t seg = (int64_t)b * p.segments + s;
+  const int64_t begin = c.lo + s * p.segment_rows, end = min((int64_t)c.hi, begin + p.segment_rows);
+  // (asked for before the digit is known)
+  float v[kTurn];
+#pragma unroll
+  for (int i = 0; i < kTurn; ++i) v[i] = begin + tid + i * kSelectBlock < end ? l.w[begin + tid + i * kSelectBlock] : 0.0f;
+  for (int i = tid; i < BINS; i += kSelectBlock) hist[i] = 0;
   if (PASS == 0) l.begin(p, b, c, s, p.segments);
   if (c.all) return;
-  const int64_t seg = (int64_t)b * p.segments + s;
   Found f{0, c.take, {0, 0}};
-  if constexpr (PASS == 1) {
-    f = next_digit<kTopBins>(p, f, p.top_hists + (int64_t)b * p.segments * kTopBins, s, buf, found, sums);
-  } else if constexpr (PASS == 2) {
+  if constexpr (PASS == 2) {
     const int32_t* st = p.states + 4 * seg;
     f = Found{(uint32_t)st[0], st[1], {st[2], 0}};
-    f = next_digit<kLowBins>(p, f, p.low_hists + (int64_t)b * p.segments * kLowBins, s, buf, found, sums);
   }
-  for (int i = tid; i < BINS; i += kSelectBlock) hist[i] = 0;
+  if constexpr (PASS > 0)
+    f = next_digit<1 << kSegBits[PASS - 1]>(p, f, hists_of(p, PASS - 1, (int64_t)b * p.segments), s, buf, found, sums);
   __syncthreads();
-  const int64_t begin = c.lo + s * p.segment_rows, end = min((int64_t)c.hi, begin + p.segment_rows);
-#pragma unroll 4
-  for (int64_t r = begin + tid; r < end; r += kSelectBlock) {
-    const uint32_t k = weight_key(l.w[r]);
-    if (PASS == 0) atomicAdd(&hist[k >> kShift[0]], 1u);
-    else if (k >> (kShift[PASS] + kLowBits) == f.key) atomicAdd(&hist[k >> kShift[PASS] & (kLowBins - 1)], 1u);
-  }
+  auto count = [&](float w, bool in) {
+    const uint32_t k = weight_key(w);
+    const uint64_t up = (uint64_t)k >> (kSegShift[PASS] + kSegBits[PASS]);
+    if (in && up == f.key) atomicAdd(&hist[k >> kSegShift[PASS] & (BINS - 1)], 1u);
+  };
+#pragma unroll
+  for (int i = 0; i < kTurn; ++i) count(v[i], begin + tid + i * kSelectBlock < end);
+  for (int64_t r = begin + tid + kTurn * kSelectBlock; r < end; r += kSelectBlock) count(l.w[r], true);
   __syncthreads();
-  uint32_t* out = PASS == 0 ? p.top_hists + seg * kTopBins
-                            : p.low_hists + ((int64_t)(PASS - 1) * p.num_slots * p.segments + seg) * kLowBins;
+  uint32_t* out = hists_of(p, PASS, seg);
   for (int i = tid; i < BINS; i += kSelectBlock) out[i] = hist[i];
   if (PASS > 0 && tid == 0) {
     int32_t* st = p.states + 4 * seg;
@@ -363,21 +379,27 @@ __global__ __launch_bounds__(kSelectBlock) void select_write_kernel(SelectParams
   if (c.all) return;
   const Lists l(p, b);
   const int64_t seg = (int64_t)b * p.segments + s;
+  const int64_t begin = c.lo + s * p.segment_rows, end = min((int64_t)c.hi, begin + p.segment_rows);
+  // turns of 16 waves of 1,024 rows
+  float v[kTurn];
+  int64_t r0 = begin + wave * kTurn * kLanes + lane;
+  auto fetch = [&]() {
+#pragma unroll
+    for (int i = 0; i < kTurn; ++i) v[i] = r0 + i * kLanes < end ? l.w[r0 + i * kLanes] : 0.0f;
+  };
+  fetch();
   const int32_t* st = p.states + 4 * seg;
   Found f{(uint32_t)st[0], st[1], {st[2], 0}};
-  f = next_digit<kLowBins>(p, f, p.low_hists + (int64_t)(p.num_slots + b) * p.segments * kLowBins, s, buf, found, sums);
-  // turns of 16 waves of 256 rows
-  constexpr int E = 4;
-  const int64_t begin = c.lo + s * p.segment_rows, end = min((int64_t)c.hi, begin + p.segment_rows);
+  f = next_digit<1 << kSegBits[2]>(p, f, hists_of(p, 2, (int64_t)b * p.segments), s, buf, found, sums);
   int turn = 0;
-  for (int64_t t0 = begin; t0 < end; t0 += kSelectBlock * E, turn ^= 1) {
-    const int64_t r0 = t0 + wave * E * kLanes + lane;
-    float v[E];
+  for (int64_t t0 = begin; t0 < end; t0 += kSelectBlock * kTurn, turn ^= 1) {
+    if (t0 > begin) {
+      r0 += kSelectBlock * kTurn;
+      fetch();
+    }
     Written at{0, 0};
 #pragma unroll
-    for (int i = 0; i < E; ++i) v[i] = r0 + i * kLanes < end ? l.w[r0 + i * kLanes] : 0.0f;
-#pragma unroll
-    for (int i = 0; i < E; ++i) {
+    for (int i = 0; i < kTurn; ++i) {
       const uint32_t k = weight_key(v[i]);
       const bool in = r0 + i * kLanes < end;
       at.above += __builtin_popcountll(__ballot(in && k > f.key));
@@ -391,7 +413,7 @@ __global__ __launch_bounds__(kSelectBlock) void select_write_kernel(SelectParams
       f.before.above += counts[turn][w][0], f.before.equal += counts[turn][w][1];
     }
 #pragma unroll
-    for (int i = 0; i < E; ++i)
+    for (int i = 0; i < kTurn; ++i)
       write_rows(l, c, at, f.key, f.left, (int32_t)(r0 + i * kLanes), v[i], r0 + i * kLanes < end);
   }
 }

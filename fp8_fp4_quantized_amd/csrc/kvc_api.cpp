@@ -337,7 +337,7 @@ int64_t evict_bytes(int32_t slots, int64_t width) {
   if (width <= kvc::kSelectRegisterRows) return 0;
   const int64_t n = (width + kvc::kSelectSegmentRows - 1) / kvc::kSelectSegmentRows * slots;
   const int64_t segments = n < kvc::kSelectSegments ? n : kvc::kSelectSegments;
-  return segments * (kvc::kSelectTopWords + 2 * kvc::kSelectLowWords + 4) * 4;
+  return segments * (3 * kvc::kSelectWords + 4) * 4;
 }
 
 }  // namespace
@@ -854,7 +854,7 @@ int kvc_evict_select(const kvc_evict_args* a, void* stream) {
     return fail(KVC_EINVAL, "%s: kept_weights needs a stride >= kept_width, and is not weights", who);
   const int32_t segments = evict_segments(a->num_slots, a->w_width);
   const int64_t all = (int64_t)segments * a->num_slots;
-  const int64_t need = all * (kvc::kSelectTopWords + 2 * kvc::kSelectLowWords + 4) * 4;
+  const int64_t need = all * (3 * kvc::kSelectWords + 4) * 4;
   if (need > 0 && (a->workspace == nullptr || ((uintptr_t)a->workspace & 255u) != 0 || a->workspace_bytes < need))
     return fail(KVC_EINVAL, "%s: workspace needs %lld bytes, 256-byte aligned", who, (long long)need);
   if (kvc::launch_select == nullptr) return fail(KVC_ELAUNCH, "%s: built without kernels", who);
@@ -879,9 +879,8 @@ int kvc_evict_select(const kvc_evict_args* a, void* stream) {
   if (segments > 0) {
     p.segments = segments;
     p.segment_rows = (a->w_width + segments - 1) / segments;
-    p.top_hists = static_cast<uint32_t*>(a->workspace);
-    p.low_hists = p.top_hists + all * kvc::kSelectTopWords;
-    p.states = reinterpret_cast<int32_t*>(p.low_hists + 2 * all * kvc::kSelectLowWords);
+    p.hists = static_cast<uint32_t*>(a->workspace);
+    p.states = reinterpret_cast<int32_t*>(p.hists + 3 * all * kvc::kSelectWords);
   }
   return launched(kvc::launch_select(p, static_cast<hipStream_t>(stream)), who);
 }

@@ -91,8 +91,8 @@ constexpr int kSelectRegisterRows = 16384;
 constexpr int kSelectSegmentSlots = 256;
 constexpr int kSelectSegmentRows = 16384;
 constexpr int kSelectSegments = 512;
-// words of a segment in the workspace: histograms of 12, 10 and 10 bits, a state of 4
-constexpr int kSelectTopWords = 4096, kSelectLowWords = 1024;
+// words of a segment in the workspace: three histograms, a state of 4
+constexpr int kSelectWords = 2048;
 
 struct SelectParams {
   int32_t ratio;
@@ -113,8 +113,7 @@ struct SelectParams {
   // segments a slot (0: none), their rows, and the workspace
   int32_t segments;
   int64_t segment_rows;
-  uint32_t* top_hists;         // [slots][segments][kSelectTopWords]
-  uint32_t* low_hists;         // [2][slots][segments][kSelectLowWords]
+  uint32_t* hists;             // [3][slots][segments][kSelectWords]
   int32_t* states;             // [slots][segments][4]
 };
 

@@ -20,6 +20,7 @@ namespace kvc {
 namespace {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
@@ -131,6 +132,27 @@ struct Codes {
     }
     return __builtin_bit_cast(bf16x8, u32x4{v.x, v.y, v.z, v.w});
   }
+  // V41_FP4: 8 dims of step j as fp16.  The magnitudes 0, .5, 1, 1.5, 2, 3, 4, 6 have
+  // no low byte in fp16, so their high bytes are looked up four at a time (v_perm_b32
+  // takes bytes of an 8-byte table), the signs set, and the 8 products with the scale
+  // are exact: at most 2,688, no less than 2^-10, 6 significant bits.  16 instructions
+  // and a few a group where the conversions to fp32 and bf16 take 19, six of them slow.
+  typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+  static __device__ __forceinline__ f16x8 expand_f16(uint32_t w, f16x2 s) {
+    const uint32_t even = __builtin_amdgcn_perm(0x46444240u, 0x3E3C3800u, w & 0x07070707u) | (w << 4 & 0x80808080u);
+    const uint32_t odd = __builtin_amdgcn_perm(0x46444240u, 0x3E3C3800u, w >> 4 & 0x07070707u) | (w & 0x80808080u);
+    u32x4 v;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t pair = __builtin_amdgcn_perm(odd, even, 0x040C000Cu + 0x01000100u * k);
+      v[k] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, pair) * s);
+    }
+    return __builtin_bit_cast(f16x8, v);
+  }
+  // the scales of step j's load, of its two groups
+  __device__ __forceinline__ f16x2 scales_f16(int j, int h) const {
+    return __builtin_bit_cast(f16x2, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)(scale[j >> 2] >> (16 * h)), 1.0f, false));
+  }
   // 8-dim chunk of step j in a row of queries: that of half 0, and how far half 1 is
   static constexpr int chunk(int j) {
     return L == kV41Fp4 ? 8 * (j >> 2) + (j & 3) : L == kV4 && j >= 28 ? 56 + 2 * (j - 28) : 4 * (j >> 1) + (j & 1);
@@ -189,6 +211,7 @@ __device__ __forceinline__ float sum_halves(float v) {
 // nothing and has -lse = -inf.
 struct QueryRows {
   float neg_lse[32];
+  float factor[32];            // (few queries of FP4 rows) what their scores are multiplied by
   int32_t limit[32];
   uint64_t mask[32];
 };
@@ -245,6 +268,28 @@ struct Staged {
     typedef const __attribute__((address_space(1))) u32x4* vec;
     v[i] = *(vec)((uint64_t)(uintptr_t)q.at + 128 * i + 16 * (lane_id() & 7));
   }
+  // The query in fp16, times the power of two that brings its greatest value to
+  // [2^14, 2^15); returns the power's inverse.  Exact for values down to 2^-31 of the
+  // greatest; what is less is off by 2^-40 of that at the most, below the rounding of
+  // an fp32 sum.  (A power past 2^100 either way is left at that.)
+  __device__ __forceinline__ float to_f16() {
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top = max(top, absmax_bf16x8(make_uint4(v[i].x, v[i].y, v[i].z, v[i].w)));
+    top = group_max_u32<8>(top);
+    const int up = min(max(127 + 14 - (int)(top >> 7), -100), 100);
+    const float by = __uint_as_float((uint32_t)(127 + up) << 23);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t lo = __builtin_bit_cast(uint16_t, (_Float16)(bf16_lo(v[i][k]) * by));
+        const uint32_t hi = __builtin_bit_cast(uint16_t, (_Float16)(bf16_hi(v[i][k]) * by));
+        v[i][k] = lo | hi << 16;
+      }
+    }
+    return __uint_as_float((uint32_t)(127 - up) << 23);
+  }
   static __device__ __forceinline__ uint32_t place(int m) {
     return m * 1024 + 16 * ((lane_id() & 7) ^ (m & 15));
   }
@@ -271,14 +316,18 @@ __device__ __forceinline__ void scores_done(f32x16& sc) { asm("s_nop 15" : "+v"(
 
 // Adds a lane's 16 weights of a 32 x 32 result to v.  masked: some of the
 // queries may not see some of the rows, or give nothing.
+// OWN: each query has its own factor.
+template <bool OWN>
 __device__ __forceinline__ float add_weights(float v, const f32x16& s, float scale, const QueryRows& q, int h,
                                              bool masked, int32_t r, bool tree, int32_t base) {
 #pragma unroll
   for (int a = 0; a < 4; ++a) {
     const f32x4 nl = *(const f32x4*)&q.neg_lse[8 * a + 4 * h];
+    f32x4 factor = f32x4{scale, scale, scale, scale};
+    if constexpr (OWN) factor = *(const f32x4*)&q.factor[8 * a + 4 * h];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      float w = __builtin_amdgcn_exp2f(__builtin_fmaf(s[4 * a + i], scale, nl[i]));
+      float w = __builtin_amdgcn_exp2f(__builtin_fmaf(s[4 * a + i], factor[i], nl[i]));
       if (masked) {
         const int m = 8 * a + 4 * h + i;
         if (nl[i] == kNegInf || !sees(r, q.limit[m], tree, tree ? q.mask[m] : 0, base)) w = 0.0f;
@@ -333,15 +382,19 @@ constexpr int kFewWaves = kFewBlock / kLanes;
 constexpr int kFewGrid = 256;
 
 // A slot's begin, its queries brought to LDS, as the blocks that take the same time
-constexpr uint32_t kSlotBlocks = 8;
+constexpr uint32_t kSlotBlocks = 16;
 __device__ __forceinline__ uint32_t few_cost(int32_t rows) {
   return rows > 0 ? (uint32_t)((rows + 31) >> 5) + kSlotBlocks : 0;
 }
+
+template <int NC> constexpr int kReadAheadOf = NC > 2 ? 2 : 3;   // (what registers are left)
 
 template <int L, int NC, int SLOTS>
 __global__ __launch_bounds__(kFewBlock) void weigh_few_kernel(WeighParams p) {
   __shared__ __attribute__((aligned(16))) uint8_t rows[NC * 32 * 1024];
   __shared__ QueryRows info[NC];
+  constexpr bool kF16 = L == kV41Fp4;          // (rows and queries in fp16)
+  constexpr int kReadAhead = kReadAheadOf<NC>;
   // cost of the slots before each second one
   __shared__ uint32_t before[SLOTS / 2];
   __shared__ int64_t buf[kFewWaves];
@@ -398,6 +451,10 @@ __global__ __launch_bounds__(kFewBlock) void weigh_few_kernel(WeighParams p) {
       // (zeros in place of a query that gives nothing: its weights are then 0 of
       // themselves)
       const bool gives = g.q.neg_lse() != kNegInf;
+      if constexpr (kF16) {
+        const float back = g.to_f16();
+        if ((lane & 7) == 0) info[m0 >> 5].factor[m & 31] = p.scale_log2 * back;
+      }
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         if (!gives) g.v[i] = u32x4{0, 0, 0, 0};
@@ -420,8 +477,8 @@ __global__ __launch_bounds__(kFewBlock) void weigh_few_kernel(WeighParams p) {
       for (; k < k1; k += kFewWaves) {
         // (the queries' fragments are read again for every block: kept over the
         // loop they would not fit)
-        int row_base = (lane & 31) * 1024, low = lane & 15;
-        asm volatile("" : "+v"(row_base), "+v"(low));
+        asm volatile("" ::: "memory");
+        const int row_base = (lane & 31) * 1024, low = lane & 15;
         const int32_t r = row_of(k);
         const float old = old_weight(p, b, s, min(r, s.rows - 1));
         Codes<L> after;                       // its scales
@@ -430,16 +487,48 @@ __global__ __launch_bounds__(kFewBlock) void weigh_few_kernel(WeighParams p) {
         f32x16 acc[NC];
 #pragma unroll
         for (int n = 0; n < NC; ++n) acc[n] = f32x16{};
-#pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          const bf16x8 x = c.expand(j, h);
-          if (Codes<L>::last_of(j)) c.load_code(next.data, Codes<L>::load_of(j));
+        // (fragments are read kReadAhead steps and a step's dims expanded one before their
+        // products, which they share the time with)
+        typename Codes<L>::f16x2 pair = {};
+        auto dims_of = [&](int j) {
+          if constexpr (kF16) {
+            if ((j & 3) == 0) pair = c.scales_f16(j, h);
+            const _Float16 g = pair[j >> 1 & 1];
+            return __builtin_bit_cast(bf16x8, Codes<L>::expand_f16(c.code[j >> 2][j & 3], typename Codes<L>::f16x2{g, g}));
+          } else {
+            return c.expand(j, h);
+          }
+        };
+        bf16x8 q[kReadAhead][NC];
+        auto read = [&](int j) {
           const uint32_t at_row = row_base + 16 * ((Codes<L>::chunk(j) + Codes<L>::half_chunks(j) * h) ^ low);
 #pragma unroll
+          for (int n = 0; n < NC; ++n) q[j % kReadAhead][n] = *(const bf16x8*)(rows + n * 32 * 1024 + at_row);
+        };
+#pragma unroll
+        for (int j = 0; j < kReadAhead; ++j) read(j);
+        bf16x8 x = dims_of(0);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+#pragma unroll
           for (int n = 0; n < NC; ++n) {
-            const bf16x8 a = *(const bf16x8*)(rows + n * 32 * 1024 + at_row);
-            acc[n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, x, acc[n], 0, 0, 0);
+            const bf16x8 a = q[j % kReadAhead][n];
+            if constexpr (kF16)
+              acc[n] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a),
+                                                              __builtin_bit_cast(f16x8, x), acc[n], 0, 0, 0);
+            else
+              acc[n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, x, acc[n], 0, 0, 0);
           }
+          if (j + kReadAhead < 32) read(j + kReadAhead);
+          if (j + 1 < 32) x = dims_of(j + 1);
+          // (the loads of a row's 128 bytes together: a line is then fetched once)
+          constexpr int kLast = Codes<L>::N - 1;
+          const int i = Codes<L>::load_of(j);
+          if (Codes<L>::last_of(j) && ((i & 3) == 3 || i == kLast)) {
+#pragma unroll
+            for (int t = i & ~3; t <= i; ++t) c.load_code(next.data, t);
+          }
+          __builtin_amdgcn_sched_barrier(0);
         }
 #pragma unroll
         for (int n = 0; n < NC; ++n) scores_done(acc[n]);
@@ -447,8 +536,8 @@ __global__ __launch_bounds__(kFewBlock) void weigh_few_kernel(WeighParams p) {
         float v = 0.0f;
 #pragma unroll
         for (int n = 0; n < NC; ++n)
-          v = masked ? add_weights(v, acc[n], p.scale_log2, info[n], h, true, r, p.tree != nullptr, s.pos)
-                     : add_weights(v, acc[n], p.scale_log2, info[n], h, false, r, false, 0);
+          v = masked ? add_weights<kF16>(v, acc[n], p.scale_log2, info[n], h, true, r, p.tree != nullptr, s.pos)
+                     : add_weights<kF16>(v, acc[n], p.scale_log2, info[n], h, false, r, false, 0);
         v = sum_halves(v);
         if (lane < 32 && r < s.rows) put_weight(p, b, r, old, here.ok ? v : 0.0f);
         here = next;
@@ -785,7 +874,7 @@ __global__ __launch_bounds__(kManyBlock) void weigh_many_kernel(WeighParams p) {
     auto add_chunk = [&](f32x16 (&of)[2], const QueryRows& q) {
 #pragma unroll
       for (int n = 0; n < 2; ++n)
-        total[n].add(add_weights(0.0f, of[n], p.scale_log2, q, h, true, r0 + 32 * n + (lane & 31), p.tree != nullptr,
+        total[n].add(add_weights<false>(0.0f, of[n], p.scale_log2, q, h, true, r0 + 32 * n + (lane & 31), p.tree != nullptr,
                                  s.pos));
     };
     // (the running sums are added up in fp32 for 8 turns, then into the totals)
