@@ -219,7 +219,9 @@ __global__ __launch_bounds__(kSelectBlock) void select_registers_kernel(SelectPa
   if (lane == 0) counts[wave][0] = at.above, counts[wave][1] = at.equal;
   __syncthreads();
   at = Written{0, 0};
-  for (int w = 0; w < wave; ++w) at.above += counts[w][0], at.equal += counts[w][1];
+  for (int w = 0; w < kSelectWaves; ++w) {
+    if (w < wave) at.above += counts[w][0], at.equal += counts[w][1];
+  }
 #pragma unroll
   for (int i = 0; i < E; ++i)
     write_rows(l, c, at, key, d.left, r0 + i * kLanes, v[i], r0 + i * kLanes < c.hi);
@@ -296,7 +298,7 @@ __device__ __forceinline__ Found next_digit(const SelectParams& p, Found f, cons
   int32_t n[N], before[N];
 #pragma unroll
   for (int k = 0; k < N; ++k) n[k] = before[k] = 0;
-#pragma unroll 16
+#pragma unroll 32
   for (int t = 0; t < p.segments; ++t) {
     const bins_t h = *(const bins_t*)(hists + (int64_t)t * kSegBins + top);
 #pragma unroll
@@ -372,7 +374,7 @@ __global__ __launch_bounds__(kSelectBlock) void select_count_kernel(SelectParams
 }
 
 __global__ __launch_bounds__(kSelectBlock) void select_write_kernel(SelectParams p) {
-  __shared__ int32_t buf[2 * kSelectWaves], found[2], sums[1];
+  __shared__ int32_t buf[2 * kSelectWaves], found[2], places[1];
   __shared__ int32_t counts[2][kSelectWaves][2];
   const int s = blockIdx.x, b = blockIdx.y, lane = lane_id(), wave = uniform((int)(threadIdx.x >> 6));
   const Choice c = choice_of(p, b, false);
@@ -390,7 +392,7 @@ __global__ __launch_bounds__(kSelectBlock) void select_write_kernel(SelectParams
   fetch();
   const int32_t* st = p.states + 4 * seg;
   Found f{(uint32_t)st[0], st[1], {st[2], 0}};
-  f = next_digit<1 << kSegBits[2]>(p, f, hists_of(p, 2, (int64_t)b * p.segments), s, buf, found, sums);
+  f = next_digit<1 << kSegBits[2]>(p, f, hists_of(p, 2, (int64_t)b * p.segments), s, buf, found, places);
   int turn = 0;
   for (int64_t t0 = begin; t0 < end; t0 += kSelectBlock * kTurn, turn ^= 1) {
     if (t0 > begin) {
@@ -407,11 +409,15 @@ __global__ __launch_bounds__(kSelectBlock) void select_write_kernel(SelectParams
     }
     if (lane == 0) counts[turn][wave][0] = at.above, counts[turn][wave][1] = at.equal;
     __syncthreads();
+    const int32_t above = wave_incl_scan_i32(lane < kSelectWaves ? counts[turn][lane][0] : 0);
+    const int32_t equal = wave_incl_scan_i32(lane < kSelectWaves ? counts[turn][lane][1] : 0);
     at = f.before;
-    for (int w = 0; w < kSelectWaves; ++w) {
-      if (w < wave) at.above += counts[turn][w][0], at.equal += counts[turn][w][1];
-      f.before.above += counts[turn][w][0], f.before.equal += counts[turn][w][1];
+    if (wave > 0) {
+      at.above += __builtin_amdgcn_readlane(above, wave - 1);
+      at.equal += __builtin_amdgcn_readlane(equal, wave - 1);
     }
+    f.before.above += __builtin_amdgcn_readlane(above, kLanes - 1);
+    f.before.equal += __builtin_amdgcn_readlane(equal, kLanes - 1);
 #pragma unroll
     for (int i = 0; i < kTurn; ++i)
       write_rows(l, c, at, f.key, f.left, (int32_t)(r0 + i * kLanes), v[i], r0 + i * kLanes < end);

@@ -308,7 +308,7 @@ int weigh(const kvc_weigh_args* a, bool tree, void* stream, const char* who) {
   p.pt_width = a->pt_width;
   p.tree = tree ? a->tree : nullptr;
   p.decay = a->decay;
-  p.prev = a->prev;
+  p.prev = a->decay == 0.0f ? nullptr : a->prev;   // (not read: 0 times anything)
   p.prev_stride = a->prev_stride;
   p.weights = a->weights;
   p.w_stride = a->w_stride;

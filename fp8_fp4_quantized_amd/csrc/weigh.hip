@@ -171,7 +171,7 @@ __device__ __forceinline__ Place place_of(const WeighParams& p, int64_t b, int32
   Place a;
   const int pb = p.cache.page_bits;
   int32_t page = 0;
-  a.ok = r < rows;
+  a.ok = (uint32_t)r < (uint32_t)rows;       // (a block past the last one may pass 2^31)
   if (a.ok) {
     page = p.page_table[b * p.pt_stride + (r >> pb)];
     if (page < 0 || page >= p.cache.num_pages) {

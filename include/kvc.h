@@ -608,7 +608,8 @@ int kvc_rope_rows(const kvc_rope_args* args, void* stream);
  *   for every row r < (start_pos[b] + count) / ratio; weights past these, and
  *   those of skipped slots, are left as they are.  prev counts as 0 for the rows
  *   r >= start_pos[b] / ratio, which the call's tokens complete (they need no
- *   preparation), and everywhere where it is NULL; it may be weights itself.
+ *   preparation), and everywhere where it is NULL or decay is 0; it may be weights
+ *   itself.
  *   A query whose lse is not finite adds nothing; a row that is not finite
  *   collects nothing, and neither does a row whose page is outside the cache
  *   (KVC_STATUS_PAGE_RANGE).  Rows past pt_width pages or w_width entries are

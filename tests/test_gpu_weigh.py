@@ -257,6 +257,21 @@ def test_masked_rows_hold_anything(kvc):  # noqa: F811
         check(out.cpu()[0], torch.zeros(start + D), total, tol, 0.0, 0)
 
 
+@pytest.mark.parametrize("H,D", [(16, 1), (64, 4)])
+def test_decay_0_forgets(kvc, H, D):  # noqa: F811
+    """With decay 0 what the rows had counts for nothing, whatever it is; rows that
+    the call's tokens complete begin at 0 whatever lies there."""
+    f = Filled(kvc, "V41", 64, [300 + D], seed=2)
+    q = queries(D, H, seed=4).cuda()
+    lse = torch.full((D, H), 8.0, device="cuda")
+    st = torch.tensor([300], dtype=torch.int32, device="cuda")
+    a, b = (torch.full((1, 300 + D), math.nan, device="cuda") for _ in range(2))
+    b[0, :300] = 0
+    kvc.kvc_weigh_tree(f.cache, q, lse, st, dev(f.table), a, scale=SCALE, draft_len=D, prev=a, decay=0.0)
+    kvc.kvc_weigh_tree(f.cache, q, lse, st, dev(f.table), b, scale=SCALE, draft_len=D, prev=b)
+    assert torch.isfinite(a).all() and torch.equal(a, b)
+
+
 @pytest.mark.parametrize("H,D", [(16, 1), (48, 4)])
 @pytest.mark.parametrize("S", [1025, 8191])
 def test_many_slots_few_of_them_active(kvc, S, H, D):  # noqa: F811
