@@ -213,7 +213,9 @@ struct QueryRows {
   float neg_lse[32];
   float factor[32];            // (few queries of FP4 rows) what their scores are multiplied by
   int32_t limit[32];
-  uint64_t mask[32];
+  // a tree: which drafted rows it sees, 32 a word, then a word for the rows of the
+  // context and one for those past the drafts
+  __attribute__((aligned(16))) uint32_t words[32][4];
 };
 
 // tree mask of a token
@@ -243,9 +245,10 @@ struct LaneQuery {
     entry = (uint64_t)row * (uint32_t)p.heads + head;
     limit = p.tree != nullptr ? s.pos : (s.pos + token + 1) >> (p.ratio - 1);
   }
-  __device__ __forceinline__ void fetch(const WeighParams& p, int64_t b, const SlotTokens& s) {
+  // masks: whether a tree's masks matter (rows of drafted tokens are among those at hand)
+  __device__ __forceinline__ void fetch(const WeighParams& p, int64_t b, const SlotTokens& s, bool masks) {
     lse = p.lse[entry];
-    mask = p.tree != nullptr ? mask_of(p, b, s, token) : 0;
+    mask = masks ? mask_of(p, b, s, token) : 0;
   }
   __device__ __forceinline__ float neg_lse() const {
     return real && __builtin_fabsf(lse) < __builtin_inff() ? -lse : kNegInf;
@@ -254,7 +257,7 @@ struct LaneQuery {
     const float v = neg_lse();
     info.neg_lse[m] = v;
     info.limit[m] = v == kNegInf ? 0 : limit;
-    info.mask[m] = v == kNegInf ? 0 : mask;
+    *(u32x4*)info.words[m] = v == kNegInf ? u32x4{0, 0, 0, 0} : u32x4{(uint32_t)mask, (uint32_t)(mask >> 32), ~0u, 0};
   }
 };
 
@@ -301,15 +304,21 @@ struct Staged {
   }
 };
 
-// whether a query with that limit and mask sees row r; base: the row of mask bit 0
-__device__ __forceinline__ bool sees(int32_t r, int32_t limit, bool tree, uint64_t mask, int32_t base) {
-  bool see = r < limit;
-  if (tree) {
+// The word and bit of a query's that say whether it sees row r; base: the first
+// drafted row
+struct TreeBit {
+  int32_t word, bit;
+  __device__ __forceinline__ TreeBit(int32_t r, int32_t base) {
     const uint32_t x = (uint32_t)(r - base);
-    see |= x < 64u && (mask >> (x & 63u) & 1) != 0;
+    word = r < base ? 2 : x < 64u ? (int32_t)(x >> 5) : 3;
+    bit = r < base ? 0 : (int32_t)(x & 31u);
   }
-  return see;
-}
+  // v where it is seen, else 0 (whatever v is)
+  __device__ __forceinline__ float kept(float v, const QueryRows& q, int m) const {
+    const int32_t all = __builtin_amdgcn_sbfe((int)q.words[m][word], bit, 1);
+    return __uint_as_float(__float_as_uint(v) & (uint32_t)all);
+  }
+};
 
 // wait states from a last product to what reads, or overwrites, its result
 __device__ __forceinline__ void scores_done(f32x16& sc) { asm("s_nop 15" : "+v"(sc)); }
@@ -320,6 +329,7 @@ __device__ __forceinline__ void scores_done(f32x16& sc) { asm("s_nop 15" : "+v"(
 template <bool OWN>
 __device__ __forceinline__ float add_weights(float v, const f32x16& s, float scale, const QueryRows& q, int h,
                                              bool masked, int32_t r, bool tree, int32_t base) {
+  const TreeBit of(r, base);
 #pragma unroll
   for (int a = 0; a < 4; ++a) {
     const f32x4 nl = *(const f32x4*)&q.neg_lse[8 * a + 4 * h];
@@ -330,7 +340,7 @@ __device__ __forceinline__ float add_weights(float v, const f32x16& s, float sca
       float w = __builtin_amdgcn_exp2f(__builtin_fmaf(s[4 * a + i], factor[i], nl[i]));
       if (masked) {
         const int m = 8 * a + 4 * h + i;
-        if (nl[i] == kNegInf || !sees(r, q.limit[m], tree, tree ? q.mask[m] : 0, base)) w = 0.0f;
+        w = tree ? of.kept(w, q, m) : r < q.limit[m] ? w : 0.0f;
       }
       v += w;
     }
@@ -444,7 +454,7 @@ __global__ __launch_bounds__(kFewBlock) void weigh_few_kernel(WeighParams p) {
       Staged g;
       const int m = m0 + (lane >> 3);
       g.q.locate(p, s, m, nq);
-      g.q.fetch(p, b, s);
+      g.q.fetch(p, b, s, p.tree != nullptr);
 #pragma unroll
       for (int i = 0; i < 8; ++i) g.load(i);
       g.put(info[m0 >> 5], m & 31);
@@ -611,11 +621,12 @@ __device__ __forceinline__ int64_t parts_of(const WeighParams& p, const SlotToke
   return s.n > 0 ? parts_before(p, s, cut, segments_of(s, cut)) : 0;
 }
 
-// The first cut tried: segments of `share` queries, a sixteenth of a
-// workgroup's share of the work, but 2,048 or the whole share where it is less.
+// The first cut tried: segments of `share` queries, a sixteenth of a workgroup's
+// share of the work, but 2,048 or the whole share where that is less, and 128 at the
+// least (4 chunks; fewer would not pay for the block's begin).
 __device__ __forceinline__ int first_cut(const WeighParams& p, int64_t work) {
   const int64_t each = (work + kWeighWorkgroups - 1) / kWeighWorkgroups;
-  const int64_t share = max(each / 16, min(each, (int64_t)2048));
+  const int64_t share = max(max(each / 16, min(each, (int64_t)2048)), (int64_t)128);
   int cut = 0;
   while ((int64_t)p.heads << (cut + 1) <= share && cut < 30) ++cut;
   return cut;
@@ -742,11 +753,12 @@ constexpr int kAhead = 4;        // fragments of queries read ahead
 // The scores of a chunk of 32 queries with the wave's 64 rows.  SUM 1: the weights
 // of the chunk before (scores prev, queries of) are added up meanwhile, one a step,
 // their three instructions a step apart; 2: those of rows below each query's own
-// limit (r: the lane's first row).  beside(j) is done in step j.
+// limit (r: the lane's first row); 3: those that a tree's queries see (base: the first
+// drafted row).  beside(j) is done in step j.
 template <int L, int SUM, typename Beside>
 __device__ __forceinline__ void scores_of(f32x16 (&sc)[2], const bf16x8 (&x)[2][32], lds_cptr rows, int lane,
-                                          const f32x16 (&prev)[2], const QueryRows& of, int32_t r, float scale,
-                                          float (&sum)[2], Beside&& beside) {
+                                          const f32x16 (&prev)[2], const QueryRows& of, int32_t r, int32_t base,
+                                          float scale, float (&sum)[2], Beside&& beside) {
   bf16x8 q[kAhead];
   float arg = 0.0f, w = 0.0f;
   const int h = lane >> 5;
@@ -761,8 +773,10 @@ __device__ __forceinline__ void scores_of(f32x16 (&sc)[2], const bf16x8 (&x)[2][
     for (int a = 0; a < 4; ++a) lim[a] = *(const i32x4*)&of.limit[8 * a + 4 * h];
   }
   // weight of step j: of scores prev[j % 2], element j / 2
+  const TreeBit bit0(r, base), bit1(r + 32, base);
   auto kept = [&](float v, int j) {
     if constexpr (SUM == 2) return r + 32 * (j & 1) < lim[j >> 3][j >> 1 & 3] ? v : 0.0f;
+    if constexpr (SUM == 3) return ((j & 1) ? bit1 : bit0).kept(v, of, 8 * (j >> 3) + 4 * h + (j >> 1 & 3));
     return v;
   };
 #pragma unroll
@@ -840,7 +854,8 @@ __global__ __launch_bounds__(kManyBlock) void weigh_many_kernel(WeighParams p) {
     g[0].locate(p, s, m0 + mine, end);
     const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_ptr)sh.rows[0] + 8192 * wave;
     g[0].load_all(lds0, part8);
-    g[0].fetch(p, blk.b, s);
+    const bool masks = p.tree != nullptr && (int64_t)(blk.k + 1) << kManyRowBits > s.pos;
+    g[0].fetch(p, blk.b, s, masks);
     g[1].locate(p, s, m0 + 32 + mine, end);
     // its rows
     const int32_t r0 = (blk.k << kManyRowBits) + 64 * wave;
@@ -865,7 +880,7 @@ __global__ __launch_bounds__(kManyBlock) void weigh_many_kernel(WeighParams p) {
     // The queries, 32 a turn, the weights of a turn's scores added in the next one.
     // Where the queries of a chunk all see the same rows (those of a token's heads do),
     // a lane takes its sum or leaves it (`limit`); where they do not, each weight has
-    // its own condition, and a tree's are added by themselves.
+    // its own condition.
     Total total[2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};
     f32x16 sc[2][2];
     bool waiting = false, same = false;
@@ -890,19 +905,20 @@ __global__ __launch_bounds__(kManyBlock) void weigh_many_kernel(WeighParams p) {
         if (j == 1) next.load<2>(there, part8), next.load<3>(there, part8);
         if (j == 2) next.load<4>(there, part8), next.load<5>(there, part8);
         if (j == 3) next.load<6>(there, part8), next.load<7>(there, part8);
-        if (j == 4) next.fetch(p, blk.b, s);
+        if (j == 4) next.fetch(p, blk.b, s, masks);
         if (j == 20) after.locate(p, s, m0 + 64 + mine, end);
       };
       float sum[2] = {0.0f, 0.0f};
       if (waiting && same) {
-        scores_of<L, 1>(cur, x, here, lane, prev, before, 0, p.scale_log2, sum, beside);
+        scores_of<L, 1>(cur, x, here, lane, prev, before, 0, 0, p.scale_log2, sum, beside);
 #pragma unroll
         for (int n = 0; n < 2; ++n) sum[n] = r0 + 32 * n + (lane & 31) < limit ? sum[n] : 0.0f;
       } else if (waiting && p.tree == nullptr) {
-        scores_of<L, 2>(cur, x, here, lane, prev, before, r0 + (lane & 31), p.scale_log2, sum, beside);
+        scores_of<L, 2>(cur, x, here, lane, prev, before, r0 + (lane & 31), 0, p.scale_log2, sum, beside);
+      } else if (waiting) {
+        scores_of<L, 3>(cur, x, here, lane, prev, before, r0 + (lane & 31), s.pos, p.scale_log2, sum, beside);
       } else {
-        if (waiting) add_chunk(prev, before);
-        scores_of<L, 0>(cur, x, here, lane, prev, before, 0, 0.0f, sum, beside);
+        scores_of<L, 0>(cur, x, here, lane, prev, before, 0, 0, 0.0f, sum, beside);
       }
       part[0] += sum[0];
       part[1] += sum[1];
@@ -958,6 +974,7 @@ __global__ __launch_bounds__(kJoinBlock) void weigh_join_kernel(WeighParams p) {
   __shared__ uint32_t blocks[SLOTS / 2], stored[SLOTS / 2];
   __shared__ int64_t buf[kJoinBlock / kLanes];
   __shared__ float sums[kJoinGroups][kWeighRows];
+  __shared__ int32_t place[kJoinBlock];
   const int cut = uniform(p.head->cut), S = p.num_slots;
   int64_t count = 0, places = 0;
   int32_t none = 0;
@@ -991,9 +1008,15 @@ __global__ __launch_bounds__(kJoinBlock) void weigh_join_kernel(WeighParams p) {
     // the block's parts: of the segments from the one of the first token that sees it
     const int32_t G = segments_of(s, cut), g0 = first_token(p, s, (int32_t)k << kManyRowBits) >> cut;
     float v = 0.0f;
-#pragma unroll 4
-    for (int32_t g = g0 + group; g < G; g += kJoinGroups)
-      v += p.parts[(base + parts_before(p, s, cut, g) + k) * kWeighRows + row];
+    for (int32_t t0 = g0; t0 < G; t0 += kJoinBlock) {
+      // their places, a thread each
+      const int32_t mine_at = t0 + (int32_t)threadIdx.x, n = min(G - t0, kJoinBlock);
+      __syncthreads();
+      if (mine_at < G) place[threadIdx.x] = (int32_t)(base + parts_before(p, s, cut, mine_at) + k);
+      __syncthreads();
+#pragma unroll 8
+      for (int32_t t = group; t < n; t += kJoinGroups) v += p.parts[(int64_t)place[t] * kWeighRows + row];
+    }
     sums[group][row] = v;
     __syncthreads();
     const int32_t r = ((int32_t)k << kManyRowBits) + row;
