@@ -86,9 +86,14 @@ struct WeighParams {
 // ---------------------------------------------------------------- choice
 // Rows of weights that one workgroup keeps in registers; of longer ones of up to
 // kSelectSegmentSlots slots, a slot's rows are cut into segments of at least
-// kSelectSegmentRows, kSelectSegments for all slots together at the most.
+// kSelectSegmentRows, kSelectSegments for all slots together at the most; those of
+// more slots are read by one workgroup a slot, once a digit.  Measured, us a call:
+// 64 slots of 16,384 rows in registers 13, in segments 26; of 32,768 rows in segments
+// and read by one workgroup each, 1 slot 27 and 38, 64 slots 29 and 41, 256 slots 61 and
+// 51, 512 slots 112 and 74; 16 slots of 131,072 rows 35 and 141.  (Segments of 32,768 rows
+// take a million rows from 44 to 59.)
 constexpr int kSelectRegisterRows = 16384;
-constexpr int kSelectSegmentSlots = 256;
+constexpr int kSelectSegmentSlots = 128;
 constexpr int kSelectSegmentRows = 16384;
 constexpr int kSelectSegments = 512;
 // words of a segment in the workspace: three histograms, a state of 4

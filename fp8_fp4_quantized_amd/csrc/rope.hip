@@ -6,12 +6,13 @@
 // a position; a thread makes its first entry and the turn from one of its
 // entries to the next by sincospi in 64 bits and goes on by complex products in
 // 64 bits (kTableRun of them: the error stays below 2^-45, far under the one
-// rounding to fp32).  Bound by the writes.
+// rounding to fp32).  Bound by the writes: a million positions of 64 dims, 268 MB, take
+// 46 to 48 us (5.6 to 5.8 TB/s); 4,096 of them 4.6.
 //
 // Rotation: with (c, s) = freqs[position] the pair (a, b) becomes
 //   (a c - b s, a s + b c), transposed (a c + b s, b c - a s),
 // in fp32, rounded once to the heads' type.  Bound by HBM; in place only the
-// rotated dims move.
+// rotated dims move.  A decode step's 64 tokens of 64 heads take 4 us.
 #include <type_traits>
 
 #include "launch_evict.hpp"
@@ -368,6 +369,10 @@ hipError_t launch_vectors(RopeRowsParams p, hipStream_t stream) {
   return hipGetLastError();
 }
 
+// Measured, 8,192 tokens of 128 heads of 512 dims in bf16 from one tensor to another,
+// 2.15 GB: 366 us with pairs of neighbours and 414 with pairs of halves (5.9 and 5.2 TB/s);
+// by rope_any_kernel 565 and 686, which also takes an odd offset (665) and 511 dims
+// (734); element by element 1,745.
 // Whether heads can be taken by 16 bytes: addresses, strides and dims of whole
 // ones, pairs inside one of them (or their halves at whole ones).
 bool by_vectors(const RopeRowsParams& p) {

@@ -10,6 +10,18 @@
 // the codes of its row straight from the page into the operand's place (dims in
 // the order the codes come in; the queries are read from LDS in the same order),
 // so pages of any size are alike and nothing of a row passes through LDS.
+//
+// What bounds it: a (query, row) pair is 1,024 flops, half of the attention's, and a
+// row 288 to 584 bytes; at 1.5 PFLOP/s and 5.2 TB/s the two take the same time at 152
+// queries a slot for V41, 83 for V41_FP4, 168 for V4.  Slots of few queries are bound by
+// HBM: one token of 64 requests over V41 rows 70 us with 32 heads and 77 with 64 (4.6 and
+// 4.2 TB/s), 128 chains of 4 with 16 heads over V4 rows 83 (4.3 TB/s); over V41_FP4 rows
+// with 64 heads 57 us (2.9 TB/s), where the expansion, the products and the sums of
+// half as many bytes share the time.  Slots of many are bound by the matrix units: a
+// prompt of 8,192 tokens with 128 heads 3.7 to 3.9 ms (1.13 to 1.19 PFLOP/s; the same loop
+// with products alone reaches 1.55 at the clock that the card holds under them), 16
+// prompts of some 2,000 tokens with 32 heads over V41_FP4 rows pooled by two 0.74 to
+// 0.77 ms.
 #include <algorithm>
 
 #include "launch_evict.hpp"
@@ -385,13 +397,16 @@ __device__ __forceinline__ int slot_at(const T* before, int n, T at) {
 }
 
 // ------------------------------------------------------------------ few queries
-// Slots of up to 32 NC queries each: they stay in LDS while 8 waves go over the
-// slot's rows, 32 at a time.
+// Slots of up to 32 NC queries each, 128 at the most: they stay in LDS while 8 waves,
+// two to a SIMD, go over the slot's rows, 32 at a time.  Measured beside the kernel for
+// many queries, one token of 64 requests with 128 heads: V41 111 us and 195, V41_FP4 98
+// and 177; of one request of 1,000 rows 12 and 24.
 constexpr int kFewBlock = 512;
 constexpr int kFewWaves = kFewBlock / kLanes;
 constexpr int kFewGrid = 256;
 
 // A slot's begin, its queries brought to LDS, as the blocks that take the same time
+// (64 decodes: 8 blocks 63.1 us, 16 62.7, 24 61.8, 40 63.9)
 constexpr uint32_t kSlotBlocks = 16;
 __device__ __forceinline__ uint32_t few_cost(int32_t rows) {
   return rows > 0 ? (uint32_t)((rows + 31) >> 5) + kSlotBlocks : 0;
@@ -623,7 +638,10 @@ __device__ __forceinline__ int64_t parts_of(const WeighParams& p, const SlotToke
 
 // The first cut tried: segments of `share` queries, a sixteenth of a workgroup's
 // share of the work, but 2,048 or the whole share where that is less, and 128 at the
-// least (4 chunks; fewer would not pay for the block's begin).
+// least (4 chunks; fewer would not pay for the block's begin).  Measured for the
+// prompt of 8,192 tokens and the 16 of some 2,000, us: a 32nd and 1,024 4,372 and 961, a
+// 16th and 2,048 4,290 and 910, a 16th and 4,096 4,283 and 878, an 8th and 2,048 4,538
+// and 905.  (Longer segments leave fewer parts to deal.)
 __device__ __forceinline__ int first_cut(const WeighParams& p, int64_t work) {
   const int64_t each = (work + kWeighWorkgroups - 1) / kWeighWorkgroups;
   const int64_t share = max(max(each / 16, min(each, (int64_t)2048)), (int64_t)128);
@@ -748,7 +766,7 @@ __device__ __forceinline__ uint32_t query_at(int j, int lane) {
   return (base ^ (16 * (c & 7))) + 1024 * (c >> 3);
 }
 
-constexpr int kAhead = 4;        // fragments of queries read ahead
+constexpr int kAhead = 4;        // fragments of queries read ahead (3 and 6 measure the same, 8 2% slower)
 
 // The scores of a chunk of 32 queries with the wave's 64 rows.  SUM 1: the weights
 // of the chunk before (scores prev, queries of) are added up meanwhile, one a step,

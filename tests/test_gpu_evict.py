@@ -108,6 +108,14 @@ def test_select_long_and_short_together(kvc):
     check_select(kvc, lens, weights_of(8, 200000, 3, "ties"), 4000, first=4, recent=100)
 
 
+@pytest.mark.parametrize("S", [127, 128, 129])
+def test_select_long_rows_of_many_slots(kvc, S):
+    rng = np.random.default_rng(S)
+    lens = rng.integers(0, 16500, S)
+    lens[:3] = [16500, 16385, -1]
+    check_select(kvc, lens, weights_of(S, 16500, 4, "ties"), 500, first=2, recent=30)
+
+
 def test_select_many_slots(kvc):
     rng = np.random.default_rng(1)
     lens = rng.integers(-1, 40, 8191)
