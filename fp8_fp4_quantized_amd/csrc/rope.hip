@@ -13,6 +13,7 @@
 //   (a c - b s, a s + b c), transposed (a c + b s, b c - a s),
 // in fp32, rounded once to the heads' type.  Bound by HBM; in place only the
 // rotated dims move.  A decode step's 64 tokens of 64 heads take 4 us.
+#include <algorithm>
 #include <type_traits>
 
 #include "launch_evict.hpp"
@@ -111,11 +112,11 @@ __device__ __forceinline__ bool position_ok(const RopeRowsParams& p, int32_t pos
 }
 
 // Element by element: a unit is one pair, or one dim that is only copied.  For
-// dims, strides and addresses that the kernel by 16 bytes does not take.
+// dims, strides and addresses that the kernel by 16 bytes does not take.  u0: the
+// workgroup's first unit.
 template <int T>
-__global__ __launch_bounds__(kRopeBlock) void rope_elements_kernel(RopeRowsParams p) {
+__device__ __forceinline__ void rope_element(const RopeRowsParams& p, int64_t u0) {
   typedef typename Elem<T>::type E;
-  const int64_t u0 = (int64_t)blockIdx.x * kRopeBlock;
   const int64_t token0 = u0 / p.token_units;
   if (u0 + threadIdx.x >= p.units) return;
   const Unit u = unit_at(p, token0, (uint32_t)(u0 - token0 * p.token_units) + threadIdx.x);
@@ -139,13 +140,22 @@ __global__ __launch_bounds__(kRopeBlock) void rope_elements_kernel(RopeRowsParam
   }
 }
 
+// (a launch has less than 2^32 threads, and 20 GB of heads have as many units)
+constexpr int64_t kElementsGrid = int64_t(1) << 23;
+
+template <int T>
+__global__ __launch_bounds__(kRopeBlock) void rope_elements_kernel(RopeRowsParams p) {
+  for (int64_t u0 = (int64_t)blockIdx.x * kRopeBlock; u0 < p.units; u0 += (int64_t)gridDim.x * kRopeBlock)
+    rope_element<T>(p, u0);
+}
+
 hipError_t launch_elements(RopeRowsParams p, hipStream_t stream) {
   p.head_units = p.rot / 2 + (p.in_place ? 0 : p.dim - p.rot);
   p.token_units = p.head_units * p.heads;
   p.head_div = div_magic((uint32_t)p.head_units);
   p.token_div = div_magic((uint32_t)p.token_units);
   p.units = p.tokens * p.token_units;
-  const dim3 grid((uint32_t)((p.units + kRopeBlock - 1) / kRopeBlock));
+  const dim3 grid((uint32_t)std::min((p.units + kRopeBlock - 1) / kRopeBlock, kElementsGrid));
   switch (p.type) {
     case kRopeBf16: rope_elements_kernel<kRopeBf16><<<grid, kRopeBlock, 0, stream>>>(p); break;
     case kRopeF16: rope_elements_kernel<kRopeF16><<<grid, kRopeBlock, 0, stream>>>(p); break;
@@ -253,7 +263,13 @@ __global__ __launch_bounds__(kRopeBlock) void rope_vectors_kernel(RopeRowsParams
           const Turned r = turn(v.f[e], v.f[e + 1], t[0], p.transpose ? -t[1] : t[1]);
           v.f[e] = r.a, v.f[e + 1] = r.b;
         }
-        a[i] = v.bits();
+        // (dims that are copied keep their bits: a conversion changes some NaNs')
+        const u32x4 made = v.bits();
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int r = at + k * E / 4;
+          a[i][k] = r >= 0 && r < p.rot ? made[k] : a[i][k];
+        }
       }
     }
     *(u32x4*)out[i] = a[i];
@@ -334,7 +350,19 @@ __global__ __launch_bounds__(kRopeBlock) void rope_any_kernel(RopeRowsParams p) 
         const float y = second ? turn(other[e], own.f[e], t[0], sn).b : turn(own.f[e], other[e], t[0], sn).a;
         if (r == rel[i] + e) made.f[e] = y;
       }
-      v[i] = made.bits();
+      // (dims that are copied keep their bits: a conversion changes some NaNs')
+      constexpr int per = E / 4;
+      const u32x4 bits = made.bits();
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        uint32_t turned = 0;
+#pragma unroll
+        for (int e = 0; e < per; ++e) {
+          const int r = rel[i] + k * per + e;
+          if (r >= 0 && r < p.rot) turned |= (per == 1 ? 0xFFFFFFFFu : 0xFFFFu) << (16 * e);
+        }
+        v[i][k] = (bits[k] & turned) | (v[i][k] & ~turned);
+      }
     }
     *(u32x4_any*)out[i] = v[i];
   }

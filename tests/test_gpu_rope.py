@@ -265,3 +265,39 @@ def test_other_stream_and_graph(kvc):
         kvc.kvc_rope_table(f)
         kvc.kvc_rope_rows(x, pos, f, eager)
         assert torch.equal(out, eager)
+
+
+# dim, rot, offset, half: by 16 bytes, by any address, pair by pair
+@pytest.mark.parametrize("kind", [BF, HF, FL])
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("D,R,off,half", [(32, 6, 2, False), (32, 18, 10, False), (32, 6, 3, False), (29, 6, 2, False),
+                                          (32, 16, 8, True), (32, 6, 5, True), (3, 2, 0, False)])
+def test_copied_dims_keep_their_bits(kvc, kind, in_place, D, R, off, half):
+    """Also those of a signalling NaN, a subnormal or a negative zero."""
+    whole = torch.int32 if kind == FL else torch.int16
+    odd = {BF: [0x7F81, -0x7F, 1, -0x8000, 0x7F80], HF: [0x7C01, -0x3FF, 1, -0x8000, 0x7C00],
+           FL: [0x7F800001, -0x7FFFFF, 1, -0x80000000, 0x7F800000]}[kind]
+    x = torch.tensor(odd, dtype=whole).repeat(5 * 3 * D)[:5 * 3 * D].view(5, 3, D).cuda()
+    pos = torch.arange(5, dtype=torch.int32, device="cuda")
+    out = x.clone() if in_place else torch.zeros_like(x)
+    kvc.kvc_rope_rows(out.view(kind) if in_place else x.view(kind), pos, freqs_of(8, R).cuda(), out.view(kind),
+                      offset=off, half=half)
+    copied = [d for d in range(D) if not off <= d < off + R]
+    assert torch.equal(out[..., copied], x[..., copied])
+
+
+def test_more_pairs_than_a_launch_has_threads(kvc):
+    """Pair by pair (in place, an odd offset), 2^32 pairs and some."""
+    T, D, R, n = 2 ** 24 + 5, 515, 512, 300
+    some = make(HF, n, 1, D, 9).cuda()
+    f = freqs_of(64, R).cuda()
+    pos = torch.arange(T, dtype=torch.int32, device="cuda") % 64
+    x = torch.zeros(T, 1, D, dtype=HF, device="cuda")
+    for at in (0, 2 ** 23 - 100, T - n):
+        x[at:at + n] = some
+    kvc.kvc_rope_rows(x, pos, f, offset=1)
+    for at in (0, 2 ** 23 - 100, T - n):
+        want = some.clone()
+        kvc.kvc_rope_rows(want, pos[at:at + n].contiguous(), f, offset=1)
+        assert torch.equal(x[at:at + n], want) and not torch.equal(want, some)
+    assert not x[n:2 ** 23 - 100].any() and not x[2 ** 23 - 100 + n:T - n].any()
