@@ -305,7 +305,7 @@ int weigh(const kvc_weigh_args* a, bool tree, void* stream, const char* who) {
   p.start_pos = a->start_pos;
   p.page_table = a->page_table;
   p.pt_stride = a->pt_stride;
-  p.pt_width = a->pt_width;
+  p.pt_width = a->pt_width < 0x7FFFFFFF ? a->pt_width : 0x7FFFFFFF;   // (no row has a later page)
   p.tree = tree ? a->tree : nullptr;
   p.decay = a->decay;
   p.prev = a->decay == 0.0f ? nullptr : a->prev;   // (not read: 0 times anything)
@@ -326,7 +326,7 @@ int weigh(const kvc_weigh_args* a, bool tree, void* stream, const char* who) {
 int32_t evict_segments(int32_t slots, int64_t width) {
   if (width <= kvc::kSelectRegisterRows || slots < 1 || slots > kvc::kSelectSegmentSlots) return 0;
   const int64_t most = kvc::kSelectSegments / slots;
-  const int64_t n = (width + kvc::kSelectSegmentRows - 1) / kvc::kSelectSegmentRows;
+  const int64_t n = (width - 1) / kvc::kSelectSegmentRows + 1;
   return (int32_t)(n < most ? n : most);
 }
 
@@ -335,7 +335,8 @@ int32_t evict_segments(int32_t slots, int64_t width) {
 // all, up to the most there are.
 int64_t evict_bytes(int32_t slots, int64_t width) {
   if (width <= kvc::kSelectRegisterRows) return 0;
-  const int64_t n = (width + kvc::kSelectSegmentRows - 1) / kvc::kSelectSegmentRows * slots;
+  const int64_t each = (width - 1) / kvc::kSelectSegmentRows + 1;
+  const int64_t n = (each < kvc::kSelectSegments ? each : kvc::kSelectSegments) * slots;
   const int64_t segments = n < kvc::kSelectSegments ? n : kvc::kSelectSegments;
   return segments * (3 * kvc::kSelectWords + 4) * 4;
 }
@@ -878,7 +879,7 @@ int kvc_evict_select(const kvc_evict_args* a, void* stream) {
   p.status = a->status;
   if (segments > 0) {
     p.segments = segments;
-    p.segment_rows = (a->w_width + segments - 1) / segments;
+    p.segment_rows = (a->w_width - 1) / segments + 1;
     p.hists = static_cast<uint32_t*>(a->workspace);
     p.states = reinterpret_cast<int32_t*>(p.hists + 3 * all * kvc::kSelectWords);
   }
@@ -896,7 +897,13 @@ int kvc_cache_compact(const kvc_compact_args* a, void* stream) {
     return fail(KVC_EINVAL, "%s: num_slots %d outside [0, %d]", who, a->num_slots, kvc::kMaxSlots);
   if (a->n_free < 0 || a->n_free >= 0x7FFFFFFF || a->freed_cap < 0 || a->freed_cap >= 0x7FFFFFFF)
     return fail(KVC_EINVAL, "%s: n_free and freed_cap must lie in [0, 2^31 - 2]", who);
-  if (a->num_slots == 0) return ok();
+  if (a->num_slots == 0) {
+    if (a->totals == nullptr) return ok();
+    if (kvc::launch_compact == nullptr) return fail(KVC_ELAUNCH, "%s: built without kernels", who);
+    p.ratio = a->ratio;
+    p.totals = a->totals;
+    return launched(kvc::launch_compact(p, static_cast<hipStream_t>(stream)), who);
+  }
   if (a->lens == nullptr || a->counts == nullptr || a->new_lens == nullptr)
     return fail(KVC_EINVAL, "%s: NULL lens, counts or new_lens", who);
   if (a->new_lens == a->lens || a->new_lens == a->counts)

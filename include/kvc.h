@@ -606,12 +606,13 @@ int kvc_rope_rows(const kvc_rope_args* args, void* stream);
  *   and heads h of the slot that see r,
  *     weights[b][r] = decay * prev[b][r] + sum_th 2^(scale log2(e) (q_th . x_r) - lse_th)
  *   for every row r < (start_pos[b] + count) / ratio; weights past these, and
- *   those of skipped slots, are left as they are.  prev counts as 0 for the rows
+ *   those of slots without tokens (start_pos < 0, a count of 0, a skipped slot),
+ *   are left as they are, whatever prev and decay.  prev counts as 0 for the rows
  *   r >= start_pos[b] / ratio, which the call's tokens complete (they need no
  *   preparation), and everywhere where it is NULL or decay is 0; it may be weights
  *   itself.
  *   A query whose lse is not finite adds nothing; a row that is not finite
- *   collects nothing, and neither does a row whose page is outside the cache
+ *   collects nothing (and one whose sum passes fp32, as with another call's lse), and neither does a row whose page is outside the cache
  *   (KVC_STATUS_PAGE_RANGE).  Rows past pt_width pages or w_width entries are
  *   left out with KVC_STATUS_PT_RANGE.  Scores and sums are fp32; the order of a
  *   sum depends on the call's sizes and lengths alone, so results repeat.
@@ -712,6 +713,7 @@ int kvc_evict_select(const kvc_evict_args* args, void* stream);
  *   freed        [freed_cap] or NULL
  *   totals       [4] or NULL: pages taken, pages given back, rows dropped
  *                (at most 2^31 - 1), slots refused
+ *                (num_slots 0: zeros)
  * A slot is refused, and stays as it is, when its rows pass pt_width pages or its
  * count kept_width or w_width (KVC_STATUS_PT_RANGE), or when the pages asked for
  * or given back up to and including it pass n_free (or num_pages - 1) or

@@ -141,8 +141,8 @@ def test_evict_workspace_covers_smaller_calls(kvc):
     """What a call needs never passes the workspace of a larger one."""
     size = kvc.kvc_evict_workspace
     assert size(1, 16384) == 0 and size(8191, 16384) == 0
-    widths = [1, 16384, 16385, 20000, 32768, 32769, 100000, 1 << 20, 1 << 23, 1 << 31]
-    slots = [0, 1, 2, 3, 60, 64, 255, 256, 257, 8191]
+    widths = [1, 16384, 16385, 20000, 32768, 32769, 100000, 1 << 20, 1 << 23, 1 << 31, (1 << 63) - 1]
+    slots = [0, 1, 2, 3, 60, 64, 127, 128, 129, 255, 256, 257, 8191]
     for i, s in enumerate(slots):
         for j, w in enumerate(widths):
             for s2 in slots[:i + 1]:
@@ -180,7 +180,7 @@ def test_compact_arguments(kvc):
         dict(cache_page_size=3), dict(cache_num_pages=0)])
     refused(kvc, compact, kvc.KVC_EUNSUPPORTED, [dict(ratio=0), dict(ratio=3), dict(cache_layout=9)])
     assert kvc.lib().kvc_cache_compact(None, None) == kvc.KVC_EINVAL
-    assert compact(kvc, num_slots=0) == kvc.KVC_OK
+    assert compact(kvc, num_slots=0, totals=None) == kvc.KVC_OK
 
 
 # ------------------------------------------------------------------- binding

@@ -350,3 +350,14 @@ def test_compact_streams_and_graphs(kvc):
         torch.cuda.synchronize()
         assert np.array_equal(host(cache.data), want["cache"]) and np.array_equal(host(new), want["new_table"])
         assert np.array_equal(host(lens), want["new_lens"])
+
+
+def test_compact_of_no_slots(kvc):
+    """An empty batch takes and gives back nothing, and says so."""
+    cache = kvc.Cache(torch.zeros(3, 64 * 528, dtype=torch.uint8, device="cuda"), "V41", 64)
+    none = torch.zeros(0, dtype=torch.int32, device="cuda")
+    table, kept = torch.zeros(0, 2, dtype=torch.int32, device="cuda"), torch.zeros(0, 4, dtype=torch.int32, device="cuda")
+    totals = torch.full((4,), 7, dtype=torch.int32, device="cuda")
+    kvc.kvc_cache_compact(cache, none, kept, none, table, torch.tensor([1, 2], dtype=torch.int32, device="cuda"),
+                          torch.zeros_like(table), torch.zeros_like(none), totals=totals)
+    assert totals.tolist() == [0, 0, 0, 0]

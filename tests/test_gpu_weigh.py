@@ -2,6 +2,7 @@
 references: packed prompts, chains, trees and single tokens, every layout, few
 and many queries, ragged and odd sizes, masks that leave nothing, rows and
 queries that are not finite, decay, strides, streams, captured graphs."""
+import ctypes as C
 import math
 import random
 
@@ -391,3 +392,39 @@ def test_weights_of_an_attention_call(kvc, sink):  # noqa: F811
     if sink:
         total -= torch.exp2(sinks.double() * ref.LOG2E - lse.double()).sum().item()
     assert abs(out.double().sum().item() - total) <= 2e-5 * total
+
+
+@pytest.mark.parametrize("H,counts", [(16, [3, 0, 4, 0]), (48, [30, 0, 5, 0])])
+def test_slots_without_tokens_are_left(kvc, H, counts):  # noqa: F811
+    """Neither their weights nor prev move, whatever decay is."""
+    starts = [100, 70, 50, -1]
+    f = Filled(kvc, "V41", 64, [s + c for s, c in zip(starts[:3], counts)] + [64], seed=5)
+    at = torch.cat([torch.tensor([0]), torch.tensor(counts[:-1]).cumsum(0)])
+    q = queries(sum(counts), H, seed=6)
+    lse = torch.zeros(sum(counts), H)
+    prev, out = torch.rand(4, 200, device="cuda"), torch.full((4, 200), 9.0, device="cuda")
+    kvc.kvc_weigh_prefill(f.cache, q.cuda(), lse.cuda(), torch.stack([at, torch.tensor(counts)]).int().cuda(),
+                          torch.tensor(starts, dtype=torch.int32, device="cuda"), dev(f.table), out, scale=SCALE,
+                          prev=prev, decay=0.5)
+    assert (out[[1, 3]] == 9).all()
+    for b in (0, 2):
+        assert (out[b, :starts[b]] >= 0.5 * prev[b, :starts[b]]).all() and (out[b, starts[b] + counts[b]:] == 9).all()
+
+
+@pytest.mark.parametrize("H,D", [(16, 1), (64, 4)])
+def test_a_width_past_every_page(kvc, H, D):  # noqa: F811
+    """One row of the table may be said to be as wide as 64 bits go."""
+    f = Filled(kvc, "V41", 64, [130 + D], seed=7)
+    q = queries(D, H, seed=8).cuda()
+    lse = torch.zeros(D, H, device="cuda")
+    start, table = torch.tensor([130], dtype=torch.int32, device="cuda"), dev(f.table)
+    want = torch.zeros(1, 130 + D, device="cuda")
+    kvc.kvc_weigh_tree(f.cache, q, lse, start, table, want, scale=SCALE, draft_len=D)
+    got = torch.zeros_like(want)
+    space = torch.empty(kvc.kvc_weigh_workspace(), dtype=torch.uint8, device="cuda")
+    a = kvc.kvc_weigh_args(1, H, 1, D, q.data_ptr(), q.stride(0), q.stride(1), D, lse.data_ptr(), None,
+                           start.data_ptr(), table.data_ptr(), 2 ** 62, 2 ** 62, None, SCALE, 1.0, None, 0,
+                           got.data_ptr(), 130 + D, 130 + D, f.cache.desc(), space.data_ptr(), space.numel(), None)
+    assert kvc.lib().kvc_weigh_tree(C.byref(a), torch.cuda.current_stream().cuda_stream) == 0
+    torch.cuda.synchronize()
+    assert torch.equal(got, want) and (want > 0).any()
