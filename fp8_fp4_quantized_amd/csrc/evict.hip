@@ -7,8 +7,8 @@
 // is found digit by digit.
 //
 // It is latency: 64 slots of 4,200 to 16,384 rows take 12.4 us in one launch (three
-// histograms in LDS, the writes); a million rows of one slot 44 us in four launches of 6,
-// 13, 13 and 12 (one workgroup that reads them four times took 1,348).
+// histograms in LDS, the writes); a million rows of one slot 34 us in four launches of 6,
+// 9, 8 and 12 (one workgroup that reads them four times took 1,348).
 //
 // Move: row i of a slot's list goes to row i of pages taken from the free list,
 // in slot order.  Every workgroup scans all slots into LDS, as the slot map
@@ -36,9 +36,10 @@ namespace {
 //                            rows in segments, one workgroup each; a launch a digit
 //                            and one that writes.  A segment's histogram lies in
 //                            the workspace, and each workgroup of the next launch
-//                            adds the slot's for itself -- no atomics in memory,
-//                            nothing to clear -- together with those of the
-//                            segments before its own, which say where it writes.
+//                            adds what it needs of the slot's for itself -- no
+//                            atomics in memory, nothing to clear -- together with
+//                            those of the segments before its own, which say where
+//                            it writes.
 //   select_stream_kernel     longer ones of more slots, which fill the card with a
 //                            workgroup each: the keys are read once a digit
 constexpr int kSelectBlock = 1024;
@@ -284,8 +285,9 @@ __global__ __launch_bounds__(kSelectBlock) void select_stream_kernel(SelectParam
 
 // ---- segments
 constexpr int kSegBits[3] = {11, 11, 10}, kSegShift[3] = {21, 10, 0};
-constexpr int kSegBins = kSelectWords;        // of the first two; the third has half as many
-static_assert(kSegBins == 1 << kSegBits[0] && kSegBins == 1 << kSegBits[1], "words of a histogram");
+constexpr int kCoarse = 64;                   // a histogram's sums of so many equal stretches lie in front of it
+static_assert(kSelectWords == kCoarse + (1 << kSegBits[0]) && kSegBits[1] <= kSegBits[0] && kSegBits[2] <= kSegBits[0],
+              "words of a histogram");
 constexpr int kTurn = 16;                     // rows a thread has in registers
 
 // A segment of a slot: what is known of the key, and of the segments before it
@@ -295,45 +297,75 @@ struct Found {
   Written before;              // in the segments before this one: rows kept for certain, rows with all digits
 };
 
-// The digit that the histograms of the last launch give, from the slot's sums
+// Sums over the segments' counts, a lane each: all of them, and those of segments before
+// this one.  Every wave has them.
+struct Sums {
+  int32_t all, before;
+};
+struct SumsBuf {
+  int32_t all[kSelectWaves][kLanes], before[kSelectWaves][kLanes];
+};
+// W lanes of counts at `at` of each segment's words; lanes past W get 0
+template <int W>
+__device__ __forceinline__ Sums sum_segments(const SelectParams& p, const uint32_t* at, int s, SumsBuf& buf) {
+  constexpr int G = kLanes / W;                // segments a wave reads at once
+  const int lane = lane_id(), wave = uniform((int)(threadIdx.x >> 6));
+  Sums v{0, 0};
+#pragma unroll 8
+  for (int t = wave * G + lane / W; t < p.segments; t += kSelectWaves * G) {
+    const int32_t n = (int32_t)at[(int64_t)t * kSelectWords + lane % W];
+    v.all += n;
+    v.before += t < s ? n : 0;
+  }
+#pragma unroll
+  for (int d = W; d < kLanes; d <<= 1) {
+    v.all += __shfl_xor(v.all, d);
+    v.before += __shfl_xor(v.before, d);
+  }
+  buf.all[wave][lane] = v.all;
+  buf.before[wave][lane] = v.before;
+  __syncthreads();
+  v = Sums{0, 0};
+  // (of the waves that had any)
+  const int waves = min(kSelectWaves, (p.segments + G - 1) / G);
+#pragma unroll 4
+  for (int w = 0; w < waves; ++w) v.all += buf.all[w][lane], v.before += buf.before[w][lane];
+  return lane < W ? v : Sums{0, 0};
+}
+
+// The lane (greatest first) whose counts hold the left-th key, which of that lane's it
+// is, and the counts before this segment in greater lanes and in that one
+struct LaneFound {
+  int32_t lane, left;
+  Written before;
+};
+__device__ __forceinline__ LaneFound find_lane(const Sums& v, int32_t left) {
+  const int32_t above = __builtin_amdgcn_readlane(wave_incl_scan_i32(v.all), kLanes - 1) - wave_incl_scan_i32(v.all);
+  const int32_t end = wave_incl_scan_i32(v.before);
+  const uint64_t hit = __ballot(above < left && above + v.all >= left);
+  const int lane = __builtin_ctzll(hit | 1ull << 63);   // (a lane, also if the counts were another call's)
+  return LaneFound{lane, left - __builtin_amdgcn_readlane(above, lane),
+                   {__builtin_amdgcn_readlane(end, kLanes - 1) - __builtin_amdgcn_readlane(end, lane),
+                    __builtin_amdgcn_readlane(v.before, lane)}};
+}
+
+// The digit that the histograms of the last launch give, from the slot's sums: first of
+// their stretches, then of the bins of the one that holds it (24 KB a workgroup for
+// 64 segments, where the whole histograms are 512: a million rows took 44 us with them)
 template <int BINS>
-__device__ __forceinline__ Found next_digit(const SelectParams& p, Found f, const uint32_t* hists, int s, int32_t* buf,
-                                            int32_t* found, int32_t* sums) {
-  constexpr int N = BINS / kSelectBlock;
-  typedef uint32_t bins_t __attribute__((ext_vector_type(N)));
-  const int top = N * kSelectBlock - N - N * (int)threadIdx.x;   // the thread's least bin
-  int32_t n[N], before[N];
-#pragma unroll
-  for (int k = 0; k < N; ++k) n[k] = before[k] = 0;
-#pragma unroll 32
-  for (int t = 0; t < p.segments; ++t) {
-    const bins_t h = *(const bins_t*)(hists + (int64_t)t * kSegBins + top);
-#pragma unroll
-    for (int k = 0; k < N; ++k) {
-      n[k] += (int32_t)h[N - 1 - k];
-      before[k] += t < s ? (int32_t)h[N - 1 - k] : 0;
-    }
-  }
-  const Digit d = find_digit(n, f.left, buf, found);
-  // rows in the segments before this one whose digit is greater, and that have it
-  int32_t above = 0;
-#pragma unroll
-  for (int k = 0; k < N; ++k) {
-    const uint32_t bin = (uint32_t)(top + N - 1 - k);
-    if (bin > d.bin) above += before[k];
-    if (bin == d.bin) sums[0] = before[k];
-  }
-  int32_t total;
-  block_scan(above, buf + kSelectWaves, &total);
-  f.key = f.key * BINS + d.bin;
+__device__ __forceinline__ Found next_digit(const SelectParams& p, Found f, const uint32_t* hists, int s, SumsBuf (&buf)[2]) {
+  constexpr int W = BINS / kCoarse;
+  const LaneFound c = find_lane(sum_segments<kCoarse>(p, hists, s, buf[0]), f.left);
+  const LaneFound d = find_lane(sum_segments<W>(p, hists + kCoarse + c.lane * W, s, buf[1]), c.left);
+  f.key = f.key * BINS + (uint32_t)(c.lane * W + d.lane);
   f.left = d.left;
-  f.before.above += total;
-  f.before.equal = sums[0];
+  f.before.above += c.before.above + d.before.above;
+  f.before.equal = d.before.equal;
   return f;
 }
 
 __device__ __forceinline__ uint32_t* hists_of(const SelectParams& p, int pass, int64_t seg) {
-  return p.hists + ((int64_t)pass * p.num_slots * p.segments + seg) * kSegBins;
+  return p.hists + ((int64_t)pass * p.num_slots * p.segments + seg) * kSelectWords;
 }
 
 // Counts the segment's keys that begin with the PASS digits found -- the last of them
@@ -342,7 +374,7 @@ template <int PASS>
 __global__ __launch_bounds__(kSelectBlock) void select_count_kernel(SelectParams p) {
   constexpr int BINS = 1 << kSegBits[PASS];
   __shared__ uint32_t hist[BINS];
-  __shared__ int32_t buf[2 * kSelectWaves], found[2], sums[1];
+  __shared__ SumsBuf buf[2];
   const int s = blockIdx.x, b = blockIdx.y, tid = threadIdx.x;
   const Choice c = choice_of(p, b, PASS == 0 && s == 0);
   const Lists l(p, b);
@@ -361,7 +393,7 @@ __global__ __launch_bounds__(kSelectBlock) void select_count_kernel(SelectParams
     f = Found{(uint32_t)st[0], st[1], {st[2], 0}};
   }
   if constexpr (PASS > 0)
-    f = next_digit<1 << kSegBits[PASS - 1]>(p, f, hists_of(p, PASS - 1, (int64_t)b * p.segments), s, buf, found, sums);
+    f = next_digit<1 << kSegBits[PASS - 1]>(p, f, hists_of(p, PASS - 1, (int64_t)b * p.segments), s, buf);
   __syncthreads();
   auto count = [&](float w, bool in) {
     const uint32_t k = weight_key(w);
@@ -373,7 +405,15 @@ __global__ __launch_bounds__(kSelectBlock) void select_count_kernel(SelectParams
   for (int64_t r = begin + tid + kTurn * kSelectBlock; r < end; r += kSelectBlock) count(l.w[r], true);
   __syncthreads();
   uint32_t* out = hists_of(p, PASS, seg);
-  for (int i = tid; i < BINS; i += kSelectBlock) out[i] = hist[i];
+  constexpr int W = BINS / kCoarse;
+#pragma unroll
+  for (int i = tid; i < BINS; i += kSelectBlock) {
+    int32_t n = (int32_t)hist[i];
+    out[kCoarse + i] = (uint32_t)n;
+#pragma unroll
+    for (int d = 1; d < W; d <<= 1) n += __shfl_xor(n, d);
+    if (tid % W == 0) out[i / W] = (uint32_t)n;
+  }
   if (PASS > 0 && tid == 0) {
     int32_t* st = p.states + 4 * seg;
     st[0] = (int32_t)f.key, st[1] = f.left, st[2] = f.before.above;
@@ -381,7 +421,7 @@ __global__ __launch_bounds__(kSelectBlock) void select_count_kernel(SelectParams
 }
 
 __global__ __launch_bounds__(kSelectBlock) void select_write_kernel(SelectParams p) {
-  __shared__ int32_t buf[2 * kSelectWaves], found[2], places[1];
+  __shared__ SumsBuf buf[2];
   __shared__ int32_t counts[2][kSelectWaves][2];
   const int s = blockIdx.x, b = blockIdx.y, lane = lane_id(), wave = uniform((int)(threadIdx.x >> 6));
   const Choice c = choice_of(p, b, false);
@@ -399,7 +439,7 @@ __global__ __launch_bounds__(kSelectBlock) void select_write_kernel(SelectParams
   fetch();
   const int32_t* st = p.states + 4 * seg;
   Found f{(uint32_t)st[0], st[1], {st[2], 0}};
-  f = next_digit<1 << kSegBits[2]>(p, f, hists_of(p, 2, (int64_t)b * p.segments), s, buf, found, places);
+  f = next_digit<1 << kSegBits[2]>(p, f, hists_of(p, 2, (int64_t)b * p.segments), s, buf);
   int turn = 0;
   for (int64_t t0 = begin; t0 < end; t0 += kSelectBlock * kTurn, turn ^= 1) {
     if (t0 > begin) {

@@ -90,14 +90,14 @@ struct WeighParams {
 // more slots are read by one workgroup a slot, once a digit.  Measured, us a call:
 // 64 slots of 16,384 rows in registers 13, in segments 26; of 32,768 rows in segments
 // and read by one workgroup each, 1 slot 27 and 38, 64 slots 29 and 41, 256 slots 61 and
-// 51, 512 slots 112 and 74; 16 slots of 131,072 rows 35 and 141.  (Segments of 32,768 rows
-// take a million rows from 44 to 59.)
+// 51, 512 slots 112 and 74; 16 slots of 131,072 rows 29 and 141.  Segments of 8,192 rows
+// take a million rows of one slot from 34 to 36, 20,000 of 100 slots from 28 to 47.
 constexpr int kSelectRegisterRows = 16384;
 constexpr int kSelectSegmentSlots = 128;
 constexpr int kSelectSegmentRows = 16384;
 constexpr int kSelectSegments = 512;
-// words of a segment in the workspace: three histograms, a state of 4
-constexpr int kSelectWords = 2048;
+// words of a segment in the workspace: three histograms with their sums, a state of 4
+constexpr int kSelectWords = 2048 + 64;
 
 struct SelectParams {
   int32_t ratio;

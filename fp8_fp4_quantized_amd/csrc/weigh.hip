@@ -837,7 +837,7 @@ struct Total {
 
 template <int L, int SLOTS>
 __global__ __launch_bounds__(kManyBlock) void weigh_many_kernel(WeighParams p) {
-  // (one object, the chunks at its begin: the loads that fill them reach 64 KB)
+  // (one object, the chunks at its begin)
   __shared__ struct {
     __attribute__((aligned(1024))) uint8_t rows[2][kChunkBytes];
     QueryRows info[3];

@@ -98,7 +98,8 @@ def test_select(kvc, lens, W, K, more, kind, pad):
 
 
 @pytest.mark.parametrize("n,K,kind", [(131072, 5000, "tail"), (131073, 100000, "ties"), (300001, 4096, "close"),
-                                      (262144, 262143, "signs"), (1000003, 65537, "ties")])
+                                      (262144, 262143, "signs"), (1000003, 65537, "ties"),
+                                      (9000001, 70001, "tail")])      # (the most segments)
 def test_select_long(kvc, n, K, kind):
     check_select(kvc, [n], weights_of(1, n, n, kind), K, first=4, recent=100)
 
