@@ -30,7 +30,7 @@ STATUS_TOKEN_RANGE = 64
 STATUS_NO_PAGE = 128
 ROPE_SCALING = {"none": 0, "linear": 1, "base": 2, "parts": 3}
 WEIGH_FEW = 128        # (token, head) pairs a slot may have without a workspace
-SELECT_NO_WORKSPACE = 16384   # weights a row may hold without a workspace
+SELECT_NO_WORKSPACE = 32768   # weights a row may hold without a workspace
 
 
 class KvcError(RuntimeError):

@@ -193,8 +193,16 @@ __global__ __launch_bounds__(kSelectBlock) void select_registers_kernel(SelectPa
   if (c.all) return;
   Digit d{0, c.take};
   uint32_t key = 0;
+  // (32 keys are made from the weights wherever they are needed: both would not fit, and
+  // the spills cost more -- 512 slots 62 us for 57; with 16 they fit, 13 us for 15)
+  auto keep_weights = [&]() {
+    if constexpr (E <= 24) return;
+#pragma unroll
+    for (int i = 0; i < E; ++i) asm volatile("" : "+v"(v[i]));
+  };
 #pragma unroll
   for (int pass = 0; pass < 3; ++pass) {
+    keep_weights();
     for (int i = tid; i < (pass == 0 ? kTopBins : kLowBins); i += kSelectBlock) hist[i] = 0;
     __syncthreads();
 #pragma unroll
@@ -217,6 +225,7 @@ __global__ __launch_bounds__(kSelectBlock) void select_registers_kernel(SelectPa
     }
   }
   Written at{0, 0};
+  keep_weights();
 #pragma unroll
   for (int i = 0; i < E; ++i) {
     const uint32_t k = weight_key(v[i]);
@@ -230,6 +239,7 @@ __global__ __launch_bounds__(kSelectBlock) void select_registers_kernel(SelectPa
   for (int w = 0; w < kSelectWaves; ++w) {
     if (w < wave) at.above += counts[w][0], at.equal += counts[w][1];
   }
+  keep_weights();
 #pragma unroll
   for (int i = 0; i < E; ++i)
     write_rows(l, c, at, key, d.left, r0 + i * kLanes, v[i], r0 + i * kLanes < c.hi);
@@ -735,6 +745,10 @@ hipError_t launch_select(const SelectParams& p, hipStream_t stream) {
     select_registers_kernel<1><<<slots, kSelectBlock, 0, stream>>>(p);
   } else if (p.w_width <= 4 * kSelectBlock) {
     select_registers_kernel<4><<<slots, kSelectBlock, 0, stream>>>(p);
+  } else if (p.w_width <= 16 * kSelectBlock) {
+    select_registers_kernel<16><<<slots, kSelectBlock, 0, stream>>>(p);
+  } else if (p.w_width <= 24 * kSelectBlock) {
+    select_registers_kernel<24><<<slots, kSelectBlock, 0, stream>>>(p);
   } else if (p.w_width <= kSelectRegisterRows) {
     select_registers_kernel<kSelectRegisterRows / kSelectBlock><<<slots, kSelectBlock, 0, stream>>>(p);
   } else {

@@ -88,11 +88,12 @@ struct WeighParams {
 // kSelectSegmentSlots slots, a slot's rows are cut into segments of at least
 // kSelectSegmentRows, kSelectSegments for all slots together at the most; those of
 // more slots are read by one workgroup a slot, once a digit.  Measured, us a call:
-// 64 slots of 16,384 rows in registers 13, in segments 26; of 32,768 rows in segments
-// and read by one workgroup each, 1 slot 27 and 38, 64 slots 29 and 41, 256 slots 61 and
-// 51, 512 slots 112 and 74; 16 slots of 131,072 rows 29 and 141.  Segments of 8,192 rows
-// take a million rows of one slot from 34 to 36, 20,000 of 100 slots from 28 to 47.
-constexpr int kSelectRegisterRows = 16384;
+// in registers and in segments, 64 slots of 16,384 rows 13 and 26, of 17,000 17 and 27, of
+// 32,768 26 and 29 (512 slots: 57, and 73 read once a digit); in segments and read once a
+// digit, 40,000 rows of 64 slots 29 and 47, of 128 slots 50 and 55, of 200 slots 69 and 69,
+// 100,000 of 64 slots 51 and 129.  Segments of 8,192 rows take a million rows of one slot
+// from 34 to 36.
+constexpr int kSelectRegisterRows = 32768;
 constexpr int kSelectSegmentSlots = 128;
 constexpr int kSelectSegmentRows = 16384;
 constexpr int kSelectSegments = 512;

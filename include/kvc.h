@@ -664,7 +664,7 @@ int kvc_weigh_tree(const kvc_weigh_args* args, void* stream);
  *                whose rows pass w_width (KVC_STATUS_PT_RANGE): its kept are -1
  *   kept_weights their weights, then 0, or NULL
  * workspace: kvc_evict_workspace bytes, 256-byte aligned, as the attention's; 0
- *   bytes (may be NULL) for rows of up to 16,384 weights. */
+ *   bytes (may be NULL) for rows of up to 32,768 weights. */
 typedef struct kvc_evict_args {
   int32_t ratio;              /* 1 or 2 */
   int32_t num_slots;          /* S, 0..8191 */

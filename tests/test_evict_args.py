@@ -140,7 +140,8 @@ def test_select_arguments(kvc):
 def test_evict_workspace_covers_smaller_calls(kvc):
     """What a call needs never passes the workspace of a larger one."""
     size = kvc.kvc_evict_workspace
-    assert size(1, 16384) == 0 and size(8191, 16384) == 0
+    assert size(1, kvc.SELECT_NO_WORKSPACE) == 0 and size(8191, kvc.SELECT_NO_WORKSPACE) == 0
+    assert size(1, kvc.SELECT_NO_WORKSPACE + 1) > 0
     widths = [1, 16384, 16385, 20000, 32768, 32769, 100000, 1 << 20, 1 << 23, 1 << 31, (1 << 63) - 1]
     slots = [0, 1, 2, 3, 60, 64, 127, 128, 129, 255, 256, 257, 8191]
     for i, s in enumerate(slots):

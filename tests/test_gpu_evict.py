@@ -110,11 +110,19 @@ def test_select_long_and_short_together(kvc):
 
 
 @pytest.mark.parametrize("S", [127, 128, 129])
-def test_select_long_rows_of_many_slots(kvc, S):
+@pytest.mark.parametrize("W", [16500, 33000])
+def test_select_long_rows_of_many_slots(kvc, S, W):
     rng = np.random.default_rng(S)
-    lens = rng.integers(0, 16500, S)
-    lens[:3] = [16500, 16385, -1]
-    check_select(kvc, lens, weights_of(S, 16500, 4, "ties"), 500, first=2, recent=30)
+    lens = rng.integers(0, W, S)
+    lens[:3] = [W, 16385, -1]
+    check_select(kvc, lens, weights_of(S, W, 4, "ties"), 500, first=2, recent=30)
+
+
+@pytest.mark.parametrize("W", [16384, 16385, 24576, 24577, 32768, 32769, 49153])
+@pytest.mark.parametrize("kind", ["tail", "ties", "signs"])
+def test_select_where_the_kernels_change(kvc, W, kind):
+    check_select(kvc, [W, W - 1, 9000, W, 0], weights_of(5, W, 6, kind), 4000, first=3, recent=77)
+    check_select(kvc, [W], weights_of(1, W, 7, kind), W - 1)
 
 
 def test_select_many_slots(kvc):
