@@ -263,13 +263,18 @@ __global__ __launch_bounds__(kRopeBlock) void rope_vectors_kernel(RopeRowsParams
           const Turned r = turn(v.f[e], v.f[e + 1], t[0], p.transpose ? -t[1] : t[1]);
           v.f[e] = r.a, v.f[e + 1] = r.b;
         }
-        // (dims that are copied keep their bits: a conversion changes some NaNs')
+        // (dims that are copied keep their bits: a conversion changes some NaNs'.  In
+        // place they are not stored at all: another stream may be writing them.  A 4-byte
+        // word is rotated whole or not, the first dim being even)
         const u32x4 made = v.bits();
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const int r = at + k * E / 4;
-          a[i][k] = r >= 0 && r < p.rot ? made[k] : a[i][k];
+          const bool turned = r >= 0 && r < p.rot;
+          if (p.in_place && turned) ((uint32_t*)out[i])[k] = made[k];
+          a[i][k] = turned ? made[k] : a[i][k];
         }
+        if (p.in_place) continue;
       }
     }
     *(u32x4*)out[i] = a[i];
