@@ -285,7 +285,8 @@ int weigh(const kvc_weigh_args* a, bool tree, void* stream, const char* who) {
   if (a->prev != nullptr && a->prev_stride < a->w_width)
     return fail(KVC_EINVAL, "%s: prev_stride %lld below w_width %lld", who, (long long)a->prev_stride,
                 (long long)a->w_width);
-  if (a->prev == a->weights && a->prev_stride != a->w_stride)
+  // (one slot's row has no next one)
+  if (a->prev == a->weights && a->num_slots > 1 && a->prev_stride != a->w_stride)
     return fail(KVC_EINVAL, "%s: prev is weights, with another stride", who);
   if (a->weights == a->lse) return fail(KVC_EINVAL, "%s: weights must not be an input", who);
   const int64_t slot_queries = (tree ? (int64_t)a->draft_len : a->q_rows) * a->num_heads;

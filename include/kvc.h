@@ -610,7 +610,7 @@ int kvc_rope_rows(const kvc_rope_args* args, void* stream);
  *   are left as they are, whatever prev and decay.  prev counts as 0 for the rows
  *   r >= start_pos[b] / ratio, which the call's tokens complete (they need no
  *   preparation), and everywhere where it is NULL or decay is 0; it may be weights
- *   itself.
+ *   itself (of several slots: with its stride).
  *   A query whose lse is not finite adds nothing; a row that is not finite
  *   collects nothing (and one whose sum passes fp32, as with another call's lse), and neither does a row whose page is outside the cache
  *   (KVC_STATUS_PAGE_RANGE).  Rows past pt_width pages or w_width entries are
