@@ -5,9 +5,13 @@
 // (first + i) * w_j.  The speeds w_j come from the host in 64 bits as half turns
 // a position; a thread makes its first entry and the turn from one of its
 // entries to the next by sincospi in 64 bits and goes on by complex products in
-// 64 bits (kTableRun of them: the error stays below 2^-45, far under the one
-// rounding to fp32).  Bound by the writes: a million positions of 64 dims, 268 MB, take
-// 46 to 48 us (5.6 to 5.8 TB/s); 4,096 of them 4.6.
+// 64 bits, kTableRun of them.  Where the positions of a turn are a power of two their
+// angle is exact and the products add 2^-48; elsewhere (10 dims: 51 positions) the
+// angle, up to 27 half turns at speeds up to 1, is rounded, which 31 products carry to
+// 31 pi 2^-49, below 2^-42, and in proportion for faster speeds: far under the one rounding
+// to fp32.  The angle of the first entry has a rounding of its own size.  Bound by the
+// writes: a million positions of 64 dims, 268 MB, take 46 to 48 us (5.6 to 5.8 TB/s);
+// 4,096 of them 4.6.
 //
 // Rotation: with (c, s) = freqs[position] the pair (a, b) becomes
 //   (a c - b s, a s + b c), transposed (a c + b s, b c - a s),
