@@ -286,13 +286,14 @@ struct Staged {
   // The query in fp16, times the power of two that brings its greatest value to
   // [2^14, 2^15); returns the power's inverse.  Exact for values down to 2^-31 of the
   // greatest; what is less is off by 2^-40 of that at the most, below the rounding of
-  // an fp32 sum.  (A power past 2^100 either way is left at that.)
+  // an fp32 sum.  (The power is 2^126 at the most, for a greatest value below 2^-112; the
+  // least, 2^-113, and the inverses of both are fp32 numbers.)
   __device__ __forceinline__ float to_f16() {
     uint32_t top = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) top = max(top, absmax_bf16x8(make_uint4(v[i].x, v[i].y, v[i].z, v[i].w)));
     top = group_max_u32<8>(top);
-    const int up = min(max(127 + 14 - (int)(top >> 7), -100), 100);
+    const int up = min(127 + 14 - (int)(top >> 7), 126);
     const float by = __uint_as_float((uint32_t)(127 + up) << 23);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
