@@ -911,6 +911,12 @@ def kvc_evict_workspace(num_slots: int, w_width: int) -> int:
     return n.value
 
 
+def _rows_32(n: int) -> int:
+    """A number of rows as the 32 bits that the library takes: one past them is as
+    many as there can be."""
+    return min(max(n, -1), 0x7FFFFFFF)
+
+
 def kvc_evict_select(lens: torch.Tensor, weights: torch.Tensor, kept: torch.Tensor,
                      counts: torch.Tensor, *, budget: int | None = None, ratio: int = 1,
                      first: int = 0, recent: int = 0, budgets: torch.Tensor | None = None,
@@ -934,8 +940,8 @@ def kvc_evict_select(lens: torch.Tensor, weights: torch.Tensor, kept: torch.Tens
         workspace = _scratch(kvc_evict_workspace(S, W), lens.device, stream)
     space, size = _bytes(workspace, "workspace", on)
     _call_on(lens.device, stream, lib().kvc_evict_select, kvc_evict_args(
-        ratio, S, lens_p, w, w_stride, W, K if budget is None else budget, first, recent,
-        _i32_on(budgets, S, "budgets", on), k, k_stride, K, _i32_on(counts, S, "counts", on), kw,
+        ratio, S, lens_p, w, w_stride, W, K if budget is None else _rows_32(budget), _rows_32(first),
+        _rows_32(recent), _i32_on(budgets, S, "budgets", on), k, k_stride, K, _i32_on(counts, S, "counts", on), kw,
         kw_stride, space, size, _i32_on(status, 1, "status", on)))
 
 
