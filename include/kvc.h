@@ -663,6 +663,9 @@ int kvc_weigh_tree(const kvc_weigh_args* args, void* stream);
  *   counts       their number; -1 for a slot that is inactive (lens[b] < 0) or
  *                whose rows pass w_width (KVC_STATUS_PT_RANGE): its kept are -1
  *   kept_weights their weights, then 0, or NULL
+ * To cut only the slots past a mark, to fewer rows than that: kept as wide as the
+ * mark, budgets[b] the mark itself for the slots within it.  Their count is then
+ * their rows, and kvc_cache_compact leaves them as they are.
  * workspace: kvc_evict_workspace bytes, 256-byte aligned, as the attention's; 0
  *   bytes (may be NULL) for rows of up to 32,768 weights. */
 typedef struct kvc_evict_args {
