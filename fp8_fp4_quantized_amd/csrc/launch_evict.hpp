@@ -92,7 +92,8 @@ struct WeighParams {
 // 32,768 26 and 29 (512 slots: 57, and 73 read once a digit); in segments and read once a
 // digit, 40,000 rows of 64 slots 29 and 47, of 128 slots 50 and 55, of 200 slots 69 and 69,
 // 100,000 of 64 slots 51 and 129.  Segments of 8,192 rows take a million rows of one slot
-// from 34 to 36.
+// from 34 to 36.  The width alone decides: 64 slots of 4,200 to 16,384 rows take 12 in rows
+// of weights that wide, 20 in 32,768 and 47 in 131,072 or more; 200 slots 12, 21 and 22.
 constexpr int kSelectRegisterRows = 32768;
 constexpr int kSelectSegmentSlots = 128;
 constexpr int kSelectSegmentRows = 16384;

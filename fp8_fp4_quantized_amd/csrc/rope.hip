@@ -409,7 +409,9 @@ hipError_t launch_vectors(RopeRowsParams p, hipStream_t stream) {
 // Measured, 8,192 tokens of 128 heads of 512 dims in bf16 from one tensor to another,
 // 2.15 GB: 366 us with pairs of neighbours and 414 with pairs of halves (5.9 and 5.2 TB/s);
 // by rope_any_kernel 565 and 686, which also takes an odd offset (665) and 511 dims
-// (734); element by element 1,745.
+// (734); element by element 1,745.  fp16 takes the same, fp32 370 and 389 for as many bytes.
+// In place all dims 386, the last 64 48, 36 dims from 6 on (half of 16 bytes at the ends,
+// stored by words) 55; pair by pair, an odd offset, 1,275.
 // Whether heads can be taken by 16 bytes: addresses, strides and dims of whole
 // ones, pairs inside one of them (or their halves at whole ones).
 bool by_vectors(const RopeRowsParams& p) {

@@ -674,7 +674,7 @@ typedef struct kvc_evict_args {
   const int32_t* lens;        /* device int32 [S]: tokens */
   const float* weights;       /* device fp32 [S, w_stride] */
   int64_t w_stride;           /* >= w_width */
-  int64_t w_width;            /* >= 1 */
+  int64_t w_width;            /* >= 1; no more than the longest slot's rows is faster */
   int32_t budget;             /* rows a slot keeps */
   int32_t first;              /* >= 0 */
   int32_t recent;             /* >= 0 */
